@@ -8,3 +8,5 @@ does, and it raises if the library is missing.
 from .api import (ZyfaError, flash_attn_func, hadamard_quantize_e4m3, hadamard_quantize_qk_e4m3,  # noqa: F401
                   library_path, load_library, zyfa_attn_fwd_causal, zyfa_attn_fwd_causal_ex, zyfa_check_errors,
                   zyfa_kernel_launches)
+from .paged import (PagedPlan, Rope, paged_decode_attn, paged_decode_workspace_bytes, paged_plan,  # noqa: F401
+                    rope_paged_store)

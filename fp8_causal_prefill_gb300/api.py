@@ -20,13 +20,15 @@ _lock = threading.Lock()
 ZYFA_DTYPE_E4M3 = 0
 ZYFA_DTYPE_BF16 = 1
 STATUS = {0: "ZYFA_OK", 1: "ZYFA_ERR_INVALID_ARG", 2: "ZYFA_ERR_UNSUPPORTED", 3: "ZYFA_ERR_MISALIGNED",
-          4: "ZYFA_ERR_CUDA", 5: "ZYFA_ERR_TIMEOUT"}
+          4: "ZYFA_ERR_CUDA", 5: "ZYFA_ERR_TIMEOUT", 6: "ZYFA_ERR_CAPACITY", 7: "ZYFA_ERR_BAD_PAGE"}
 EXPORTED = ("zyfa_attn_fwd_causal", "zyfa_attn_fwd_causal_ex", "zyfa_attn_fwd_causal_host", "zyfa_check_errors",
             "zyfa_status_string",
             "zyfa_kernel_launches", "zyfa_selftest_stalled_pipeline", "zyfa_hadamard_quantize_e4m3",
             "zyfa_hadamard_quantize_e4m3_noalloc", "zyfa_hadamard_quantize_qk_e4m3", "zyfa_hadamard_workspace_bytes",
             "zyfa_probe_mma_rate",
-            "zyfa_probe_mma_flops_per_iter", "zyfa_probe_mma_form_rate", "zyfa_probe_mma_form_flops_per_iter")
+            "zyfa_probe_mma_flops_per_iter", "zyfa_probe_mma_form_rate", "zyfa_probe_mma_form_flops_per_iter",
+            "zyfa_paged_plan", "zyfa_rope_paged_store", "zyfa_attn_decode_paged",
+            "zyfa_attn_decode_paged_workspace_bytes")
 ZYFA_P_LEAN = 0
 ZYFA_P_EXACT = 1
 ZYFA_P_EXACT_NO_BLOCK_SCALE = 2
@@ -36,6 +38,21 @@ _P_MODES = {"lean": ZYFA_P_LEAN, "exact": ZYFA_P_EXACT, "exact-noblock": ZYFA_P_
 class FwdOptions(ctypes.Structure):
     """zyfa_fwd_options_t: p_mode, descale_per_kv_head, lse (device pointer or None)."""
     _fields_ = [("p_mode", ctypes.c_int), ("descale_per_kv_head", ctypes.c_int), ("lse", ctypes.c_void_p)]
+
+
+class PagedCache(ctypes.Structure):
+    """zyfa_paged_cache_t: addresses, type, sizes and element strides of a paged key/value cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_longlong), ("H_kv", ctypes.c_int), ("D_qk", ctypes.c_int), ("D_v", ctypes.c_int),
+                ("k_page_stride", ctypes.c_longlong), ("k_token_stride", ctypes.c_longlong),
+                ("k_head_stride", ctypes.c_longlong), ("v_page_stride", ctypes.c_longlong),
+                ("v_token_stride", ctypes.c_longlong), ("v_head_stride", ctypes.c_longlong)]
+
+
+class RopeOptions(ctypes.Structure):
+    """zyfa_rope_t: frequencies, rotated channels and position axes of a rotary embedding."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("rot_offset", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("num_axes", ctypes.c_int), ("axis_pairs", ctypes.c_int * 4)]
 
 
 class ZyfaError(RuntimeError):
@@ -91,6 +108,17 @@ def load_library() -> ctypes.CDLL:
         lib.zyfa_probe_mma_form_rate.restype = ci
         lib.zyfa_probe_mma_form_flops_per_iter.argtypes = [ci]
         lib.zyfa_probe_mma_form_flops_per_iter.restype = ll
+        cache, rope = ctypes.POINTER(PagedCache), ctypes.POINTER(RopeOptions)
+        lib.zyfa_paged_plan.argtypes = [vp, vp, ci, ci, vp, ll, ci, vp, ci, vp, vp, vp, vp, vp, vp, ci, vp]
+        lib.zyfa_paged_plan.restype = ci
+        lib.zyfa_rope_paged_store.argtypes = [vp, vp, vp, ll, ll, ll, vp, vp, vp, vp, ll, vp, ll, ci, cache, rope,
+                                              vp, vp, vp, ci, vp]
+        lib.zyfa_rope_paged_store.restype = ci
+        lib.zyfa_attn_decode_paged.argtypes = [vp, ll, cache, vp, ll, ci, vp, vp, vp, ci, ci, cf, vp, vp, vp, ci, vp,
+                                               sz, vp]
+        lib.zyfa_attn_decode_paged.restype = ci
+        lib.zyfa_attn_decode_paged_workspace_bytes.argtypes = [ci, ci, ci, ci]
+        lib.zyfa_attn_decode_paged_workspace_bytes.restype = sz
         _lib = lib
         return lib
 

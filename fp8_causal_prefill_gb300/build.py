@@ -1,6 +1,6 @@
 """Build libzyfa.so (the C-ABI library) in-tree for sm_103a with nvcc.
 
-The three translation units compile in parallel; the shared library lands next to this file, where
+The translation units compile in parallel; the shared library lands next to this file, where
 ``fp8_causal_prefill_gb300.api`` loads it.  Run as ``python -m fp8_causal_prefill_gb300.build``.
 """
 from __future__ import annotations
@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzyfa.so")
 SOURCES = ["zyfa_api.cu", "zyfa_kernels_fp8.cu", "zyfa_kernels_fp8_exact.cu", "zyfa_kernels_bf16.cu",
-           "zyfa_hadamard.cu", "zyfa_probe.cu"]
+           "zyfa_hadamard.cu", "zyfa_probe.cu", "zyfa_paged_plan.cu", "zyfa_rope_store.cu", "zyfa_decode.cu"]
 # The attention kernel splits its registers between warpgroups at run time (setmaxnreg); the split is
 # sized for exactly this many registers per thread at launch, which every instantiation must get.
 KERNEL_REGS = 168

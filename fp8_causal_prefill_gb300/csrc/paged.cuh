@@ -1,0 +1,65 @@
+// What the paged serving operators share: status bits, the device view of a paged cache, its host checks.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "zyfa.h"
+
+namespace zyfa {
+
+// Bits of the library's per-device status word (zyfa_check_errors clears and reports them).
+enum : int { kStatusTimeoutBit = 1, kStatusCapacityBit = 2, kStatusBadPageBit = 4 };
+
+// Per-device lookups of zyfa_api.cu (cached per device): the status word's address, the SM count.
+// nullptr / 0 if the CUDA call behind them fails.
+int* device_status_word(int dev);
+int device_sm_count(int dev);
+
+// Strides in bytes; an offset is formed in 64 bits, since a long cache passes 2^31 bytes and elements.
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  long long num_pages;
+  long long k_page, k_tok, k_head, v_page, v_tok, v_head;
+  int page_size, H_kv;
+};
+
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+inline int element_size(zyfa_dtype_t t) { return t == ZYFA_DTYPE_E4M3 ? 1 : 2; }
+
+inline zyfa_status_t check_cache(const zyfa_paged_cache_t* c, CacheView* view) {
+  if (!c) return ZYFA_ERR_INVALID_ARG;
+  if (c->dtype != ZYFA_DTYPE_E4M3 && c->dtype != ZYFA_DTYPE_BF16) return ZYFA_ERR_INVALID_ARG;
+  if (c->page_size < 1 || c->page_size > 65536 || c->num_pages < 1 || c->H_kv < 1) return ZYFA_ERR_INVALID_ARG;
+  const bool shape_ok = (c->D_qk == 64 && c->D_v == 64) || (c->D_qk == 128 && c->D_v == 128) ||
+                        (c->D_qk == 192 && c->D_v == 128);
+  if (!shape_ok) return ZYFA_ERR_UNSUPPORTED;
+  if (!c->k || !c->v) return ZYFA_ERR_INVALID_ARG;
+  const long long es = element_size(c->dtype);
+  const long long strides[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
+                                c->v_page_stride, c->v_token_stride, c->v_head_stride};
+  bool whole = aligned(c->k, 16) && aligned(c->v, 16);
+  for (long long s : strides) {
+    if (s < 0) return ZYFA_ERR_INVALID_ARG;
+    if (s > (1ll << 46)) return ZYFA_ERR_UNSUPPORTED;
+    whole = whole && (s * es) % 16 == 0;
+  }
+  if (!whole) return ZYFA_ERR_MISALIGNED;
+  if (c->num_pages > (1ll << 31) - 1) return ZYFA_ERR_UNSUPPORTED;  // page numbers are int32
+  view->k = static_cast<uint8_t*>(c->k);
+  view->v = static_cast<uint8_t*>(c->v);
+  view->num_pages = c->num_pages;
+  view->k_page = c->k_page_stride * es;
+  view->k_tok = c->k_token_stride * es;
+  view->k_head = c->k_head_stride * es;
+  view->v_page = c->v_page_stride * es;
+  view->v_tok = c->v_token_stride * es;
+  view->v_head = c->v_head_stride * es;
+  view->page_size = c->page_size;
+  view->H_kv = c->H_kv;
+  return ZYFA_OK;
+}
+
+}  // namespace zyfa

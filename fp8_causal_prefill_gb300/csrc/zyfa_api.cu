@@ -12,10 +12,11 @@
 
 #include "../../include/zyfa.h"
 #include "launch.h"
+#include "paged.cuh"
 
 namespace {
 
-// Set by a kernel that gave up on a pipeline wait; read and cleared by zyfa_check_errors.
+// Set by a kernel that gave up on a pipeline wait or met a bad page; read and cleared by zyfa_check_errors.
 __device__ int g_zyfa_status;
 
 constexpr int kMaxDevices = 64;
@@ -142,6 +143,11 @@ zyfa_status_t run(zyfa::LaunchArgs& a, const void* q, const void* k, const void*
 
 }  // namespace
 
+namespace zyfa {
+int* device_status_word(int dev) { return dev >= 0 && dev < kMaxDevices ? status_ptr(dev) : nullptr; }
+int device_sm_count(int dev) { return dev >= 0 && dev < kMaxDevices ? sm_count(dev) : 0; }
+}  // namespace zyfa
+
 extern "C" {
 
 const char* zyfa_status_string(zyfa_status_t s) {
@@ -152,6 +158,8 @@ const char* zyfa_status_string(zyfa_status_t s) {
     case ZYFA_ERR_MISALIGNED: return "ZYFA_ERR_MISALIGNED";
     case ZYFA_ERR_CUDA: return "ZYFA_ERR_CUDA";
     case ZYFA_ERR_TIMEOUT: return "ZYFA_ERR_TIMEOUT";
+    case ZYFA_ERR_CAPACITY: return "ZYFA_ERR_CAPACITY";
+    case ZYFA_ERR_BAD_PAGE: return "ZYFA_ERR_BAD_PAGE";
   }
   return "ZYFA_ERR_UNKNOWN";
 }
@@ -353,7 +361,8 @@ zyfa_status_t zyfa_check_errors(cudaStream_t stream) {
   if (value != 0) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_zyfa_status, &zero, sizeof(int)) != cudaSuccess) return ZYFA_ERR_CUDA;
-    return ZYFA_ERR_TIMEOUT;
+    if (value & zyfa::kStatusTimeoutBit) return ZYFA_ERR_TIMEOUT;
+    return value & zyfa::kStatusCapacityBit ? ZYFA_ERR_CAPACITY : ZYFA_ERR_BAD_PAGE;
   }
   return ZYFA_OK;
 }

@@ -55,7 +55,9 @@ typedef enum {
   ZYFA_ERR_UNSUPPORTED = 2, /* head shape outside the supported list, or sizes beyond int range   */
   ZYFA_ERR_MISALIGNED = 3,  /* q, k, v or out not 16-byte aligned (TMA and vector stores need it) */
   ZYFA_ERR_CUDA = 4,        /* a CUDA runtime / driver call failed (launch, attribute, tensor map) */
-  ZYFA_ERR_TIMEOUT = 5      /* a kernel gave up waiting on a pipeline barrier (see check_errors)  */
+  ZYFA_ERR_TIMEOUT = 5,     /* a kernel gave up waiting on a pipeline barrier (see check_errors)  */
+  ZYFA_ERR_CAPACITY = 6,    /* a page plan ran out of pages, table columns or token rows (check_errors) */
+  ZYFA_ERR_BAD_PAGE = 7     /* a page or slot outside the cache was met and skipped (check_errors) */
 } zyfa_status_t;
 
 /*
@@ -223,8 +225,138 @@ zyfa_status_t zyfa_hadamard_quantize_e4m3_noalloc(const void* x, void* x8, float
 size_t zyfa_hadamard_workspace_bytes(long long rows);
 
 /*
+ * The paged key/value cache of the serving entry points below (they have no counterpart in the pages,
+ * which describe the prefill only).  Token t of a request lives in slot page * page_size + t % page_size,
+ * where `page` is entry t / page_size of the request's row of a block table.  Strides are in elements, so
+ * [num_pages][page_size][H_kv][D] tensors, [num_pages][H_kv][page_size][D] tensors and the halves of one
+ * combined tensor are all described; the D elements of one token and head are contiguous.
+ */
+typedef struct {
+  void* k;               /* device pointers, 16-byte aligned                                           */
+  void* v;
+  zyfa_dtype_t dtype;    /* of both: e4m3 bytes or bf16                                                */
+  int page_size;         /* tokens per page, 1 .. 65536                                                */
+  long long num_pages;   /* >= 1                                                                       */
+  int H_kv, D_qk, D_v;   /* head shapes as for zyfa_attn_fwd_causal                                    */
+  long long k_page_stride, k_token_stride, k_head_stride;  /* >= 0, multiples of 16 bytes              */
+  long long v_page_stride, v_token_stride, v_head_stride;
+} zyfa_paged_cache_t;
+
+/*
+ * zyfa_paged_plan - pages, slots and positions of one serving step, from request lengths on the device.
+ *
+ * Request b holds cached_lens[b] tokens and adds new_lens[b] (negative lengths count as 0).  Its tokens
+ * are numbered on from cached_lens[b]; the pages that start with one of them, in order of requests and
+ * then of pages, are taken from free_pages[*cursor_in], free_pages[*cursor_in + 1], ... and written
+ * into the request's row of block_table.  Nothing else of the table is written.
+ *
+ *   cached_lens, new_lens  [B] int32.
+ *   block_table            [B][table_stride] int32, max_pages <= table_stride columns in use; read for the
+ *                          page that a request's last cached token lies in, written as above.
+ *   free_pages, num_free   [num_free] int32 page numbers (any order); cursor_in, cursor_out: one int32
+ *                          each, which may be the same address: pages before the cursor are taken.
+ *   seq_lens               [B] int32, written: lengths with the new tokens, at most max_pages * page_size.
+ *   cu_tokens              [B + 1] int32, written: cu_tokens[b] is the first token row of request b.
+ *   positions, slots       [max_tokens] int32 and int64, written in full: position and cache slot of each
+ *                          token row; rows behind the last token get position 0 and slot -1.
+ *
+ * A token that gets no slot (no free page left, a page beyond max_pages, a table entry below 0) has slot
+ * -1, the page it would have started is -1 in the table, and zyfa_check_errors() then returns
+ * ZYFA_ERR_CAPACITY, as it does when the tokens are more than max_tokens (the rows behind are dropped).
+ * Asynchronous on `stream`, one launch, allocates nothing, no atomics on results.  The outputs must not overlap
+ * one another or the inputs (cursors excepted).  Errors: ZYFA_ERR_INVALID_ARG (null pointers; B, max_tokens,
+ * num_free or max_pages < 0, table_stride < max_pages, page_size outside 1 .. 65536),
+ * ZYFA_ERR_UNSUPPORTED (max_pages * page_size beyond 2^30, B beyond 65536), ZYFA_ERR_MISALIGNED
+ * (pointers not aligned to their type), ZYFA_ERR_CUDA.  B == 0 still writes cu_tokens[0], the cursor and the rows.
+ */
+zyfa_status_t zyfa_paged_plan(const int* cached_lens, const int* new_lens, int B, int page_size, int* block_table,
+                              long long table_stride, int max_pages, const int* free_pages, int num_free,
+                              const int* cursor_in, int* cursor_out, int* seq_lens, int* cu_tokens, int* positions,
+                              long long* slots, int max_tokens, cudaStream_t stream);
+
+/* Rotary positions with one to four axes (for example time, height and width of an image or video patch). */
+typedef struct {
+  const float* inv_freq; /* device, [rot_dim / 2]: radians per unit of position, magnitude below 2^24    */
+  int rot_dim;           /* rotated channels, a multiple of 16 (0: no rotation)                          */
+  int rot_offset;        /* first rotated channel, a multiple of 8; rot_offset + rot_dim <= D_qk         */
+  int interleaved;       /* pair i of the rotated channels: 0: (i, i + rot_dim/2); 1: (2i, 2i + 1)       */
+  int num_axes;          /* 1 .. 4                                                                       */
+  int axis_pairs[4];     /* the first axis_pairs[0] pairs turn with axis 0, the next [1] with axis 1 ... */
+                         /* (each >= 0, together rot_dim / 2)                                            */
+} zyfa_rope_t;
+
+/*
+ * zyfa_rope_paged_store - rotate a step's queries and keys by their positions and write keys and values
+ * into their slots of a paged cache, in one pass.
+ *
+ * Pair i of token n turns by the angle positions[axis(i)][n] * inv_freq[i] (taken exactly, then reduced):
+ * (a, b) -> (a cos - b sin, a sin + b cos) in fp32.  Values are rounded once to the cache's type:
+ * bf16, or the e4m3 code rne_satfinite(fl32(y * fl32(1 / descale))).
+ *
+ *   q, k, v           bf16 device tensors [N][H][D_qk], [N][H_kv][D_qk], [N][H_kv][D_v] whose token strides
+ *                     (elements, multiples of 8) are given; heads are dense within a token.  16-byte aligned.
+ *                     q may be NULL (then q_out is ignored); k and v may be NULL together.
+ *   q_out             [N][H][D_qk] dense, in the cache's type, 16-byte aligned.
+ *   k_out, v_out      NULL, or dense [N][H_kv][D_qk] and [N][H_kv][D_v] copies in the cache's type, as
+ *                     zyfa_attn_fwd_causal reads them.
+ *   positions         int32 [num_axes][position_stride >= N]; may be NULL without rotation.
+ *   slots             int64 [N]: the token's cache slot.  Below 0: the token is padding, and nothing at all is
+ *                     written for it.  Slots of one call are distinct (two tokens of one slot leave
+ *                     an unspecified mixture).  A slot beyond the cache is not written (q_out and the dense
+ *                     copies are) and zyfa_check_errors() returns ZYFA_ERR_BAD_PAGE.
+ *   rope              NULL: no rotation.
+ *   q/k/v_descale     e4m3 only: device pointers to one float (or H_kv floats with descale_per_kv_head = 1;
+ *                     query head h uses hk = h / (H / H_kv)); NULL means 1.  Ignored for bf16.
+ *
+ * Outputs must not overlap one another or the inputs.  One launch, asynchronous on `stream`, allocates
+ * nothing.  N == 0 returns ZYFA_OK.
+ */
+zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v, long long q_token_stride,
+                                    long long k_token_stride, long long v_token_stride, void* q_out, void* k_out,
+                                    void* v_out, const int* positions, long long position_stride,
+                                    const long long* slots, long long N, int H, const zyfa_paged_cache_t* cache,
+                                    const zyfa_rope_t* rope, const float* q_descale, const float* k_descale,
+                                    const float* v_descale, int descale_per_kv_head, cudaStream_t stream);
+
+/*
+ * zyfa_attn_decode_paged - attention of one new token per request over a paged cache:
+ *
+ *     out[b, h, :] = sum_{j < seq_lens[b]} softmax_j(scale * q[b,h,:] . k[slot(b,j), hk, :]) * v[slot(b,j), hk, :]
+ *
+ *   q                 [B][H][D_qk] in the cache's type, requests q_batch_stride elements apart (a multiple of
+ *                     16 bytes), heads dense; 16-byte aligned.
+ *   block_table       [B][table_stride >= max_pages] int32; only the entries that seq_lens[b] tokens need are
+ *                     read.  Requests may share pages.
+ *   seq_lens          [B] int32, on the device; taken as 0 below 0 and as max_pages * page_size above it.
+ *   out               [B][H][D_v] bf16 dense, written in full: 0 for a request without tokens.
+ *   lse               NULL, or [B][H] floats: ln sum_j exp(scale q.k) in real units, -inf without tokens.
+ *   softmax_scale     0 selects 1/sqrt(D_qk); negative, NaN or infinite values are rejected.
+ *   q/k/v_descale     e4m3 only: one float, or [B][H_kv] floats with descale_per_kv_head = 1; NULL means 1.
+ *   workspace         device scratch of zyfa_attn_decode_paged_workspace_bytes() bytes, 16-byte aligned; its
+ *                     contents on entry do not matter.  Calls that may overlap on the GPU (other streams, two
+ *                     captured graphs) need one each.
+ *
+ * Tokens whose page lies outside [0, num_pages) are left out of the softmax and zyfa_check_errors() returns
+ * ZYFA_ERR_BAD_PAGE.  Cache rows behind a request's length are never read, whatever they hold.
+ * Scores and sums are held in fp32; the weights exp(s - max) are rounded to 16 bits before they
+ * multiply V (fp16 for an e4m3 cache, whose values fp16 holds exactly, else bf16).  Bitwise reproducible
+ * for identical inputs on one GPU model.  Asynchronous on `stream`, allocates nothing, no host synchronisation.
+ */
+zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache,
+                                     const int* block_table, long long table_stride, int max_pages,
+                                     const int* seq_lens, void* out, float* lse, int B, int H, float softmax_scale,
+                                     const float* q_descale, const float* k_descale, const float* v_descale,
+                                     int descale_per_kv_head, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+/* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged for these sizes on the current
+ * device; the same whatever the lengths are.  0 for sizes that the call refuses. */
+size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v);
+
+/*
  * zyfa_check_errors - synchronise `stream`, then read and clear the current device's status word.
- * Returns ZYFA_ERR_TIMEOUT if any kernel of this library timed out since the last check,
+ * Returns ZYFA_ERR_TIMEOUT if any kernel of this library timed out since the last check, else
+ * ZYFA_ERR_CAPACITY or ZYFA_ERR_BAD_PAGE (the first that applies) if a serving call met one,
  * ZYFA_ERR_CUDA if the synchronisation itself failed, ZYFA_OK otherwise.
  */
 zyfa_status_t zyfa_check_errors(cudaStream_t stream);
