@@ -263,7 +263,7 @@ def rope_paged_store(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Te
 
 
 def paged_decode_workspace_bytes(B: int, H: int, H_kv: int, D_v: int) -> int:
-    """Bytes of the ``workspace`` that ``paged_decode_attn`` needs for these sizes on the current device."""
+    """Bytes of the ``workspace`` that ``paged_decode_attn`` needs for these sizes."""
     return load_library().zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v)
 
 
@@ -305,9 +305,7 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         per_head = 0
     lib = load_library()
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = lib.zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(lib.zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v), dtype=torch.uint8, device=q.device)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
         raise TypeError("workspace must be a contiguous uint8 tensor on the cache's device")
     _call(dev, lib.zyfa_attn_decode_paged, q.data_ptr(), s[0] if B > 1 else H * D, ctypes.byref(c), table, stride, width,

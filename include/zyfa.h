@@ -349,8 +349,8 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
                                      int descale_per_kv_head, void* workspace, size_t workspace_bytes,
                                      cudaStream_t stream);
 
-/* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged for these sizes on the current
- * device; the same whatever the lengths are.  0 for sizes that the call refuses. */
+/* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged for these sizes, the same whatever
+ * the lengths are.  Pure host arithmetic; 0 for sizes that the call refuses. */
 size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v);
 
 /*
