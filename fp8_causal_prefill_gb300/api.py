@@ -117,7 +117,7 @@ def load_library() -> ctypes.CDLL:
         lib.zyfa_attn_decode_paged.argtypes = [vp, ll, cache, vp, ll, ci, vp, vp, vp, ci, ci, cf, vp, vp, vp, ci, vp,
                                                sz, vp]
         lib.zyfa_attn_decode_paged.restype = ci
-        lib.zyfa_attn_decode_paged_workspace_bytes.argtypes = [ci, ci, ci, ci]
+        lib.zyfa_attn_decode_paged_workspace_bytes.argtypes = [ci, ci, ci, ci, ll]
         lib.zyfa_attn_decode_paged_workspace_bytes.restype = sz
         _lib = lib
         return lib

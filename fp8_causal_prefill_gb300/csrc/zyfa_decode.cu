@@ -594,7 +594,10 @@ long long round_up(long long x, long long n) { return (x + n - 1) / n * n; }
 // Chunks of up to 16 query heads that the heads of one KV head are cut into, as equal as they come.
 int chunks_of(int group) { return (group + 15) / 16; }
 
-int groups_of(int warps, int units) { return warps / units > 1 ? warps / units : 1; }
+// Groups of `units` warps that work on a call: as many as are resident at once, and no more than there can be tiles.
+long long groups_of(long long warps, long long units, long long tiles) { return std::max(1ll, std::min(warps / units, tiles)); }
+
+long long tiles_at_most(int B, long long max_len, int keys) { return B * ((max_len + keys - 1) / keys); }
 
 constexpr int kMaxDevices = 64;
 
@@ -606,7 +609,7 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   const int smem = a.ring_bytes * kWarps;
   // one wave of resident blocks: 228 KiB of shared memory per SM, 1 KiB of it taken per block
   const int fit = std::min(T::blocks(NT), 233472 / (smem + 1024));
-  a.groups = groups_of(nsm * fit * kWarps, a.units);
+  a.groups = static_cast<int>(groups_of(nsm * fit * kWarps, a.units, tiles_at_most(a.B, a.max_len, T::kKeys)));
   // workspace: plan, (m, l), O
   a.starts = reinterpret_cast<int*>(ws);
   ws += round_up((a.B + 2ll) * 4, 256);
@@ -639,10 +642,10 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
 
 extern "C" {
 
-size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v) {
-  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || (D_v != 64 && D_v != 128)) return 0;
+size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v, long long max_len) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || (D_v != 64 && D_v != 128) || max_len < 0) return 0;
   const long long units = static_cast<long long>(H_kv) * chunks_of(H / H_kv);
-  const long long groups = groups_of(kMaxSms * kMaxWarpsPerSm, static_cast<int>(units));
+  const long long groups = groups_of(kMaxSms * kMaxWarpsPerSm, units, tiles_at_most(B, max_len, 16));
   return static_cast<size_t>(round_up((B + 2ll) * 4, 256) + round_up(2 * groups * H * 8, 256) + 2 * groups * H * D_v * 4);
 }
 
@@ -673,7 +676,9 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
       !aligned(block_table, 4) || !aligned(lse, 4) || !aligned(q_descale, 4) || !aligned(k_descale, 4) ||
       !aligned(v_descale, 4))
     return ZYFA_ERR_MISALIGNED;
-  if (!workspace || workspace_bytes < zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v)) return ZYFA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < zyfa_attn_decode_paged_workspace_bytes(
+                                          B, H, H_kv, D_v, static_cast<long long>(max_pages) * cache->page_size))
+    return ZYFA_ERR_INVALID_ARG;
   if (!aligned(workspace, 16)) return ZYFA_ERR_MISALIGNED;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ZYFA_ERR_CUDA;

@@ -4,15 +4,22 @@
 // which are free_pages[cursor + sum_{a<b} need_a ...]; its token rows begin at cu_b = sum_{a<b} n_a.  Token i
 // has position c_b + i, and slot page * P + position % P, where the page is a fresh one or the one of the
 // table that the last cached token lies in.
+//
+// Bound: latency (the tables of a step are a few KB to a MB).  One launch: every block takes a run of token rows,
+// forms the two prefix sums over the requests itself (1024 requests at a time in shared memory; the lengths come from
+// L2 once another block has read them) rather than wait for another block, and finds the request of a row by
+// bisection.  A fresh page always begins with a new token, so the thread of that token's row writes the table entry and
+// no block depends on another's writes.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "paged.cuh"
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256, kPerThread = 4, kChunk = kThreads * kPerThread, kWarps = kThreads / 32;
 
 struct PlanArgs {
   const int* cached;
@@ -28,69 +35,135 @@ struct PlanArgs {
   int* status;
   long long table_stride;
   int B, page, max_pages, num_free, max_tokens;
+  int rows;             // token rows per block
+  int cursor_only;      // a second launch that only moves the cursor
+  int write_cursor;
+  uint32_t page_magic;  // floor(t / page) = t * page_magic >> page_shift for t < 2^31
+  int page_shift;
 };
 
 __device__ __forceinline__ int saturated(long long x) { return x > 0x7fffffffll ? 0x7fffffff : static_cast<int>(x); }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
-  __shared__ long long s_tok, s_page;
-  __shared__ int s_bad;
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    s_tok = 0;
-    s_page = 0;
-    s_bad = 0;
-  }
-  __syncthreads();
-  const long long cursor = max(0, *a.cursor_in);
-  const long long cap = static_cast<long long>(a.max_pages) * a.page;
-  for (int b = 0; b < a.B; ++b) {
-    const long long c = max(0, a.cached[b]), n = max(0, a.fresh[b]);
-    const long long len = c + n;
-    const int had = static_cast<int>(min((c + a.page - 1) / a.page, static_cast<long long>(a.max_pages)));
-    const int has = static_cast<int>(min((len + a.page - 1) / a.page, static_cast<long long>(a.max_pages)));
-    const long long first = cursor + s_page, row = s_tok;
-    int* table = a.table + b * a.table_stride;
-    bool bad = len > cap || row + n > a.max_tokens;
-    for (int p = had + tid; p < has; p += kThreads) {
-      const long long f = first + p - had;
-      table[p] = f < a.num_free ? a.free_pages[f] : -1;
-      bad |= f >= a.num_free;
+__global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
+  __shared__ long long s_tok[kChunk + 1], s_page[kChunk];  // exclusive sums of n and need within the chunk
+  __shared__ int s_cached[kChunk];
+  __shared__ long long s_wtok[kWarps], s_wpage[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool lead = blockIdx.x == 0 && !a.cursor_only;      // writes the per-request results
+  const bool tail = blockIdx.x == gridDim.x - 1;            // takes rows behind max_tokens (their pages count) too
+  const int cursor = max(0, __ldg(a.cursor_in));
+  const int cap = a.max_pages * a.page;                     // at most 2^30
+  const long long r0 = static_cast<long long>(blockIdx.x) * a.rows;
+  const long long r1 = min(r0 + a.rows, static_cast<long long>(a.max_tokens));
+  auto pages_before = [&](long long t) {                    // floor(t / page) of t <= cap + page
+    return static_cast<int>((static_cast<unsigned long long>(t) * a.page_magic) >> a.page_shift);
+  };
+  long long tok = 0, page = 0;                              // sums over the chunks so far
+  bool bad = false;
+  for (int b0 = 0; b0 < a.B; b0 += kChunk) {
+    // per-thread sums over its four requests, then across the warp and the block
+    long long n[kPerThread], need[kPerThread], nsum = 0, psum = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int b = b0 + tid * kPerThread + i;
+      const int c = b < a.B ? max(0, __ldg(a.cached + b)) : 0;
+      n[i] = b < a.B ? max(0, __ldg(a.fresh + b)) : 0;
+      const long long len = c + n[i];
+      const int had = pages_before(min(c, cap) + a.page - 1), has = pages_before(min(len, static_cast<long long>(cap)) + a.page - 1);
+      need[i] = has - had;
+      if (b < a.B) {
+        s_cached[tid * kPerThread + i] = c;
+        if (lead) {
+          a.seq_lens[b] = static_cast<int>(min(len, static_cast<long long>(cap)));
+          bad |= len > cap;
+        }
+      }
+      nsum += n[i];
+      psum += need[i];
     }
-    for (long long i = tid; i < n && row + i < a.max_tokens; i += kThreads) {
-      const long long pos = c + i;
+    long long ntok = nsum, npage = psum;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, ntok, s), v = __shfl_up_sync(0xffffffffu, npage, s);
+      if (lane >= s) {
+        ntok += u;
+        npage += v;
+      }
+    }
+    if (lane == 31) {
+      s_wtok[warp] = ntok;
+      s_wpage[warp] = npage;
+    }
+    __syncthreads();
+    long long all_tok = 0, all_page = 0;
+    ntok -= nsum;
+    npage -= psum;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) {
+        ntok += s_wtok[i];
+        npage += s_wpage[i];
+      }
+      all_tok += s_wtok[i];
+      all_page += s_wpage[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int x = tid * kPerThread + i;
+      s_tok[x] = ntok;
+      s_page[x] = npage;
+      if (lead && b0 + x < a.B) a.cu_tokens[b0 + x] = saturated(tok + ntok);
+      ntok += n[i];
+      npage += need[i];
+    }
+    if (tid == 0) s_tok[kChunk] = all_tok;
+    __syncthreads();
+    // this block's rows among the chunk's
+    const long long end = a.cursor_only ? 0 : tail ? tok + all_tok : min(r1, tok + all_tok);
+    for (long long r = max(r0, tok) + tid; r < end; r += kThreads) {
+      const long long x = r - tok;
+      int lo = 0, hi = min(kChunk, a.B - b0);               // s_tok[lo] <= x < s_tok[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tok[mid] <= x) lo = mid; else hi = mid;
+      }
+      const int c = s_cached[lo];
+      const long long pos = c + (x - s_tok[lo]);
       long long slot = -1;
       if (pos < cap) {
-        const int p = static_cast<int>(pos / a.page);
-        const long long f = first + p - had;
-        const int pg = p < had ? table[p] : f < a.num_free ? a.free_pages[f] : -1;
-        if (pg >= 0) slot = static_cast<long long>(pg) * a.page + pos % a.page;
+        const int p = pages_before(pos), had = pages_before(min(c, cap) + a.page - 1), off = static_cast<int>(pos) - p * a.page;
+        int* entry = a.table + static_cast<long long>(b0 + lo) * a.table_stride + p;
+        int pg;
+        if (p < had) {
+          pg = *entry;
+        } else {
+          const long long f = cursor + page + s_page[lo] + (p - had);
+          pg = f < a.num_free ? __ldg(a.free_pages + f) : -1;
+          if (off == 0) *entry = pg;
+        }
         bad |= pg < 0;
+        if (pg >= 0) slot = static_cast<long long>(pg) * a.page + off;
       }
-      a.positions[row + i] = saturated(pos);
-      a.slots[row + i] = slot;
+      if (r < a.max_tokens) {
+        a.positions[r] = saturated(pos);
+        a.slots[r] = slot;
+      }
     }
-    if (bad) s_bad = 1;
-    if (tid == 0) {
-      a.seq_lens[b] = static_cast<int>(min(len, cap));
-      a.cu_tokens[b] = saturated(row);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      s_tok = row + n;
-      s_page += has - had;
-    }
+    tok += all_tok;
+    page += all_page;
     __syncthreads();
   }
-  for (long long i = s_tok + tid; i < a.max_tokens; i += kThreads) {
-    a.positions[i] = 0;
-    a.slots[i] = -1;
+  for (long long r = max(r0, tok) + tid; r < r1 && !a.cursor_only; r += kThreads) {
+    a.positions[r] = 0;
+    a.slots[r] = -1;
   }
-  if (tid == 0) {
-    a.cu_tokens[a.B] = saturated(s_tok);
-    *a.cursor_out = static_cast<int>(min(cursor + s_page, static_cast<long long>(max(a.num_free, static_cast<int>(cursor)))));
-    if (s_bad) atomicOr(a.status, zyfa::kStatusCapacityBit);
+  if (lead && tid == 0) {
+    a.cu_tokens[a.B] = saturated(tok);
+    bad |= tok > a.max_tokens;
   }
+  if (bad) atomicOr(a.status, zyfa::kStatusCapacityBit);
+  if (tail && a.write_cursor && tid == 0)
+    *a.cursor_out = static_cast<int>(min(cursor + page, static_cast<long long>(max(a.num_free, cursor))));
 }
 
 }  // namespace
@@ -116,9 +189,41 @@ extern "C" zyfa_status_t zyfa_paged_plan(const int* cached_lens, const int* new_
   if (cudaGetDevice(&dev) != cudaSuccess) return ZYFA_ERR_CUDA;
   int* status = zyfa::device_status_word(dev);
   if (!status) return ZYFA_ERR_CUDA;
-  const PlanArgs a = {cached_lens, new_lens,  block_table, free_pages, cursor_in, cursor_out, seq_lens,   cu_tokens,
-                      positions,   slots,     status,      table_stride, B,       page_size,  max_pages,  num_free,
-                      max_tokens};
-  plan_kernel<<<1, kThreads, 0, stream>>>(a);
+  PlanArgs a = {};
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.table = block_table;
+  a.free_pages = free_pages;
+  a.cursor_in = cursor_in;
+  a.cursor_out = cursor_out;
+  a.seq_lens = seq_lens;
+  a.cu_tokens = cu_tokens;
+  a.positions = positions;
+  a.slots = slots;
+  a.status = status;
+  a.table_stride = table_stride;
+  a.B = B;
+  a.page = page_size;
+  a.max_pages = max_pages;
+  a.num_free = num_free;
+  a.max_tokens = max_tokens;
+  // t / page_size for t < 2^31: with s = ceil(log2 page_size) and M = floor(2^(31+s) / page_size) + 1 the error of
+  // t M / 2^(31+s) is below 1 / page_size
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  a.page_shift = 31 + s;
+  a.page_magic = static_cast<uint32_t>((1ull << (31 + s)) / static_cast<unsigned>(page_size) + 1);
+  // One row per thread until the blocks fill the GPU several times over, then longer runs: each block repeats the sums.
+  const long long most = 8ll * std::max(1, zyfa::device_sm_count(dev));
+  const long long blocks = std::max(1ll, std::min(most, (max_tokens + kThreads - 1ll) / kThreads));
+  a.rows = static_cast<int>((max_tokens + blocks - 1) / blocks);
+  // Updated in place, the cursor may only be written once every block has read it.
+  a.write_cursor = cursor_in != cursor_out || blocks == 1;
+  plan_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return ZYFA_ERR_CUDA;
+  if (!a.write_cursor) {
+    a.write_cursor = a.cursor_only = 1;
+    plan_kernel<<<1, kThreads, 0, stream>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
 }

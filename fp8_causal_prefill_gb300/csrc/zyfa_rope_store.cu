@@ -5,6 +5,12 @@
 // fp32 number m * 2^e, turns-per-position = m * 2^e / (2 pi) is formed once from the integer m and 2^66 / (2 pi)
 // to within 2^-64 of a turn, and position * fraction mod 2^64 is the exact reduction.  Its top 32 bits,
 // read as signed, are the angle in half turns within [-1, 1).
+//
+// Bound: HBM.  Each value is read once (bf16) and written once or twice (cache, dense copy).  A block takes a few
+// tokens; its threads first form the tokens' cosines and sines, once per (token, pair), in shared memory, then walk over
+// items of 16 channels: two 16-byte loads whose channels pair up (8 channels and their partners half the rotated width
+// away, or 16 neighbours), eight rotations, one or two 8- or 16-byte stores per half.  The next item's loads are in flight
+// while one is computed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,6 +21,7 @@
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxTokens = 4;  // tokens per block
 
 struct StoreArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -28,9 +35,10 @@ struct StoreArgs {
   int* status;
   long long N;
   zyfa::CacheView cache;
-  int H, D_qk, D_v;
+  int H;
   int rot, offset, axis_end[4];
   int desc_per_head;
+  int tokens;  // per block
 };
 
 // 2^64 * |f| / (2 pi) modulo 2^64, with f's sign.
@@ -57,77 +65,192 @@ __device__ __forceinline__ void angle_sincos(uint64_t fraction, int position, fl
   sincospif(static_cast<float>(half_turns) * 4.656612873077393e-10f, s, c);  // * 2^-31
 }
 
-template <bool FP8>
-__device__ __forceinline__ void put(uint8_t* row, int d, float y, float inv) {
-  if constexpr (FP8) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(y * inv));
-    row[d] = static_cast<uint8_t>(r);
-  } else {
-    reinterpret_cast<__nv_bfloat16*>(row)[d] = __float2bfloat16_rn(y);
+__device__ __forceinline__ float inverse(const float* desc, int i) { return desc ? __frcp_rn(desc[i]) : 1.0f; }
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+__device__ __forceinline__ void widen8(const uint4& x, float (&y)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = __uint_as_float(w[i] << 16);
+    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 
-__device__ __forceinline__ float inverse(const float* desc, int i) { return desc ? __frcp_rn(desc[i]) : 1.0f; }
+// Eight neighbouring values in the cache's type, `d` channels into `row` (and `copy`, where given).
+template <bool FP8>
+__device__ __forceinline__ void put8(uint8_t* row, uint8_t* copy, int d, const float (&y)[8], float inv) {
+  if constexpr (FP8) {
+    const uint2 x = make_uint2(codes4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                               codes4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+    if (row) *reinterpret_cast<uint2*>(row + d) = x;
+    if (copy) *reinterpret_cast<uint2*>(copy + d) = x;
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(y[2 * i + 1]), "f"(y[2 * i]));
+    const uint4 x = make_uint4(w[0], w[1], w[2], w[3]);
+    if (row) *reinterpret_cast<uint4*>(row + 2 * d) = x;
+    if (copy) *reinterpret_cast<uint4*>(copy + 2 * d) = x;
+  }
+}
+
+// 16 channels of one head of one token.
+struct Item {
+  uint4 x0, x1;
+  int token, head;  // head: query heads, then key heads, then value heads
+  int d0, d1;       // first channel of either half
+  int pair;         // first pair, or -1: not rotated
+};
+
+template <bool FP8, bool INTERLEAVED, int DQK, int DV>
+__global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__ StoreArgs a) {
+  constexpr int es = FP8 ? 1 : 2;
+  constexpr int kItemsK = DQK / 16, kItemsV = DV / 16, kHalf = DQK / 2;
+  __shared__ __align__(16) float s_cos[kMaxTokens][kHalf], s_sin[kMaxTokens][kHalf];
+  __shared__ long long s_krow[kMaxTokens], s_vrow[kMaxTokens];  // offsets in the cache; -1: not written, -2: padding
+  const int tid = threadIdx.x;
+  const int tokens = a.tokens;
+  const long long n0 = static_cast<long long>(blockIdx.x) * tokens;
+  const int here = static_cast<int>(min(static_cast<long long>(tokens), a.N - n0));
+  const int H_kv = a.cache.H_kv, half = a.rot / 2;
+  if (tid < here) {
+    const long long slot = a.slots[n0 + tid];
+    long long krow = -2, vrow = 0;
+    if (slot >= 0) {
+      long long page, off;
+      if (slot <= 0x7fffffffll) {
+        page = static_cast<unsigned>(slot) / static_cast<unsigned>(a.cache.page_size);
+        off = static_cast<unsigned>(slot) % static_cast<unsigned>(a.cache.page_size);
+      } else {
+        page = slot / a.cache.page_size;
+        off = slot % a.cache.page_size;
+      }
+      krow = -1;
+      if (page < a.cache.num_pages) {
+        krow = page * a.cache.k_page + off * a.cache.k_tok;
+        vrow = page * a.cache.v_page + off * a.cache.v_tok;
+      } else if (a.k) {
+        atomicOr(a.status, zyfa::kStatusBadPageBit);
+      }
+    }
+    s_krow[tid] = krow;
+    s_vrow[tid] = vrow;
+  }
+  for (int i = tid; i < here * half; i += kThreads) {
+    const int t = i / half, p = i - t * half;
+    const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
+    angle_sincos(turn_fraction(a.inv_freq[p]), a.positions[axis * a.pos_stride + n0 + t], &s_sin[t][p], &s_cos[t][p]);
+  }
+  const int first = a.q ? 0 : a.H, heads_k = a.H - first + (a.k ? H_kv : 0);
+  const int items_k = heads_k * kItemsK, items = items_k + (a.k ? H_kv * kItemsV : 0);
+  __syncthreads();
+
+  int token = 0, at = tid;
+  auto fetch = [&](Item& it) {
+    while (at >= items && token < here) {
+      at -= items;
+      ++token;
+    }
+    it.token = token;
+    if (token >= here) return false;
+    const __nv_bfloat16* x;
+    if (at < items_k) {
+      const int h = at / kItemsK, j = at % kItemsK;
+      it.head = first + h;
+      if (j * 8 < half) {
+        it.pair = j * 8;
+        it.d0 = a.offset + (INTERLEAVED ? j * 16 : j * 8);
+        it.d1 = INTERLEAVED ? it.d0 + 8 : it.d0 + half;
+      } else {  // the plain channels in order, eight by eight
+        it.pair = -1;
+        const int d = 16 * j - a.rot;
+        it.d0 = d < a.offset ? d : d + a.rot;
+        it.d1 = d + 8 < a.offset ? d + 8 : d + 8 + a.rot;
+      }
+      x = it.head < a.H ? a.q + (n0 + token) * a.q_tok + it.head * DQK : a.k + (n0 + token) * a.k_tok + (it.head - a.H) * DQK;
+    } else {
+      const int h = (at - items_k) / kItemsV, j = (at - items_k) % kItemsV;
+      it.head = a.H + H_kv + h;
+      it.pair = -1;
+      it.d0 = j * 16;
+      it.d1 = j * 16 + 8;
+      x = a.v + (n0 + token) * a.v_tok + h * DV;
+    }
+    it.x0 = *reinterpret_cast<const uint4*>(x + it.d0);
+    it.x1 = *reinterpret_cast<const uint4*>(x + it.d1);
+    at += kThreads;
+    return true;
+  };
+  Item next;
+  bool more = fetch(next);
+  while (more) {
+    const Item it = next;
+    more = fetch(next);
+    const long long krow = s_krow[it.token];
+    if (krow == -2) continue;
+    float u[8], w[8];
+    widen8(it.x0, u);
+    widen8(it.x1, w);
+    if (it.pair >= 0) {
+      float c[8], s[8];
+      *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&s_cos[it.token][it.pair]);
+      *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(&s_cos[it.token][it.pair + 4]);
+      *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(&s_sin[it.token][it.pair]);
+      *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(&s_sin[it.token][it.pair + 4]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // half-split: u[i], w[i] are pair i; interleaved: neighbours of u, then of w
+        float& p = INTERLEAVED ? (i < 4 ? u[2 * (i & 3)] : w[2 * (i & 3)]) : u[i];
+        float& q = INTERLEAVED ? (i < 4 ? u[2 * (i & 3) + 1] : w[2 * (i & 3) + 1]) : w[i];
+        const float y = p * c[i] - q * s[i], z = p * s[i] + q * c[i];
+        p = y;
+        q = z;
+      }
+    }
+    const long long n = n0 + it.token;
+    uint8_t *row = nullptr, *copy = nullptr;
+    const float* desc;
+    int hk;
+    if (it.head < a.H) {
+      row = a.q_out + (n * a.H + it.head) * DQK * es;
+      hk = FP8 && a.desc_per_head ? it.head / (a.H / H_kv) : 0;
+      desc = a.q_desc;
+    } else if (it.head < a.H + H_kv) {
+      hk = it.head - a.H;
+      if (krow >= 0) row = a.cache.k + krow + hk * a.cache.k_head;
+      if (a.k_out) copy = a.k_out + (n * H_kv + hk) * DQK * es;
+      desc = a.k_desc;
+    } else {
+      hk = it.head - a.H - H_kv;
+      if (krow >= 0) row = a.cache.v + s_vrow[it.token] + hk * a.cache.v_head;
+      if (a.v_out) copy = a.v_out + (n * H_kv + hk) * DV * es;
+      desc = a.v_desc;
+    }
+    const float inv = FP8 ? inverse(desc, a.desc_per_head ? hk : 0) : 1.0f;
+    put8<FP8>(row, copy, it.d0, u, inv);
+    put8<FP8>(row, copy, it.d1, w, inv);
+  }
+}
 
 template <bool FP8, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) store_kernel(const StoreArgs a) {
-  constexpr int es = FP8 ? 1 : 2;
-  const long long n = blockIdx.x;
-  const long long slot = a.slots[n];
-  if (slot < 0) return;
-  const int H_kv = a.cache.H_kv, group = a.H / H_kv;
-  const long long page = slot / a.cache.page_size, off = slot % a.cache.page_size;
-  const bool in_cache = page < a.cache.num_pages;
-  if (!in_cache && a.k && threadIdx.x == 0) atomicOr(a.status, zyfa::kStatusBadPageBit);
-  // queries and keys: pairs of channels (rotated ones, then the plain ones two by two)
-  const int pairs = a.D_qk / 2, half = a.rot / 2;
-  const int first = a.q ? 0 : a.H, last = a.k ? a.H + H_kv : a.H;
-  for (int i = threadIdx.x; i < (last - first) * pairs; i += kThreads) {
-    const int h = first + i / pairs, p = i % pairs;
-    int d0, d1;
-    float s = 0.0f, c = 1.0f;
-    if (p < half) {
-      d0 = a.offset + (INTERLEAVED ? 2 * p : p);
-      d1 = a.offset + (INTERLEAVED ? 2 * p + 1 : p + half);
-      const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
-      angle_sincos(turn_fraction(a.inv_freq[p]), a.positions[axis * a.pos_stride + n], &s, &c);
-    } else {
-      d0 = 2 * (p - half);
-      if (d0 >= a.offset) d0 += a.rot;
-      d1 = d0 + 1;
-    }
-    const bool is_q = h < a.H;
-    const int hk = is_q ? h / group : h - a.H;
-    const __nv_bfloat16* x = is_q ? a.q + n * a.q_tok + h * a.D_qk : a.k + n * a.k_tok + hk * a.D_qk;
-    const float u = __bfloat162float(x[d0]), w = __bfloat162float(x[d1]);
-    const float y0 = u * c - w * s, y1 = u * s + w * c;
-    const float inv = FP8 ? inverse(is_q ? a.q_desc : a.k_desc, a.desc_per_head ? hk : 0) : 1.0f;
-    if (is_q) {
-      uint8_t* o = a.q_out + (n * a.H + h) * a.D_qk * es;
-      put<FP8>(o, d0, y0, inv);
-      put<FP8>(o, d1, y1, inv);
-    } else {
-      if (in_cache) {
-        uint8_t* o = a.cache.k + page * a.cache.k_page + off * a.cache.k_tok + hk * a.cache.k_head;
-        put<FP8>(o, d0, y0, inv);
-        put<FP8>(o, d1, y1, inv);
-      }
-      if (a.k_out) {
-        uint8_t* o = a.k_out + (n * H_kv + hk) * a.D_qk * es;
-        put<FP8>(o, d0, y0, inv);
-        put<FP8>(o, d1, y1, inv);
-      }
-    }
-  }
-  if (!a.k) return;
-  for (int i = threadIdx.x; i < H_kv * a.D_v; i += kThreads) {
-    const int hk = i / a.D_v, d = i % a.D_v;
-    const float y = __bfloat162float(a.v[n * a.v_tok + i]);
-    const float inv = FP8 ? inverse(a.v_desc, a.desc_per_head ? hk : 0) : 1.0f;
-    if (in_cache) put<FP8>(a.cache.v + page * a.cache.v_page + off * a.cache.v_tok + hk * a.cache.v_head, d, y, inv);
-    if (a.v_out) put<FP8>(a.v_out + (n * H_kv + hk) * a.D_v * es, d, y, inv);
-  }
+cudaError_t launch(const StoreArgs& a, int D_qk, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((a.N + a.tokens - 1) / a.tokens);
+  if (D_qk == 64)
+    store_kernel<FP8, INTERLEAVED, 64, 64><<<grid, kThreads, 0, stream>>>(a);
+  else if (D_qk == 128)
+    store_kernel<FP8, INTERLEAVED, 128, 128><<<grid, kThreads, 0, stream>>>(a);
+  else
+    store_kernel<FP8, INTERLEAVED, 192, 128><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -213,17 +336,13 @@ extern "C" zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, con
   a.desc_per_head = descale_per_kv_head;
   a.N = N;
   a.H = H;
-  a.D_qk = D_qk;
-  a.D_v = D_v;
-  const unsigned grid = static_cast<unsigned>(N);
+  // Several tokens per block share its start-up, as soon as there are blocks enough for the GPU without them.
+  a.tokens = N >= 8ll * zyfa::device_sm_count(dev) ? kMaxTokens : 1;
   const bool il = rope && rope->interleaved;
-  if (fp8 && il)
-    store_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
-  else if (fp8)
-    store_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
-  else if (il)
-    store_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
+  cudaError_t e;
+  if (fp8)
+    e = il ? launch<true, true>(a, D_qk, stream) : launch<true, false>(a, D_qk, stream);
   else
-    store_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
+    e = il ? launch<false, true>(a, D_qk, stream) : launch<false, false>(a, D_qk, stream);
+  return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
 }

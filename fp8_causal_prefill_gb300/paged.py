@@ -23,6 +23,10 @@ from .api import ZYFA_DTYPE_BF16, ZYFA_DTYPE_E4M3, PagedCache, RopeOptions, Zyfa
 _CODES = {torch.float8_e4m3fn: ZYFA_DTYPE_E4M3, torch.uint8: ZYFA_DTYPE_E4M3, torch.bfloat16: ZYFA_DTYPE_BF16}
 
 
+# address of a device's current stream (torch.cuda.current_stream builds a Stream object for it: 1 us of a 10 us call)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class PagedPlan(NamedTuple):
     """What a serving step needs beside its block table: see ``paged_plan``."""
     seq_lens: torch.Tensor    # [B] int32, lengths with the new tokens
@@ -34,10 +38,10 @@ class PagedPlan(NamedTuple):
 
 def _call(dev: int, fn, *args) -> None:
     if dev == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _stream(dev))
     if st != 0:
         raise ZyfaError(st, fn.__name__)
 
@@ -262,9 +266,10 @@ def rope_paged_store(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Te
     return q_out
 
 
-def paged_decode_workspace_bytes(B: int, H: int, H_kv: int, D_v: int) -> int:
-    """Bytes of the ``workspace`` that ``paged_decode_attn`` needs for these sizes."""
-    return load_library().zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v)
+def paged_decode_workspace_bytes(B: int, H: int, H_kv: int, D_v: int, max_len: int) -> int:
+    """Bytes of the ``workspace`` that ``paged_decode_attn`` needs for these sizes, with ``max_len`` the tokens a row
+    of the block table can name (its columns times the page size)."""
+    return load_library().zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v, max_len)
 
 
 def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -305,7 +310,8 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         per_head = 0
     lib = load_library()
     if workspace is None:
-        workspace = torch.empty(lib.zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(lib.zyfa_attn_decode_paged_workspace_bytes(B, H, H_kv, D_v, width * c.page_size), dtype=torch.uint8,
+                                device=q.device)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
         raise TypeError("workspace must be a contiguous uint8 tensor on the cache's device")
     _call(dev, lib.zyfa_attn_decode_paged, q.data_ptr(), s[0] if B > 1 else H * D, ctypes.byref(c), table, stride, width,

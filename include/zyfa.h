@@ -263,7 +263,7 @@ typedef struct {
  * A token that gets no slot (no free page left, a page beyond max_pages, a table entry below 0) has slot
  * -1, the page it would have started is -1 in the table, and zyfa_check_errors() then returns
  * ZYFA_ERR_CAPACITY, as it does when the tokens are more than max_tokens (the rows behind are dropped).
- * Asynchronous on `stream`, one launch, allocates nothing, no atomics on results.  The outputs must not overlap
+ * Asynchronous on `stream`, one launch (two for many rows with the cursor updated in place), allocates nothing.  The outputs must not overlap
  * one another or the inputs (cursors excepted).  Errors: ZYFA_ERR_INVALID_ARG (null pointers; B, max_tokens,
  * num_free or max_pages < 0, table_stride < max_pages, page_size outside 1 .. 65536),
  * ZYFA_ERR_UNSUPPORTED (max_pages * page_size beyond 2^30, B beyond 65536), ZYFA_ERR_MISALIGNED
@@ -349,9 +349,10 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
                                      int descale_per_kv_head, void* workspace, size_t workspace_bytes,
                                      cudaStream_t stream);
 
-/* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged for these sizes, the same whatever
- * the lengths are.  Pure host arithmetic; 0 for sizes that the call refuses. */
-size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v);
+/* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged for these sizes, with max_len =
+ * max_pages * page_size; the same whatever the lengths are, at most about 500 * H * D_v floats per KV head's group.
+ * Pure host arithmetic; 0 for sizes that the call refuses. */
+size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v, long long max_len);
 
 /*
  * zyfa_check_errors - synchronise `stream`, then read and clear the current device's status word.

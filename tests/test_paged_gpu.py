@@ -389,7 +389,7 @@ def test_decode_shared_pages_streams_and_repeats(kind):
         outs = [paged_decode_attn(q, kc, vc, table, lens) for _ in range(20)]
     side.synchronize()
     assert all(torch.equal(o, out) for o in outs)
-    ws = torch.full((paged_decode_workspace_bytes(6, 8, 2, 128),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((paged_decode_workspace_bytes(6, 8, 2, 128, 4000),), 0xFF, dtype=torch.uint8, device="cuda")
     mine = torch.empty_like(out)
     assert paged_decode_attn(q, kc, vc, table, lens, out=mine, workspace=ws) is mine and torch.equal(mine, out)
     assert torch.equal(paged_decode_attn(q, kc, vc, table, lens, workspace=ws), out)
@@ -546,7 +546,7 @@ def test_two_captured_graphs_with_their_own_workspaces():
     graphs, outs = [], []
     for q in qs:
         g = torch.cuda.CUDAGraph()
-        ws = torch.empty(paged_decode_workspace_bytes(2, 8, 2, 128), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(paged_decode_workspace_bytes(2, 8, 2, 128, 2048), dtype=torch.uint8, device="cuda")
         with torch.cuda.graph(g):
             outs.append(paged_decode_attn(q, kc, vc, table, lens, workspace=ws))
         graphs.append((g, ws))

@@ -67,8 +67,9 @@ def test_decode_needs_a_cache(lib):
 
 def test_decode_workspace_sizes(lib):
     f = lib.zyfa_attn_decode_paged_workspace_bytes
-    assert f(0, 4, 2, 128) == 0 and f(1, 3, 2, 128) == 0 and f(1, 0, 1, 128) == 0 and f(1, 2, 0, 128) == 0
-    assert f(1, 2, 2, 96) == 0
+    assert f(0, 4, 2, 128, 64) == 0 and f(1, 3, 2, 128, 64) == 0 and f(1, 0, 1, 128, 64) == 0 and f(1, 2, 0, 128, 64) == 0
+    assert f(1, 2, 2, 96, 64) == 0 and f(1, 2, 2, 128, -1) == 0
+    assert 0 < f(1, 2, 2, 128, 0) <= f(1, 2, 2, 128, 256) < f(1, 2, 2, 128, 1 << 20) < f(4, 64, 2, 128, 1 << 20) < 1 << 26
 
 
 def _store(lib, cache, rope=None, **kw):
