@@ -1,4 +1,4 @@
-"""Build libzyfa.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Build libzyfa.so (the C-ABI library) in-tree for sm_103a with nvcc, and the native tensor binding beside it.
 
 The translation units compile in parallel; the shared library lands next to this file, where
 ``fp8_causal_prefill_gb300.api`` loads it.  Run as ``python -m fp8_causal_prefill_gb300.build``.
@@ -10,6 +10,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzyfa.so")
+BINDING = os.path.join(PKG, "_paged.so")
 SOURCES = ["zyfa_api.cu", "zyfa_kernels_fp8.cu", "zyfa_kernels_fp8_exact.cu", "zyfa_kernels_bf16.cu",
            "zyfa_hadamard.cu", "zyfa_probe.cu", "zyfa_paged_plan.cu", "zyfa_rope_store.cu", "zyfa_decode.cu"]
 # The attention kernel splits its registers between warpgroups at run time (setmaxnreg); the split is
@@ -61,9 +63,45 @@ def _inputs_newer(target: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _cxx() -> str:
+    for cand in (os.environ.get("CXX"), shutil.which("g++")):
+        if cand and shutil.which(cand):
+            return cand
+    raise RuntimeError("g++ not found: the tensor binding cannot be built")
+
+
+def compile_binding() -> str:
+    """The CPython module that checks tensors and calls libzyfa.so (host code only)."""
+    torch_dir, cuda = _torch_dir(), os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD, "paged_binding.o")
+    inc = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+           os.path.join(cuda, "include")]
+    cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", *("-I" + d for d in inc), "-c", os.path.join(CSRC, "paged_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on paged_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def link_binding(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING + ".tmp"
+    r = subprocess.run([_cxx(), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libzyfa.so", "-Wl,-rpath,$ORIGIN", "-L" + lib,
+                        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the tensor binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if any source is newer than the library) and return the library path."""
-    if not force and not _inputs_newer(LIB):
+    """Compile (if any source is newer than the library or its binding) and return the library path."""
+    if not force and not _inputs_newer(LIB) and not _inputs_newer(BINDING):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -79,13 +117,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    link_binding(binding_obj)
     return LIB
 
 
