@@ -1,5 +1,6 @@
 // What the paged serving operators share: status bits, the device view of a paged cache, its host checks.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -15,6 +16,10 @@ enum : int { kStatusTimeoutBit = 1, kStatusCapacityBit = 2, kStatusBadPageBit = 
 // nullptr / 0 if the CUDA call behind them fails.
 int* device_status_word(int dev);
 int device_sm_count(int dev);
+
+// cuTensorMapEncodeTiled with unit element strides' usual options; false if the driver refuses the map.
+bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, unsigned rank, void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* estr, CUtensorMapSwizzle sw);
 
 // Strides in bytes; an offset is formed in 64 bits, since a long cache passes 2^31 bytes and elements.
 struct CacheView {

@@ -145,6 +145,11 @@ zyfa_status_t run(zyfa::LaunchArgs& a, const void* q, const void* k, const void*
 
 namespace zyfa {
 int* device_status_word(int dev) { return dev >= 0 && dev < kMaxDevices ? status_ptr(dev) : nullptr; }
+bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, unsigned rank, void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* estr, CUtensorMapSwizzle sw) {
+  return get_encode() && g_encode(m, type, rank, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 int device_sm_count(int dev) { return dev >= 0 && dev < kMaxDevices ? sm_count(dev) : 0; }
 }  // namespace zyfa
 
