@@ -20,7 +20,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzyfa.so")
 BINDING = os.path.join(PKG, "_paged.so")
 SOURCES = ["zyfa_api.cu", "zyfa_kernels_fp8.cu", "zyfa_kernels_fp8_exact.cu", "zyfa_kernels_bf16.cu",
-           "zyfa_hadamard.cu", "zyfa_probe.cu", "zyfa_paged_plan.cu", "zyfa_rope_store.cu", "zyfa_decode.cu"]
+           "zyfa_hadamard.cu", "zyfa_probe.cu", "zyfa_paged_plan.cu", "zyfa_rope_store.cu", "zyfa_decode.cu",
+           "zyfa_decode_fp8.cu", "zyfa_decode_bf16.cu"]
 # The attention kernel splits its registers between warpgroups at run time (setmaxnreg); the split is
 # sized for exactly this many registers per thread at launch, which every instantiation must get.
 KERNEL_REGS = 168

@@ -1,0 +1,1109 @@
+// Attention of one new token per request over a paged key/value cache: device code.
+//
+// One pass over the keys with the running maximum m and sum l of the softmax (in units of log2):
+//   x_j = a q.k_j,  m' = max(m, max_j x_j),  l' = l 2^(m-m') + sum_j 2^(x_j-m'),  O' = O 2^(m-m') + sum_j 2^(x_j-m') v_j
+// and out = dv O / l, lse = ln2 (m + log2 l), with a = scale dq dk log2(e).
+//
+// Bound: the cache is read once (H_kv (D_qk + D_v) values per token) and a key costs 2 (D_qk + D_v) operations per
+// query head, so with the usual 1 to 16 heads per KV head this is far below the tensor cores and HBM is the limit.
+// The design keeps the loads running:
+//
+// * A block takes KV heads side by side: a tile is a run of tokens of several heads, whose rows are neighbours in memory,
+//   and each compute warp takes one head, one run of 16 or 32 of the tokens and up to 8 of the query heads of it.  Warps
+//   share nothing but the ring of tiles.
+// * Products run with the keys (or the channels of V) as the 16 rows of mma.sync and the query heads as its 8
+//   columns: S^T = K q^T, O^T = V^T P^T.  Few heads waste no second half of a tile, K and V fragments come
+//   straight from ldmatrix, and the accumulators of a 128-channel head take 32 registers.  An e4m3 K multiplies an e4m3 q
+//   as it is (m16n8k32, accumulated exactly to fp32); V is widened to fp16 in registers (exact) and multiplies P in
+//   fp16 lifted by 2^15, so that the weights keep 11 bits.
+// * Work is split over (request, key tile) evenly whatever the lengths: the tiles of all requests are numbered one after
+//   the other and each group of blocks (one block per chunk of heads) takes an equal run of them.  A block finds its run
+//   from seq_lens on the device, so the host never needs the lengths.
+// * A request that lies in one group's run is written directly; otherwise each group leaves (m, l, O) of its
+//   part in the workspace and a second kernel joins the parts in group order.
+// * The join is launched while the first kernel still runs and waits for it on the device (programmatic dependent
+//   launch), which hides its launch.
+//
+// Two kernels differ in how tiles arrive.  boxes_kernel: pages whose size is a multiple of 8 tokens, by TMA; a warp of its
+// own loads a block's tiles, one box for K and one for V per page.  (Compute warps that loaded for themselves spent 500 to
+// 950 clocks per tile on it, as long as on the tile.)  rows_kernel: any page size and stride, by cp.async; each warp
+// loads its own tiles row by row into a ring of its own.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+#include <utility>
+
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace zyfa {
+namespace decode {
+
+constexpr int kMaxSms = 160;          // the workspace is sized for at most this many SMs ...
+constexpr int kMaxWarpsPerSm = 16;    // ... of this many compute warps
+constexpr int kMaxDevices = 64;
+constexpr int kSmemPerBlock = 232448, kSmemPerSm = 233472;
+constexpr long long kWaitClocks = 1ll << 31;  // bound of every wait, about a second
+
+struct DecodeArgs {
+  const uint8_t* q;
+  long long q_batch;  // bytes
+  CacheView cache;
+  const int* table;
+  long long table_stride;
+  const int* seq_lens;
+  __nv_bfloat16* out;
+  float* lse;
+  const float *q_desc, *k_desc, *v_desc;
+  int* status;
+  float scale_log2;
+  int desc_per_head;
+  int max_len;  // max_pages * page_size
+  int B, H, group;
+  uint32_t page_magic;  // floor(t / page_size) = t * page_magic >> page_shift for t < 2^30
+  int page_shift;
+  // schedule and workspace
+  int groups, units;            // `units` blocks (boxes_kernel) or warps (rows_kernel) make a group
+  int chunks, chunk_heads;      // the query heads of a KV head are cut into chunks of at most chunk_heads
+  int heads, chunk_warps, subs; // of a block: KV heads, chunks of each, token runs of a tile (warps = the product)
+  int stages, tile_tokens;      // of a ring; tokens of a tile, subs * keys of a warp
+  int q_bytes;                  // of a block's queries in shared memory
+  int box_log2;                 // tokens of a TMA box, at most a tile's
+  int joint_k, joint_v;         // rows of 64 (or 192) bytes lie in shared memory in 128-byte columns across heads
+  unsigned* starts;  // [B + 2]: first tile of each request, then the total, then the tiles per group
+  float2* ml;        // [groups][2][subs][H]
+  float* part;       // [groups][2][subs][H][DV]
+};
+
+// ------------------------------------------------------------------------------------------------
+// warp-level pieces
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// Waits for a phase, for at most kWaitClocks; the whole warp gets the same answer.
+__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity) {
+  bool done = ptx::mbar_try_wait(bar, parity);
+  if (!done) {
+    const long long t0 = clock64();
+    do done = ptx::mbar_try_wait(bar, parity);
+    while (!done && clock64() - t0 < kWaitClocks);
+  }
+  return __all_sync(0xffffffffu, done);
+}
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
+// Untiled bulk copy: both addresses 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(bar)
+               : "memory");
+}
+
+// 16 bytes global -> shared; `bytes` 0 writes zeros without reading.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+enum { kF16, kBf16, kE4m3 };
+// D += A B for 16 rows, 8 columns and a contraction of 16 (16-bit operands) or 32 (e4m3).
+template <int KIND>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+#define ZYFA_MMA(SHAPE_AND_TYPES)                                                                                       \
+  asm("mma.sync.aligned." SHAPE_AND_TYPES " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                      \
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                                  \
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if constexpr (KIND == kF16)
+    ZYFA_MMA("m16n8k16.row.col.f32.f16.f16.f32");
+  else if constexpr (KIND == kBf16)
+    ZYFA_MMA("m16n8k16.row.col.f32.bf16.bf16.f32");
+  else
+    ZYFA_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32");
+#undef ZYFA_MMA
+}
+// Two e4m3 codes (low half of `x`) as two fp16 values.
+__device__ __forceinline__ uint32_t widen(uint32_t x) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t x) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Pairs of fp32 values in one instruction, each rounded as alone.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+template <bool FP8>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  if constexpr (FP8)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+template <bool FP8, int DQK, int DV>
+struct Tile {
+  static constexpr int kEs = FP8 ? 1 : 2;
+  static constexpr int kRowK = DQK * kEs, kRowV = DV * kEs;
+  static constexpr int kKeyBytes = kRowK + kRowV;
+  static constexpr int kKeys = kKeyBytes <= 128 ? 32 : 16;  // per stage: 4 to 10 KiB
+  static constexpr int kTileBytes = kKeys * kKeyBytes;
+  static constexpr uint32_t kFull = kKeys == 32 ? 0xffffffffu : 0xffffu;
+};
+
+// K or V rows of a run of tokens lie in shared memory as columns of CB bytes, each [tokens][CB] with the 16-byte pieces of a
+// row exchanged as TMA's 128-byte (64-byte) swizzle does, so that the 8 rows that one ldmatrix phase reads lie in 8
+// different bank groups.  CB = 128 where the rows are a multiple of that.  Rows of an odd number of 64-byte halves are columns of
+// 64 bytes, or (`joint`), where heads follow one another without a gap, 128-byte columns that two heads share: TMA spends
+// its time by rows of a box, and half as long ones reached 5.3 of 6.8 TB/s.
+template <int ROW>
+constexpr bool kWhole = ROW % 128 == 0;
+
+// Where one lane's ldmatrix reads go: piece p (16 bytes, p even, plus the lane's own 0 or 1) of row 16 n + the lane's, of one
+// head, is at ((tile + base[n]) ^ flip) + add for the 64-byte half that p lies in.
+template <int ROW, int KB>
+struct Reader {
+  static constexpr int kHalves = ROW / 64;
+  uint32_t base[KB], add[kHalves], flip[kHalves];
+
+  // tokens: of a box; head: within the box, of `heads`; row, hi: the lane's row of the first 16 and its piece of a pair
+  __device__ __forceinline__ void set(int tokens_log2, int head, int heads, int first_row, int row, int hi, bool joint) {
+    const int tokens = 1 << tokens_log2;
+    const bool wide = kWhole<ROW> || joint;
+    const int cb = wide ? 128 : 64;
+#pragma unroll
+    for (int n = 0; n < KB; ++n) {
+      const int r = first_row + n * 16 + row, box = r >> tokens_log2, in = r & (tokens - 1);
+      base[n] = box * heads * tokens * ROW + in * cb + ((hi ^ (wide ? in & 7 : (in >> 1) & 3)) << 4);
+    }
+#pragma unroll
+    for (int j = 0; j < kHalves; ++j) {
+      const int half = head * kHalves + j;
+      add[j] = (wide ? half >> 1 : half) * tokens * cb;
+      flip[j] = wide ? (half & 1) << 6 : 0;
+    }
+  }
+  __device__ __forceinline__ uint32_t at(uint32_t tile, int n, int p) const {
+    const int j = p / 4;
+    if constexpr (kWhole<ROW>)
+      return ((tile + base[n]) ^ ((p % 8) << 4)) + add[j];  // halves of a head alternate
+    else
+      return ((tile + base[n]) ^ (flip[j] | (p % 4) << 4)) + add[j];
+  }
+};
+
+// Address of 16-byte piece p of row r in a lone head's run of `tokens` rows that is not joint.
+template <int ROW>
+__device__ __forceinline__ uint32_t place(int tokens, int r, int p) {
+  constexpr int CB = kWhole<ROW> ? 128 : 64, PIECES = CB / 16;
+  const int c = p / PIECES, q = p % PIECES;
+  return static_cast<uint32_t>((c * tokens + r) * CB + ((q ^ (CB == 128 ? (r & 7) : ((r >> 1) & 3))) << 4));
+}
+
+// What the load side tells the compute side about a stage.
+struct Header {
+  int b, flags;
+  int valid;       // tokens of the request in the tile
+  uint32_t boxes;  // boxes_kernel: those whose page is in the cache; rows_kernel: such rows
+};
+// first and last tile of a request's part, last tile of the run; the part is the whole request; it begins the request
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kDirect = 8, kSlot1 = 16 };
+
+__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) { return max(0, min(__ldg(a.seq_lens + b), a.max_len)); }
+
+__device__ __forceinline__ void page_of(const DecodeArgs& a, int t, int* p, int* off) {
+  *p = static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(t)) * a.page_magic) >> a.page_shift);
+  *off = t - *p * a.cache.page_size;
+}
+
+// ------------------------------------------------------------------------------------------------
+// the state of a compute warp: up to 8 query heads against its tiles
+
+template <bool FP8, int DQK, int DV>
+struct Rows {
+  using T = Tile<FP8, DQK, DV>;
+  static constexpr int KT = T::kKeys, KB = KT / 16;
+  static constexpr int kKSteps = T::kRowK / 32, kMTiles = DV / 16;
+  static constexpr int kScoreKind = FP8 ? kE4m3 : kBf16, kValueKind = FP8 ? kF16 : kBf16;
+  static constexpr float kLift = FP8 ? 15.0f : 0.0f;  // e4m3: weights in fp16 up to 2^15, so that light ones keep their bits
+
+  uint32_t qf[kKSteps][2];      // B fragments of the queries
+  float o[kMTiles][4], m[2], l[2];  // this lane's two heads
+  float scale, dv;
+
+  // Begins a request's part: its queries from shared memory, `count` dense rows.
+  __device__ __forceinline__ void begin(uint32_t queries, int count, float scale_, float dv_, int lane) {
+    // rows behind the last head repeat it: their columns are computed and never written
+    const uint32_t row = queries + min(lane & 7, count - 1) * T::kRowK + (lane >> 3) * 16;
+#pragma unroll
+    for (int i = 0; i < kKSteps; i += 2) {
+      uint32_t x[4];
+      ldsm4(row + i * 32, x);
+      qf[i][0] = x[0];
+      qf[i][1] = x[1];
+      qf[i + 1][0] = x[2];
+      qf[i + 1][1] = x[3];
+    }
+#pragma unroll
+    for (int i = 0; i < kMTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
+    scale = scale_;
+    dv = dv_;
+  }
+
+  // One tile of K at ks and V at vs; mask: valid keys, at least one.  clear(): called where V rows of keys that are not valid
+  // may hold anything.
+  template <typename F>
+  __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, const Reader<T::kRowK, KB>& kr, const Reader<T::kRowV, KB>& vr, uint32_t mask,
+                                       int lane, F clear) {
+    // S^T: rows are keys, columns heads; then scores in units of log2
+    F2 x[KB][2];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kKSteps; ++i) {
+        uint32_t r[4];
+        ldsm4(kr.at(ks, kb, 2 * i), r);
+        mma<kScoreKind>(c, r[0], r[1], r[2], r[3], qf[i][0], qf[i][1]);
+      }
+      x[kb][0] = mul2({c[0], c[1]}, {scale, scale});
+      x[kb][1] = mul2({c[2], c[3]}, {scale, scale});
+    }
+    if (mask != T::kFull) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (!((mask >> (kb * 16 + j * 8 + (lane >> 2))) & 1)) x[kb][j] = {-INFINITY, -INFINITY};
+      clear();
+    }
+    // The reference m moves only when a key exceeds it: log2 of a weight is then above the lift.  (Before a part's first valid
+    // key m is -inf and every valid key's log2 weight +inf.)
+    F2 y[KB][2];
+    float over = -INFINITY;
+    auto weigh = [&]() {
+      const F2 ref = {kLift - m[0], kLift - m[1]};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          y[kb][j] = add2(x[kb][j], ref);
+          over = fmaxf(over, fmaxf(y[kb][j].x, y[kb][j].y));
+        }
+    };
+    weigh();
+    if (__any_sync(0xffffffffu, over > kLift)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = m[e];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) t = e ? fmaxf(t, fmaxf(x[kb][0].y, x[kb][1].y)) : fmaxf(t, fmaxf(x[kb][0].x, x[kb][1].x));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+        const float f = exp2_approx(m[e] - t);
+        m[e] = t;
+        l[e] *= f;
+#pragma unroll
+        for (int i = 0; i < kMTiles; ++i) {
+          o[i][e] *= f;
+          o[i][e + 2] *= f;
+        }
+      }
+      weigh();
+    }
+    // weights, transposed into the B operand (keys are now the contraction)
+    uint32_t pf[KB][2];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const F2 w = {exp2_approx(y[kb][j].x), exp2_approx(y[kb][j].y)};
+        const F2 sum = add2({l[0], l[1]}, w);
+        l[0] = sum.x;
+        l[1] = sum.y;
+        pf[kb][j] = transpose8x8(pack2<FP8>(w.x, w.y));
+      }
+    // O^T += V^T P^T: rows are channels of V
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      if constexpr (FP8) {
+#pragma unroll
+        for (int i = 0; i < kMTiles; i += 2) {
+          // a register holds channels 2r, 2r+1 of two keys: the even channel is row r, the odd one row r + 8
+          uint32_t r[4], v[8];
+          ldsm4t(vr.at(vs, kb, i), r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t q = __byte_perm(r[j], 0, 0x3120);
+            v[2 * j] = widen(q);
+            v[2 * j + 1] = widen_hi(q);
+          }
+          mma<kValueKind>(o[i], v[0], v[1], v[2], v[3], pf[kb][0], pf[kb][1]);
+          mma<kValueKind>(o[i + 1], v[4], v[5], v[6], v[7], pf[kb][0], pf[kb][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kMTiles; ++i) {
+          uint32_t r[4];
+          ldsm4t(vr.at(vs, kb, 2 * i), r);
+          mma<kValueKind>(o[i], r[0], r[1], r[2], r[3], pf[kb][0], pf[kb][1]);
+        }
+      }
+    }
+  }
+
+  // Ends a request's part: writes its rows (`count` query heads from `first`), or (m, l, O) to part `slot` of the workspace.
+  __device__ __forceinline__ void finish(const DecodeArgs& a, int b, int first, int count, bool direct, long long slot, int lane) {
+    const int t4 = lane & 3, g8 = lane >> 2;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[e];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int head = t4 * 2 + e;
+      if (head < count) {
+        const long long row = (direct ? static_cast<long long>(b) : slot) * a.H + first + head;
+        const float f = !direct ? dv : sum > 0.0f ? dv / sum : 0.0f;
+        if (g8 == 0) {
+          if (!direct)
+            a.ml[row] = make_float2(m[e] - kLift, sum);
+          else if (a.lse)
+            a.lse[row] = sum > 0.0f ? (m[e] + log2f(sum) - kLift) * 0.69314718055994531f : -INFINITY;
+        }
+        __nv_bfloat16* out = a.out + row * DV;
+        float* part = a.part + row * DV;
+        // rows r and r + 8: channels 2r and 2r + 1 of the tile's 16 (e4m3), or r and r + 8
+        constexpr int kStep = FP8 ? 2 : 1;
+        if (direct) {
+#pragma unroll
+          for (int i = 0; i < kMTiles; ++i) {
+            const float y0 = o[i][e] * f, y1 = o[i][e + 2] * f;
+            if constexpr (FP8) {
+              *reinterpret_cast<__nv_bfloat162*>(out + i * 16 + kStep * g8) = __floats2bfloat162_rn(y0, y1);
+            } else {
+              out[i * 16 + g8] = __float2bfloat16_rn(y0);
+              out[i * 16 + g8 + 8] = __float2bfloat16_rn(y1);
+            }
+          }
+        } else if (m[e] != -INFINITY) {  // without a valid key the join does not read O
+#pragma unroll
+          for (int i = 0; i < kMTiles; ++i) {
+            if constexpr (FP8) {
+              *reinterpret_cast<float2*>(part + i * 16 + kStep * g8) = make_float2(o[i][e] * f, o[i][e + 2] * f);
+            } else {
+              part[i * 16 + g8] = o[i][e] * f;
+              part[i * 16 + g8 + 8] = o[i][e + 2] * f;
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+// The Readers of a warp whose run of keys begins at row `first_row` of a tile of boxes.
+template <bool FP8, int DQK, int DV, int KB>
+__device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head, int heads, int first_row, bool joint_k, bool joint_v,
+                                            Reader<Tile<FP8, DQK, DV>::kRowK, KB>* k, Reader<Tile<FP8, DQK, DV>::kRowV, KB>* v) {
+  k->set(tokens_log2, head, heads, first_row, lane & 15, lane >> 4, joint_k);
+  if (FP8)
+    v->set(tokens_log2, head, heads, first_row, lane & 15, lane >> 4, joint_v);
+  else
+    v->set(tokens_log2, head, heads, first_row, (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, joint_v);
+}
+
+// ------------------------------------------------------------------------------------------------
+// the schedule
+
+// The tiles (of `tokens` tokens) of all requests, and the run of group `g`: the request and the tile within it that it begins
+// with, for every thread that asks (`finds`).  The whole block takes part; counts fit 32 bits (the host has checked their sum).
+struct Schedule {
+  unsigned total = 0, per = 0;
+
+  // prefix: [blockDim.x] and sums: [33] in shared memory
+  __device__ __forceinline__ void find(const DecodeArgs& a, unsigned tokens, unsigned* prefix, unsigned* sums, bool finds, unsigned g, int* b,
+                                       unsigned* tile) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, warps = n_threads >> 5;
+    const bool one_pass = a.B <= n_threads;
+    auto tiles = [&](int r) { return r < a.B ? (length_of(a, r) + tokens - 1u) / tokens : 0u; };
+    if (!one_pass) {
+      unsigned t = 0;
+      for (int r = tid; r < a.B; r += n_threads) t += tiles(r);
+      t = __reduce_add_sync(0xffffffffu, t);
+      if (lane == 0) sums[warp] = t;
+      __syncthreads();
+      total = 0;
+      for (int i = 0; i < warps; ++i) total += sums[i];
+      __syncthreads();
+    }
+    unsigned before = 0;
+    *b = -1;
+    *tile = 0;
+    for (int b0 = 0; b0 < a.B; b0 += n_threads) {
+      const unsigned n = tiles(b0 + tid);
+      unsigned incl = n;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const unsigned o = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += o;
+      }
+      if (lane == 31) sums[warp] = incl;
+      __syncthreads();
+      unsigned sum = 0, mine = 0;
+      for (int i = 0; i < warps; ++i) {
+        if (i == warp) mine = sum;
+        sum += sums[i];
+      }
+      const unsigned start = before + mine + incl - n;
+      prefix[tid] = start;
+      if (blockIdx.x == 0 && b0 + tid < a.B) a.starts[b0 + tid] = start;
+      if (one_pass) total = sum;
+      per = (total + a.groups - 1) / a.groups;
+      __syncthreads();
+      const unsigned first = g * per;
+      if (finds && *b < 0 && first < total && first < before + sum) {
+        int lo = 0, hi = min(n_threads, a.B - b0);  // prefix[lo] <= first, and the last such: requests without tiles are passed
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (prefix[mid] <= first) lo = mid; else hi = mid;
+        }
+        *b = b0 + lo;
+        *tile = first - prefix[lo];
+      }
+      before += sum;
+      if (!one_pass) __syncthreads();
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+      a.starts[a.B] = total;
+      a.starts[a.B + 1] = per;
+    }
+  }
+};
+
+// Where the load side of a ring is: the next tile, and what has been loaded about it ahead of its turn.
+struct Cursor {
+  int b, len, t, left;     // request, its length, first token of the next tile, tiles left in the run
+  bool first, from_start;  // the tile begins a part; the part begins its request
+  __device__ __forceinline__ void start(const DecodeArgs& a, int b_, unsigned tile, unsigned left_, int tokens) {
+    b = b_;
+    t = static_cast<int>(tile) * tokens;
+    left = static_cast<int>(left_);
+    len = left > 0 ? length_of(a, b) : 0;
+    first = true;
+    from_start = t == 0;
+  }
+  __device__ __forceinline__ int flags(int tokens) const {
+    const bool ends = t + tokens >= len;
+    return (first ? kFirst : 0) | (ends || left == 1 ? kLast : 0) | (left == 1 ? kEnd : 0) | (from_start && ends ? kDirect : 0) |
+           (from_start ? kSlot1 : 0);
+  }
+  // to the next tile of the run, which has one
+  __device__ __forceinline__ void advance(const DecodeArgs& a, int tokens) {
+    first = false;
+    t += tokens;
+    if (t >= len) {
+      do {
+        ++b;
+        len = length_of(a, b);
+      } while (len == 0 && b + 1 < a.B);
+      t = 0;
+      first = true;
+      from_start = true;
+    }
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+// tiles by TMA
+
+// Compute warps of a block at most.  Two blocks and their load warps share an SM: 18 warps of 96 registers a thread, 10 of 168.
+template <int KEY_BYTES>
+constexpr int kBoxWarps = KEY_BYTES <= 320 ? 8 : 4;
+constexpr int kMaxStages = 8, kMaxHeads = 8;
+
+template <bool FP8, int DQK, int DV>
+__global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1) * 32, 2)
+    boxes_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using T = Tile<FP8, DQK, DV>;
+  constexpr int KT = T::kKeys, KB = KT / 16, kMaxWarps = kBoxWarps<T::kKeyBytes> + 1;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ unsigned s_prefix[kMaxWarps * 32], s_sums[kMaxWarps];
+  __shared__ __align__(16) Header s_header[kMaxStages];
+  __shared__ float2 s_scale[kMaxStages][kMaxHeads];  // of the scores, and of V
+  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x >> 5) - 1;  // compute warps; the next one loads
+  const int S = a.stages, TT = a.tile_tokens;
+  const uint32_t k_bytes = a.heads * TT * T::kRowK, stage_bytes = a.heads * TT * T::kKeyBytes;
+  const uint32_t tiles_s = smem_addr(smem), query_s = tiles_s + S * stage_bytes, full_s = smem_addr(s_full), empty_s = smem_addr(s_empty);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(full_s + 8 * i, 1);
+      ptx::mbar_init(empty_s + 8 * i, warps);
+    }
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  wait_for_predecessor();
+  let_successor_start();
+
+  // this block: group g, KV heads from head0, chunks of query heads from chunk0
+  const unsigned g = blockIdx.x / a.units;
+  const int unit = blockIdx.x % a.units, chunk_units = (a.chunks + a.chunk_warps - 1) / a.chunk_warps;
+  const int head0 = unit / chunk_units * a.heads, chunk0 = unit % chunk_units * a.chunk_warps;
+  Schedule plan;
+  int b;
+  unsigned tile0;
+  plan.find(a, TT, s_prefix, s_sums, warp == warps, g, &b, &tile0);
+  const unsigned run = g * plan.per;
+  if (g >= static_cast<unsigned>(a.groups) || run >= plan.total) return;
+  const int tiles = static_cast<int>(min(plan.per, plan.total - run));
+  __syncthreads();
+
+  if (warp == warps) {
+    Cursor c;
+    c.start(a, b, tile0, tiles, TT);
+    const int box = 1 << a.box_log2, row = lane << a.box_log2;  // this lane's box of a tile: its first token
+    // the block's query rows: whole heads, or (more chunks than warps) part of one head's
+    const int q0 = head0 * a.group + chunk0 * a.chunk_heads;
+    const int nq = chunk_units > 1 ? min(a.chunk_warps * a.chunk_heads, a.group - chunk0 * a.chunk_heads)
+                                   : min(a.heads, a.cache.H_kv - head0) * a.group;
+    int pg, off;
+    float2 scale = {a.scale_log2, 1.0f};
+    // the page of this lane's box in the next tile, and (lane: a head) the descales of its request: a turn ahead of their use
+    auto look_up = [&]() {
+      pg = -1;
+      off = 0;
+      if (row < TT && c.t + row < c.len) {
+        int p;
+        page_of(a, c.t + row, &p, &off);
+        pg = __ldg(a.table + c.b * a.table_stride + p);
+      }
+      if (FP8 && c.first && lane < a.heads) {
+        const int di = a.desc_per_head ? c.b * a.cache.H_kv + min(head0 + lane, a.cache.H_kv - 1) : 0;
+        scale.x = a.scale_log2 * (a.q_desc ? __ldg(a.q_desc + di) : 1.0f) * (a.k_desc ? __ldg(a.k_desc + di) : 1.0f);
+        scale.y = a.v_desc ? __ldg(a.v_desc + di) : 1.0f;
+      }
+    };
+    look_up();
+    bool bad = false;
+    int stage = 0;
+    uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
+    for (int i = 0; i < tiles; ++i) {
+      if (!mbar_wait_bounded(empty_s + 8 * stage, parity)) {
+        if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+        break;
+      }
+      const uint32_t ks = tiles_s + stage * stage_bytes, bar = full_s + 8 * stage;
+      const int valid = min(TT, c.len - c.t);
+      const bool ok = pg >= 0 && pg < a.cache.num_pages;
+      const unsigned boxes = __ballot_sync(0xffffffffu, ok);
+      bad |= row < valid && !ok;
+      if (c.first && lane < a.heads) s_scale[stage][lane] = scale;
+      __syncwarp();
+      if (lane == 0) {
+        s_header[stage] = {c.b, c.flags(TT), valid, boxes};
+        const uint32_t q_bytes = c.first ? nq * T::kRowK : 0;
+        ptx::mbar_arrive_expect_tx(bar, (__popc(boxes) << a.box_log2) * a.heads * T::kKeyBytes + q_bytes);
+        if (c.first) bulk_load(query_s + stage * a.q_bytes, a.q + c.b * a.q_batch + static_cast<long long>(q0) * T::kRowK, q_bytes, bar);
+      }
+      __syncwarp();
+      if (ok) {
+        const uint32_t at = ks + lane * (a.heads * box) * T::kRowK, vt = ks + k_bytes + lane * (a.heads * box) * T::kRowV;
+        const bool jk = !kWhole<T::kRowK> && a.joint_k, jv = !kWhole<T::kRowV> && a.joint_v;
+        tma_load_5d(at, &kmap, bar, 0, off, jk ? head0 * T::kRowK / 128 : 0, jk ? 0 : head0, pg);
+        tma_load_5d(vt, &vmap, bar, 0, off, jv ? head0 * T::kRowV / 128 : 0, jv ? 0 : head0, pg);
+      }
+      if (--c.left > 0) {
+        c.advance(a, TT);
+        look_up();
+      }
+      if (++stage == S) {
+        stage = 0;
+        parity ^= 1;
+      }
+    }
+    if (bad) atomicOr(a.status, kStatusBadPageBit);
+    return;
+  }
+
+  // this warp: a run of keys, a KV head, a chunk of its query heads
+  const int head = warp % a.heads, chunk = chunk0 + warp / a.heads % a.chunk_warps, sub = warp / (a.heads * a.chunk_warps);
+  const int hk = head0 + head, q0 = hk * a.group + chunk * a.chunk_heads, nq = min(a.chunk_heads, a.group - chunk * a.chunk_heads);
+  const bool idle = hk >= a.cache.H_kv || nq <= 0;  // the last block of a group may have heads or chunks too many
+  Reader<T::kRowK, KB> kr;
+  Reader<T::kRowV, KB> vr;
+  set_readers<FP8, DQK, DV, KB>(lane, a.box_log2, head, a.heads, sub * KT, a.joint_k, a.joint_v, &kr, &vr);
+  const uint32_t my_query = query_s + (head * a.group + (chunk - chunk0) * a.chunk_heads) * T::kRowK;
+  Rows<FP8, DQK, DV> rows;
+  int stage = 0;
+  uint32_t parity = 0;
+  for (int i = 0; i < tiles; ++i) {
+    if (!mbar_wait_bounded(full_s + 8 * stage, parity)) {
+      // copies still in flight write to this block's shared memory: wait for them, again for a bounded time
+      for (int j = 1; j < S && i + j < tiles; ++j) {
+        if (++stage == S) {
+          stage = 0;
+          parity ^= 1;
+        }
+        mbar_wait_bounded(full_s + 8 * stage, parity);
+      }
+      if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+      return;
+    }
+    const Header h = s_header[stage];
+    const uint32_t ks = tiles_s + stage * stage_bytes, vs = ks + k_bytes;
+    if (!idle) {
+      if (h.flags & kFirst) rows.begin(my_query + stage * a.q_bytes, nq, s_scale[stage][head].x, s_scale[stage][head].y, lane);
+      const int valid = min(KT, h.valid - sub * KT);
+      if (valid > 0) {
+        uint32_t mask = 0xffffffffu >> (32 - valid);
+        if (~h.boxes << (31 - ((h.valid - 1) >> a.box_log2)))  // a box without a page
+          mask &= __ballot_sync(0xffffffffu, h.boxes >> ((sub * KT + lane) >> a.box_log2) & 1);
+        if (mask)
+          rows.tile(ks, vs, kr, vr, mask, lane, [&]() {
+            // whatever V holds behind the request's end is not a number to multiply by 0: its pieces as this warp reads them
+#pragma unroll
+            for (int n = 0; n < KB; ++n) {
+              const int r = FP8 ? lane & 15 : (lane >> 4) * 8 + (lane & 7);
+              if (!((mask >> (n * 16 + r)) & 1))
+#pragma unroll
+                for (int p = 0; p < T::kRowV / 16; p += 2) ptx::st_shared_v4(vr.at(vs, n, p), 0, 0, 0, 0);
+            }
+            ptx::fence_proxy_async_smem();  // before a later TMA load into this stage
+            __syncwarp();
+          });
+      }
+      if (h.flags & kLast) {
+        const bool direct = (h.flags & kDirect) && a.subs == 1;
+        rows.finish(a, h.b, q0, nq, direct, (static_cast<long long>(g) * 2 + (h.flags & kSlot1 ? 1 : 0)) * a.subs + sub, lane);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(empty_s + 8 * stage);
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// tiles by cp.async, row by row: any page size, any stride
+
+constexpr int kRowStages = 3;
+
+template <int KEY_BYTES>
+constexpr int kRowWarps = KEY_BYTES <= 320 ? 12 : 8;
+
+template <bool FP8, int DQK, int DV>
+__global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 32, 1) rows_kernel(const __grid_constant__ DecodeArgs a) {
+  using T = Tile<FP8, DQK, DV>;
+  constexpr int KT = T::kKeys, KB = KT / 16, kLog2 = KT == 32 ? 5 : 4, kMaxWarps = kRowWarps<T::kKeyBytes>, S = kRowStages;
+  constexpr int kPiecesK = T::kRowK / 16, kPiecesV = T::kRowV / 16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ unsigned s_prefix[kMaxWarps * 32], s_sums[kMaxWarps];
+  __shared__ __align__(16) Header s_header[kMaxWarps][S];
+  __shared__ float2 s_scale[kMaxWarps][S];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_for_predecessor();
+  let_successor_start();
+  const unsigned w = warp * gridDim.x + blockIdx.x, g = w / a.units;  // few workers are spread over the blocks
+  Schedule plan;
+  int b;
+  unsigned tile0;
+  plan.find(a, KT, s_prefix, s_sums, g < static_cast<unsigned>(a.groups), g, &b, &tile0);
+  const unsigned run = g * plan.per;
+  if (g >= static_cast<unsigned>(a.groups) || run >= plan.total) return;
+  const int tiles = static_cast<int>(min(plan.per, plan.total - run));
+  const int unit = static_cast<int>(w % a.units), hk = unit / a.chunks, chunk = unit % a.chunks;
+  const int q0 = hk * a.group + chunk * a.chunk_heads, nq = min(a.chunk_heads, a.group - chunk * a.chunk_heads);
+  const uint8_t* kbase = a.cache.k + hk * a.cache.k_head;
+  const uint8_t* vbase = a.cache.v + hk * a.cache.v_head;
+  const uint32_t tiles_s = smem_addr(smem) + warp * S * T::kTileBytes;
+  const uint32_t query_s = smem_addr(smem) + (blockDim.x >> 5) * S * T::kTileBytes + warp * S * a.q_bytes;
+
+  Cursor c;
+  c.start(a, b, tile0, tiles, KT);
+  int pg, off;  // page and offset in it of token c.t + lane
+  bool bad = false;
+  auto look_up = [&]() {
+    pg = -1;
+    off = 0;
+    if (lane < KT && c.t + lane < c.len) {
+      int p;
+      page_of(a, c.t + lane, &p, &off);
+      pg = __ldg(a.table + c.b * a.table_stride + p);
+    }
+  };
+  look_up();
+  auto issue = [&](int stage) {
+    if (c.left > 0) {
+      const bool inside = lane < KT && c.t + lane < c.len, ok = inside && pg >= 0 && pg < a.cache.num_pages;
+      bad |= inside && !ok;
+      const unsigned mask = __ballot_sync(0xffffffffu, ok);
+      const uint32_t ks = tiles_s + stage * T::kTileBytes, vs = ks + KT * T::kRowK;
+      const long long krow = ok ? pg * a.cache.k_page + off * a.cache.k_tok : 0;
+      const long long vrow = ok ? pg * a.cache.v_page + off * a.cache.v_tok : 0;
+#pragma unroll
+      for (int i = 0; i < KT * kPiecesK / 32; ++i) {
+        const int x = i * 32 + lane, r = x / kPiecesK, p = x % kPiecesK;
+        copy16(ks + place<T::kRowK>(KT, r, p), kbase + __shfl_sync(0xffffffffu, krow, r) + p * 16, (mask >> r) & 1 ? 16 : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < KT * kPiecesV / 32; ++i) {
+        const int x = i * 32 + lane, r = x / kPiecesV, p = x % kPiecesV;
+        copy16(vs + place<T::kRowV>(KT, r, p), vbase + __shfl_sync(0xffffffffu, vrow, r) + p * 16, (mask >> r) & 1 ? 16 : 0);
+      }
+      if (c.first) {
+        const uint8_t* q = a.q + c.b * a.q_batch + static_cast<long long>(q0) * T::kRowK;
+        for (int x = lane; x < nq * kPiecesK; x += 32) copy16(query_s + stage * a.q_bytes + x * 16, q + x * 16, 16);
+      }
+      if (lane == 0) {
+        s_header[warp][stage] = {c.b, c.flags(KT), KT, mask};
+        if (c.first) {
+          float2 scale = {a.scale_log2, 1.0f};
+          if (FP8) {
+            const int di = a.desc_per_head ? c.b * a.cache.H_kv + hk : 0;
+            scale.x *= (a.q_desc ? __ldg(a.q_desc + di) : 1.0f) * (a.k_desc ? __ldg(a.k_desc + di) : 1.0f);
+            scale.y = a.v_desc ? __ldg(a.v_desc + di) : 1.0f;
+          }
+          s_scale[warp][stage] = scale;
+        }
+      }
+      if (--c.left > 0) {
+        c.advance(a, KT);
+        look_up();
+      }
+    }
+    copy_commit();
+  };
+
+  Reader<T::kRowK, KB> kr;
+  Reader<T::kRowV, KB> vr;
+  set_readers<FP8, DQK, DV, KB>(lane, kLog2, 0, 1, 0, false, false, &kr, &vr);
+  Rows<FP8, DQK, DV> rows;
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  int stage = 0;
+  for (int it = 0; it < tiles; ++it) {
+    copy_wait<S - 2>();
+    __syncwarp();  // this tile has landed, and every lane has read the one before it, whose stage is refilled
+    issue(stage == 0 ? S - 1 : stage - 1);
+    const Header h = s_header[warp][stage];
+    const uint32_t ks = tiles_s + stage * T::kTileBytes, vs = ks + KT * T::kRowK;
+    if (h.flags & kFirst) rows.begin(query_s + stage * a.q_bytes, nq, s_scale[warp][stage].x, s_scale[warp][stage].y, lane);
+    if (h.boxes) rows.tile(ks, vs, kr, vr, h.boxes, lane, []() {});  // rows that are not valid were filled with zeros
+    if (h.flags & kLast) rows.finish(a, h.b, q0, nq, h.flags & kDirect, static_cast<long long>(g) * 2 + (h.flags & kSlot1 ? 1 : 0), lane);
+    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+  copy_wait<0>();
+  if (bad) atomicOr(a.status, kStatusBadPageBit);
+}
+
+// ------------------------------------------------------------------------------------------------
+// the join
+
+// Joins the parts of the requests that several groups worked on, and writes the rows of empty requests: one block of W
+// warps per (request, head).  A warp takes every W-th part, 32 at a time: a lane reads one's maximum and sum while the rows of O
+// come in, none of which depends on another; then the warps meet in shared memory in a fixed order.
+template <int DV, int W>
+__global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int kThreads = W * 32, kVec = DV / 32, kBatch = 8;
+  using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
+  __shared__ float s_o[W][DV], s_m[W], s_l[W];
+  wait_for_predecessor();
+  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned p0 = a.starts[b], p1 = a.starts[b + 1], per = a.starts[a.B + 1];
+  const long long row = static_cast<long long>(b) * a.H + h;
+  if (p0 == p1) {
+    for (int i = threadIdx.x; i < DV; i += kThreads) a.out[row * DV + i] = __float2bfloat16_rn(0.0f);
+    if (a.lse && threadIdx.x == 0) a.lse[row] = -INFINITY;
+    return;
+  }
+  const int g0 = static_cast<int>(p0 / per), n = (static_cast<int>((p1 - 1) / per) - g0 + 1) * a.subs;
+  if (n == 1) return;
+  // part i: group g0 + i / subs, its slot 1 (a request that begins there) for the first, else slot 0
+  const int subs_log2 = 31 - __clz(a.subs);
+  auto part = [&](int i) {
+    const int k = i >> subs_log2;
+    return (((static_cast<long long>(g0 + k) * 2 + (k == 0 ? 1 : 0)) << subs_log2) + (i & (a.subs - 1))) * a.H + h;
+  };
+  float m = -INFINITY, l = 0.0f, o[kVec] = {};
+  for (int base = warp; base < n; base += 32 * W) {
+    const int count = min(32, (n - base + W - 1) / W);  // parts base, base + W, ...
+    const float2 ml = lane < count ? a.ml[part(base + lane * W)] : make_float2(-INFINITY, 0.0f);
+    float top = ml.x;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.0f : mn;
+    const float f = exp2_approx(m - ref), e = exp2_approx(ml.x - ref);  // 0 for parts without a valid key
+    m = mn;
+    l = l * f + ml.y * e;  // this lane's share
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) o[j] *= f;
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+      Vec x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < count) x[k] = *reinterpret_cast<const Vec*>(a.part + part(base + (k0 + k) * W) * DV + lane * kVec);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float ek = __shfl_sync(0xffffffffu, e, k0 + k);
+        const float* y = reinterpret_cast<const float*>(&x[k]);
+        if (k0 + k < count && ek > 0.0f) {  // a part without a valid key has no O
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) o[j] = fmaf(y[j], ek, o[j]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) s_o[warp][lane * kVec + j] = o[j];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  float M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[i]);
+  float e[W], L = 0.0f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    e[i] = s_m[i] == -INFINITY ? 0.0f : exp2_approx(s_m[i] - M);
+    L = fmaf(s_l[i], e[i], L);
+  }
+  for (int i = threadIdx.x; i < DV; i += kThreads) {
+    float x = 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) x = fmaf(s_o[j][i], e[j], x);
+    a.out[row * DV + i] = __float2bfloat16_rn(L > 0.0f ? x / L : 0.0f);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ------------------------------------------------------------------------------------------------
+// host side
+
+inline long long round_up(long long x, long long n) { return (x + n - 1) / n * n; }
+
+// Parts that one request and head can have at most, for the workspace: one per group and token run.  A group has H_kv warps per
+// chunk of 8 query heads and token run at least, and there are no more than tiles.
+inline long long parts_at_most(int B, int H, int H_kv, long long max_len) {
+  const long long warps = static_cast<long long>(H_kv) * ((H / H_kv + 7) / 8);
+  return std::max<long long>(kMaxHeads, std::min(kMaxSms * kMaxWarpsPerSm / warps, B * ((max_len + 15) / 16 + kMaxHeads)));
+}
+
+inline long long tiles_at_most(int B, long long max_len, int keys) { return B * ((max_len + keys - 1) / keys); }
+
+// Boxes of `tokens` rows of `heads` heads of one page.  The column dimension follows the tokens, so that a box lands as
+// [head][column][token][CB]; `joint`: the heads' rows as one, in columns of 128 bytes.
+inline bool make_map(CUtensorMap* m, const uint8_t* base, bool fp8, int row, const CacheView& c, long long page, long long tok, long long head,
+                     int tokens, int heads, bool joint) {
+  const int es = fp8 ? 1 : 2, cb = row % 128 == 0 || joint ? 128 : 64;
+  using u64 = cuuint64_t;
+  using u32 = cuuint32_t;
+  const u64 dims[5] = {u64(cb / es), u64(c.page_size), u64(joint ? static_cast<long long>(c.H_kv) * row / cb : row / cb), u64(joint ? 1 : c.H_kv),
+                       u64(c.num_pages)};
+  const u64 strides[4] = {u64(tok), u64(cb), u64(joint ? tok : head), u64(page)};
+  const u32 box[5] = {u32(cb / es), u32(tokens), u32(joint ? heads * row / cb : row / cb), u32(joint ? 1 : heads), 1};
+  const u32 estr[5] = {1, 1, 1, 1, 1};
+  return encode_tensor_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint8_t*>(base), dims, strides, box,
+                           estr, cb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, int smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+
+// Both kernels ask for the largest share of shared memory: an SM changes the share only when it is empty, so blocks
+// launched beside a predecessor of another share would find too little (1.5 times the time, 128 requests).
+template <typename K>
+bool prepare(K* kernel, int smem, int dev, std::atomic<int>* set) {
+  if (set[dev].load(std::memory_order_acquire) >= smem) return true;
+  const void* f = reinterpret_cast<const void*>(kernel);
+  if (cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess) return false;
+  if (smem > 1 && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock - 8192) != cudaSuccess) return false;
+  set[dev].store(smem > 1 ? kSmemPerBlock : 1, std::memory_order_release);
+  return true;
+}
+
+// Fewest equal pieces of `n` that are at most `most`, as the size of a piece.
+inline int piece(int n, int most) { return (n + (n + most - 1) / most - 1) / ((n + most - 1) / most); }
+
+// A block of boxes_kernel: chunks of a head first (they read the same tile), then heads side by side, then runs of tokens.
+template <bool FP8, int DQK, int DV>
+cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream_t stream) {
+  using T = Tile<FP8, DQK, DV>;
+  const CacheView& c = a.cache;
+  constexpr int kWarps = kBoxWarps<T::kKeyBytes>;
+  *done = false;
+  a.chunk_warps = piece(a.chunks, kWarps);
+  a.heads = piece(c.H_kv, kWarps / a.chunk_warps);
+  a.subs = 1;
+  while (a.subs * 2 * a.heads * a.chunk_warps <= kWarps) a.subs *= 2;
+  a.tile_tokens = a.subs * T::kKeys;
+  a.units = (c.H_kv + a.heads - 1) / a.heads * ((a.chunks + a.chunk_warps - 1) / a.chunk_warps);
+  // Boxes: as many tokens of a page as divide both the page and the tile.  A broadcast (stride 0) or very large stride has no
+  // tensor map, and a page of an odd size no boxes that fill the swizzle pattern (8 rows).
+  int tokens = a.tile_tokens;
+  while (tokens > 1 && c.page_size % tokens != 0) tokens /= 2;
+  if (tokens < 8) return cudaSuccess;
+  for (long long s : {c.k_page, c.k_tok, c.k_head, c.v_page, c.v_tok, c.v_head})
+    if (s <= 0 || s >= (1ll << 40)) return cudaSuccess;
+  a.box_log2 = 0;
+  while ((1 << a.box_log2) < tokens) ++a.box_log2;
+  auto joint = [&](int row, long long head) {
+    return row % 128 != 0 && head == row && static_cast<long long>(c.H_kv) * row % 128 == 0 && a.heads * row % 128 == 0;
+  };
+  a.joint_k = joint(T::kRowK, c.k_head);
+  a.joint_v = joint(T::kRowV, c.v_head);
+  CUtensorMap kmap, vmap;
+  if (!make_map(&kmap, c.k, FP8, T::kRowK, c, c.k_page, c.k_tok, c.k_head, tokens, a.heads, a.joint_k) ||
+      !make_map(&vmap, c.v, FP8, T::kRowV, c, c.v_page, c.v_tok, c.v_head, tokens, a.heads, a.joint_v))
+    return cudaSuccess;
+  // a block's queries: whole heads, or (more chunks than warps) part of one head's
+  const int nq = a.chunks > a.chunk_warps ? a.chunk_warps * a.chunk_heads : a.heads * a.group;
+  a.q_bytes = static_cast<int>(round_up(nq * T::kRowK, 16));
+  const int warps = a.heads * a.chunk_warps * a.subs, stage = a.heads * a.tile_tokens * T::kKeyBytes + a.q_bytes;
+  // two blocks an SM (more where they are small), or one if two would not have two stages each
+  constexpr int kStatic = 4096;  // the schedule's tables and headers, with the 1 KiB that each block takes
+  int blocks = std::max(2, 2 * kWarps / warps);
+  while (blocks > 1 && blocks * (2 * stage + kStatic) > kSmemPerSm) --blocks;
+  a.stages = std::min(kMaxStages, std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) / stage);
+  if (a.stages < 2) return cudaSuccess;
+  a.groups = static_cast<int>(std::max(1ll, std::min<long long>(static_cast<long long>(nsm) * blocks / a.units, tiles_at_most(a.B, a.max_len, a.tile_tokens))));
+  static std::atomic<int> set[kMaxDevices];
+  if (!prepare(boxes_kernel<FP8, DQK, DV>, 2, dev, set)) return cudaErrorUnknown;
+  *done = true;
+  return launch_dependent(boxes_kernel<FP8, DQK, DV>, static_cast<unsigned>(a.groups) * a.units, (warps + 1) * 32, a.stages * stage, stream, a, kmap,
+                          vmap);
+}
+
+template <bool FP8, int DQK, int DV>
+cudaError_t launch_rows(DecodeArgs& a, int nsm, int dev, cudaStream_t stream) {
+  using T = Tile<FP8, DQK, DV>;
+  a.subs = 1;
+  a.units = a.cache.H_kv * a.chunks;
+  a.q_bytes = a.chunk_heads * T::kRowK;
+  const int ring = kRowStages * (T::kTileBytes + a.q_bytes), most = std::min(kRowWarps<T::kKeyBytes>, (kSmemPerBlock - 8192) / ring);
+  const long long resident = static_cast<long long>(nsm) * most;
+  a.groups = static_cast<int>(std::max(1ll, std::min(resident / a.units, tiles_at_most(a.B, a.max_len, T::kKeys))));
+  const long long w = static_cast<long long>(a.groups) * a.units;
+  const unsigned grid = static_cast<unsigned>(w <= resident ? std::min<long long>(nsm, w) : (w + most - 1) / most);
+  const int warps = static_cast<int>((w + grid - 1) / grid);
+  static std::atomic<int> set[kMaxDevices];
+  if (!prepare(rows_kernel<FP8, DQK, DV>, 2, dev, set)) return cudaErrorUnknown;
+  return launch_dependent(rows_kernel<FP8, DQK, DV>, grid, warps * 32, ring * warps, stream, a);
+}
+
+template <bool FP8, int DQK, int DV>
+zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t stream) {
+  // workspace: plan, (m, l), O
+  const long long parts = parts_at_most(a.B, a.H, a.cache.H_kv, a.max_len);
+  a.starts = reinterpret_cast<unsigned*>(ws);
+  ws += round_up((a.B + 2ll) * 4, 256);
+  a.ml = reinterpret_cast<float2*>(ws);
+  ws += round_up(2 * parts * a.H * 8, 256);
+  a.part = reinterpret_cast<float*>(ws);
+  // chunks of up to 8 query heads, as equal as they come
+  a.chunks = (a.group + 7) / 8;
+  a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
+  bool done;
+  cudaError_t e = launch_boxes<FP8, DQK, DV>(a, &done, nsm, dev, stream);
+  if (e == cudaSuccess && !done) e = launch_rows<FP8, DQK, DV>(a, nsm, dev, stream);
+  if (e != cudaSuccess) return ZYFA_ERR_CUDA;
+  // Few rows have many parts each: more warps per row.
+  const unsigned rows = static_cast<unsigned>(a.B) * a.H;
+  static std::atomic<int> set[2][kMaxDevices];
+  if (!prepare(join_kernel<DV, 4>, 1, dev, set[0]) || !prepare(join_kernel<DV, 16>, 1, dev, set[1])) return ZYFA_ERR_CUDA;
+  e = rows <= 4u * nsm ? launch_dependent(join_kernel<DV, 16>, rows, 512, 0, stream, a) : launch_dependent(join_kernel<DV, 4>, rows, 128, 0, stream, a);
+  return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
+}
+
+}  // namespace decode
+
+// Instantiated in zyfa_decode_fp8.cu and zyfa_decode_bf16.cu.
+zyfa_status_t decode_fp8(decode::DecodeArgs& a, int D_qk, int nsm, int dev, uint8_t* ws, cudaStream_t stream);
+zyfa_status_t decode_bf16(decode::DecodeArgs& a, int D_qk, int nsm, int dev, uint8_t* ws, cudaStream_t stream);
+
+}  // namespace zyfa
