@@ -39,7 +39,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <type_traits>
 #include <utility>
 
 #include "paged.cuh"
@@ -632,24 +631,39 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     const int q0 = head0 * a.group + chunk0 * a.chunk_heads;
     const int nq = chunk_units > 1 ? min(a.chunk_warps * a.chunk_heads, a.group - chunk0 * a.chunk_heads)
                                    : min(a.heads, a.cache.H_kv - head0) * a.group;
-    int pg, off;
-    float2 scale = {a.scale_log2, 1.0f};
-    // the page of this lane's box in the next tile, and (lane: a head) the descales of its request: a turn ahead of their use
-    auto look_up = [&]() {
-      pg = -1;
-      off = 0;
-      if (row < TT && c.t + row < c.len) {
-        int p;
-        page_of(a, c.t + row, &p, &off);
-        pg = __ldg(a.table + c.b * a.table_stride + p);
-      }
-      if (FP8 && c.first && lane < a.heads) {
-        const int di = a.desc_per_head ? c.b * a.cache.H_kv + min(head0 + lane, a.cache.H_kv - 1) : 0;
-        scale.x = a.scale_log2 * (a.q_desc ? __ldg(a.q_desc + di) : 1.0f) * (a.k_desc ? __ldg(a.k_desc + di) : 1.0f);
-        scale.y = a.v_desc ? __ldg(a.v_desc + di) : 1.0f;
-      }
+    // The pages of 32 boxes of the request at a time (a tile's boxes are among one such 32), the next 32, or the first ones of
+    // the next request, being read meanwhile; likewise (lane: a head) the next request's descales.
+    auto pages = [&](int request, int len, int box0) {
+      const int t = (box0 + lane) << a.box_log2;
+      if (t >= len) return -1;
+      int p, off;
+      page_of(a, t, &p, &off);
+      return __ldg(a.table + request * a.table_stride + p);
     };
-    look_up();
+    auto scales = [&](int request) {
+      float2 x = {a.scale_log2, 1.0f};
+      if (FP8 && lane < a.heads) {
+        const int di = a.desc_per_head ? request * a.cache.H_kv + min(head0 + lane, a.cache.H_kv - 1) : 0;
+        x.x *= (a.q_desc ? __ldg(a.q_desc + di) : 1.0f) * (a.k_desc ? __ldg(a.k_desc + di) : 1.0f);
+        x.y = a.v_desc ? __ldg(a.v_desc + di) : 1.0f;
+      }
+      return x;
+    };
+    int next_b = 0, next_len = 0, pg_next = -1;
+    float2 scale = scales(c.b), scale_next = scale;
+    int pg_now = pages(c.b, c.len, c.t >> a.box_log2 & ~31);
+    auto look_ahead = [&](bool new_request) {
+      if (new_request) {
+        next_len = 0;
+        if ((c.len - c.t + TT - 1) / TT < c.left)  // the run goes on behind this request
+          for (next_b = c.b + 1; next_b < a.B && next_len == 0; ++next_b) next_len = length_of(a, next_b);
+        --next_b;
+        if (next_len > 0) scale_next = scales(next_b);
+      }
+      const int box0 = (c.t >> a.box_log2 & ~31) + 32;
+      pg_next = box0 << a.box_log2 < c.len ? pages(c.b, c.len, box0) : next_len > 0 ? pages(next_b, next_len, 0) : -1;
+    };
+    look_ahead(true);
     bool bad = false;
     int stage = 0;
     uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
@@ -660,7 +674,10 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       }
       const uint32_t ks = tiles_s + stage * stage_bytes, bar = full_s + 8 * stage;
       const int valid = min(TT, c.len - c.t);
-      const bool ok = pg >= 0 && pg < a.cache.num_pages;
+      int p, off;
+      page_of(a, c.t + row, &p, &off);
+      const int pg = __shfl_sync(0xffffffffu, pg_now, (c.t >> a.box_log2 & 31) + lane);
+      const bool ok = row < valid && pg >= 0 && pg < a.cache.num_pages;
       const unsigned boxes = __ballot_sync(0xffffffffu, ok);
       bad |= row < valid && !ok;
       if (c.first && lane < a.heads) s_scale[stage][lane] = scale;
@@ -679,8 +696,20 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
         tma_load_5d(vt, &vmap, bar, 0, off, jv ? head0 * T::kRowV / 128 : 0, jv ? 0 : head0, pg);
       }
       if (--c.left > 0) {
-        c.advance(a, TT);
-        look_up();
+        c.first = false;
+        c.t += TT;
+        if (c.t >= c.len) {
+          c.b = next_b;
+          c.len = next_len;
+          c.t = 0;
+          c.first = c.from_start = true;
+          pg_now = pg_next;
+          scale = scale_next;
+          look_ahead(true);
+        } else if ((c.t >> a.box_log2 & 31) == 0) {
+          pg_now = pg_next;
+          look_ahead(false);
+        }
       }
       if (++stage == S) {
         stage = 0;
@@ -867,22 +896,27 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
 // ------------------------------------------------------------------------------------------------
 // the join
 
-// Joins the parts of the requests that several groups worked on, and writes the rows of empty requests: one block of W
-// warps per (request, head).  A warp takes every W-th part, 32 at a time: a lane reads one's maximum and sum while the rows of O
-// come in, none of which depends on another; then the warps meet in shared memory in a fixed order.
-template <int DV, int W>
-__global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int kThreads = W * 32, kVec = DV / 32, kBatch = 8;
-  using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
-  __shared__ float s_o[W][DV], s_m[W], s_l[W];
+// Joins the parts of the requests that several groups worked on, and writes the rows of empty requests.  W warps take a (request,
+// head): every W-th part each, 32 at a time.  A lane reads one part's maximum and sum while the rows of O come in, none of
+// which depends on another; then the warps meet in shared memory in a fixed order.  A block takes ROWS of them (W = 1), or VEC
+// * 32 of the channels of one.
+template <int DV, int W, int ROWS, int VEC, int BATCH>
+__global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
+  static_assert(W == 1 || ROWS == 1);
+  constexpr int kThreads = W * 32, D = VEC * 32;
+  struct alignas(VEC * 4) Vec {
+    float y[VEC];
+  };
+  __shared__ float s_o[W][D], s_m[W], s_l[W];
   wait_for_predecessor();
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = blockIdx.y * D;
+  const long long row = static_cast<long long>(blockIdx.x) * ROWS + (ROWS > 1 ? warp : 0);
+  if (row >= static_cast<long long>(a.B) * a.H) return;
+  const int b = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H), w = ROWS > 1 ? 0 : warp, tid = w * 32 + lane;
   const unsigned p0 = a.starts[b], p1 = a.starts[b + 1], per = a.starts[a.B + 1];
-  const long long row = static_cast<long long>(b) * a.H + h;
   if (p0 == p1) {
-    for (int i = threadIdx.x; i < DV; i += kThreads) a.out[row * DV + i] = __float2bfloat16_rn(0.0f);
-    if (a.lse && threadIdx.x == 0) a.lse[row] = -INFINITY;
+    for (int i = tid; i < D; i += kThreads) a.out[row * DV + d0 + i] = __float2bfloat16_rn(0.0f);
+    if (a.lse && tid == 0 && d0 == 0) a.lse[row] = -INFINITY;
     return;
   }
   const int g0 = static_cast<int>(p0 / per), n = (static_cast<int>((p1 - 1) / per) - g0 + 1) * a.subs;
@@ -893,8 +927,8 @@ __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ De
     const int k = i >> subs_log2;
     return (((static_cast<long long>(g0 + k) * 2 + (k == 0 ? 1 : 0)) << subs_log2) + (i & (a.subs - 1))) * a.H + h;
   };
-  float m = -INFINITY, l = 0.0f, o[kVec] = {};
-  for (int base = warp; base < n; base += 32 * W) {
+  float m = -INFINITY, l = 0.0f, o[VEC] = {};
+  for (int base = w; base < n; base += 32 * W) {
     const int count = min(32, (n - base + W - 1) / W);  // parts base, base + W, ...
     const float2 ml = lane < count ? a.ml[part(base + lane * W)] : make_float2(-INFINITY, 0.0f);
     float top = ml.x;
@@ -905,48 +939,55 @@ __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ De
     m = mn;
     l = l * f + ml.y * e;  // this lane's share
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) o[j] *= f;
-    for (int k0 = 0; k0 < count; k0 += kBatch) {
-      Vec x[kBatch];
+    for (int j = 0; j < VEC; ++j) o[j] *= f;
+    for (int k0 = 0; k0 < count; k0 += BATCH) {
+      Vec x[BATCH];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (k0 + k < count) x[k] = *reinterpret_cast<const Vec*>(a.part + part(base + (k0 + k) * W) * DV + lane * kVec);
+      for (int k = 0; k < BATCH; ++k)
+        if (k0 + k < count) x[k] = *reinterpret_cast<const Vec*>(a.part + part(base + (k0 + k) * W) * DV + d0 + lane * VEC);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < BATCH; ++k) {
         const float ek = __shfl_sync(0xffffffffu, e, k0 + k);
-        const float* y = reinterpret_cast<const float*>(&x[k]);
         if (k0 + k < count && ek > 0.0f) {  // a part without a valid key has no O
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) o[j] = fmaf(y[j], ek, o[j]);
+          for (int j = 0; j < VEC; ++j) o[j] = fmaf(x[k].y[j], ek, o[j]);
         }
       }
     }
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+  if constexpr (W == 1) {
+    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+    __nv_bfloat16* out = a.out + row * DV + d0 + lane * VEC;
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) s_o[warp][lane * kVec + j] = o[j];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+    for (int j = 0; j < VEC; j += 2) *reinterpret_cast<__nv_bfloat162*>(out + j) = __floats2bfloat162_rn(o[j] * f, o[j + 1] * f);
+    if (a.lse && lane == 0 && d0 == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s_o[w][lane * VEC + j] = o[j];
+    if (lane == 0) {
+      s_m[w] = m;
+      s_l[w] = l;
+    }
+    __syncthreads();
+    float M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[i]);
+    float e[W], L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      e[i] = s_m[i] == -INFINITY ? 0.0f : exp2_approx(s_m[i] - M);
+      L = fmaf(s_l[i], e[i], L);
+    }
+    for (int i = tid; i < D; i += kThreads) {
+      float x = 0.0f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) x = fmaf(s_o[j][i], e[j], x);
+      a.out[row * DV + d0 + i] = __float2bfloat16_rn(L > 0.0f ? x / L : 0.0f);
+    }
+    if (a.lse && tid == 0 && d0 == 0) a.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
   }
-  __syncthreads();
-  float M = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[i]);
-  float e[W], L = 0.0f;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    e[i] = s_m[i] == -INFINITY ? 0.0f : exp2_approx(s_m[i] - M);
-    L = fmaf(s_l[i], e[i], L);
-  }
-  for (int i = threadIdx.x; i < DV; i += kThreads) {
-    float x = 0.0f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) x = fmaf(s_o[j][i], e[j], x);
-    a.out[row * DV + i] = __float2bfloat16_rn(L > 0.0f ? x / L : 0.0f);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -980,12 +1021,12 @@ inline bool make_map(CUtensorMap* m, const uint8_t* base, bool fp8, int row, con
 }
 
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, int smem, cudaStream_t stream, Args&&... args) {
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, int smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
@@ -1055,7 +1096,7 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   static std::atomic<int> set[kMaxDevices];
   if (!prepare(boxes_kernel<FP8, DQK, DV>, 2, dev, set)) return cudaErrorUnknown;
   *done = true;
-  return launch_dependent(boxes_kernel<FP8, DQK, DV>, static_cast<unsigned>(a.groups) * a.units, (warps + 1) * 32, a.stages * stage, stream, a, kmap,
+  return launch_dependent(boxes_kernel<FP8, DQK, DV>, dim3(static_cast<unsigned>(a.groups) * a.units), (warps + 1) * 32, a.stages * stage, stream, a, kmap,
                           vmap);
 }
 
@@ -1073,7 +1114,7 @@ cudaError_t launch_rows(DecodeArgs& a, int nsm, int dev, cudaStream_t stream) {
   const int warps = static_cast<int>((w + grid - 1) / grid);
   static std::atomic<int> set[kMaxDevices];
   if (!prepare(rows_kernel<FP8, DQK, DV>, 2, dev, set)) return cudaErrorUnknown;
-  return launch_dependent(rows_kernel<FP8, DQK, DV>, grid, warps * 32, ring * warps, stream, a);
+  return launch_dependent(rows_kernel<FP8, DQK, DV>, dim3(grid), warps * 32, ring * warps, stream, a);
 }
 
 template <bool FP8, int DQK, int DV>
@@ -1092,11 +1133,21 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   cudaError_t e = launch_boxes<FP8, DQK, DV>(a, &done, nsm, dev, stream);
   if (e == cudaSuccess && !done) e = launch_rows<FP8, DQK, DV>(a, nsm, dev, stream);
   if (e != cudaSuccess) return ZYFA_ERR_CUDA;
-  // Few rows have many parts each: more warps per row.
+  // Few rows have many parts each, and their channels are spread over blocks too; of many rows most lie in one or two groups.
   const unsigned rows = static_cast<unsigned>(a.B) * a.H;
-  static std::atomic<int> set[2][kMaxDevices];
-  if (!prepare(join_kernel<DV, 4>, 1, dev, set[0]) || !prepare(join_kernel<DV, 16>, 1, dev, set[1])) return ZYFA_ERR_CUDA;
-  e = rows <= 4u * nsm ? launch_dependent(join_kernel<DV, 16>, rows, 512, 0, stream, a) : launch_dependent(join_kernel<DV, 4>, rows, 128, 0, stream, a);
+  const long long parts_each = static_cast<long long>(a.groups) * a.subs / a.B;
+  constexpr int V = DV / 32;
+  static std::atomic<int> set[3][kMaxDevices];
+  if (rows * V <= 2u * nsm) {
+    if (!prepare(join_kernel<DV, 16, 1, 1, 20>, 1, dev, set[0])) return ZYFA_ERR_CUDA;
+    e = launch_dependent(join_kernel<DV, 16, 1, 1, 20>, dim3(rows, V), 512, 0, stream, a);
+  } else if (parts_each > 8) {
+    if (!prepare(join_kernel<DV, 4, 1, V, 8>, 1, dev, set[1])) return ZYFA_ERR_CUDA;
+    e = launch_dependent(join_kernel<DV, 4, 1, V, 8>, dim3(rows), 128, 0, stream, a);
+  } else {
+    if (!prepare(join_kernel<DV, 1, 8, V, 4>, 1, dev, set[2])) return ZYFA_ERR_CUDA;
+    e = launch_dependent(join_kernel<DV, 1, 8, V, 4>, dim3((rows + 7) / 8), 256, 0, stream, a);
+  }
   return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
 }
 
