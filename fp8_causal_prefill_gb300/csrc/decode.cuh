@@ -220,33 +220,37 @@ template <int ROW>
 constexpr bool kWhole = ROW % 128 == 0;
 
 // Where one lane's ldmatrix reads go: piece p (16 bytes, p even, plus the lane's own 0 or 1) of row 16 n + the lane's, of one
-// head, is at ((tile + base[n]) ^ flip) + add for the 64-byte half that p lies in.
+// head, is at ((tile + base[n]) ^ flip) + add for the 64-byte half that p lies in (relative to the first half's column).
 template <int ROW, int KB>
 struct Reader {
   static constexpr int kHalves = ROW / 64;
-  uint32_t base[KB], add[kHalves], flip[kHalves];
+  uint32_t base[KB], column, add[kWhole<ROW> ? 1 : kHalves], flip[kWhole<ROW> ? 1 : kHalves];
 
   // tokens: of a box; head: within the box, of `heads`; row, hi: the lane's row of the first 16 and its piece of a pair
   __device__ __forceinline__ void set(int tokens_log2, int head, int heads, int first_row, int row, int hi, bool joint) {
     const int tokens = 1 << tokens_log2;
     const bool wide = kWhole<ROW> || joint;
     const int cb = wide ? 128 : 64;
+    column = tokens * cb;
+    const uint32_t first = head * kHalves / (wide ? 2 : 1) * column;
 #pragma unroll
     for (int n = 0; n < KB; ++n) {
       const int r = first_row + n * 16 + row, box = r >> tokens_log2, in = r & (tokens - 1);
-      base[n] = box * heads * tokens * ROW + in * cb + ((hi ^ (wide ? in & 7 : (in >> 1) & 3)) << 4);
+      base[n] = first + box * heads * tokens * ROW + in * cb + ((hi ^ (wide ? in & 7 : (in >> 1) & 3)) << 4);
     }
+    if constexpr (!kWhole<ROW>) {
 #pragma unroll
-    for (int j = 0; j < kHalves; ++j) {
-      const int half = head * kHalves + j;
-      add[j] = (wide ? half >> 1 : half) * tokens * cb;
-      flip[j] = wide ? (half & 1) << 6 : 0;
+      for (int j = 0; j < kHalves; ++j) {
+        const int half = head * kHalves + j;
+        add[j] = (wide ? half >> 1 : half) * column - first;
+        flip[j] = wide ? (half & 1) << 6 : 0;
+      }
     }
   }
   __device__ __forceinline__ uint32_t at(uint32_t tile, int n, int p) const {
     const int j = p / 4;
     if constexpr (kWhole<ROW>)
-      return ((tile + base[n]) ^ ((p % 8) << 4)) + add[j];  // halves of a head alternate
+      return ((tile + base[n]) ^ ((p % 8) << 4)) + (j / 2) * column;
     else
       return ((tile + base[n]) ^ (flip[j] | (p % 4) << 4)) + add[j];
   }
@@ -266,8 +270,8 @@ struct Header {
   int valid;       // tokens of the request in the tile
   uint32_t boxes;  // boxes_kernel: those whose page is in the cache; rows_kernel: such rows
 };
-// first and last tile of a request's part, last tile of the run; the part is the whole request; it begins the request
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kDirect = 8, kSlot1 = 16 };
+// first and last tile of a request's part; the part is the whole request; it begins the request; not every key is valid
+enum : int { kFirst = 1, kLast = 2, kDirect = 4, kSlot1 = 8, kPartial = 16 };
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) { return max(0, min(__ldg(a.seq_lens + b), a.max_len)); }
 
@@ -289,6 +293,7 @@ struct Rows {
 
   uint32_t qf[kKSteps][2];      // B fragments of the queries
   float o[kMTiles][4], m[2], l[2];  // this lane's two heads
+  F2 ref;                           // kLift - m
   float scale, dv;
 
   // Begins a request's part: its queries from shared memory, `count` dense rows.
@@ -307,14 +312,15 @@ struct Rows {
 #pragma unroll
     for (int i = 0; i < kMTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     m[0] = m[1] = -INFINITY;
+    ref = {INFINITY, INFINITY};
     l[0] = l[1] = 0.0f;
     scale = scale_;
     dv = dv_;
   }
 
-  // One tile of K at ks and V at vs; mask: valid keys, at least one.  clear(): called where V rows of keys that are not valid
-  // may hold anything.
-  template <typename F>
+  // One tile of K at ks and V at vs.  FULL: all keys are valid; else mask: those that are, at least one, and clear() is called
+  // since V rows of the others may hold anything.
+  template <bool FULL, typename F>
   __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, const Reader<T::kRowK, KB>& kr, const Reader<T::kRowV, KB>& vr, uint32_t mask,
                                        int lane, F clear) {
     // S^T: rows are keys, columns heads; then scores in units of log2
@@ -331,7 +337,7 @@ struct Rows {
       x[kb][0] = mul2({c[0], c[1]}, {scale, scale});
       x[kb][1] = mul2({c[2], c[3]}, {scale, scale});
     }
-    if (mask != T::kFull) {
+    if constexpr (!FULL) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -344,7 +350,6 @@ struct Rows {
     F2 y[KB][2];
     float over = -INFINITY;
     auto weigh = [&]() {
-      const F2 ref = {kLift - m[0], kLift - m[1]};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -365,6 +370,7 @@ struct Rows {
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
         const float f = exp2_approx(m[e] - t);
         m[e] = t;
+        (e ? ref.y : ref.x) = kLift - t;
         l[e] *= f;
 #pragma unroll
         for (int i = 0; i < kMTiles; ++i) {
@@ -558,8 +564,8 @@ struct Cursor {
   }
   __device__ __forceinline__ int flags(int tokens) const {
     const bool ends = t + tokens >= len;
-    return (first ? kFirst : 0) | (ends || left == 1 ? kLast : 0) | (left == 1 ? kEnd : 0) | (from_start && ends ? kDirect : 0) |
-           (from_start ? kSlot1 : 0);
+    const bool last = ends || left == 1;
+    return (first ? kFirst : 0) | (last ? kLast | (from_start && ends ? kDirect : 0) | (from_start ? kSlot1 : 0) : 0);
   }
   // to the next tile of the run, which has one
   __device__ __forceinline__ void advance(const DecodeArgs& a, int tokens) {
@@ -606,6 +612,10 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     }
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
+  }
+  if (threadIdx.x == 32) {
+    ptx::tma_prefetch_desc(&kmap);
+    ptx::tma_prefetch_desc(&vmap);
   }
   wait_for_predecessor();
   let_successor_start();
@@ -683,7 +693,8 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       if (c.first && lane < a.heads) s_scale[stage][lane] = scale;
       __syncwarp();
       if (lane == 0) {
-        s_header[stage] = {c.b, c.flags(TT), valid, boxes};
+        const bool whole = valid == TT && boxes == 0xffffffffu >> (32 - (TT >> a.box_log2));
+        s_header[stage] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, boxes};
         const uint32_t q_bytes = c.first ? nq * T::kRowK : 0;
         ptx::mbar_arrive_expect_tx(bar, (__popc(boxes) << a.box_log2) * a.heads * T::kKeyBytes + q_bytes);
         if (c.first) bulk_load(query_s + stage * a.q_bytes, a.q + c.b * a.q_batch + static_cast<long long>(q0) * T::kRowK, q_bytes, bar);
@@ -748,13 +759,13 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     const uint32_t ks = tiles_s + stage * stage_bytes, vs = ks + k_bytes;
     if (!idle) {
       if (h.flags & kFirst) rows.begin(my_query + stage * a.q_bytes, nq, s_scale[stage][head].x, s_scale[stage][head].y, lane);
-      const int valid = min(KT, h.valid - sub * KT);
-      if (valid > 0) {
-        uint32_t mask = 0xffffffffu >> (32 - valid);
-        if (~h.boxes << (31 - ((h.valid - 1) >> a.box_log2)))  // a box without a page
-          mask &= __ballot_sync(0xffffffffu, h.boxes >> ((sub * KT + lane) >> a.box_log2) & 1);
+      if (!(h.flags & kPartial)) {
+        rows.template tile<true>(ks, vs, kr, vr, T::kFull, lane, []() {});
+      } else if (h.valid > sub * KT) {
+        uint32_t mask = T::kFull >> (KT - min(KT, h.valid - sub * KT));
+        mask &= __ballot_sync(0xffffffffu, h.boxes >> ((sub * KT + lane) >> a.box_log2 & 31) & 1);
         if (mask)
-          rows.tile(ks, vs, kr, vr, mask, lane, [&]() {
+          rows.template tile<false>(ks, vs, kr, vr, mask, lane, [&]() {
             // whatever V holds behind the request's end is not a number to multiply by 0: its pieces as this warp reads them
 #pragma unroll
             for (int n = 0; n < KB; ++n) {
@@ -885,7 +896,10 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
     const Header h = s_header[warp][stage];
     const uint32_t ks = tiles_s + stage * T::kTileBytes, vs = ks + KT * T::kRowK;
     if (h.flags & kFirst) rows.begin(query_s + stage * a.q_bytes, nq, s_scale[warp][stage].x, s_scale[warp][stage].y, lane);
-    if (h.boxes) rows.tile(ks, vs, kr, vr, h.boxes, lane, []() {});  // rows that are not valid were filled with zeros
+    if (h.boxes == T::kFull)
+      rows.template tile<true>(ks, vs, kr, vr, T::kFull, lane, []() {});
+    else if (h.boxes)
+      rows.template tile<false>(ks, vs, kr, vr, h.boxes, lane, []() {});  // rows that are not valid were filled with zeros
     if (h.flags & kLast) rows.finish(a, h.b, q0, nq, h.flags & kDirect, static_cast<long long>(g) * 2 + (h.flags & kSlot1 ? 1 : 0), lane);
     stage = stage + 1 == S ? 0 : stage + 1;
   }
