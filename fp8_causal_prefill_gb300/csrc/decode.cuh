@@ -486,13 +486,54 @@ __device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head,
 // the schedule
 
 // The tiles (of `tokens` tokens) of all requests, and the run of group `g`: the request and the tile within it that it begins
-// with, for every thread that asks (`finds`).  The whole block takes part; counts fit 32 bits (the host has checked their sum).
+// with, for every thread that asks (`finds`).  Counts fit 32 bits (the host has checked their sum).
 struct Schedule {
   unsigned total = 0, per = 0;
 
-  // prefix: [blockDim.x] and sums: [33] in shared memory
+  // Up to 128 requests: every warp by itself, four requests a lane, without a barrier.
+  __device__ __forceinline__ void find_few(const DecodeArgs& a, unsigned tokens, unsigned g, int* b, unsigned* tile) {
+    const int lane = threadIdx.x & 31;
+    unsigned n[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = lane * 4 + i;
+      n[i] = r < a.B ? (length_of(a, r) + tokens - 1u) / tokens : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += n[i];
+    unsigned incl = sum;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const unsigned o = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += o;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    per = (total + a.groups - 1) / a.groups;
+    const unsigned first = g * per;
+    unsigned start = incl - sum, at = 0, rest = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // the request among this lane's that holds tile `first`, if one does
+      if (blockIdx.x == 0 && threadIdx.x < 32 && lane * 4 + i < a.B) a.starts[lane * 4 + i] = start;
+      if (first >= start && first < start + n[i]) {
+        at = lane * 4 + i;
+        rest = first - start;
+      }
+      start += n[i];
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, first >= incl - sum && first < incl);
+    const int l = hit ? __ffs(hit) - 1 : 0;
+    *b = hit ? static_cast<int>(__shfl_sync(0xffffffffu, at, l)) : -1;
+    *tile = __shfl_sync(0xffffffffu, rest, l);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      a.starts[a.B] = total;
+      a.starts[a.B + 1] = per;
+    }
+  }
+
+  // Any number, the whole block: prefix: [blockDim.x] and sums: [33] in shared memory.
   __device__ __forceinline__ void find(const DecodeArgs& a, unsigned tokens, unsigned* prefix, unsigned* sums, bool finds, unsigned g, int* b,
                                        unsigned* tile) {
+    if (a.B <= 128) return find_few(a, tokens, g, b, tile);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, warps = n_threads >> 5;
     const bool one_pass = a.B <= n_threads;
     auto tiles = [&](int r) { return r < a.B ? (length_of(a, r) + tokens - 1u) / tokens : 0u; };
@@ -617,6 +658,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     ptx::tma_prefetch_desc(&kmap);
     ptx::tma_prefetch_desc(&vmap);
   }
+  __syncthreads();
   wait_for_predecessor();
   let_successor_start();
 
@@ -631,7 +673,6 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   const unsigned run = g * plan.per;
   if (g >= static_cast<unsigned>(a.groups) || run >= plan.total) return;
   const int tiles = static_cast<int>(min(plan.per, plan.total - run));
-  __syncthreads();
 
   if (warp == warps) {
     Cursor c;
@@ -673,7 +714,6 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       const int box0 = (c.t >> a.box_log2 & ~31) + 32;
       pg_next = box0 << a.box_log2 < c.len ? pages(c.b, c.len, box0) : next_len > 0 ? pages(next_b, next_len, 0) : -1;
     };
-    look_ahead(true);
     bool bad = false;
     int stage = 0;
     uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
@@ -690,22 +730,23 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       const bool ok = row < valid && pg >= 0 && pg < a.cache.num_pages;
       const unsigned boxes = __ballot_sync(0xffffffffu, ok);
       bad |= row < valid && !ok;
-      if (c.first && lane < a.heads) s_scale[stage][lane] = scale;
-      __syncwarp();
-      if (lane == 0) {
-        const bool whole = valid == TT && boxes == 0xffffffffu >> (32 - (TT >> a.box_log2));
-        s_header[stage] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, boxes};
-        const uint32_t q_bytes = c.first ? nq * T::kRowK : 0;
-        ptx::mbar_arrive_expect_tx(bar, (__popc(boxes) << a.box_log2) * a.heads * T::kKeyBytes + q_bytes);
-        if (c.first) bulk_load(query_s + stage * a.q_bytes, a.q + c.b * a.q_batch + static_cast<long long>(q0) * T::kRowK, q_bytes, bar);
-      }
-      __syncwarp();
+      // the copies first: the barrier's phase cannot end before the arrival below
       if (ok) {
         const uint32_t at = ks + lane * (a.heads * box) * T::kRowK, vt = ks + k_bytes + lane * (a.heads * box) * T::kRowV;
         const bool jk = !kWhole<T::kRowK> && a.joint_k, jv = !kWhole<T::kRowV> && a.joint_v;
         tma_load_5d(at, &kmap, bar, 0, off, jk ? head0 * T::kRowK / 128 : 0, jk ? 0 : head0, pg);
         tma_load_5d(vt, &vmap, bar, 0, off, jv ? head0 * T::kRowV / 128 : 0, jv ? 0 : head0, pg);
       }
+      if (c.first && lane < a.heads) s_scale[stage][lane] = scale;
+      __syncwarp();
+      if (lane == 0) {
+        const bool whole = valid == TT && boxes == 0xffffffffu >> (32 - (TT >> a.box_log2));
+        s_header[stage] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, boxes};
+        const uint32_t q_bytes = c.first ? nq * T::kRowK : 0;
+        if (c.first) bulk_load(query_s + stage * a.q_bytes, a.q + c.b * a.q_batch + static_cast<long long>(q0) * T::kRowK, q_bytes, bar);
+        ptx::mbar_arrive_expect_tx(bar, (__popc(boxes) << a.box_log2) * a.heads * T::kKeyBytes + q_bytes);
+      }
+      if (i == 0) look_ahead(true);
       if (--c.left > 0) {
         c.first = false;
         c.t += TT;
@@ -1159,8 +1200,8 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
     if (!prepare(join_kernel<DV, 4, 1, V, 8>, 1, dev, set[1])) return ZYFA_ERR_CUDA;
     e = launch_dependent(join_kernel<DV, 4, 1, V, 8>, dim3(rows), 128, 0, stream, a);
   } else {
-    if (!prepare(join_kernel<DV, 1, 8, V, 4>, 1, dev, set[2])) return ZYFA_ERR_CUDA;
-    e = launch_dependent(join_kernel<DV, 1, 8, V, 4>, dim3((rows + 7) / 8), 256, 0, stream, a);
+    if (!prepare(join_kernel<DV, 1, 8, V, 8>, 1, dev, set[2])) return ZYFA_ERR_CUDA;
+    e = launch_dependent(join_kernel<DV, 1, 8, V, 8>, dim3((rows + 7) / 8), 256, 0, stream, a);
   }
   return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
 }
