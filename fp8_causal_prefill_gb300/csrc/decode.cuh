@@ -78,7 +78,7 @@ struct DecodeArgs {
   int q_bytes;                  // of a block's queries in shared memory
   int box_log2;                 // tokens of a TMA box, at most a tile's
   int joint_k, joint_v;         // rows of 64 (or 192) bytes lie in shared memory in 128-byte columns across heads
-  unsigned* starts;  // [B + 2]: first tile of each request, then the total, then the tiles per group
+  unsigned* starts;  // [B + 2], for more than kFew requests: first tile of each, then the total, then the tiles per group
   float2* ml;        // [groups][2][subs][H]
   float* part;       // [groups][2][subs][H][DV]
 };
@@ -486,19 +486,19 @@ __device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head,
 // the schedule
 
 // The tiles (of `tokens` tokens) of all requests, and the run of group `g`: the request and the tile within it that it begins
-// with, for every thread that asks (`finds`).  Counts fit 32 bits (the host has checked their sum).
+// with, for every thread that asks (`finds`; of one warp, the same g).  Counts fit 32 bits (the host has checked their sum).
+constexpr int kFew = 128;
+
 struct Schedule {
   unsigned total = 0, per = 0;
 
-  // Up to 128 requests: every warp by itself, four requests a lane, without a barrier.
-  __device__ __forceinline__ void find_few(const DecodeArgs& a, unsigned tokens, unsigned g, int* b, unsigned* tile) {
+  // Up to kFew requests: every warp by itself, four requests a lane, without a barrier.  Returns the lane's first tile.
+  __device__ __forceinline__ unsigned scan_few(const DecodeArgs& a, unsigned (&n)[4]) {
     const int lane = threadIdx.x & 31;
-    unsigned n[4], sum = 0;
+    const unsigned tokens = a.tile_tokens;
+    unsigned sum = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = lane * 4 + i;
-      n[i] = r < a.B ? (length_of(a, r) + tokens - 1u) / tokens : 0u;
-    }
+    for (int i = 0; i < 4; ++i) n[i] = lane * 4 + i < a.B ? (length_of(a, lane * 4 + i) + tokens - 1u) / tokens : 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum += n[i];
     unsigned incl = sum;
@@ -509,31 +509,42 @@ struct Schedule {
     }
     total = __shfl_sync(0xffffffffu, incl, 31);
     per = (total + a.groups - 1) / a.groups;
+    return incl - sum;
+  }
+  __device__ __forceinline__ void find_few(const DecodeArgs& a, unsigned g, int* b, unsigned* tile) {
+    unsigned n[4], start = scan_few(a, n), at = 0, rest = 0;
     const unsigned first = g * per;
-    unsigned start = incl - sum, at = 0, rest = 0;
+    bool here = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // the request among this lane's that holds tile `first`, if one does
-      if (blockIdx.x == 0 && threadIdx.x < 32 && lane * 4 + i < a.B) a.starts[lane * 4 + i] = start;
       if (first >= start && first < start + n[i]) {
-        at = lane * 4 + i;
+        at = (threadIdx.x & 31) * 4 + i;
         rest = first - start;
+        here = true;
       }
       start += n[i];
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, first >= incl - sum && first < incl);
+    const unsigned hit = __ballot_sync(0xffffffffu, here);
     const int l = hit ? __ffs(hit) - 1 : 0;
     *b = hit ? static_cast<int>(__shfl_sync(0xffffffffu, at, l)) : -1;
     *tile = __shfl_sync(0xffffffffu, rest, l);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      a.starts[a.B] = total;
-      a.starts[a.B + 1] = per;
-    }
+  }
+  // First tile of request b and of the one after it.
+  __device__ __forceinline__ void bounds_few(const DecodeArgs& a, int b, unsigned* p0, unsigned* p1) {
+    unsigned n[4], start = scan_few(a, n), mine = start;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < (b & 3)) mine += n[i];
+    const unsigned len = (b & 3) == 0 ? n[0] : (b & 3) == 1 ? n[1] : (b & 3) == 2 ? n[2] : n[3];
+    *p0 = __shfl_sync(0xffffffffu, mine, b >> 2);
+    *p1 = *p0 + __shfl_sync(0xffffffffu, len, b >> 2);
   }
 
-  // Any number, the whole block: prefix: [blockDim.x] and sums: [33] in shared memory.
-  __device__ __forceinline__ void find(const DecodeArgs& a, unsigned tokens, unsigned* prefix, unsigned* sums, bool finds, unsigned g, int* b,
+  // Any number, the whole block: prefix: [blockDim.x] and sums: [33] in shared memory.  Leaves a.starts for the join.
+  __device__ __forceinline__ void find(const DecodeArgs& a, unsigned* prefix, unsigned* sums, bool finds, unsigned g, int* b,
                                        unsigned* tile) {
-    if (a.B <= 128) return find_few(a, tokens, g, b, tile);
+    if (a.B <= kFew) return find_few(a, g, b, tile);
+    const unsigned tokens = a.tile_tokens;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, warps = n_threads >> 5;
     const bool one_pass = a.B <= n_threads;
     auto tiles = [&](int r) { return r < a.B ? (length_of(a, r) + tokens - 1u) / tokens : 0u; };
@@ -669,7 +680,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   Schedule plan;
   int b;
   unsigned tile0;
-  plan.find(a, TT, s_prefix, s_sums, warp == warps, g, &b, &tile0);
+  plan.find(a, s_prefix, s_sums, warp == warps, g, &b, &tile0);
   const unsigned run = g * plan.per;
   if (g >= static_cast<unsigned>(a.groups) || run >= plan.total) return;
   const int tiles = static_cast<int>(min(plan.per, plan.total - run));
@@ -691,25 +702,29 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       page_of(a, t, &p, &off);
       return __ldg(a.table + request * a.table_stride + p);
     };
-    auto scales = [&](int request) {
-      float2 x = {a.scale_log2, 1.0f};
+    struct Descales {
+      float q, k, v;
+    };
+    auto descales = [&](int request) {
+      Descales d = {1.0f, 1.0f, 1.0f};
       if (FP8 && lane < a.heads) {
-        const int di = a.desc_per_head ? request * a.cache.H_kv + min(head0 + lane, a.cache.H_kv - 1) : 0;
-        x.x *= (a.q_desc ? __ldg(a.q_desc + di) : 1.0f) * (a.k_desc ? __ldg(a.k_desc + di) : 1.0f);
-        x.y = a.v_desc ? __ldg(a.v_desc + di) : 1.0f;
+        const int i = a.desc_per_head ? request * a.cache.H_kv + min(head0 + lane, a.cache.H_kv - 1) : 0;
+        if (a.q_desc) d.q = __ldg(a.q_desc + i);
+        if (a.k_desc) d.k = __ldg(a.k_desc + i);
+        if (a.v_desc) d.v = __ldg(a.v_desc + i);
       }
-      return x;
+      return d;
     };
     int next_b = 0, next_len = 0, pg_next = -1;
-    float2 scale = scales(c.b), scale_next = scale;
     int pg_now = pages(c.b, c.len, c.t >> a.box_log2 & ~31);
+    Descales desc = descales(c.b), desc_next = desc;
     auto look_ahead = [&](bool new_request) {
       if (new_request) {
         next_len = 0;
         if ((c.len - c.t + TT - 1) / TT < c.left)  // the run goes on behind this request
           for (next_b = c.b + 1; next_b < a.B && next_len == 0; ++next_b) next_len = length_of(a, next_b);
         --next_b;
-        if (next_len > 0) scale_next = scales(next_b);
+        if (next_len > 0) desc_next = descales(next_b);
       }
       const int box0 = (c.t >> a.box_log2 & ~31) + 32;
       pg_next = box0 << a.box_log2 < c.len ? pages(c.b, c.len, box0) : next_len > 0 ? pages(next_b, next_len, 0) : -1;
@@ -737,7 +752,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
         tma_load_5d(at, &kmap, bar, 0, off, jk ? head0 * T::kRowK / 128 : 0, jk ? 0 : head0, pg);
         tma_load_5d(vt, &vmap, bar, 0, off, jv ? head0 * T::kRowV / 128 : 0, jv ? 0 : head0, pg);
       }
-      if (c.first && lane < a.heads) s_scale[stage][lane] = scale;
+      if (c.first && lane < a.heads) s_scale[stage][lane] = {a.scale_log2 * desc.q * desc.k, desc.v};
       __syncwarp();
       if (lane == 0) {
         const bool whole = valid == TT && boxes == 0xffffffffu >> (32 - (TT >> a.box_log2));
@@ -756,7 +771,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
           c.t = 0;
           c.first = c.from_start = true;
           pg_now = pg_next;
-          scale = scale_next;
+          desc = desc_next;
           look_ahead(true);
         } else if ((c.t >> a.box_log2 & 31) == 0) {
           pg_now = pg_next;
@@ -857,7 +872,7 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
   Schedule plan;
   int b;
   unsigned tile0;
-  plan.find(a, KT, s_prefix, s_sums, g < static_cast<unsigned>(a.groups), g, &b, &tile0);
+  plan.find(a, s_prefix, s_sums, g < static_cast<unsigned>(a.groups), g, &b, &tile0);
   const unsigned run = g * plan.per;
   if (g >= static_cast<unsigned>(a.groups) || run >= plan.total) return;
   const int tiles = static_cast<int>(min(plan.per, plan.total - run));
@@ -963,12 +978,22 @@ __global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_consta
     float y[VEC];
   };
   __shared__ float s_o[W][D], s_m[W], s_l[W];
-  wait_for_predecessor();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = blockIdx.y * D;
   const long long row = static_cast<long long>(blockIdx.x) * ROWS + (ROWS > 1 ? warp : 0);
   if (row >= static_cast<long long>(a.B) * a.H) return;
   const int b = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H), w = ROWS > 1 ? 0 : warp, tid = w * 32 + lane;
-  const unsigned p0 = a.starts[b], p1 = a.starts[b + 1], per = a.starts[a.B + 1];
+  // Up to kFew requests the bounds come from their lengths, read before the first kernel has ended: it does not write them, and
+  // what did had ended before that kernel let this one start.
+  Schedule plan;
+  unsigned p0, p1;
+  if (a.B <= kFew) plan.bounds_few(a, b, &p0, &p1);
+  wait_for_predecessor();
+  if (a.B > kFew) {
+    p0 = a.starts[b];
+    p1 = a.starts[b + 1];
+    plan.per = a.starts[a.B + 1];
+  }
+  const unsigned per = plan.per;
   if (p0 == p1) {
     for (int i = tid; i < D; i += kThreads) a.out[row * DV + d0 + i] = __float2bfloat16_rn(0.0f);
     if (a.lse && tid == 0 && d0 == 0) a.lse[row] = -INFINITY;
@@ -986,23 +1011,26 @@ __global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_consta
   for (int base = w; base < n; base += 32 * W) {
     const int count = min(32, (n - base + W - 1) / W);  // parts base, base + W, ...
     const float2 ml = lane < count ? a.ml[part(base + lane * W)] : make_float2(-INFINITY, 0.0f);
-    float top = ml.x;
-#pragma unroll
-    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = exp2_approx(m - ref), e = exp2_approx(ml.x - ref);  // 0 for parts without a valid key
-    m = mn;
-    l = l * f + ml.y * e;  // this lane's share
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] *= f;
+    float e = 0.0f;
     for (int k0 = 0; k0 < count; k0 += BATCH) {
       Vec x[BATCH];
 #pragma unroll
       for (int k = 0; k < BATCH; ++k)
         if (k0 + k < count) x[k] = *reinterpret_cast<const Vec*>(a.part + part(base + (k0 + k) * W) * DV + d0 + lane * VEC);
+      if (k0 == 0) {  // with the first rows on their way
+        float top = ml.x;
+#pragma unroll
+        for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.0f : mn, f = exp2_approx(m - ref);
+        e = exp2_approx(ml.x - ref);  // 0 for parts without a valid key
+        m = mn;
+        l = l * f + ml.y * e;  // this lane's share
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o[j] *= f;
+      }
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
-        const float ek = __shfl_sync(0xffffffffu, e, k0 + k);
+        const float ek = __shfl_sync(0xffffffffu, e, (k0 + k) & 31);
         if (k0 + k < count && ek > 0.0f) {  // a part without a valid key has no O
 #pragma unroll
           for (int j = 0; j < VEC; ++j) o[j] = fmaf(x[k].y[j], ek, o[j]);
@@ -1159,6 +1187,7 @@ template <bool FP8, int DQK, int DV>
 cudaError_t launch_rows(DecodeArgs& a, int nsm, int dev, cudaStream_t stream) {
   using T = Tile<FP8, DQK, DV>;
   a.subs = 1;
+  a.tile_tokens = T::kKeys;
   a.units = a.cache.H_kv * a.chunks;
   a.q_bytes = a.chunk_heads * T::kRowK;
   const int ring = kRowStages * (T::kTileBytes + a.q_bytes), most = std::min(kRowWarps<T::kKeyBytes>, (kSmemPerBlock - 8192) / ring);
