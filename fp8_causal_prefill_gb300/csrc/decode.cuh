@@ -640,11 +640,11 @@ struct Cursor {
 
 // Compute warps of a block at most.  Two blocks and their load warps share an SM: 18 warps of 96 registers a thread, 10 of 168.
 template <int KEY_BYTES>
-constexpr int kBoxWarps = KEY_BYTES <= 320 ? 8 : 4;
+constexpr int kBoxWarps = KEY_BYTES <= 320 ? 4 : 2;
 constexpr int kMaxStages = 8, kMaxHeads = 8;
 
 template <bool FP8, int DQK, int DV>
-__global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1) * 32, 2)
+__global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1) * 32, 3)
     boxes_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using T = Tile<FP8, DQK, DV>;
   constexpr int KT = T::kKeys, KB = KT / 16, kMaxWarps = kBoxWarps<T::kKeyBytes> + 1;
@@ -1171,7 +1171,7 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   const int warps = a.heads * a.chunk_warps * a.subs, stage = a.heads * a.tile_tokens * T::kKeyBytes + a.q_bytes;
   // two blocks an SM (more where they are small), or one if two would not have two stages each
   constexpr int kStatic = 4096;  // the schedule's tables and headers, with the 1 KiB that each block takes
-  int blocks = std::max(2, 2 * kWarps / warps);
+  int blocks = 3;
   while (blocks > 1 && blocks * (2 * stage + kStatic) > kSmemPerSm) --blocks;
   a.stages = std::min(kMaxStages, std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) / stage);
   if (a.stages < 2) return cudaSuccess;

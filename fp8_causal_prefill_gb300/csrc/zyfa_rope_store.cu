@@ -8,20 +8,24 @@
 //
 // Bound: HBM.  Each value is read once (bf16) and written once or twice (cache, dense copy).  A block takes a few
 // tokens; its threads first form the tokens' cosines and sines, once per (token, pair), in shared memory, then walk over
-// items of 16 channels: two 16-byte loads whose channels pair up (8 channels and their partners half the rotated width
-// away, or 16 neighbours), eight rotations, one or two 8- or 16-byte stores per half.  The next item's loads are in flight
-// while one is computed.
+// the tokens' heads.  A thread keeps its 16 channels of a head: two 16-byte loads whose channels pair up (8 channels and
+// their partners half the rotated width away, or 16 neighbours), eight rotations in packed fp32 pairs, one or two 8- or
+// 16-byte stores per half.  The next head's loads are in flight while one is computed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "paged.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // tokens per block
+constexpr int kMaxTokens = 8;  // tokens per block at most
+
+// A multiple of the 16-channel pieces of a key head and of a value head.
+template <int DQK>
+constexpr int kThreads = DQK == 192 ? 192 : 256;
 
 struct StoreArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -103,25 +107,75 @@ __device__ __forceinline__ void put8(uint8_t* row, uint8_t* copy, int d, const f
   }
 }
 
-// 16 channels of one head of one token.
-struct Item {
-  uint4 x0, x1;
-  int token, head;  // head: query heads, then key heads, then value heads
-  int d0, d1;       // first channel of either half
-  int pair;         // first pair, or -1: not rotated
+// (a, b) -> (a c - b s, a s + b c) for two pairs at once
+__device__ __forceinline__ void rotate2(float& a0, float& a1, float& b0, float& b1, const float* c, const float* s) {
+  asm("{\n\t.reg .b64 a, b, c, s, n, y, z;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
+      "mov.b64 s, {%6, %7};\n\tmov.b64 n, {%8, %9};\n\tmul.rn.f32x2 y, b, n;\n\tfma.rn.f32x2 y, a, c, y;\n\tmul.rn.f32x2 z, b, c;\n\t"
+      "fma.rn.f32x2 z, a, s, z;\n\tmov.b64 {%0, %1}, y;\n\tmov.b64 {%2, %3}, z;\n\t}"
+      : "+f"(a0), "+f"(a1), "+f"(b0), "+f"(b1)
+      : "f"(c[0]), "f"(c[1]), "f"(s[0]), "f"(s[1]), "f"(-s[0]), "f"(-s[1]));
+}
+
+// A thread's walk over (token, head) with a stride of `lanes` heads.
+struct Walk {
+  int token, head, heads, lanes;
+  __device__ __forceinline__ void settle() {
+    while (head >= heads) {
+      head -= heads;
+      ++token;
+    }
+  }
 };
 
 template <bool FP8, bool INTERLEAVED, int DQK, int DV>
-__global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__ StoreArgs a) {
-  constexpr int es = FP8 ? 1 : 2;
-  constexpr int kItemsK = DQK / 16, kItemsV = DV / 16, kHalf = DQK / 2;
+__global__ void __launch_bounds__(kThreads<DQK>) store_kernel(const __grid_constant__ StoreArgs a) {
+  constexpr int es = FP8 ? 1 : 2, kN = kThreads<DQK>;
+  constexpr int kPiecesK = DQK / 16, kPiecesV = DV / 16, kHalf = DQK / 2;
+  static_assert(kN % kPiecesK == 0 && kN % kPiecesV == 0);
   __shared__ __align__(16) float s_cos[kMaxTokens][kHalf], s_sin[kMaxTokens][kHalf];
   __shared__ long long s_krow[kMaxTokens], s_vrow[kMaxTokens];  // offsets in the cache; -1: not written, -2: padding
   const int tid = threadIdx.x;
   const int tokens = a.tokens;
   const long long n0 = static_cast<long long>(blockIdx.x) * tokens;
   const int here = static_cast<int>(min(static_cast<long long>(tokens), a.N - n0));
-  const int H_kv = a.cache.H_kv, half = a.rot / 2;
+  const int H_kv = a.cache.H_kv, half = a.rot / 2, heads_q = a.q ? a.H : 0;
+
+  // queries and keys: this thread's 16 channels, the same of every head
+  const int j = tid % kPiecesK;
+  int pair = -1, d0, d1;
+  if (j * 8 < half) {
+    pair = j * 8;
+    d0 = a.offset + (INTERLEAVED ? j * 16 : j * 8);
+    d1 = INTERLEAVED ? d0 + 8 : d0 + half;
+  } else {  // the plain channels in order, eight by eight
+    const int d = 16 * j - a.rot;
+    d0 = d < a.offset ? d : d + a.rot;
+    d1 = d + 8 < a.offset ? d + 8 : d + 8 + a.rot;
+  }
+  Walk w = {0, tid / kPiecesK, heads_q + (a.k ? H_kv : 0), kN / kPiecesK};
+  w.settle();
+  uint4 x0, x1;
+  auto fetch = [&]() {
+    if (w.token >= here) return;
+    const long long n = n0 + w.token;
+    const __nv_bfloat16* x = w.head < heads_q ? a.q + n * a.q_tok + w.head * DQK : a.k + n * a.k_tok + (w.head - heads_q) * DQK;
+    x0 = *reinterpret_cast<const uint4*>(x + d0);
+    x1 = *reinterpret_cast<const uint4*>(x + d1);
+  };
+  // values
+  const int dv = tid % kPiecesV * 16;
+  Walk wv = {0, tid / kPiecesV, H_kv, kN / kPiecesV};
+  wv.settle();
+  uint4 y0, y1;
+  auto fetch_v = [&]() {
+    if (wv.token >= here) return;
+    const __nv_bfloat16* x = a.v + (n0 + wv.token) * a.v_tok + wv.head * DV + dv;
+    y0 = *reinterpret_cast<const uint4*>(x);
+    y1 = *reinterpret_cast<const uint4*>(x + 8);
+  };
+  // the first loads run while the tables are made
+  fetch();
+  if (a.k) fetch_v();
   if (tid < here) {
     const long long slot = a.slots[n0 + tid];
     long long krow = -2, vrow = 0;
@@ -145,99 +199,71 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__
     s_krow[tid] = krow;
     s_vrow[tid] = vrow;
   }
-  for (int i = tid; i < here * half; i += kThreads) {
+  for (int i = tid; i < here * half; i += kN) {
     const int t = i / half, p = i - t * half;
     const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
     angle_sincos(turn_fraction(a.inv_freq[p]), a.positions[axis * a.pos_stride + n0 + t], &s_sin[t][p], &s_cos[t][p]);
   }
-  const int first = a.q ? 0 : a.H, heads_k = a.H - first + (a.k ? H_kv : 0);
-  const int items_k = heads_k * kItemsK, items = items_k + (a.k ? H_kv * kItemsV : 0);
   __syncthreads();
+  const bool per_head = a.desc_per_head;
+  const float q_inv = FP8 ? inverse(a.q_desc, 0) : 1.0f, k_inv = FP8 ? inverse(a.k_desc, 0) : 1.0f, v_inv = FP8 ? inverse(a.v_desc, 0) : 1.0f;
 
-  int token = 0, at = tid;
-  auto fetch = [&](Item& it) {
-    while (at >= items && token < here) {
-      at -= items;
-      ++token;
-    }
-    it.token = token;
-    if (token >= here) return false;
-    const __nv_bfloat16* x;
-    if (at < items_k) {
-      const int h = at / kItemsK, j = at % kItemsK;
-      it.head = first + h;
-      if (j * 8 < half) {
-        it.pair = j * 8;
-        it.d0 = a.offset + (INTERLEAVED ? j * 16 : j * 8);
-        it.d1 = INTERLEAVED ? it.d0 + 8 : it.d0 + half;
-      } else {  // the plain channels in order, eight by eight
-        it.pair = -1;
-        const int d = 16 * j - a.rot;
-        it.d0 = d < a.offset ? d : d + a.rot;
-        it.d1 = d + 8 < a.offset ? d + 8 : d + 8 + a.rot;
-      }
-      x = it.head < a.H ? a.q + (n0 + token) * a.q_tok + it.head * DQK : a.k + (n0 + token) * a.k_tok + (it.head - a.H) * DQK;
-    } else {
-      const int h = (at - items_k) / kItemsV, j = (at - items_k) % kItemsV;
-      it.head = a.H + H_kv + h;
-      it.pair = -1;
-      it.d0 = j * 16;
-      it.d1 = j * 16 + 8;
-      x = a.v + (n0 + token) * a.v_tok + h * DV;
-    }
-    it.x0 = *reinterpret_cast<const uint4*>(x + it.d0);
-    it.x1 = *reinterpret_cast<const uint4*>(x + it.d1);
-    at += kThreads;
-    return true;
-  };
-  Item next;
-  bool more = fetch(next);
-  while (more) {
-    const Item it = next;
-    more = fetch(next);
-    const long long krow = s_krow[it.token];
+  while (a.k && wv.token < here) {
+    const int token = wv.token, head = wv.head;
+    float u[8], v[8];
+    widen8(y0, u);
+    widen8(y1, v);
+    wv.head += wv.lanes;
+    wv.settle();
+    fetch_v();
+    const long long krow = s_krow[token];
     if (krow == -2) continue;
-    float u[8], w[8];
-    widen8(it.x0, u);
-    widen8(it.x1, w);
-    if (it.pair >= 0) {
+    uint8_t* row = krow >= 0 ? a.cache.v + s_vrow[token] + head * a.cache.v_head : nullptr;
+    uint8_t* copy = a.v_out ? a.v_out + ((n0 + token) * H_kv + head) * DV * es : nullptr;
+    const float inv = FP8 && per_head ? inverse(a.v_desc, head) : v_inv;
+    put8<FP8>(row, copy, dv, u, inv);
+    put8<FP8>(row, copy, dv + 8, v, inv);
+  }
+  while (w.token < here) {
+    const int token = w.token, head = w.head;
+    float u[8], v[8];
+    widen8(x0, u);
+    widen8(x1, v);
+    w.head += w.lanes;
+    w.settle();
+    fetch();
+    const long long krow = s_krow[token];
+    if (krow == -2) continue;
+    if (pair >= 0) {
       float c[8], s[8];
-      *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&s_cos[it.token][it.pair]);
-      *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(&s_cos[it.token][it.pair + 4]);
-      *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(&s_sin[it.token][it.pair]);
-      *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(&s_sin[it.token][it.pair + 4]);
+      *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&s_cos[token][pair]);
+      *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(&s_cos[token][pair + 4]);
+      *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(&s_sin[token][pair]);
+      *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(&s_sin[token][pair + 4]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // half-split: u[i], w[i] are pair i; interleaved: neighbours of u, then of w
-        float& p = INTERLEAVED ? (i < 4 ? u[2 * (i & 3)] : w[2 * (i & 3)]) : u[i];
-        float& q = INTERLEAVED ? (i < 4 ? u[2 * (i & 3) + 1] : w[2 * (i & 3) + 1]) : w[i];
-        const float y = p * c[i] - q * s[i], z = p * s[i] + q * c[i];
-        p = y;
-        q = z;
+      for (int i = 0; i < 8; i += 2) {
+        if constexpr (INTERLEAVED) {  // pairs are neighbours of u, then of v
+          float* y = i < 4 ? u + 2 * i : v + 2 * i - 8;
+          rotate2(y[0], y[2], y[1], y[3], c + i, s + i);
+        } else {
+          rotate2(u[i], u[i + 1], v[i], v[i + 1], c + i, s + i);
+        }
       }
     }
-    const long long n = n0 + it.token;
+    const long long n = n0 + token;
     uint8_t *row = nullptr, *copy = nullptr;
-    const float* desc;
-    int hk;
-    if (it.head < a.H) {
-      row = a.q_out + (n * a.H + it.head) * DQK * es;
-      hk = FP8 && a.desc_per_head ? it.head / (a.H / H_kv) : 0;
-      desc = a.q_desc;
-    } else if (it.head < a.H + H_kv) {
-      hk = it.head - a.H;
+    float inv;
+    if (head < heads_q) {
+      row = a.q_out + (n * a.H + head) * DQK * es;
+      inv = FP8 && per_head ? inverse(a.q_desc, head / (a.H / H_kv)) : q_inv;
+    } else {
+      const int hk = head - heads_q;
       if (krow >= 0) row = a.cache.k + krow + hk * a.cache.k_head;
       if (a.k_out) copy = a.k_out + (n * H_kv + hk) * DQK * es;
-      desc = a.k_desc;
-    } else {
-      hk = it.head - a.H - H_kv;
-      if (krow >= 0) row = a.cache.v + s_vrow[it.token] + hk * a.cache.v_head;
-      if (a.v_out) copy = a.v_out + (n * H_kv + hk) * DV * es;
-      desc = a.v_desc;
+      inv = FP8 && per_head ? inverse(a.k_desc, hk) : k_inv;
     }
-    const float inv = FP8 ? inverse(desc, a.desc_per_head ? hk : 0) : 1.0f;
-    put8<FP8>(row, copy, it.d0, u, inv);
-    put8<FP8>(row, copy, it.d1, w, inv);
+    put8<FP8>(row, copy, d0, u, inv);
+    put8<FP8>(row, copy, d1, v, inv);
   }
 }
 
@@ -245,11 +271,11 @@ template <bool FP8, bool INTERLEAVED>
 cudaError_t launch(const StoreArgs& a, int D_qk, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((a.N + a.tokens - 1) / a.tokens);
   if (D_qk == 64)
-    store_kernel<FP8, INTERLEAVED, 64, 64><<<grid, kThreads, 0, stream>>>(a);
+    store_kernel<FP8, INTERLEAVED, 64, 64><<<grid, kThreads<64>, 0, stream>>>(a);
   else if (D_qk == 128)
-    store_kernel<FP8, INTERLEAVED, 128, 128><<<grid, kThreads, 0, stream>>>(a);
+    store_kernel<FP8, INTERLEAVED, 128, 128><<<grid, kThreads<128>, 0, stream>>>(a);
   else
-    store_kernel<FP8, INTERLEAVED, 192, 128><<<grid, kThreads, 0, stream>>>(a);
+    store_kernel<FP8, INTERLEAVED, 192, 128><<<grid, kThreads<192>, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -336,8 +362,11 @@ extern "C" zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, con
   a.desc_per_head = descale_per_kv_head;
   a.N = N;
   a.H = H;
-  // Several tokens per block share its start-up, as soon as there are blocks enough for the GPU without them.
-  a.tokens = N >= 8ll * zyfa::device_sm_count(dev) ? kMaxTokens : 1;
+  // Several tokens per block share its start-up (its tables, 1 to 2 us of latency): as many as leave each of the four blocks
+  // that fit an SM one, at most 8.  32768 tokens (FP8, 32 + 8 heads of 128): 157.7 us with 2, 115.5 with 4, 112.7 with 8;
+  // 2048 tokens: 11.7 us with 4, 14.1 with 8 (half the SMs' slots).
+  const long long slots_gpu = 4ll * zyfa::device_sm_count(dev);
+  a.tokens = static_cast<int>(std::min<long long>(kMaxTokens, std::max(1ll, (N + slots_gpu - 1) / std::max(1ll, slots_gpu))));
   const bool il = rope && rope->interleaved;
   cudaError_t e;
   if (fp8)
