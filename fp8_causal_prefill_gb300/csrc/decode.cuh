@@ -641,7 +641,7 @@ struct Cursor {
 // Compute warps of a block at most.  Two blocks and their load warps share an SM: 18 warps of 96 registers a thread, 10 of 168.
 template <int KEY_BYTES>
 constexpr int kBoxWarps = KEY_BYTES <= 320 ? 4 : 2;
-constexpr int kMaxStages = 8, kMaxHeads = 8;
+constexpr int kMaxStages = 3, kMaxHeads = 8;
 
 template <bool FP8, int DQK, int DV>
 __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1) * 32, 3)
