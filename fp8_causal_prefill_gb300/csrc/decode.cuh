@@ -74,7 +74,8 @@ struct DecodeArgs {
   int groups, units;            // `units` blocks (boxes_kernel) or warps (rows_kernel) make a group
   int chunks, chunk_heads;      // the query heads of a KV head are cut into chunks of at most chunk_heads
   int heads, chunk_warps, subs; // of a block: KV heads, chunks of each, token runs of a tile (warps = the product)
-  int stages, tile_tokens;      // of a ring; tokens of a tile, subs * keys of a warp
+  int stages, tile_tokens;      // of a ring; tokens of a tile, subs * turns * keys of a warp's turn
+  int turns;                    // of a warp at a tile
   int q_bytes;                  // of a block's queries in shared memory
   int box_log2;                 // tokens of a TMA box, at most a tile's
   int joint_k, joint_v;         // rows of 64 (or 192) bytes lie in shared memory in 128-byte columns across heads
@@ -793,7 +794,11 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   const bool idle = hk >= a.cache.H_kv || nq <= 0;  // the last block of a group may have heads or chunks too many
   Reader<T::kRowK, KB> kr;
   Reader<T::kRowV, KB> vr;
-  set_readers<FP8, DQK, DV, KB>(lane, a.box_log2, head, a.heads, sub * KT, a.joint_k, a.joint_v, &kr, &vr);
+  const int run_keys = a.turns * KT;
+  set_readers<FP8, DQK, DV, KB>(lane, a.box_log2, head, a.heads, sub * run_keys, a.joint_k, a.joint_v, &kr, &vr);
+  // bytes from a box to the next, and from a row of one to the next
+  const uint32_t k_box = a.heads * T::kRowK << a.box_log2, v_box = a.heads * T::kRowV << a.box_log2;
+  const uint32_t k_pitch = kWhole<T::kRowK> || a.joint_k ? 128 : 64, v_pitch = kWhole<T::kRowV> || a.joint_v ? 128 : 64;
   const uint32_t my_query = query_s + (head * a.group + (chunk - chunk0) * a.chunk_heads) * T::kRowK;
   Rows<FP8, DQK, DV> rows;
   int stage = 0;
@@ -815,20 +820,27 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     const uint32_t ks = tiles_s + stage * stage_bytes, vs = ks + k_bytes;
     if (!idle) {
       if (h.flags & kFirst) rows.begin(my_query + stage * a.q_bytes, nq, s_scale[stage][head].x, s_scale[stage][head].y, lane);
-      if (!(h.flags & kPartial)) {
-        rows.template tile<true>(ks, vs, kr, vr, T::kFull, lane, []() {});
-      } else if (h.valid > sub * KT) {
-        uint32_t mask = T::kFull >> (KT - min(KT, h.valid - sub * KT));
-        mask &= __ballot_sync(0xffffffffu, h.boxes >> ((sub * KT + lane) >> a.box_log2 & 31) & 1);
+      for (int turn = 0; turn < a.turns; ++turn) {
+        // (a warp's run of keys begins with a box, or lies in one)
+        const int r = turn * KT, boxes = r >> a.box_log2, in = r & ((1 << a.box_log2) - 1);
+        const uint32_t kt = ks + boxes * k_box + in * k_pitch, vt = vs + boxes * v_box + in * v_pitch;
+        if (!(h.flags & kPartial)) {
+          rows.template tile<true>(kt, vt, kr, vr, T::kFull, lane, []() {});
+          continue;
+        }
+        const int row0 = sub * run_keys + r;
+        if (h.valid <= row0) break;
+        uint32_t mask = T::kFull >> (KT - min(KT, h.valid - row0));
+        mask &= __ballot_sync(0xffffffffu, h.boxes >> ((row0 + lane) >> a.box_log2 & 31) & 1);
         if (mask)
-          rows.template tile<false>(ks, vs, kr, vr, mask, lane, [&]() {
+          rows.template tile<false>(kt, vt, kr, vr, mask, lane, [&]() {
             // whatever V holds behind the request's end is not a number to multiply by 0: its pieces as this warp reads them
 #pragma unroll
             for (int n = 0; n < KB; ++n) {
-              const int r = FP8 ? lane & 15 : (lane >> 4) * 8 + (lane & 7);
-              if (!((mask >> (n * 16 + r)) & 1))
+              const int row = FP8 ? lane & 15 : (lane >> 4) * 8 + (lane & 7);
+              if (!((mask >> (n * 16 + row)) & 1))
 #pragma unroll
-                for (int p = 0; p < T::kRowV / 16; p += 2) ptx::st_shared_v4(vr.at(vs, n, p), 0, 0, 0, 0);
+                for (int p = 0; p < T::kRowV / 16; p += 2) ptx::st_shared_v4(vr.at(vt, n, p), 0, 0, 0, 0);
             }
             ptx::fence_proxy_async_smem();  // before a later TMA load into this stage
             __syncwarp();
@@ -1145,7 +1157,11 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   a.heads = piece(c.H_kv, kWarps / a.chunk_warps);
   a.subs = 1;
   while (a.subs * 2 * a.heads * a.chunk_warps <= kWarps) a.subs *= 2;
-  a.tile_tokens = a.subs * T::kKeys;
+  // Where chunks of one head share a tile it has fewer rows; as many more tokens keep its bytes, which the work per tile of
+  // the load warp and of the barriers is spread over.
+  a.turns = 1;
+  while (a.turns * 2 * a.subs * a.heads <= kWarps) a.turns *= 2;
+  a.tile_tokens = a.subs * a.turns * T::kKeys;
   a.units = (c.H_kv + a.heads - 1) / a.heads * ((a.chunks + a.chunk_warps - 1) / a.chunk_warps);
   // Boxes: as many tokens of a page as divide both the page and the tile.  A broadcast (stride 0) or very large stride has no
   // tensor map, and a page of an odd size no boxes that fill the swizzle pattern (8 rows).
