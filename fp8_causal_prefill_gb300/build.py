@@ -94,7 +94,7 @@ def link_binding(obj: str) -> None:
     lib = os.path.join(_torch_dir(), "lib")
     tmp = BINDING + ".tmp"
     r = subprocess.run([_cxx(), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libzyfa.so", "-Wl,-rpath,$ORIGIN", "-L" + lib,
-                        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], capture_output=True, text=True)
+                        "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the tensor binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)

@@ -7,11 +7,12 @@
 #include <Python.h>
 
 #include <ATen/Functions.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <optional>
 #include <vector>
@@ -140,7 +141,14 @@ Descales descales_of(PyObject* const* o, int64_t per_head, int dev) {
 }
 
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+  return Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
+}
+
+// `n` elements of a larger allocation, from byte `offset` on, as a tensor of its own.
+Tensor piece(const Tensor& all, at::ScalarType type, int64_t offset, int64_t n) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{n}, at::IntArrayRef{1}, offset / static_cast<int64_t>(c10::elementSize(type)));
+  return t;
 }
 
 cudaStream_t stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
@@ -185,9 +193,17 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   std::optional<Tensor> made[5];
   if (a[7] == Py_None) {
+    // one allocation for the five (each costs a microsecond, a third of the kernel), slots first for their alignment
+    static const int order[5] = {3, 0, 1, 2, 4};
+    int64_t bytes = 0, at_byte[5];
+    for (int i : order) {
+      at_byte[i] = bytes;
+      bytes += sizes[i] * (i == 3 ? 8 : 4);
+    }
+    const Tensor all = fresh({bytes}, at::kByte, dev);
     for (int i = 0; i < 5; ++i) {
-      made[i] = fresh({sizes[i]}, i == 3 ? at::kLong : at::kInt, dev);
-      o[i] = made[i]->data_ptr();
+      made[i] = piece(all, i == 3 ? at::kLong : at::kInt, at_byte[i], sizes[i]);
+      o[i] = static_cast<char*>(all.data_ptr()) + at_byte[i];
     }
   } else {
     static const char* const names[5] = {"out.seq_lens", "out.cu_tokens", "out.positions", "out.slots", "out.cursor"};
@@ -219,6 +235,29 @@ void* dense(const Tensor& t, const char* name, int code, at::IntArrayRef shape, 
   NEED_TYPE(code_of(t.scalar_type()) == code && t.is_contiguous(), name, " must be a contiguous CUDA tensor of the cache's type");
   NEED_VALUE(t.sizes() == shape && cuda_index(t) == dev, name, " must have shape ", shape, " on the cache's device, got ", t.sizes());
   return t.data_ptr();
+}
+
+// rope(inv_freq, axis_pairs or None, offset, interleaved) -> the checked specification that store() takes
+PyObject* rope(PyObject* const* a, Py_ssize_t n) {
+  count(n, 4);
+  const Tensor& inv = tensor(a[0], "inv_freq");
+  NEED_TYPE(inv.scalar_type() == at::kFloat && inv.dim() == 1 && inv.is_contiguous(),
+            "inv_freq must be a contiguous float32 CUDA tensor [rot_dim / 2]");
+  NEED_VALUE(inv.is_cuda() && inv.size(0) <= 4096, "inv_freq must be a CUDA tensor of at most 4096 pairs");
+  integer(a[2], "offset");
+  PyObject* pairs = a[1] == Py_None ? Py_BuildValue("(L)", static_cast<long long>(inv.size(0))) : PySequence_Tuple(a[1]);
+  if (!pairs) throw python_error();
+  const THPObjectPtr holder(pairs);
+  const Py_ssize_t axes = PyTuple_GET_SIZE(pairs);
+  NEED_VALUE(axes >= 1 && axes <= 4, "axis_pairs must be 1 to 4 counts");
+  int64_t total = 0;
+  for (Py_ssize_t i = 0; i < axes; ++i) {
+    const int64_t x = integer(PyTuple_GET_ITEM(pairs, i), "axis_pairs");
+    NEED_VALUE(x >= 0, "axis_pairs must not be negative");
+    total += x;
+  }
+  NEED_VALUE(total == inv.size(0), "axis_pairs must sum to ", inv.size(0), ", got ", total);
+  return pack({keep(a[0]), keep(pairs), keep(a[2]), keep(a[3])});
 }
 
 // store(q, k, v, k_cache, v_cache, slots, positions, (inv_freq, axis_pairs, offset, interleaved) or None, q_descale, k_descale,
@@ -256,7 +295,7 @@ PyObject* store(PyObject* const* a, Py_ssize_t n) {
   void* vop = vo ? dense(*vo, "v_out", code, {N, H_kv, D_v}, dev) : nullptr;
   NEED_VALUE(N == 0 || ((!kop || kop != k->data_ptr()) && (!vop || vop != v->data_ptr())), "k_out and v_out must not be k and v");
   void* slots = exact(tensor(a[5], "slots"), "slots", at::kLong, dev, {N});
-  zyfa_rope_t rope = {};
+  zyfa_rope_t spec = {};
   const int* positions = nullptr;
   int64_t stride = 0;
   const bool turns = a[7] != Py_None;
@@ -265,14 +304,14 @@ PyObject* store(PyObject* const* a, Py_ssize_t n) {
     const Tensor& inv = tensor(PyTuple_GET_ITEM(a[7], 0), "rope.inv_freq");
     PyObject* pairs = PyTuple_GET_ITEM(a[7], 1);
     NEED_VALUE(inv.dim() == 1 && inv.size(0) <= 4096, "rope.inv_freq must be [rot_dim / 2]");
-    rope.inv_freq = static_cast<const float*>(exact(inv, "rope.inv_freq", at::kFloat, dev, {inv.size(0)}));
-    rope.rot_dim = static_cast<int>(2 * inv.size(0));
-    rope.rot_offset = static_cast<int>(integer(PyTuple_GET_ITEM(a[7], 2), "rope.offset"));
-    rope.interleaved = PyObject_IsTrue(PyTuple_GET_ITEM(a[7], 3)) == 1;
+    spec.inv_freq = static_cast<const float*>(exact(inv, "rope.inv_freq", at::kFloat, dev, {inv.size(0)}));
+    spec.rot_dim = static_cast<int>(2 * inv.size(0));
+    spec.rot_offset = static_cast<int>(integer(PyTuple_GET_ITEM(a[7], 2), "rope.offset"));
+    spec.interleaved = PyObject_IsTrue(PyTuple_GET_ITEM(a[7], 3)) == 1;
     const Py_ssize_t axes = PyTuple_GET_SIZE(pairs);
     NEED_VALUE(axes >= 1 && axes <= 4, "rope.axis_pairs must be 1 to 4 counts");
-    rope.num_axes = static_cast<int>(axes);
-    for (Py_ssize_t i = 0; i < axes; ++i) rope.axis_pairs[i] = static_cast<int>(integer(PyTuple_GET_ITEM(pairs, i), "rope.axis_pairs"));
+    spec.num_axes = static_cast<int>(axes);
+    for (Py_ssize_t i = 0; i < axes; ++i) spec.axis_pairs[i] = static_cast<int>(integer(PyTuple_GET_ITEM(pairs, i), "rope.axis_pairs"));
     const Tensor* pos = optional(a[6], "positions");
     NEED_TYPE(pos && pos->scalar_type() == at::kInt, "positions must be an int32 CUDA tensor [N] or [axes, N]");
     const bool flat = pos->dim() == 1 && axes == 1;
@@ -286,7 +325,7 @@ PyObject* store(PyObject* const* a, Py_ssize_t n) {
   const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 8, H_kv, dev) : Descales();
   succeed(zyfa_rope_paged_store(q ? q->data_ptr() : nullptr, k ? k->data_ptr() : nullptr, v ? v->data_ptr() : nullptr, qs, ks, vs, qop,
                                 kop, vop, positions, stride, static_cast<const long long*>(slots), N, static_cast<int>(H), &cache.c,
-                                turns ? &rope : nullptr, d.p[0], d.p[1], d.p[2], d.per_head, stream_of(dev)),
+                                turns ? &spec : nullptr, d.p[0], d.p[1], d.p[2], d.per_head, stream_of(dev)),
           "zyfa_rope_paged_store");
   return made ? THPVariable_Wrap(std::move(*made)) : keep(a[11]);
 }
@@ -359,6 +398,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyMethodDef g_methods[] = {
     {"plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<plan>)), METH_FASTCALL, nullptr},
+    {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<rope>)), METH_FASTCALL, nullptr},
     {"store", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<store>)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<decode>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

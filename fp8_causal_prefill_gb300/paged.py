@@ -56,7 +56,8 @@ def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     Pages that the new tokens start are taken from ``free_pages`` (int32) at ``cursor`` (int32, one value)
     and written into ``block_table`` (int32 [B, max_pages]; other entries stay as they are).  Token rows are
     numbered request after request; rows from the last token up to ``max_tokens`` get position 0 and slot -1.
-    ``out`` gives the result's tensors (for captured graphs); ``out.cursor`` may be ``cursor`` itself.
+    ``out`` gives the result's tensors (for captured graphs); ``out.cursor`` may be ``cursor`` itself.  Without it they
+    are made in one allocation.
     """
     r = (_native or _load()).plan(cached_lens, new_lens, block_table, free_pages, cursor, page_size, max_tokens, out)
     return r if out is not None else PagedPlan._make(r)
@@ -70,15 +71,13 @@ class Rope:
     ``offset``: first rotated channel; ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2).
     """
 
+    __slots__ = ("_spec",)
+
     def __init__(self, inv_freq: torch.Tensor, axis_pairs=None, offset: int = 0, interleaved: bool = False):
-        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
-            raise TypeError("inv_freq must be a contiguous float32 CUDA tensor [rot_dim / 2]")
-        pairs = inv_freq.shape[0]
-        axis_pairs = (pairs,) if axis_pairs is None else tuple(axis_pairs)
-        if not inv_freq.is_cuda or not 1 <= len(axis_pairs) <= 4 or sum(axis_pairs) != pairs or min(axis_pairs) < 0:
-            raise ValueError(f"inv_freq must be a CUDA tensor and axis_pairs 1 to 4 counts that sum to {pairs}")
-        self.inv_freq, self.num_axes = inv_freq, len(axis_pairs)
-        self._spec = (inv_freq, axis_pairs, offset, interleaved)
+        self._spec = (_native or _load()).rope(inv_freq, axis_pairs, offset, interleaved)
+
+    inv_freq = property(lambda self: self._spec[0])
+    axis_pairs = property(lambda self: self._spec[1])
 
 
 def rope_paged_store(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, k_cache: torch.Tensor,
