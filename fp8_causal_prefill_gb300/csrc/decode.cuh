@@ -80,8 +80,8 @@ struct DecodeArgs {
   int box_log2;                 // tokens of a TMA box, at most a tile's
   int joint_k, joint_v;         // rows of 64 (or 192) bytes lie in shared memory in 128-byte columns across heads
   unsigned* starts;  // [B + 2], for more than kFew requests: first tile of each, then the total, then the tiles per group
-  float2* ml;        // [groups][2][subs][H]
-  float* part;       // [groups][2][subs][H][DV]
+  float2* ml;        // [groups][2][H]
+  float* part;       // [groups][2][H][DV]
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -427,46 +427,99 @@ struct Rows {
     const int t4 = lane & 3, g8 = lane >> 2;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float sum = l[e];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const float sum = total(e);
       const int head = t4 * 2 + e;
       if (head < count) {
         const long long row = (direct ? static_cast<long long>(b) : slot) * a.H + first + head;
         const float f = !direct ? dv : sum > 0.0f ? dv / sum : 0.0f;
-        if (g8 == 0) {
-          if (!direct)
-            a.ml[row] = make_float2(m[e] - kLift, sum);
-          else if (a.lse)
-            a.lse[row] = sum > 0.0f ? (m[e] + log2f(sum) - kLift) * 0.69314718055994531f : -INFINITY;
-        }
+        if (g8 == 0) put_sums(a, row, direct, m[e], sum);
         __nv_bfloat16* out = a.out + row * DV;
         float* part = a.part + row * DV;
-        // rows r and r + 8: channels 2r and 2r + 1 of the tile's 16 (e4m3), or r and r + 8
-        constexpr int kStep = FP8 ? 2 : 1;
         if (direct) {
 #pragma unroll
           for (int i = 0; i < kMTiles; ++i) {
             const float y0 = o[i][e] * f, y1 = o[i][e + 2] * f;
             if constexpr (FP8) {
-              *reinterpret_cast<__nv_bfloat162*>(out + i * 16 + kStep * g8) = __floats2bfloat162_rn(y0, y1);
+              *reinterpret_cast<__nv_bfloat162*>(out + channel(i, g8)) = __floats2bfloat162_rn(y0, y1);
             } else {
-              out[i * 16 + g8] = __float2bfloat16_rn(y0);
-              out[i * 16 + g8 + 8] = __float2bfloat16_rn(y1);
+              out[channel(i, g8)] = __float2bfloat16_rn(y0);
+              out[channel(i, g8) + 8] = __float2bfloat16_rn(y1);
             }
           }
         } else if (m[e] != -INFINITY) {  // without a valid key the join does not read O
-#pragma unroll
-          for (int i = 0; i < kMTiles; ++i) {
-            if constexpr (FP8) {
-              *reinterpret_cast<float2*>(part + i * 16 + kStep * g8) = make_float2(o[i][e] * f, o[i][e + 2] * f);
-            } else {
-              part[i * 16 + g8] = o[i][e] * f;
-              part[i * 16 + g8 + 8] = o[i][e + 2] * f;
-            }
-          }
+          put_o(part, e, f, g8);
         }
+      }
+    }
+  }
+
+  // The same for a request's part whose tiles' token runs `subs` warps shared (this one the sub-th): they leave (m, l, O) in
+  // shared memory, meet, join them in order, each warp some of the heads, and meet again before the memory is used anew.
+  // all_ml, all_o: [subs][8] and [subs][8][DV], `stride` warps from one sub's to the next; meet() is false if it gave up.
+  template <typename F>
+  __device__ __forceinline__ bool finish_shared(const DecodeArgs& a, int b, int first, int count, bool direct, long long slot, int lane, int sub,
+                                                int subs, int stride, float2* all_ml, float* all_o, F meet) {
+    const int g8 = lane >> 2;
+    float2* my_ml = all_ml + sub * stride * 8;
+    float* my_o = all_o + sub * stride * 8 * DV;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float sum = total(e);
+      const int head = (lane & 3) * 2 + e;
+      if (g8 == 0) my_ml[head] = make_float2(m[e], sum);
+      put_o(my_o + head * DV, e, dv, g8);
+    }
+    if (!meet()) return false;
+    constexpr int V = DV / 32;
+    for (int head = sub; head < count; head += subs) {
+      float M = -INFINITY, L = 0.0f, x[V] = {};
+      for (int k = 0; k < subs; ++k) M = fmaxf(M, all_ml[k * stride * 8 + head].x);
+      for (int k = 0; k < subs && M != -INFINITY; ++k) {
+        const float2 ml = all_ml[k * stride * 8 + head];
+        const float e = exp2_approx(ml.x - M);  // 0 for a run without a valid key, whose O is 0
+        L = fmaf(ml.y, e, L);
+        const float* y = all_o + (k * stride * 8 + head) * DV + lane * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = fmaf(y[j], e, x[j]);
+      }
+      const long long row = (direct ? static_cast<long long>(b) : slot) * a.H + first + head;
+      if (lane == 0) put_sums(a, row, direct, M, L);
+      const float f = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        if (direct)
+          *reinterpret_cast<__nv_bfloat162*>(a.out + row * DV + lane * V + j) = __floats2bfloat162_rn(x[j] * f, x[j + 1] * f);
+        else if (M != -INFINITY)
+          *reinterpret_cast<float2*>(a.part + row * DV + lane * V + j) = make_float2(x[j], x[j + 1]);
+      }
+    }
+    return meet();
+  }
+
+ private:
+  // This lane's first channel of tile i (the other: the next one for e4m3, the 8th from it for bf16).
+  static __device__ __forceinline__ int channel(int i, int g8) { return i * 16 + (FP8 ? 2 : 1) * g8; }
+  __device__ __forceinline__ float total(int e) const {
+    float sum = l[e];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    return sum;
+  }
+  static __device__ __forceinline__ void put_sums(const DecodeArgs& a, long long row, bool direct, float top, float sum) {
+    if (!direct)
+      a.ml[row] = make_float2(top - kLift, sum);
+    else if (a.lse)
+      a.lse[row] = sum > 0.0f ? (top + log2f(sum) - kLift) * 0.69314718055994531f : -INFINITY;
+  }
+  __device__ __forceinline__ void put_o(float* to, int e, float f, int g8) const {
+#pragma unroll
+    for (int i = 0; i < kMTiles; ++i) {
+      if constexpr (FP8) {
+        *reinterpret_cast<float2*>(to + channel(i, g8)) = make_float2(o[i][e] * f, o[i][e + 2] * f);
+      } else {
+        to[channel(i, g8)] = o[i][e] * f;
+        to[channel(i, g8) + 8] = o[i][e + 2] * f;
       }
     }
   }
@@ -653,7 +706,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   __shared__ unsigned s_prefix[kMaxWarps * 32], s_sums[kMaxWarps];
   __shared__ __align__(16) Header s_header[kMaxStages];
   __shared__ float2 s_scale[kMaxStages][kMaxHeads];  // of the scores, and of V
-  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages];
+  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_meet[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x >> 5) - 1;  // compute warps; the next one loads
   const int S = a.stages, TT = a.tile_tokens;
   const uint32_t k_bytes = a.heads * TT * T::kRowK, stage_bytes = a.heads * TT * T::kKeyBytes;
@@ -663,6 +716,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       ptx::mbar_init(full_s + 8 * i, 1);
       ptx::mbar_init(empty_s + 8 * i, warps);
     }
+    for (int i = 0; i < a.heads * a.chunk_warps; ++i) ptx::mbar_init(smem_addr(s_meet + i), a.subs);
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
@@ -800,20 +854,29 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   const uint32_t k_box = a.heads * T::kRowK << a.box_log2, v_box = a.heads * T::kRowV << a.box_log2;
   const uint32_t k_pitch = kWhole<T::kRowK> || a.joint_k ? 128 : 64, v_pitch = kWhole<T::kRowV> || a.joint_v ? 128 : 64;
   const uint32_t my_query = query_s + (head * a.group + (chunk - chunk0) * a.chunk_heads) * T::kRowK;
+  // where warps that share a head's tokens meet
+  const int peers = a.heads * a.chunk_warps, peer = warp % peers;
+  float2* all_ml = reinterpret_cast<float2*>(smem + S * (stage_bytes + a.q_bytes)) + peer * 8;
+  float* all_o = reinterpret_cast<float*>(smem + S * (stage_bytes + a.q_bytes) + warps * 64) + peer * 8 * DV;
+  const uint32_t meet_s = smem_addr(s_meet + peer);
+  uint32_t meet_parity = 0;
+  // Copies still in flight write to this block's shared memory: waits for them, again for a bounded time.
+  auto give_up = [&](int tile, int st, uint32_t par) {
+    for (int j = 1; j < S && tile + j < tiles; ++j) {
+      if (++st == S) {
+        st = 0;
+        par ^= 1;
+      }
+      mbar_wait_bounded(full_s + 8 * st, par);
+    }
+    if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+  };
   Rows<FP8, DQK, DV> rows;
   int stage = 0;
   uint32_t parity = 0;
   for (int i = 0; i < tiles; ++i) {
     if (!mbar_wait_bounded(full_s + 8 * stage, parity)) {
-      // copies still in flight write to this block's shared memory: wait for them, again for a bounded time
-      for (int j = 1; j < S && i + j < tiles; ++j) {
-        if (++stage == S) {
-          stage = 0;
-          parity ^= 1;
-        }
-        mbar_wait_bounded(full_s + 8 * stage, parity);
-      }
-      if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+      give_up(i, stage, parity);
       return;
     }
     const Header h = s_header[stage];
@@ -847,8 +910,23 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
           });
       }
       if (h.flags & kLast) {
-        const bool direct = (h.flags & kDirect) && a.subs == 1;
-        rows.finish(a, h.b, q0, nq, direct, (static_cast<long long>(g) * 2 + (h.flags & kSlot1 ? 1 : 0)) * a.subs + sub, lane);
+        const bool direct = h.flags & kDirect;
+        const long long slot = static_cast<long long>(g) * 2 + (h.flags & kSlot1 ? 1 : 0);
+        if (a.subs == 1) {
+          rows.finish(a, h.b, q0, nq, direct, slot, lane);
+        } else {
+          const bool met = rows.finish_shared(a, h.b, q0, nq, direct, slot, lane, sub, a.subs, peers, all_ml, all_o, [&]() {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(meet_s);
+            const bool ok = mbar_wait_bounded(meet_s, meet_parity);
+            meet_parity ^= 1;
+            return ok;
+          });
+          if (!met) {
+            give_up(i, stage, parity);
+            return;
+          }
+        }
       }
     }
     __syncwarp();
@@ -1011,14 +1089,10 @@ __global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_consta
     if (a.lse && tid == 0 && d0 == 0) a.lse[row] = -INFINITY;
     return;
   }
-  const int g0 = static_cast<int>(p0 / per), n = (static_cast<int>((p1 - 1) / per) - g0 + 1) * a.subs;
+  const int g0 = static_cast<int>(p0 / per), n = static_cast<int>((p1 - 1) / per) - g0 + 1;
   if (n == 1) return;
-  // part i: group g0 + i / subs, its slot 1 (a request that begins there) for the first, else slot 0
-  const int subs_log2 = 31 - __clz(a.subs);
-  auto part = [&](int i) {
-    const int k = i >> subs_log2;
-    return (((static_cast<long long>(g0 + k) * 2 + (k == 0 ? 1 : 0)) << subs_log2) + (i & (a.subs - 1))) * a.H + h;
-  };
+  // part i: group g0 + i, its slot 1 (a request that begins there) for the first, else slot 0
+  auto part = [&](int i) { return (static_cast<long long>(g0 + i) * 2 + (i == 0 ? 1 : 0)) * a.H + h; };
   float m = -INFINITY, l = 0.0f, o[VEC] = {};
   for (int base = w; base < n; base += 32 * W) {
     const int count = min(32, (n - base + W - 1) / W);  // parts base, base + W, ...
@@ -1090,11 +1164,11 @@ __global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_consta
 
 inline long long round_up(long long x, long long n) { return (x + n - 1) / n * n; }
 
-// Parts that one request and head can have at most, for the workspace: one per group and token run.  A group has H_kv warps per
-// chunk of 8 query heads and token run at least, and there are no more than tiles.
+// Parts that one request and head can have at most, for the workspace: one per group.  A group has at least H_kv warps per chunk
+// of 8 query heads, and there are no more groups than tiles.
 inline long long parts_at_most(int B, int H, int H_kv, long long max_len) {
   const long long warps = static_cast<long long>(H_kv) * ((H / H_kv + 7) / 8);
-  return std::max<long long>(kMaxHeads, std::min(kMaxSms * kMaxWarpsPerSm / warps, B * ((max_len + 15) / 16 + kMaxHeads)));
+  return std::max(1ll, std::min(kMaxSms * kMaxWarpsPerSm / warps, B * ((max_len + 15) / 16)));
 }
 
 inline long long tiles_at_most(int B, long long max_len, int keys) { return B * ((max_len + keys - 1) / keys); }
@@ -1185,17 +1259,18 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   const int nq = a.chunks > a.chunk_warps ? a.chunk_warps * a.chunk_heads : a.heads * a.group;
   a.q_bytes = static_cast<int>(round_up(nq * T::kRowK, 16));
   const int warps = a.heads * a.chunk_warps * a.subs, stage = a.heads * a.tile_tokens * T::kKeyBytes + a.q_bytes;
+  const int meeting = a.subs > 1 ? warps * 8 * (DV + 2) * 4 : 0;  // (m, l, O) of the warps that share a head's tokens
   // two blocks an SM (more where they are small), or one if two would not have two stages each
   constexpr int kStatic = 4096;  // the schedule's tables and headers, with the 1 KiB that each block takes
   int blocks = 3;
-  while (blocks > 1 && blocks * (2 * stage + kStatic) > kSmemPerSm) --blocks;
-  a.stages = std::min(kMaxStages, std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) / stage);
+  while (blocks > 1 && blocks * (2 * stage + meeting + kStatic) > kSmemPerSm) --blocks;
+  a.stages = std::min(kMaxStages, (std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) - meeting) / stage);
   if (a.stages < 2) return cudaSuccess;
   a.groups = static_cast<int>(std::max(1ll, std::min<long long>(static_cast<long long>(nsm) * blocks / a.units, tiles_at_most(a.B, a.max_len, a.tile_tokens))));
   static std::atomic<int> set[kMaxDevices];
   if (!prepare(boxes_kernel<FP8, DQK, DV>, 2, dev, set)) return cudaErrorUnknown;
   *done = true;
-  return launch_dependent(boxes_kernel<FP8, DQK, DV>, dim3(static_cast<unsigned>(a.groups) * a.units), (warps + 1) * 32, a.stages * stage, stream, a, kmap,
+  return launch_dependent(boxes_kernel<FP8, DQK, DV>, dim3(static_cast<unsigned>(a.groups) * a.units), (warps + 1) * 32, a.stages * stage + meeting, stream, a, kmap,
                           vmap);
 }
 
@@ -1235,7 +1310,7 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   if (e != cudaSuccess) return ZYFA_ERR_CUDA;
   // Few rows have many parts each, and their channels are spread over blocks too; of many rows most lie in one or two groups.
   const unsigned rows = static_cast<unsigned>(a.B) * a.H;
-  const long long parts_each = static_cast<long long>(a.groups) * a.subs / a.B;
+  const long long parts_each = a.groups / a.B;
   constexpr int V = DV / 32;
   static std::atomic<int> set[3][kMaxDevices];
   if (rows * V <= 2u * nsm) {

@@ -323,7 +323,9 @@ PyObject* store(PyObject* const* a, Py_ssize_t n) {
     NEED_VALUE(stride >= N, "positions rows must not overlap");
   }
   const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 8, H_kv, dev) : Descales();
-  succeed(zyfa_rope_paged_store(q ? q->data_ptr() : nullptr, k ? k->data_ptr() : nullptr, v ? v->data_ptr() : nullptr, qs, ks, vs, qop,
+  // (an empty tensor has no address, which the C call would take for one that is not given)
+  if (N > 0)
+    succeed(zyfa_rope_paged_store(q ? q->data_ptr() : nullptr, k ? k->data_ptr() : nullptr, v ? v->data_ptr() : nullptr, qs, ks, vs, qop,
                                 kop, vop, positions, stride, static_cast<const long long*>(slots), N, static_cast<int>(H), &cache.c,
                                 turns ? &spec : nullptr, d.p[0], d.p[1], d.p[2], d.per_head, stream_of(dev)),
           "zyfa_rope_paged_store");

@@ -332,15 +332,17 @@ zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v,
  *   lse               NULL, or [B][H] floats: ln sum_j exp(scale q.k) in real units, -inf without tokens.
  *   softmax_scale     0 selects 1/sqrt(D_qk); negative, NaN or infinite values are rejected.
  *   q/k/v_descale     e4m3 only: one float, or [B][H_kv] floats with descale_per_kv_head = 1; NULL means 1.
+ *                     out and lse must not overlap the inputs or the workspace.
  *   workspace         device scratch of zyfa_attn_decode_paged_workspace_bytes() bytes, 16-byte aligned; its
  *                     contents on entry do not matter.  Calls that may overlap on the GPU (other streams, two
  *                     captured graphs) need one each.
  *
  * Tokens whose page lies outside [0, num_pages) are left out of the softmax and zyfa_check_errors() returns
- * ZYFA_ERR_BAD_PAGE.  Cache rows behind a request's length are never read, whatever they hold.
+ * ZYFA_ERR_BAD_PAGE.  Cache rows behind a request's length do not matter, whatever they hold.
  * Scores and sums are held in fp32; the weights exp(s - max) are rounded to 16 bits before they
  * multiply V (fp16 for an e4m3 cache, whose values fp16 holds exactly, else bf16).  Bitwise reproducible
- * for identical inputs on one GPU model.  Asynchronous on `stream`, allocates nothing, no host synchronisation.
+ * for identical inputs on one GPU model.  Two launches, asynchronous on `stream`; allocates nothing, no host
+ * synchronisation.  A kernel that gives up on a copy (about a second) records ZYFA_ERR_TIMEOUT as the prefill does.
  */
 zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache,
                                      const int* block_table, long long table_stride, int max_pages,

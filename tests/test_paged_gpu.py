@@ -97,6 +97,26 @@ def test_plan_updates_its_cursor_in_place():
     assert p.slots.tolist() == [2 * 4 + 2, 2 * 4 + 3, 4, 5, 6] and p.positions.tolist() == [10, 11, 12, 13, 14]
 
 
+def test_plan_in_place_cursor_with_many_rows():
+    # the rows take many blocks, all of which read the cursor before it moves
+    rng = np.random.default_rng(3)
+    B, page = 40, 16
+    cached, new = rng.integers(0, 100, B), rng.integers(0, 900, B)
+    need = int(sum(-(-(c + n) // page) for c, n in zip(cached, new)))
+    free = rng.permutation(need + 9).astype(np.int32)
+    table = np.full((B, 64), 5, dtype=np.int32)
+    rows = int(new.sum()) + 31
+    want = P.paged_plan(cached, new, table, free, 7, page, rows)
+    t, cursor = torch.from_numpy(table).cuda(), i32([7])
+    z = lambda n, d=torch.int32: torch.full((n,), -9, dtype=d, device="cuda")  # noqa: E731
+    out = PagedPlan(z(B), z(B + 1), z(rows), z(rows, torch.int64), cursor)
+    assert paged_plan(i32(cached), i32(new), t, torch.from_numpy(free).cuda(), cursor, page, rows, out=out) is out
+    np.testing.assert_array_equal(t.cpu().numpy(), want[0])
+    for g, w in zip(out, want[1:]):
+        np.testing.assert_array_equal(g.cpu().numpy().reshape(-1), np.atleast_1d(w))
+    assert zyfa_check_errors() == (CAPACITY if want[6] else 0)
+
+
 # ------------------------------------------------------------------------------------------------
 # rotation and store
 
@@ -208,6 +228,41 @@ def test_store_parts(kind):
     _store_case(kind, "64", 3, 71, 71, seed=15)
     _store_case(kind, "128", 700, 8, 2, seed=16, pad=60, dense=True)
     _store_case(kind, "64", 0, 4, 2, seed=17, pad=3)
+    _store_case(kind, "mla", 2500, 3, 1, rot=64, offset=128, seed=18, pad=3)    # several tokens per block, a ragged last one
+    _store_case(kind, "128", 5000, 2, 2, seed=19, strided=True, dense=True)
+
+
+def test_store_without_tokens_or_rotation():
+    kc, vc = make_cache(2, 4, 2, "64", "bf16")
+    empty = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty(0, dtype=torch.int64, device="cuda")
+    assert rope_paged_store(empty, empty, empty, kc, vc, slots).shape == (0, 2, 64)
+    assert rope_paged_store(None, empty, empty, kc, vc, slots) is None
+    x = random_values((3, 2, 64), "bf16", np.random.default_rng(1))
+    none = Rope(torch.empty(0, device="cuda"))
+    at = torch.tensor([1, 5, 2], device="cuda")
+    assert torch.equal(rope_paged_store(x, x, x, kc, vc, at, i32([9, 9, 9]), none), x)
+    assert torch.equal(kc.flatten(0, 1)[at], x) and torch.equal(vc.flatten(0, 1)[at], x)
+
+
+def test_store_tensor_refusals():
+    kc, vc = make_cache(2, 4, 2, "64", "bf16")
+    x, slots, pos = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda"), i32([0, 1, 2])
+    rope = Rope(torch.ones(32, device="cuda"))
+    for bad in (dict(q=x.float()), dict(q=x[:2]), dict(k=x[:, :1]), dict(v=None), dict(q=None, k=None, v=None), dict(slots=slots.int()),
+                dict(slots=slots[:2]), dict(slots=slots.cpu()), dict(pos=pos.long()), dict(pos=pos[:2]), dict(pos=pos[None].repeat(2, 1)),
+                dict(pos=None), dict(q_out=x), dict(q_out=x.to(E4M3)), dict(k_out=x[:2]), dict(q=x.transpose(0, 1).contiguous().transpose(0, 1)),
+                dict(q=x[..., ::2]), dict(kc=kc.float()), dict(kc=kc[:1]), dict(rope=Rope(torch.ones(32, device="cuda"), axis_pairs=(16, 16)))):
+        a = dict(q=x, k=x, v=x, kc=kc, vc=vc, slots=slots, pos=pos, rope=rope, q_out=None, k_out=None)
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            rope_paged_store(a["q"], a["k"], a["v"], a["kc"], a["vc"], a["slots"], a["pos"], a["rope"], q_out=a["q_out"], k_out=a["k_out"])
+    with pytest.raises(RuntimeError):                                             # more rotated channels than there are
+        rope_paged_store(x, x, x, kc, vc, slots, pos, Rope(torch.ones(40, device="cuda")))
+    for pairs in ((31,), (16, 17), (40, -8), (8, 8, 8, 8, 0), ()):
+        with pytest.raises(ValueError):
+            Rope(torch.ones(32, device="cuda"), axis_pairs=pairs)
+    assert np.isnan(f64(kc)).all()
 
 
 def test_store_saturates_and_keeps_slots_outside_untouched():
@@ -297,6 +352,62 @@ def test_decode_groups(kind, H, H_kv):
     _decode_case(kind, "128", [77, 1, 300], H, H_kv, seed=H, per_head=True)
     _decode_case(kind, "64", [1000], H, H_kv, seed=H + 1)
     _decode_case(kind, "mla", [70, 140], H, H_kv, seed=H + 2)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("H,H_kv", [(10, 10), (20, 10), (11, 11), (12, 6), (32, 32), (24, 8), (32, 2), (96, 4)])
+def test_decode_many_kv_heads(kind, H, H_kv):
+    # heads that do and do not fill the blocks that take them side by side
+    _decode_case(kind, "64", [37, 300], H, H_kv, seed=H, per_head=True, page=32)
+    _decode_case(kind, "128", [290, 3], H, H_kv, seed=H + 1, page=8)
+    _decode_case(kind, "mla", [64, 129], H, H_kv, seed=H + 2, page=64)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("B,page", [(128, 16), (129, 16), (200, 7), (700, 16), (1100, 24)])
+def test_decode_many_requests(kind, B, page):
+    # beyond 128 requests the schedule is formed by whole blocks, beyond a block's threads in several passes
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 90, B)
+    lens[rng.permutation(B)[: B // 4]] = 0
+    lens[3], lens[B - 1] = 800, 5
+    _decode_case(kind, "64", lens.tolist(), 2, 1, seed=B, page=page)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_decode_broadcast_cache(kind):
+    # strides of 0: every KV head (every page) reads the same rows
+    rng = np.random.default_rng(8)
+    q, table, lens = random_values((2, 8, 128), kind, rng), i32([[0, 1, 2], [2, 1, 0]]), i32([40, 47])
+    k, v = random_values((3, 16, 1, 128), kind, rng), random_values((3, 16, 1, 128), kind, rng)
+    wide = [bits(t).expand(-1, -1, 4, -1).view(t.dtype) for t in (k, v)]
+    full = [bits(t).expand(-1, -1, 4, -1).contiguous().view(t.dtype) for t in (k, v)]
+    a, b = paged_decode_attn(q, *wide, table, lens), paged_decode_attn(q, *full, table, lens)
+    assert float((a - b).abs().max()) <= 2.0 ** -7 * float(b.abs().max())        # other tiles, other order: each within its roundings
+    one = [bits(t)[:1].expand(3, -1, -1, -1).view(t.dtype) for t in (k, v)]
+    c, d = paged_decode_attn(q, *one, table, lens), paged_decode_attn(q, k, v, torch.zeros_like(table), lens)
+    assert float((c - d).abs().max()) <= 2.0 ** -7 * float(d.abs().max())
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_decode_very_long_context(kind):
+    rng = np.random.default_rng(9)
+    n, d = 300_001, 64
+    table, pages = random_table([n], 64, rng)
+    kc, vc = make_cache(pages, 64, 1, "64", kind)
+    q, k, v = (random_values(s, kind, rng) for s in ((1, 2, d), (n, 1, d), (n, 1, d)))
+    t = np.arange(n)
+    slots = torch.from_numpy(table[0, t // 64].astype(np.int64) * 64 + t % 64).cuda()
+    fill_tokens(kc, slots, k)
+    fill_tokens(vc, slots, v)
+    ds = [torch.tensor([1 / 64.0], device="cuda") if kind == "fp8" else None for _ in range(3)]
+    f = 1 / 64.0 if kind == "fp8" else 1.0
+    out, lse = paged_decode_attn(q, kc, vc, torch.from_numpy(table).cuda(), i32([n]), q_descale=ds[0], k_descale=ds[1], v_descale=ds[2], return_lse=True)
+    for h in range(2):
+        qr, kr, vr = f64(q)[0, h] * f, f64(k)[:, 0] * f, f64(v)[:, 0]
+        ref, ref_lse, w = P.decode_attention(qr, kr, vr * f, d ** -0.5)
+        tol, lse_tol = decode_tolerance(qr, kr, vr, d ** -0.5, f, ref, w, kind)
+        assert np.all(np.abs(f64(out)[0, h] - ref) <= tol) and abs(float(lse[0, h]) - ref_lse) <= lse_tol + 2.0 ** -22 * abs(ref_lse)
 
 
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
