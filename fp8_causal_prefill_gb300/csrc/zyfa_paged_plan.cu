@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   __shared__ long long s_wtok[kWarps], s_wpage[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lead = blockIdx.x == 0 && !a.cursor_only;      // writes the per-request results
+  zyfa::wait_for_predecessor();
   const bool tail = blockIdx.x == gridDim.x - 1;            // takes rows behind max_tokens (their pages count) too
   const int cursor = max(0, __ldg(a.cursor_in));
   const int cap = a.max_pages * a.page;                     // at most 2^30
@@ -219,11 +220,10 @@ extern "C" zyfa_status_t zyfa_paged_plan(const int* cached_lens, const int* new_
   a.rows = static_cast<int>((max_tokens + blocks - 1) / blocks);
   // Updated in place, the cursor may only be written once every block has read it.
   a.write_cursor = cursor_in != cursor_out || blocks == 1;
-  plan_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return ZYFA_ERR_CUDA;
+  if (zyfa::launch_dependent(plan_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream, a) != cudaSuccess) return ZYFA_ERR_CUDA;
   if (!a.write_cursor) {
     a.write_cursor = a.cursor_only = 1;
-    plan_kernel<<<1, kThreads, 0, stream>>>(a);
+    if (zyfa::launch_dependent(plan_kernel, dim3(1), kThreads, 0, stream, a) != cudaSuccess) return ZYFA_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
+  return ZYFA_OK;
 }

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads<DQK>) store_kernel(const __grid_const
     y0 = *reinterpret_cast<const uint4*>(x);
     y1 = *reinterpret_cast<const uint4*>(x + 8);
   };
+  zyfa::wait_for_predecessor();
   // the first loads run while the tables are made
   fetch();
   if (a.k) fetch_v();
@@ -271,12 +272,10 @@ template <bool FP8, bool INTERLEAVED>
 cudaError_t launch(const StoreArgs& a, int D_qk, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((a.N + a.tokens - 1) / a.tokens);
   if (D_qk == 64)
-    store_kernel<FP8, INTERLEAVED, 64, 64><<<grid, kThreads<64>, 0, stream>>>(a);
-  else if (D_qk == 128)
-    store_kernel<FP8, INTERLEAVED, 128, 128><<<grid, kThreads<128>, 0, stream>>>(a);
-  else
-    store_kernel<FP8, INTERLEAVED, 192, 128><<<grid, kThreads<192>, 0, stream>>>(a);
-  return cudaGetLastError();
+    return zyfa::launch_dependent(store_kernel<FP8, INTERLEAVED, 64, 64>, dim3(grid), kThreads<64>, 0, stream, a);
+  if (D_qk == 128)
+    return zyfa::launch_dependent(store_kernel<FP8, INTERLEAVED, 128, 128>, dim3(grid), kThreads<128>, 0, stream, a);
+  return zyfa::launch_dependent(store_kernel<FP8, INTERLEAVED, 192, 128>, dim3(grid), kThreads<192>, 0, stream, a);
 }
 
 }  // namespace
