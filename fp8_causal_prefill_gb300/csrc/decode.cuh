@@ -287,6 +287,7 @@ struct Rows {
   static constexpr int kKSteps = T::kRowK / 32, kMTiles = DV / 16;
   static constexpr int kScoreKind = FP8 ? kE4m3 : kBf16, kValueKind = FP8 ? kF16 : kBf16;
   static constexpr float kLift = FP8 ? 15.0f : 0.0f;  // e4m3: weights in fp16 up to 2^15, so that light ones keep their bits
+  static constexpr float kNoKey = 3.0e38f;            // ref before the first key: lifts any score but -inf over the limit
 
   uint32_t qf[kKSteps][2];      // B fragments of the queries
   float o[kMTiles][4], m[2], l[2];  // this lane's two heads
@@ -309,7 +310,7 @@ struct Rows {
 #pragma unroll
     for (int i = 0; i < kMTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     m[0] = m[1] = -INFINITY;
-    ref = {INFINITY, INFINITY};
+    ref = {kNoKey, kNoKey};
     l[0] = l[1] = 0.0f;
     scale = scale_;
     dv = dv_;
@@ -342,8 +343,8 @@ struct Rows {
           if (!((mask >> (kb * 16 + j * 8 + (lane >> 2))) & 1)) x[kb][j] = {-INFINITY, -INFINITY};
       clear();
     }
-    // The reference m moves only when a key exceeds it: log2 of a weight is then above the lift.  (Before a part's first valid
-    // key m is -inf and every valid key's log2 weight +inf.)
+    // The reference m moves only when a key exceeds it: log2 of a weight is then above the lift.  (Before a part's first key
+    // with a score above -inf m is -inf, and the log2 weight of such a key huge.)
     F2 y[KB][2];
     float over = -INFINITY;
     auto weigh = [&]() {
@@ -365,9 +366,10 @@ struct Rows {
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-        const float f = exp2_approx(m[e] - t);
+        const bool none = t == -INFINITY;
+        const float f = none ? 1.0f : exp2_approx(m[e] - t);
         m[e] = t;
-        (e ? ref.y : ref.x) = kLift - t;
+        (e ? ref.y : ref.x) = none ? kNoKey : kLift - t;
         l[e] *= f;
 #pragma unroll
         for (int i = 0; i < kMTiles; ++i) {

@@ -470,6 +470,34 @@ def test_decode_bad_pages_are_left_out(kind):
     assert bool((out[1] == 0).all()) and bool((lse[1] == -math.inf).all())
 
 
+@pytest.mark.parametrize("page", [7, 16])
+@pytest.mark.parametrize("n", [70, 9000])
+def test_decode_scores_of_minus_infinity(n, page):
+    # keys whose score overflows to -inf weigh nothing, also as the first ones of a part; a row of only such keys is empty
+    rng = np.random.default_rng(n + page)
+    table, pages = random_table([n, n], page, rng)
+    kc, vc = make_cache(pages, page, 1, "64", "bf16")
+    q, k, v = (random_values(s, "bf16", rng) for s in ((2, 2, 64), (2, n, 1, 64), (2, n, 1, 64)))
+    q[:, 0, 0], q[:, 1, 0] = 4.0, 0.0                                             # head 0: 4 * -3e38 is below any fp32 number
+    low = np.zeros(n, dtype=bool)
+    low[rng.permutation(n)[: n // 3]] = low[: n // 2] = True
+    k[0, torch.from_numpy(low).cuda(), 0, 0] = -3e38
+    k[1, :, 0, 0] = -3e38
+    t = np.arange(n)
+    for b in range(2):
+        slots = torch.from_numpy(table[b, t // page].astype(np.int64) * page + t % page).cuda()
+        fill_tokens(kc, slots, k[b])
+        fill_tokens(vc, slots, v[b])
+    out, lse = paged_decode_attn(q, kc, vc, torch.from_numpy(table).cuda(), i32([n, n]), return_lse=True)
+    assert bool((out[1, 0] == 0).all()) and float(lse[1, 0]) == -math.inf
+    for b, h in ((0, 0), (0, 1), (1, 1)):
+        keep = ~low if h == 0 else low | True
+        q64, k64, v64 = f64(q)[b, h], f64(k)[b, keep, 0], f64(v)[b, keep, 0]
+        ref, ref_lse, w = P.decode_attention(q64, k64, v64, 0.125)
+        tol, lse_tol = decode_tolerance(q64, k64, v64, 0.125, 1.0, ref, w, "bf16")
+        assert np.all(np.abs(f64(out)[b, h] - ref) <= tol) and abs(float(lse[b, h]) - ref_lse) <= lse_tol + 2.0 ** -22 * abs(ref_lse)
+
+
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
 def test_decode_lengths_outside_the_table(kind):
     rng = np.random.default_rng(4)
