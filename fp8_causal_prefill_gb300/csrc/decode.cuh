@@ -28,6 +28,15 @@
 // own loads a block's tiles, one box for K and one for V per page.  (Compute warps that loaded for themselves spent 500 to
 // 950 clocks per tile on it, as long as on the tile.)  rows_kernel: any page size and stride, by cp.async; each warp
 // loads its own tiles row by row into a ring of its own.
+//
+// Measured, with the bytes of the caches over the time, against 6.78 TB/s of a copy: 128 requests of 513 to 16384 tokens,
+// 8 KV heads of 128 e4m3 channels and 32 query heads, 178 us (6.8 TB/s; 0.86 of the DRAM's cycles, the tensor
+// cores busy for 0.19 of the time); 64 ragged requests in bf16 46 us (5.5 TB/s), 9 requests of 16 heads of 192/128 e4m3 channels
+// 59 us (6.0 TB/s).  The rest is the start (lengths, then pages, then tiles: three trips to memory) and the join, 6 to 8 us
+// together, which is also what a short context takes: 256 tokens 6 us, one request of 32768 tokens 18 us.
+// With 16 query heads per KV head a byte meets twice the arithmetic and widening V takes as long as its load: 4.0 TB/s
+// in e4m3, 5.8 in bf16.  Two column groups that share the fragments of K and V take 168 registers a thread, and with a
+// third fewer warps the same time (48.7 to 47.6 us, 32 heads 37 to 41), so chunks of 8 heads have a warp each.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -690,9 +699,12 @@ struct Cursor {
 // ------------------------------------------------------------------------------------------------
 // tiles by TMA
 
-// Compute warps of a block at most.  Two blocks and their load warps share an SM: 18 warps of 96 registers a thread, 10 of 168.
+// Compute warps of a block at most.  Three blocks and their load warps share an SM: 15 warps of 128 registers a thread, or 9 of
+// 168.  128 e4m3 requests, and 64 ragged ones in bf16: 179 and 46 us; two blocks of 8 (4) compute warps 187 and 48, two of 4 (2)
+// 190 and 50, four of 2 191 and 47.
 template <int KEY_BYTES>
 constexpr int kBoxWarps = KEY_BYTES <= 320 ? 4 : 2;
+// Tiles of a ring: the same 189 and 48 us with two, 179 and 46 with three, 187 and 49 with four.
 constexpr int kMaxStages = 3, kMaxHeads = 8;
 
 template <bool FP8, int DQK, int DV>
@@ -1057,7 +1069,7 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
 // Joins the parts of the requests that several groups worked on, and writes the rows of empty requests.  W warps take a (request,
 // head): every W-th part each, 32 at a time.  A lane reads one part's maximum and sum while the rows of O come in, none of
 // which depends on another; then the warps meet in shared memory in a fixed order.  A block takes ROWS of them (W = 1), or VEC
-// * 32 of the channels of one.
+// * 32 of the channels of one.  Latency bounds it: 3 to 4 us after the first kernel's end.
 template <int DV, int W, int ROWS, int VEC, int BATCH>
 __global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(W == 1 || ROWS == 1);
@@ -1242,7 +1254,7 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   a.q_bytes = static_cast<int>(round_up(nq * T::kRowK, 16));
   const int warps = a.heads * a.chunk_warps * a.subs, stage = a.heads * a.tile_tokens * T::kKeyBytes + a.q_bytes;
   const int meeting = a.subs > 1 ? warps * 8 * (DV + 2) * 4 : 0;  // (m, l, O) of the warps that share a head's tokens
-  // two blocks an SM (more where they are small), or one if two would not have two stages each
+  // three blocks an SM, or fewer if they would not have two stages each
   constexpr int kStatic = 4096;  // the schedule's tables and headers, with the 1 KiB that each block takes
   int blocks = 3;
   while (blocks > 1 && blocks * (2 * stage + meeting + kStatic) > kSmemPerSm) --blocks;
