@@ -351,6 +351,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   if (a[5] != Py_None) {
     scale = PyFloat_AsDouble(a[5]);
     if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+    NEED_VALUE(scale == 0.0 || static_cast<float>(scale) != 0.0f, "softmax_scale is below the smallest float32");  // 0: the default
   }
   const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 6, B * H_kv, dev) : Descales();
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));

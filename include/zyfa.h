@@ -263,9 +263,10 @@ typedef struct {
  * A token that gets no slot (no free page left, a page beyond max_pages, a table entry below 0) has slot
  * -1, the page it would have started is -1 in the table, and zyfa_check_errors() then returns
  * ZYFA_ERR_CAPACITY, as it does when the tokens are more than max_tokens (the rows behind are dropped).
- * Asynchronous on `stream`, one launch (two for many rows with the cursor updated in place), allocates nothing.  The outputs must not overlap
- * one another or the inputs (cursors excepted).  Errors: ZYFA_ERR_INVALID_ARG (null pointers; B, max_tokens,
- * num_free or max_pages < 0, table_stride < max_pages, page_size outside 1 .. 65536),
+ * Asynchronous on `stream`, one launch (two for many rows with the cursor updated in place), allocates
+ * nothing.  The outputs must not overlap one another or the inputs (cursors excepted).  Errors: ZYFA_ERR_INVALID_ARG (null pointers; B, max_tokens,
+ * num_free or max_pages < 0, table_stride < max_pages, page_size outside 1 .. 65536, seq_lens or cu_tokens
+ * in the place of cached_lens or new_lens),
  * ZYFA_ERR_UNSUPPORTED (max_pages * page_size beyond 2^30, B beyond 65536), ZYFA_ERR_MISALIGNED
  * (pointers not aligned to their type), ZYFA_ERR_CUDA.  B == 0 still writes cu_tokens[0], the cursor and the rows.
  */
@@ -352,7 +353,8 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
                                      cudaStream_t stream);
 
 /* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged for these sizes, with max_len =
- * max_pages * page_size; the same whatever the lengths are, at most about 500 * H * D_v floats per KV head's group.
+ * max_pages * page_size; the same whatever the lengths are: 2 * H * (D_v + 2) floats for each group that the
+ * work may be cut into, of which there are at most 2560 / (H_kv * ceil(H / H_kv / 8)), and one per 16 tokens.
  * Pure host arithmetic; 0 for sizes that the call refuses. */
 size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v, long long max_len);
 

@@ -1,6 +1,9 @@
 """GPU tests of the paged serving operators against their float64 oracle: page plan, rotation and store,
 single-token attention, and a run of them together."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -547,6 +550,9 @@ def test_decode_tensor_refusals():
             paged_decode_attn(a["q"], a["kc"], a["v"], a["table"], a["lens"], out=a["out"], workspace=a["ws"])
     with pytest.raises(RuntimeError):
         paged_decode_attn(q, kc, kc, table, lens, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    for scale in (1e-60, -1.0, math.nan, math.inf):                               # the first would round to 0, which selects the default
+        with pytest.raises((ValueError, RuntimeError)):
+            paged_decode_attn(q, kc, kc, table, lens, scale)
     k8 = kc.to(E4M3)
     one, many = torch.ones(1, device="cuda"), torch.ones(6, device="cuda")
     for kw in (dict(q_descale=one, k_descale=many), dict(q_descale=torch.ones(5, device="cuda")), dict(v_descale=one.cpu())):
@@ -698,3 +704,35 @@ def test_two_captured_graphs_with_their_own_workspaces():
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+_FIRST_IN_CAPTURE = """
+import torch
+from fp8_causal_prefill_gb300 import Rope, paged_decode_attn, paged_plan, rope_paged_store, zyfa_check_errors
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+n, page = 50, 16
+x = [torch.randn(n, h, 128, device="cuda").bfloat16() for h in (8, 2, 2)]
+kc, vc = (torch.zeros(6, page, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+table, lens, new, free, cursor = i32([[-1] * 4]), i32([0]), i32([n]), i32([4, 1, 5, 0, 2]), i32([0])
+rope = Rope(torch.rand(64, device="cuda"))
+def step():
+    plan = paged_plan(lens, new, table, free, cursor, page, n)
+    q = rope_paged_store(*x, kc, vc, plan.slots, plan.positions, rope)
+    return paged_decode_attn(q[n - 1:], kc, vc, table, plan.seq_lens)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+got = out.clone()
+kc.zero_(); vc.zero_(); table.fill_(-1)
+assert torch.equal(step(), got) and bool((got != 0).any()) and zyfa_check_errors() == 0
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    # nothing that a call does once per process or device (symbol addresses, kernel attributes) is forbidden in a capture
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_IN_CAPTURE], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0, r.stderr[-2000:]

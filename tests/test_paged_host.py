@@ -133,6 +133,13 @@ def test_plan_refusals(lib, kw, expect):
     assert _plan(lib, **kw) == expect
 
 
+def test_plan_refuses_results_in_place_of_the_lengths(lib):
+    # several blocks read the lengths, each at its own time
+    far = dict(c=A, n=A + 64, t=A + 128, free=A + 512, ci=A + 1024, co=A + 1024, sl=A + 2048, cu=A + 2560, pos=A + 4096, slots=A + 8192)
+    for kw in (dict(sl=far["c"]), dict(sl=far["n"]), dict(cu=far["c"]), dict(cu=far["n"])):
+        assert _plan(lib, **{**far, **kw}) == 1
+
+
 def test_tensor_calls_refuse_host_tensors_and_wrong_types():
     bf, i32 = torch.bfloat16, torch.int32
     cache = torch.zeros(4, 16, 2, 128, dtype=bf)
