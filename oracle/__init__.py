@@ -22,6 +22,8 @@ Functions and the passages they follow (page title, section):
 * ``bf16_causal_attention`` (O4): the BF16 twin (the pages give no BF16 numerics; plainest reading).
 * ``hadamard``: Hadamard rotation of Q and K before quantisation (spbcomputers.ru ZYFA article, FAQ
   "Что даёт поворот Адамара?"; captivela ZYFA article, "Angka Nyata").
+* ``paged``: page plan, rotary positions and single-token attention of the serving operators, float64 (no page describes
+  them; written from their formulas).
 """
 from .formats import (E4M3_MAX, bf16_bits_to_float, bf16_round, e4m3_decode,  # noqa: F401
                       e4m3_encode_rne_satfinite, fl32)
