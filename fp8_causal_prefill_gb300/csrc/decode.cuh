@@ -34,9 +34,10 @@
 // cores busy for 0.19 of the time); 64 ragged requests in bf16 46 us (5.5 TB/s), 9 requests of 16 heads of 192/128 e4m3 channels
 // 59 us (6.0 TB/s).  The rest is the start (lengths, then pages, then tiles: three trips to memory) and the join, 6 to 8 us
 // together, which is also what a short context takes: 256 tokens 6 us, one request of 32768 tokens 18 us.
-// With 16 query heads per KV head a byte meets twice the arithmetic and widening V takes as long as its load: 4.0 TB/s
-// in e4m3, 5.8 in bf16.  Two column groups that share the fragments of K and V take 168 registers a thread, and with a
-// third fewer warps the same time (48.7 to 47.6 us, 32 heads 37 to 41), so chunks of 8 heads have a warp each.
+// With 16 query heads per KV head a byte meets twice the arithmetic and widening V takes as long as its load: 4.1 TB/s
+// in e4m3, 5.8 in bf16.  (ldmatrix transposes bytes, so widening is one conversion per two values; with pairs of bytes and a
+// permutation before it, 48.4 us instead of 45.9.)  Two column groups that share the fragments of K and V take 168 registers a
+// thread, and with a third fewer warps the same time (48.7 to 47.6 us, 32 heads 37 to 41): chunks of 8 heads have a warp each.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -138,6 +139,13 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two 16 x 16 matrices of bytes, transposed: lane 4r + c gets bytes 4c .. 4c + 3 of columns r (r[0], r[2]) and r + 8 (r[1], r[3]).
+__device__ __forceinline__ void ldsm2t_bytes(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
@@ -286,6 +294,20 @@ __device__ __forceinline__ void page_of(const DecodeArgs& a, int t, int* p, int*
   *off = t - *p * a.cache.page_size;
 }
 
+// The order of a block of 16 keys in the products.  e4m3: byte e of the register that lane 4r + c gets of V is the key whose row
+// lane 4c + e gave the address of, and its halves are keys 2c, 2c + 1 and 2c + 8, 2c + 9 of the contraction, whose weights come from those
+// rows of the scores.  Rows 8 to 15 of the scores are keys 12 to 15, 8 to 11, so that neither K's reads nor V's meet rows of the same
+// remainder by 8, which lie in the same banks.
+template <bool FP8>
+__device__ __forceinline__ int key_row(int r) {  // the key in row r of the scores
+  return FP8 && r >= 8 ? r ^ 4 : r;
+}
+template <bool FP8>
+__device__ __forceinline__ int value_row(int lane) {  // the key whose row of V a lane gives the address of
+  const int c = lane >> 2 & 3, e = lane & 3;
+  return FP8 ? key_row<true>(2 * c + (e & 1) + (e >> 1) * 8) : (lane >> 4) * 8 + (lane & 7);
+}
+
 // ------------------------------------------------------------------------------------------------
 // the state of a compute warp: up to 8 query heads against its tiles
 
@@ -349,7 +371,7 @@ struct Rows {
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          if (!((mask >> (kb * 16 + j * 8 + (lane >> 2))) & 1)) x[kb][j] = {-INFINITY, -INFINITY};
+          if (!((mask >> (kb * 16 + key_row<FP8>(j * 8 + (lane >> 2)))) & 1)) x[kb][j] = {-INFINITY, -INFINITY};
       clear();
     }
     // The reference m moves only when a key exceeds it: log2 of a weight is then above the lift.  (Before a part's first key
@@ -406,17 +428,11 @@ struct Rows {
       if constexpr (FP8) {
 #pragma unroll
         for (int i = 0; i < kMTiles; i += 2) {
-          // a register holds channels 2r, 2r+1 of two keys: the even channel is row r, the odd one row r + 8
-          uint32_t r[4], v[8];
-          ldsm4t(vr.at(vs, kb, i), r);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t q = __byte_perm(r[j], 0, 0x3120);
-            v[2 * j] = widen(q);
-            v[2 * j + 1] = widen_hi(q);
-          }
-          mma<kValueKind>(o[i], v[0], v[1], v[2], v[3], pf[kb][0], pf[kb][1]);
-          mma<kValueKind>(o[i + 1], v[4], v[5], v[6], v[7], pf[kb][0], pf[kb][1]);
+          // a register holds four keys of a channel, in the order of the contraction (see key_row)
+          uint32_t r[4];
+          ldsm2t_bytes(vr.at(vs, kb, i), r);
+          mma<kValueKind>(o[i], widen(r[0]), widen(r[1]), widen_hi(r[0]), widen_hi(r[1]), pf[kb][0], pf[kb][1]);
+          mma<kValueKind>(o[i + 1], widen(r[2]), widen(r[3]), widen_hi(r[2]), widen_hi(r[3]), pf[kb][0], pf[kb][1]);
         }
       } else {
 #pragma unroll
@@ -446,12 +462,8 @@ struct Rows {
 #pragma unroll
           for (int i = 0; i < kMTiles; ++i) {
             const float y0 = o[i][e] * f, y1 = o[i][e + 2] * f;
-            if constexpr (FP8) {
-              *reinterpret_cast<__nv_bfloat162*>(out + channel(i, g8)) = __floats2bfloat162_rn(y0, y1);
-            } else {
-              out[channel(i, g8)] = __float2bfloat16_rn(y0);
-              out[channel(i, g8) + 8] = __float2bfloat16_rn(y1);
-            }
+            out[i * 16 + g8] = __float2bfloat16_rn(y0);
+            out[i * 16 + g8 + 8] = __float2bfloat16_rn(y1);
           }
         } else if (m[e] != -INFINITY) {  // without a valid key the join does not read O
           put_o(part, e, f, g8);
@@ -504,8 +516,6 @@ struct Rows {
   }
 
  private:
-  // This lane's first channel of tile i (the other: the next one for e4m3, the 8th from it for bf16).
-  static __device__ __forceinline__ int channel(int i, int g8) { return i * 16 + (FP8 ? 2 : 1) * g8; }
   __device__ __forceinline__ float total(int e) const {
     float sum = l[e];
     sum += __shfl_xor_sync(0xffffffffu, sum, 4);
@@ -522,12 +532,8 @@ struct Rows {
   __device__ __forceinline__ void put_o(float* to, int e, float f, int g8) const {
 #pragma unroll
     for (int i = 0; i < kMTiles; ++i) {
-      if constexpr (FP8) {
-        *reinterpret_cast<float2*>(to + channel(i, g8)) = make_float2(o[i][e] * f, o[i][e + 2] * f);
-      } else {
-        to[channel(i, g8)] = o[i][e] * f;
-        to[channel(i, g8) + 8] = o[i][e + 2] * f;
-      }
+      to[i * 16 + g8] = o[i][e] * f;
+      to[i * 16 + g8 + 8] = o[i][e + 2] * f;
     }
   }
 };
@@ -536,11 +542,8 @@ struct Rows {
 template <bool FP8, int DQK, int DV, int KB>
 __device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head, int heads, int first_row, bool joint_k, bool joint_v,
                                             Reader<Tile<FP8, DQK, DV>::kRowK, KB>* k, Reader<Tile<FP8, DQK, DV>::kRowV, KB>* v) {
-  k->set(tokens_log2, head, heads, first_row, lane & 15, lane >> 4, joint_k);
-  if (FP8)
-    v->set(tokens_log2, head, heads, first_row, lane & 15, lane >> 4, joint_v);
-  else
-    v->set(tokens_log2, head, heads, first_row, (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, joint_v);
+  k->set(tokens_log2, head, heads, first_row, key_row<FP8>(lane & 15), lane >> 4, joint_k);
+  v->set(tokens_log2, head, heads, first_row, value_row<FP8>(lane), FP8 ? lane >> 4 : lane >> 3 & 1, joint_v);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -910,7 +913,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
             // whatever V holds behind the request's end is not a number to multiply by 0: its pieces as this warp reads them
 #pragma unroll
             for (int n = 0; n < KB; ++n) {
-              const int row = FP8 ? lane & 15 : (lane >> 4) * 8 + (lane & 7);
+              const int row = value_row<FP8>(lane);
               if (!((mask >> (n * 16 + row)) & 1))
 #pragma unroll
                 for (int p = 0; p < T::kRowV / 16; p += 2) ptx::st_shared_v4(vr.at(vt, n, p), 0, 0, 0, 0);
