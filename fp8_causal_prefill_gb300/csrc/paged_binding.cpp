@@ -169,9 +169,10 @@ PyObject* keep(PyObject* o) {
   return o;
 }
 
-// plan(cached_lens, new_lens, block_table, free_pages, cursor, page_size, max_tokens, out or None) -> the five results
+// plan(cached_lens, new_lens, block_table, free_pages, cursor, page_size, max_tokens, out or None, result's tuple type) -> the five results
 PyObject* plan(PyObject* const* a, Py_ssize_t n) {
-  count(n, 8);
+  count(n, 9);
+  NEED_TYPE(PyType_Check(a[8]) && PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[8]), &PyTuple_Type), "expected a tuple type");
   const Tensor &cached = tensor(a[0], "cached_lens"), &fresh_lens = tensor(a[1], "new_lens"), &pool = tensor(a[3], "free_pages"),
                &cursor = tensor(a[4], "cursor");
   const int dev = cuda_index(cached);
@@ -188,7 +189,6 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
   NEED_VALUE(pool.size(0) < (1ll << 31), "too many free pages");
   int* at_ = static_cast<int*>(exact(cursor, "cursor", at::kInt, dev, {1}));
   const int64_t sizes[5] = {B, B + 1, rows, rows, 1};
-  PyObject* out[5] = {};
   void* o[5];
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   std::optional<Tensor> made[5];
@@ -218,8 +218,18 @@ PyObject* plan(PyObject* const* a, Py_ssize_t n) {
                           static_cast<long long*>(o[3]), static_cast<int>(rows), stream_of(dev)),
           "zyfa_paged_plan");
   if (a[7] != Py_None) return keep(a[7]);
-  for (int i = 0; i < 5; ++i) out[i] = THPVariable_Wrap(std::move(*made[i]));
-  return pack({out[0], out[1], out[2], out[3], out[4]});
+  PyTypeObject* type = reinterpret_cast<PyTypeObject*>(a[8]);
+  PyObject* out = type->tp_alloc(type, 5);
+  if (!out) throw python_error();
+  for (int i = 0; i < 5; ++i) {
+    PyObject* x = THPVariable_Wrap(std::move(*made[i]));
+    if (!x) {
+      Py_DECREF(out);
+      throw python_error();
+    }
+    PyTuple_SET_ITEM(out, i, x);
+  }
+  return out;
 }
 
 // A bf16 [N, heads, D] tensor with dense heads: its token stride.

@@ -59,8 +59,7 @@ def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     ``out`` gives the result's tensors (for captured graphs); ``out.cursor`` may be ``cursor`` itself.  Without it they
     are made in one allocation.
     """
-    r = (_native or _load()).plan(cached_lens, new_lens, block_table, free_pages, cursor, page_size, max_tokens, out)
-    return r if out is not None else PagedPlan._make(r)
+    return (_native or _load()).plan(cached_lens, new_lens, block_table, free_pages, cursor, page_size, max_tokens, out, PagedPlan)
 
 
 class Rope:
