@@ -17,8 +17,8 @@
 //   as it is (m16n8k32, accumulated exactly to fp32); V is widened to fp16 in registers (exact) and multiplies P in
 //   fp16 lifted by 2^15, so that the weights keep 11 bits.
 // * Work is split over (request, key tile) evenly whatever the lengths: the tiles of all requests are numbered one after
-//   the other and each group of blocks (one block per chunk of heads) takes an equal run of them.  A block finds its run
-//   from seq_lens on the device, so the host never needs the lengths.
+//   the other, with a gap behind each request for what its end costs, and each group of blocks (one block per chunk of heads) takes an
+//   equal run of the numbers.  A block finds its run from seq_lens on the device, so the host never needs the lengths.
 // * A request that lies in one group's run is written directly; otherwise each group leaves (m, l, O) of its
 //   part in the workspace and a second kernel joins the parts in group order.
 // * The join is launched while the first kernel still runs and waits for it on the device (programmatic dependent
@@ -32,7 +32,7 @@
 // Measured, with the bytes of the caches over the time, against 6.78 TB/s of a copy: 128 requests of 513 to 16384 tokens,
 // 8 KV heads of 128 e4m3 channels and 32 query heads, 178 us (6.8 TB/s; 0.86 of the DRAM's cycles, the tensor
 // cores busy for 0.19 of the time); 64 ragged requests in bf16 46 us (5.5 TB/s), 9 requests of 16 heads of 192/128 e4m3 channels
-// 59 us (6.0 TB/s).  The rest is the start (lengths, then pages, then tiles: three trips to memory) and the join, 6 to 8 us
+// 58 us (6.0 TB/s).  The rest is the start (lengths, then pages, then tiles: three trips to memory) and the join, 6 to 8 us
 // together, which is also what a short context takes: 256 tokens 6 us, one request of 32768 tokens 18 us.
 // With 16 query heads per KV head a byte meets twice the arithmetic and widening V takes as long as its load: 4.1 TB/s
 // in e4m3, 5.8 in bf16.  (ldmatrix transposes bytes, so widening is one conversion per two values; with pairs of bytes and a
@@ -85,10 +85,11 @@ struct DecodeArgs {
   int heads, chunk_warps, subs; // of a block: KV heads, chunks of each, token runs of a tile (warps = the product)
   int stages, tile_tokens;      // of a ring; tokens of a tile, subs * turns * keys of a warp's turn
   int turns;                    // of a warp at a tile
+  int tile_log2;                // of tile_tokens, a power of two
   int q_bytes;                  // of a block's queries in shared memory
   int box_log2;                 // tokens of a TMA box, at most a tile's
   int joint_k, joint_v;         // rows of 64 (or 192) bytes lie in shared memory in 128-byte columns across heads
-  unsigned* starts;  // [B + 2], for more than kFew requests: first tile of each, then the total, then the tiles per group
+  unsigned* starts;  // [B + 1], for more than kFew requests: number of each one's first tile, then the numbers of a run
   float2* ml;        // [groups][2][H]
   float* part;       // [groups][2][H][DV]
 };
@@ -284,8 +285,8 @@ struct Header {
   int valid;       // tokens of the request in the tile
   uint32_t boxes;  // boxes_kernel: those whose page is in the cache; rows_kernel: such rows
 };
-// first and last tile of a request's part; the part is the whole request; it begins the request; not every key is valid
-enum : int { kFirst = 1, kLast = 2, kDirect = 4, kSlot1 = 8, kPartial = 16 };
+// first and last tile of a request's part; the part is the whole request; it begins the request; not every key is valid; the run's last tile
+enum : int { kFirst = 1, kLast = 2, kDirect = 4, kSlot1 = 8, kPartial = 16, kEnd = 32 };
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) { return max(0, min(__ldg(a.seq_lens + b), a.max_len)); }
 
@@ -549,84 +550,111 @@ __device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head,
 // ------------------------------------------------------------------------------------------------
 // the schedule
 
-// The tiles (of `tokens` tokens) of all requests, and the run of group `g`: the request and the tile within it that it begins
-// with, for every thread that asks (`finds`; of one warp, the same g).  Counts fit 32 bits (the host has checked their sum).
-constexpr int kFew = 128;
+// The tiles (of a.tile_tokens tokens) of all requests are numbered one after the other, with a gap of kGap behind each request for what
+// its end costs; a group's run is an equal piece of the numbers.  find() gives the request and the tile within it that run `g` begins
+// with and the numbers from there to the run's end (0: the run has no tile), for every thread that asks (`finds`; of one
+// warp, the same g).  Numbers fit 32 bits (the host has checked their sum).
+//
+// The gap keeps a run of many short requests from being the last to end: 53 requests of 10 to 35,000 tokens (one KV head, bf16) 22.2
+// us without, 18.5 with a gap of 1, 18.1 with 2 (and 18.0 with 3); 42 requests with 14 query heads 30.0, 26.5, 25.4 (24.8).
+constexpr unsigned kGap = 2;
+// Up to kFew requests warps read all lengths themselves, else blocks do with barriers: 189 requests 20.0 us instead of 21.6.
+constexpr int kFew = 256;
 
 struct Schedule {
-  unsigned total = 0, per = 0;
+  unsigned total = 0, per = 0;  // numbers, and those of a run
 
-  // Up to kFew requests: every warp by itself, four requests a lane, without a barrier.  Returns the lane's first tile.
-  __device__ __forceinline__ unsigned scan_few(const DecodeArgs& a, unsigned (&n)[4]) {
+  static __device__ __forceinline__ unsigned tiles(const DecodeArgs& a, int b) {
+    return b < a.B ? (length_of(a, b) + a.tile_tokens - 1u) >> a.tile_log2 : 0u;
+  }
+  static __device__ __forceinline__ unsigned numbers(unsigned tiles) { return tiles ? tiles + kGap : 0; }
+  __device__ __forceinline__ void set(const DecodeArgs& a, unsigned sum) {
+    total = sum ? sum - kGap : 0;
+    per = (total + a.groups - 1) / a.groups;
+  }
+
+  // Up to 32 N requests: every warp by itself, N requests a lane, without a barrier.  Returns the lane's first number.
+  template <int N>
+  __device__ __forceinline__ unsigned scan_few(const DecodeArgs& a, unsigned (&n)[N]) {
     const int lane = threadIdx.x & 31;
-    const unsigned tokens = a.tile_tokens;
     unsigned sum = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n[i] = lane * 4 + i < a.B ? (length_of(a, lane * 4 + i) + tokens - 1u) / tokens : 0u;
+    for (int i = 0; i < N; ++i) n[i] = tiles(a, lane * N + i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += n[i];
+    for (int i = 0; i < N; ++i) sum += numbers(n[i]);
     unsigned incl = sum;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
       const unsigned o = __shfl_up_sync(0xffffffffu, incl, s);
       if (lane >= s) incl += o;
     }
-    total = __shfl_sync(0xffffffffu, incl, 31);
-    per = (total + a.groups - 1) / a.groups;
+    set(a, __shfl_sync(0xffffffffu, incl, 31));
     return incl - sum;
   }
-  __device__ __forceinline__ void find_few(const DecodeArgs& a, unsigned g, int* b, unsigned* tile) {
-    unsigned n[4], start = scan_few(a, n), at = 0, rest = 0;
+  template <int N>
+  __device__ __forceinline__ void find_few(const DecodeArgs& a, unsigned g, int* b, unsigned* tile, int* left) {
+    unsigned n[N], start = scan_few<N>(a, n), at = 0, number = 0, rest = 0;
     const unsigned first = g * per;
     bool here = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // the request among this lane's that holds tile `first`, if one does
-      if (first >= start && first < start + n[i]) {
-        at = (threadIdx.x & 31) * 4 + i;
-        rest = first - start;
+    for (int i = 0; i < N; ++i) {  // the first of this lane's requests that has a tile from number `first` on
+      if (!here && n[i] && start + n[i] > first) {
+        at = (threadIdx.x & 31) * N + i;
+        number = max(start, first);
+        rest = number - start;
         here = true;
       }
-      start += n[i];
+      start += numbers(n[i]);
     }
     const unsigned hit = __ballot_sync(0xffffffffu, here);
     const int l = hit ? __ffs(hit) - 1 : 0;
-    *b = hit ? static_cast<int>(__shfl_sync(0xffffffffu, at, l)) : -1;
+    *b = static_cast<int>(__shfl_sync(0xffffffffu, at, l));
     *tile = __shfl_sync(0xffffffffu, rest, l);
+    number = __shfl_sync(0xffffffffu, number, l);
+    *left = hit ? max(0, static_cast<int>(min(first + per, total) - number)) : 0;
   }
-  // First tile of request b and of the one after it.
+  // Numbers of request b's first tile and, were it one longer, of its next.
+  template <int N>
   __device__ __forceinline__ void bounds_few(const DecodeArgs& a, int b, unsigned* p0, unsigned* p1) {
-    unsigned n[4], start = scan_few(a, n), mine = start;
+    unsigned n[N], mine = scan_few<N>(a, n), len = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < (b & 3)) mine += n[i];
-    const unsigned len = (b & 3) == 0 ? n[0] : (b & 3) == 1 ? n[1] : (b & 3) == 2 ? n[2] : n[3];
-    *p0 = __shfl_sync(0xffffffffu, mine, b >> 2);
-    *p1 = *p0 + __shfl_sync(0xffffffffu, len, b >> 2);
+    for (int i = 0; i < N; ++i) {
+      if (i < b % N) mine += numbers(n[i]);
+      if (i == b % N) len = n[i];
+    }
+    *p0 = __shfl_sync(0xffffffffu, mine, b / N);
+    *p1 = *p0 + __shfl_sync(0xffffffffu, len, b / N);
+  }
+  __device__ __forceinline__ void bounds(const DecodeArgs& a, int b, unsigned* p0, unsigned* p1) {
+    if (a.B <= 32) return bounds_few<1>(a, b, p0, p1);
+    if (a.B <= 128) return bounds_few<4>(a, b, p0, p1);
+    bounds_few<8>(a, b, p0, p1);
   }
 
   // Any number, the whole block: prefix: [blockDim.x] and sums: [33] in shared memory.  Leaves a.starts for the join.
   __device__ __forceinline__ void find(const DecodeArgs& a, unsigned* prefix, unsigned* sums, bool finds, unsigned g, int* b,
-                                       unsigned* tile) {
-    if (a.B <= kFew) return find_few(a, g, b, tile);
-    const unsigned tokens = a.tile_tokens;
+                                       unsigned* tile, int* left) {
+    // (code that a case does not need costs it: four requests a lane for all made short batches 0.2 us slower, eight 0.5)
+    if (a.B <= 32) return find_few<1>(a, g, b, tile, left);
+    if (a.B <= 128) return find_few<4>(a, g, b, tile, left);
+    if (a.B <= kFew) return find_few<8>(a, g, b, tile, left);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_threads = blockDim.x, warps = n_threads >> 5;
-    const bool one_pass = a.B <= n_threads;
-    auto tiles = [&](int r) { return r < a.B ? (length_of(a, r) + tokens - 1u) / tokens : 0u; };
-    if (!one_pass) {
-      unsigned t = 0;
-      for (int r = tid; r < a.B; r += n_threads) t += tiles(r);
-      t = __reduce_add_sync(0xffffffffu, t);
-      if (lane == 0) sums[warp] = t;
-      __syncthreads();
-      total = 0;
-      for (int i = 0; i < warps; ++i) total += sums[i];
-      __syncthreads();
-    }
+    unsigned sum = 0;
+    for (int r = tid; r < a.B; r += n_threads) sum += numbers(tiles(a, r));
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int i = 0; i < warps; ++i) sum += sums[i];
+    set(a, sum);
+    __syncthreads();
+    const unsigned first = g * per;
     unsigned before = 0;
     *b = -1;
     *tile = 0;
+    *left = 0;
     for (int b0 = 0; b0 < a.B; b0 += n_threads) {
-      const unsigned n = tiles(b0 + tid);
+      const unsigned n = numbers(tiles(a, b0 + tid));
       unsigned incl = n;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
@@ -635,19 +663,16 @@ struct Schedule {
       }
       if (lane == 31) sums[warp] = incl;
       __syncthreads();
-      unsigned sum = 0, mine = 0;
+      unsigned all = 0, mine = 0;
       for (int i = 0; i < warps; ++i) {
-        if (i == warp) mine = sum;
-        sum += sums[i];
+        if (i == warp) mine = all;
+        all += sums[i];
       }
       const unsigned start = before + mine + incl - n;
       prefix[tid] = start;
       if (blockIdx.x == 0 && b0 + tid < a.B) a.starts[b0 + tid] = start;
-      if (one_pass) total = sum;
-      per = (total + a.groups - 1) / a.groups;
       __syncthreads();
-      const unsigned first = g * per;
-      if (finds && *b < 0 && first < total && first < before + sum) {
+      if (finds && *b < 0 && first < total && first < before + all) {
         int lo = 0, hi = min(n_threads, a.B - b0);  // prefix[lo] <= first, and the last such: requests without tiles are passed
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
@@ -655,33 +680,41 @@ struct Schedule {
         }
         *b = b0 + lo;
         *tile = first - prefix[lo];
+        unsigned number = first;
+        const unsigned own = tiles(a, *b);
+        if (*tile >= own) {  // in the gap behind it: on to the next (there is one: the last request's gap is not counted)
+          number += own + kGap - *tile;
+          *tile = 0;
+          do ++*b;
+          while (*b + 1 < a.B && tiles(a, *b) == 0);
+        }
+        *left = max(0, static_cast<int>(min(first + per, total) - number));
       }
-      before += sum;
-      if (!one_pass) __syncthreads();
+      before += all;
+      __syncthreads();
     }
-    if (blockIdx.x == 0 && tid == 0) {
-      a.starts[a.B] = total;
-      a.starts[a.B + 1] = per;
-    }
+    if (blockIdx.x == 0 && tid == 0) a.starts[a.B] = per;
   }
 };
 
-// Where the load side of a ring is: the next tile, and what has been loaded about it ahead of its turn.
+// Where the load side of a ring is: the next tile.
 struct Cursor {
-  int b, len, t, left;     // request, its length, first token of the next tile, tiles left in the run
+  int b, len, t, left;     // request, its length, first token of the next tile, numbers from there to the run's end
   bool first, from_start;  // the tile begins a part; the part begins its request
-  __device__ __forceinline__ void start(const DecodeArgs& a, int b_, unsigned tile, unsigned left_, int tokens) {
+  __device__ __forceinline__ void start(const DecodeArgs& a, int b_, unsigned tile, int left_) {
     b = b_;
-    t = static_cast<int>(tile) * tokens;
-    left = static_cast<int>(left_);
-    len = left > 0 ? length_of(a, b) : 0;
+    t = static_cast<int>(tile) * a.tile_tokens;
+    left = left_;
+    len = length_of(a, b);
     first = true;
     from_start = t == 0;
   }
+  __device__ __forceinline__ bool ends(int tokens) const { return t + tokens >= len; }  // this tile, its request
+  __device__ __forceinline__ int left_after(int tokens) const { return left - 1 - (ends(tokens) ? static_cast<int>(kGap) : 0); }
   __device__ __forceinline__ int flags(int tokens) const {
-    const bool ends = t + tokens >= len;
-    const bool last = ends || left == 1;
-    return (first ? kFirst : 0) | (last ? kLast | (from_start && ends ? kDirect : 0) | (from_start ? kSlot1 : 0) : 0);
+    const bool end = ends(tokens), last = end || left == 1;
+    return (first ? kFirst : 0) | (last ? kLast | (from_start && end ? kDirect : 0) | (from_start ? kSlot1 : 0) : 0) |
+           (left_after(tokens) <= 0 ? kEnd : 0);
   }
   // to the next tile of the run, which has one
   __device__ __forceinline__ void advance(const DecodeArgs& a, int tokens) {
@@ -746,16 +779,14 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   const int unit = blockIdx.x % a.units, chunk_units = (a.chunks + a.chunk_warps - 1) / a.chunk_warps;
   const int head0 = unit / chunk_units * a.heads, chunk0 = unit % chunk_units * a.chunk_warps;
   Schedule plan;
-  int b;
+  int b, left;
   unsigned tile0;
-  plan.find(a, s_prefix, s_sums, warp == warps, g, &b, &tile0);
-  const unsigned run = g * plan.per;
-  if (g >= static_cast<unsigned>(a.groups) || run >= plan.total) return;
-  const int tiles = static_cast<int>(min(plan.per, plan.total - run));
+  plan.find(a, s_prefix, s_sums, true, g, &b, &tile0, &left);
+  if (left == 0) return;
 
   if (warp == warps) {
     Cursor c;
-    c.start(a, b, tile0, tiles, TT);
+    c.start(a, b, tile0, left);
     const int box = 1 << a.box_log2, row = lane << a.box_log2;  // this lane's box of a tile: its first token
     // the block's query rows: whole heads, or (more chunks than warps) part of one head's
     const int q0 = head0 * a.group + chunk0 * a.chunk_heads;
@@ -789,7 +820,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     auto look_ahead = [&](bool new_request) {
       if (new_request) {
         next_len = 0;
-        if ((c.len - c.t + TT - 1) / TT < c.left)  // the run goes on behind this request
+        if (((c.len - c.t + TT - 1) >> a.tile_log2) + static_cast<int>(kGap) < c.left)  // the run goes on behind this request
           for (next_b = c.b + 1; next_b < a.B && next_len == 0; ++next_b) next_len = length_of(a, next_b);
         --next_b;
         if (next_len > 0) desc_next = descales(next_b);
@@ -800,7 +831,8 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     bool bad = false;
     int stage = 0;
     uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
-    for (int i = 0; i < tiles; ++i) {
+    bool begun = false;
+    while (true) {
       if (!mbar_wait_bounded(empty_s + 8 * stage, parity)) {
         if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
         break;
@@ -829,11 +861,15 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
         if (c.first) bulk_load(query_s + stage * a.q_bytes, a.q + c.b * a.q_batch + static_cast<long long>(q0) * T::kRowK, q_bytes, bar);
         ptx::mbar_arrive_expect_tx(bar, (__popc(boxes) << a.box_log2) * a.heads * T::kKeyBytes + q_bytes);
       }
-      if (i == 0) look_ahead(true);
-      if (--c.left > 0) {
+      if (!begun) look_ahead(true);
+      begun = true;
+      const bool ended = c.ends(TT);
+      c.left = c.left_after(TT);
+      if (c.left <= 0) break;
+      {
         c.first = false;
         c.t += TT;
-        if (c.t >= c.len) {
+        if (ended) {
           c.b = next_b;
           c.len = next_len;
           c.t = 0;
@@ -874,8 +910,8 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   const uint32_t meet_s = smem_addr(s_meet + peer);
   uint32_t meet_parity = 0;
   // Copies still in flight write to this block's shared memory: waits for them, again for a bounded time.
-  auto give_up = [&](int tile, int st, uint32_t par) {
-    for (int j = 1; j < S && tile + j < tiles; ++j) {
+  auto give_up = [&](int st, uint32_t par) {
+    for (int j = 1; j < S; ++j) {
       if (++st == S) {
         st = 0;
         par ^= 1;
@@ -887,9 +923,9 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   Rows<FP8, DQK, DV> rows;
   int stage = 0;
   uint32_t parity = 0;
-  for (int i = 0; i < tiles; ++i) {
+  while (true) {
     if (!mbar_wait_bounded(full_s + 8 * stage, parity)) {
-      give_up(i, stage, parity);
+      give_up(stage, parity);
       return;
     }
     const Header h = s_header[stage];
@@ -936,12 +972,13 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
             return ok;
           });
           if (!met) {
-            give_up(i, stage, parity);
+            give_up(stage, parity);
             return;
           }
         }
       }
     }
+    if (h.flags & kEnd) return;
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(empty_s + 8 * stage);
     if (++stage == S) {
@@ -973,12 +1010,10 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
   let_successor_start();
   const unsigned w = warp * gridDim.x + blockIdx.x, g = w / a.units;  // few workers are spread over the blocks
   Schedule plan;
-  int b;
+  int b, left;
   unsigned tile0;
-  plan.find(a, s_prefix, s_sums, g < static_cast<unsigned>(a.groups), g, &b, &tile0);
-  const unsigned run = g * plan.per;
-  if (g >= static_cast<unsigned>(a.groups) || run >= plan.total) return;
-  const int tiles = static_cast<int>(min(plan.per, plan.total - run));
+  plan.find(a, s_prefix, s_sums, g < static_cast<unsigned>(a.groups), g, &b, &tile0, &left);
+  if (g >= static_cast<unsigned>(a.groups) || left == 0) return;
   const int unit = static_cast<int>(w % a.units), hk = unit / a.chunks, chunk = unit % a.chunks;
   const int q0 = hk * a.group + chunk * a.chunk_heads, nq = min(a.chunk_heads, a.group - chunk * a.chunk_heads);
   const uint8_t* kbase = a.cache.k + hk * a.cache.k_head;
@@ -987,7 +1022,7 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
   const uint32_t query_s = smem_addr(smem) + (blockDim.x >> 5) * S * T::kTileBytes + warp * S * a.q_bytes;
 
   Cursor c;
-  c.start(a, b, tile0, tiles, KT);
+  c.start(a, b, tile0, left);
   int pg, off;  // page and offset in it of token c.t + lane
   bool bad = false;
   auto look_up = [&]() {
@@ -1034,7 +1069,8 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
           s_scale[warp][stage] = scale;
         }
       }
-      if (--c.left > 0) {
+      c.left = c.left_after(KT);
+      if (c.left > 0) {
         c.advance(a, KT);
         look_up();
       }
@@ -1048,7 +1084,7 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
   Rows<FP8, DQK, DV> rows;
   for (int i = 0; i < S - 1; ++i) issue(i);
   int stage = 0;
-  for (int it = 0; it < tiles; ++it) {
+  while (true) {
     copy_wait<S - 2>();
     __syncwarp();  // this tile has landed, and every lane has read the one before it, whose stage is refilled
     issue(stage == 0 ? S - 1 : stage - 1);
@@ -1060,6 +1096,7 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
     else if (h.boxes)
       rows.template tile<false>(ks, vs, kr, vr, h.boxes, lane, []() {});  // rows that are not valid were filled with zeros
     if (h.flags & kLast) rows.finish(a, h.b, q0, nq, h.flags & kDirect, static_cast<long long>(g) * 2 + (h.flags & kSlot1 ? 1 : 0), lane);
+    if (h.flags & kEnd) break;
     stage = stage + 1 == S ? 0 : stage + 1;
   }
   copy_wait<0>();
@@ -1073,8 +1110,10 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
 // head): every W-th part each, 32 at a time.  A lane reads one part's maximum and sum while the rows of O come in, none of
 // which depends on another; then the warps meet in shared memory in a fixed order.  A block takes ROWS of them (W = 1), or VEC
 // * 32 of the channels of one.  Latency bounds it: 3 to 4 us after the first kernel's end.
+// The blocks an SM leave registers for BATCH rows on their way; with 64 a thread the compiler read them one after the other (20.7 us
+// instead of 18.0 for 32 rows of 228 parts).
 template <int DV, int W, int ROWS, int VEC, int BATCH>
-__global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(W * ROWS * 32, W == 16 ? 1 : W == 4 ? 7 : 3) join_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(W == 1 || ROWS == 1);
   constexpr int kThreads = W * 32, D = VEC * 32;
   struct alignas(VEC * 4) Vec {
@@ -1089,12 +1128,12 @@ __global__ void __launch_bounds__(W * ROWS * 32) join_kernel(const __grid_consta
   // what did had ended before that kernel let this one start.
   Schedule plan;
   unsigned p0, p1;
-  if (a.B <= kFew) plan.bounds_few(a, b, &p0, &p1);
+  if (a.B <= kFew) plan.bounds(a, b, &p0, &p1);
   wait_for_predecessor();
   if (a.B > kFew) {
     p0 = a.starts[b];
-    p1 = a.starts[b + 1];
-    plan.per = a.starts[a.B + 1];
+    p1 = p0 + Schedule::tiles(a, b);
+    plan.per = a.starts[a.B];
   }
   const unsigned per = plan.per;
   if (p0 == p1) {
@@ -1214,6 +1253,12 @@ bool prepare(K* kernel, int smem, int dev, std::atomic<int>* set) {
   return true;
 }
 
+inline int log2_of(int power) {
+  int n = 0;
+  while ((1 << n) < power) ++n;
+  return n;
+}
+
 // Fewest equal pieces of `n` that are at most `most`, as the size of a piece.
 inline int piece(int n, int most) { return (n + (n + most - 1) / most - 1) / ((n + most - 1) / most); }
 
@@ -1236,13 +1281,13 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   a.units = (c.H_kv + a.heads - 1) / a.heads * ((a.chunks + a.chunk_warps - 1) / a.chunk_warps);
   // Boxes: as many tokens of a page as divide both the page and the tile.  A broadcast (stride 0) or very large stride has no
   // tensor map, and a page of an odd size no boxes that fill the swizzle pattern (8 rows).
+  a.tile_log2 = log2_of(a.tile_tokens);
   int tokens = a.tile_tokens;
   while (tokens > 1 && c.page_size % tokens != 0) tokens /= 2;
   if (tokens < 8) return cudaSuccess;
   for (long long s : {c.k_page, c.k_tok, c.k_head, c.v_page, c.v_tok, c.v_head})
     if (s <= 0 || s >= (1ll << 40)) return cudaSuccess;
-  a.box_log2 = 0;
-  while ((1 << a.box_log2) < tokens) ++a.box_log2;
+  a.box_log2 = log2_of(tokens);
   auto joint = [&](int row, long long head) {
     return row % 128 != 0 && head == row && static_cast<long long>(c.H_kv) * row % 128 == 0 && a.heads * row % 128 == 0;
   };
@@ -1276,6 +1321,7 @@ cudaError_t launch_rows(DecodeArgs& a, int nsm, int dev, cudaStream_t stream) {
   using T = Tile<FP8, DQK, DV>;
   a.subs = 1;
   a.tile_tokens = T::kKeys;
+  a.tile_log2 = log2_of(T::kKeys);
   a.units = a.cache.H_kv * a.chunks;
   a.q_bytes = a.chunk_heads * T::kRowK;
   const int ring = kRowStages * (T::kTileBytes + a.q_bytes), most = std::min(kRowWarps<T::kKeyBytes>, (kSmemPerBlock - 8192) / ring);
@@ -1305,19 +1351,25 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   cudaError_t e = launch_boxes<FP8, DQK, DV>(a, &done, nsm, dev, stream);
   if (e == cudaSuccess && !done) e = launch_rows<FP8, DQK, DV>(a, nsm, dev, stream);
   if (e != cudaSuccess) return ZYFA_ERR_CUDA;
-  // Few rows have many parts each, and their channels are spread over blocks too; of many rows most lie in one or two groups.
-  const unsigned rows = static_cast<unsigned>(a.B) * a.H;
+  // Few rows have many parts each; a ragged batch may have most of its parts in a few rows, whatever their average.  So a row has as
+  // many warps as the GPU holds at once (53 ragged requests of 8 heads: 25.5 us with one, 22.2 with four; 6 requests of 12 heads
+  // 20.6 with four, 17.4 with 16; 32 rows 19.3 with whole rows, 18.0 with their channels spread), and of many rows, most of
+  // which lie in one or two groups, a warp takes one (32 short requests of 32 heads: 7.5 us, with four warps 8.4).
+  const unsigned rows = static_cast<unsigned>(a.B) * a.H, sms = static_cast<unsigned>(nsm);
   const long long parts_each = a.groups / a.B;
   constexpr int V = DV / 32;
-  static std::atomic<int> set[3][kMaxDevices];
-  if (rows * V <= 2u * nsm) {
-    if (!prepare(join_kernel<DV, 16, 1, 1, 20>, 1, dev, set[0])) return ZYFA_ERR_CUDA;
-    e = launch_dependent(join_kernel<DV, 16, 1, 1, 20>, dim3(rows, V), 512, 0, stream, a);
-  } else if (parts_each > 8) {
-    if (!prepare(join_kernel<DV, 4, 1, V, 8>, 1, dev, set[1])) return ZYFA_ERR_CUDA;
+  static std::atomic<int> set[4][kMaxDevices];
+  if (rows * V <= sms) {
+    if (!prepare(join_kernel<DV, 16, 1, 1, 16>, 1, dev, set[0])) return ZYFA_ERR_CUDA;
+    e = launch_dependent(join_kernel<DV, 16, 1, 1, 16>, dim3(rows, V), 512, 0, stream, a);
+  } else if (rows <= sms) {
+    if (!prepare(join_kernel<DV, 16, 1, V, 8>, 1, dev, set[1])) return ZYFA_ERR_CUDA;
+    e = launch_dependent(join_kernel<DV, 16, 1, V, 8>, dim3(rows), 512, 0, stream, a);
+  } else if (rows <= 4 * sms || (rows <= 8 * sms && parts_each > 4) || parts_each > 8) {
+    if (!prepare(join_kernel<DV, 4, 1, V, 8>, 1, dev, set[2])) return ZYFA_ERR_CUDA;
     e = launch_dependent(join_kernel<DV, 4, 1, V, 8>, dim3(rows), 128, 0, stream, a);
   } else {
-    if (!prepare(join_kernel<DV, 1, 8, V, 8>, 1, dev, set[2])) return ZYFA_ERR_CUDA;
+    if (!prepare(join_kernel<DV, 1, 8, V, 8>, 1, dev, set[3])) return ZYFA_ERR_CUDA;
     e = launch_dependent(join_kernel<DV, 1, 8, V, 8>, dim3((rows + 7) / 8), 256, 0, stream, a);
   }
   return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
