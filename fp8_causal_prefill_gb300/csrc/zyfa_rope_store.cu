@@ -12,7 +12,7 @@
 // their partners half the rotated width away, or 16 neighbours), eight rotations in packed fp32 pairs, one or two 8- or
 // 16-byte stores per half.  The next head's loads are in flight while one is computed.
 //
-// Measured: a prompt of 32768 tokens (32 query and 8 KV heads of 128, e4m3 cache and dense copies) 112 us, 6.0 TB/s read and
+// Measured: a prompt of 32768 tokens (32 query and 8 KV heads of 128, e4m3 cache and dense copies) 111 us, 6.0 TB/s read and
 // written (0.88 of a copy's rate; 0.71 of the DRAM's cycles); 4099 tokens with three axes in bf16 (16 and 4 heads of 64) 5.6 us
 // (4.5 TB/s); 1 token, or 128 of them with 16 heads of 192/128, 3.3 us: a launch and three trips to memory.
 #include <cuda_bf16.h>
@@ -25,7 +25,7 @@
 
 namespace {
 
-constexpr int kMaxTokens = 8;  // tokens per block at most
+constexpr int kMaxTokens = 32;  // tokens per block at most
 
 // A multiple of the 16-channel pieces of a key head and of a value head.
 template <int DQK>
@@ -204,10 +204,14 @@ __global__ void __launch_bounds__(kThreads<DQK>) store_kernel(const __grid_const
     s_krow[tid] = krow;
     s_vrow[tid] = vrow;
   }
-  for (int i = tid; i < here * half; i += kN) {
-    const int t = i / half, p = i - t * half;
-    const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
-    angle_sincos(turn_fraction(a.inv_freq[p]), a.positions[axis * a.pos_stride + n0 + t], &s_sin[t][p], &s_cos[t][p]);
+  if (half > 0) {  // a thread keeps its pair: kN / half tokens at a time
+    const int at_once = kN / half, t0 = tid / half, p = tid - t0 * half;
+    if (t0 < min(at_once, here)) {
+      const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
+      const int* position = a.positions + axis * a.pos_stride + n0;
+      const uint64_t fraction = turn_fraction(a.inv_freq[p]);
+      for (int t = t0; t < here; t += at_once) angle_sincos(fraction, position[t], &s_sin[t][p], &s_cos[t][p]);
+    }
   }
   __syncthreads();
   const bool per_head = a.desc_per_head;
@@ -365,11 +369,14 @@ extern "C" zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, con
   a.desc_per_head = descale_per_kv_head;
   a.N = N;
   a.H = H;
-  // Several tokens per block share its start-up (its tables, 1 to 2 us of latency): as many as leave each of the four blocks
-  // that fit an SM one, at most 8.  32768 tokens (FP8, 32 + 8 heads of 128): 157.7 us with 2, 115.5 with 4, 112.7 with 8;
-  // 2048 tokens: 11.7 us with 4, 14.1 with 8 (half the SMs' slots).
-  const long long slots_gpu = 4ll * zyfa::device_sm_count(dev);
-  a.tokens = static_cast<int>(std::min<long long>(kMaxTokens, std::max(1ll, (N + slots_gpu - 1) / std::max(1ll, slots_gpu))));
+  // Several tokens per block share its start-up (its tables, 1 to 2 us of latency), few heads more than many; then as many as fill
+  // whole waves of the blocks that the GPU holds (4 an SM of 256 threads, 6 of 192).  At most 8, 12 and 16 tokens, waves filled: 112.1,
+  // 111.1 and 111.3 us for 32768 tokens (FP8, 32 + 8 heads of 128), 21.8, 20.0 and 17.0 for 19164 with 4 + 2 heads, 15.2 with 32;
+  // 5031 tokens of 32 + 8 heads of 64 as 629 blocks of 8, a wave and a bit, 15.3 us, as 559 of 9 12.6.
+  const long long slots_gpu = (D_qk == 192 ? 6ll : 4ll) * std::max(1, zyfa::device_sm_count(dev));
+  const long long most = std::min(kMaxTokens, std::max(12, 320 / (H + 2 * H_kv)));
+  const long long waves = (N + most * slots_gpu - 1) / (most * slots_gpu);
+  a.tokens = static_cast<int>((N + slots_gpu * waves - 1) / (slots_gpu * waves));
   const bool il = rope && rope->interleaved;
   cudaError_t e;
   if (fp8)

@@ -202,6 +202,15 @@ def test_store_shapes(kind, shape, interleaved):
     _store_case(kind, shape, 1, 1, 1, interleaved=interleaved, rot=16, offset=16, seed=4, page=1)
 
 
+@pytest.mark.parametrize("shape", ["64", "128", "mla"])
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_store_many_tokens(kind, shape):
+    # several tokens per block, up to 32 where heads are few; the last block has fewer, and pairs do not divide the threads
+    _store_case(kind, shape, 3001, 5, 1, pad=7, seed=13, pairs=[8, 16], rot=48, offset=8)
+    _store_case(kind, shape, 9001, 2, 2, pad=100, seed=14, interleaved=True, dense=True, strided=True)
+    _store_case(kind, shape, 20011, 1, 1, pad=3, seed=15, rot=64)
+
+
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
 @pytest.mark.parametrize("pairs", [[16, 24, 24], [0, 64], [1, 2, 3, 58], [64, 0, 0]])
 def test_store_axes(kind, pairs):
