@@ -20,7 +20,8 @@
 //   the other, with a gap behind each request for what its end costs, and each group of blocks (one block per chunk of heads) takes an
 //   equal run of the numbers.  A block finds its run from seq_lens on the device, so the host never needs the lengths.
 // * A request that lies in one group's run is written directly; otherwise each group leaves (m, l, O) of its
-//   part in the workspace and a second kernel joins the parts in group order.
+//   part in the workspace and a second kernel joins the parts in group order.  Where the table has room for a few tiles only, a
+//   group is a request, and there is no second kernel.
 // * The join is launched while the first kernel still runs and waits for it on the device (programmatic dependent
 //   launch), which hides its launch.
 //
@@ -80,6 +81,7 @@ struct DecodeArgs {
   uint32_t page_magic;  // floor(t / page_size) = t * page_magic >> page_shift for t < 2^30
   int page_shift;
   // schedule and workspace
+  int whole;                    // a group is a request; no join
   int groups, units;            // `units` blocks (boxes_kernel) or warps (rows_kernel) make a group
   int chunks, chunk_heads;      // the query heads of a KV head are cut into chunks of at most chunk_heads
   int heads, chunk_warps, subs; // of a block: KV heads, chunks of each, token runs of a tile (warps = the product)
@@ -742,6 +744,9 @@ template <int KEY_BYTES>
 constexpr int kBoxWarps = KEY_BYTES <= 320 ? 4 : 2;
 // Tiles of a ring: the same 189 and 48 us with two, 179 and 46 with three, 187 and 49 with four.
 constexpr int kMaxStages = 3, kMaxHeads = 8;
+// A lone block takes 0.6 us a tile, the join 3 us.  With 4: 32 requests of 64 tokens (32 query heads, e4m3) 6.0 us instead of 7.9, one 5.5
+// instead of 6.5, eight (16 heads, bf16) 5.7 instead of 7.0; with 8 also one of 128 tokens 8.1 instead of 6.8.
+constexpr int kSerial = 4;
 
 template <bool FP8, int DQK, int DV>
 __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1) * 32, 3)
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   }
   __syncthreads();
   wait_for_predecessor();
-  let_successor_start();
+  if (!a.whole) let_successor_start();  // to the join
 
   // this block: group g, KV heads from head0, chunks of query heads from chunk0
   const unsigned g = blockIdx.x / a.units;
@@ -781,16 +786,34 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   Schedule plan;
   int b, left;
   unsigned tile0;
-  plan.find(a, s_prefix, s_sums, true, g, &b, &tile0, &left);
-  if (left == 0) return;
+  if (a.whole) {
+    b = static_cast<int>(g);
+    tile0 = 0;
+    left = static_cast<int>(Schedule::tiles(a, b));
+  } else {
+    plan.find(a, s_prefix, s_sums, true, g, &b, &tile0, &left);
+  }
+  // a compute warp: a run of keys, a KV head, a chunk of its query heads
+  const int head = warp % a.heads, chunk = chunk0 + warp / a.heads % a.chunk_warps, sub = warp / (a.heads * a.chunk_warps);
+  const int hk = head0 + head, q0 = hk * a.group + chunk * a.chunk_heads, nq = min(a.chunk_heads, a.group - chunk * a.chunk_heads);
+  const bool idle = hk >= a.cache.H_kv || nq <= 0;  // the last block of a group may have heads or chunks too many
+  if (left == 0) {
+    if (a.whole && sub == 0 && !idle) {  // a request without tokens (the warp that loads has a larger sub)
+      const long long row = static_cast<long long>(b) * a.H + q0;
+      for (int i = lane; i < nq * DV / 2; i += 32) reinterpret_cast<__nv_bfloat162*>(a.out + row * DV)[i] = __floats2bfloat162_rn(0.0f, 0.0f);
+      if (a.lse)
+        for (int i = lane; i < nq; i += 32) a.lse[row + i] = -INFINITY;
+    }
+    return;
+  }
 
   if (warp == warps) {
     Cursor c;
     c.start(a, b, tile0, left);
     const int box = 1 << a.box_log2, row = lane << a.box_log2;  // this lane's box of a tile: its first token
     // the block's query rows: whole heads, or (more chunks than warps) part of one head's
-    const int q0 = head0 * a.group + chunk0 * a.chunk_heads;
-    const int nq = chunk_units > 1 ? min(a.chunk_warps * a.chunk_heads, a.group - chunk0 * a.chunk_heads)
+    const int first_q = head0 * a.group + chunk0 * a.chunk_heads;
+    const int queries = chunk_units > 1 ? min(a.chunk_warps * a.chunk_heads, a.group - chunk0 * a.chunk_heads)
                                    : min(a.heads, a.cache.H_kv - head0) * a.group;
     // The pages of 32 boxes of the request at a time (a tile's boxes are among one such 32), the next 32, or the first ones of
     // the next request, being read meanwhile; likewise (lane: a head) the next request's descales.
@@ -857,8 +880,8 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       if (lane == 0) {
         const bool whole = valid == TT && boxes == 0xffffffffu >> (32 - (TT >> a.box_log2));
         s_header[stage] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, boxes};
-        const uint32_t q_bytes = c.first ? nq * T::kRowK : 0;
-        if (c.first) bulk_load(query_s + stage * a.q_bytes, a.q + c.b * a.q_batch + static_cast<long long>(q0) * T::kRowK, q_bytes, bar);
+        const uint32_t q_bytes = c.first ? queries * T::kRowK : 0;
+        if (c.first) bulk_load(query_s + stage * a.q_bytes, a.q + c.b * a.q_batch + static_cast<long long>(first_q) * T::kRowK, q_bytes, bar);
         ptx::mbar_arrive_expect_tx(bar, (__popc(boxes) << a.box_log2) * a.heads * T::kKeyBytes + q_bytes);
       }
       if (!begun) look_ahead(true);
@@ -891,10 +914,6 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     return;
   }
 
-  // this warp: a run of keys, a KV head, a chunk of its query heads
-  const int head = warp % a.heads, chunk = chunk0 + warp / a.heads % a.chunk_warps, sub = warp / (a.heads * a.chunk_warps);
-  const int hk = head0 + head, q0 = hk * a.group + chunk * a.chunk_heads, nq = min(a.chunk_heads, a.group - chunk * a.chunk_heads);
-  const bool idle = hk >= a.cache.H_kv || nq <= 0;  // the last block of a group may have heads or chunks too many
   Reader<T::kRowK, KB> kr;
   Reader<T::kRowV, KB> vr;
   const int run_keys = a.turns * KT;
@@ -1308,7 +1327,12 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   while (blocks > 1 && blocks * (2 * stage + meeting + kStatic) > kSmemPerSm) --blocks;
   a.stages = std::min(kMaxStages, (std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) - meeting) / stage);
   if (a.stages < 2) return cudaSuccess;
-  a.groups = static_cast<int>(std::max(1ll, std::min<long long>(static_cast<long long>(nsm) * blocks / a.units, tiles_at_most(a.B, a.max_len, a.tile_tokens))));
+  // Runs that are equal whatever the lengths, and a join; or, where that is at most kSerial tiles behind the equal split for the
+  // longest lengths that the table has room for, a request a group, and no join.
+  const long long most = std::max(1ll, (a.max_len + a.tile_tokens - 1ll) / a.tile_tokens), at_once = std::max(1ll, static_cast<long long>(nsm) * blocks / a.units);
+  const long long turns_whole = (a.B + at_once - 1) / at_once * most, turns_split = (a.B * most + at_once - 1) / at_once;
+  a.whole = turns_whole - turns_split <= kSerial;
+  a.groups = static_cast<int>(a.whole ? a.B : std::min(at_once, a.B * most));
   static std::atomic<int> set[kMaxDevices];
   if (!prepare(boxes_kernel<FP8, DQK, DV>, 2, dev, set)) return cudaErrorUnknown;
   *done = true;
@@ -1351,6 +1375,7 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   cudaError_t e = launch_boxes<FP8, DQK, DV>(a, &done, nsm, dev, stream);
   if (e == cudaSuccess && !done) e = launch_rows<FP8, DQK, DV>(a, nsm, dev, stream);
   if (e != cudaSuccess) return ZYFA_ERR_CUDA;
+  if (a.whole) return ZYFA_OK;
   // Few rows have many parts each; a ragged batch may have most of its parts in a few rows, whatever their average.  So a row has as
   // many warps as the GPU holds at once (53 ragged requests of 8 heads: 25.5 us with one, 22.2 with four; 6 requests of 12 heads
   // 20.6 with four, 17.4 with 16; 32 rows 19.3 with whole rows, 18.0 with their channels spread), and of many rows, most of

@@ -342,7 +342,7 @@ zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v,
  * ZYFA_ERR_BAD_PAGE.  Cache rows behind a request's length do not matter, whatever they hold.
  * Scores and sums are held in fp32; the weights exp(s - max) are rounded to 16 bits before they
  * multiply V (fp16 for an e4m3 cache, whose values fp16 holds exactly, else bf16).  Bitwise reproducible
- * for identical inputs on one GPU model.  Two launches, asynchronous on `stream`; allocates nothing, no host
+ * for identical inputs on one GPU model.  One or two launches, asynchronous on `stream`; allocates nothing, no host
  * synchronisation.  A kernel that gives up on a copy (about a second) records ZYFA_ERR_TIMEOUT as the prefill does.
  */
 zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache,

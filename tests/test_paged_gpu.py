@@ -387,6 +387,20 @@ def test_decode_many_requests(kind, B, page):
 
 
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("shape", ["64", "128", "mla"])
+@pytest.mark.parametrize("B,H,H_kv", [(1, 8, 2), (7, 6, 3), (40, 20, 2), (300, 5, 5), (600, 2, 1)])
+def test_decode_small_tables(kind, shape, B, H, H_kv):
+    # tables that name few tokens, or many requests of one length: a request is one block's work
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 65, B)
+    lens[:: 5] = 0
+    lens[B // 2] = 64
+    _decode_case(kind, shape, lens.tolist(), H, H_kv, seed=B, page=16, width=4, per_head=True)
+    _decode_case(kind, shape, [0] * B, H, H_kv, seed=B, page=8, width=2)
+    _decode_case(kind, shape, [130] * min(B, 300), H, H_kv, seed=B + 1, page=32)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
 def test_decode_broadcast_cache(kind):
     # strides of 0: every KV head (every page) reads the same rows
     rng = np.random.default_rng(8)
