@@ -32,7 +32,7 @@
 //
 // Measured, with the bytes of the caches over the time, against 6.78 TB/s of a copy: 128 requests of 513 to 16384 tokens,
 // 8 KV heads of 128 e4m3 channels and 32 query heads, 178 us (6.8 TB/s; 0.86 of the DRAM's cycles, the tensor
-// cores busy for 0.19 of the time); 64 ragged requests in bf16 46 us (5.5 TB/s), 9 requests of 16 heads of 192/128 e4m3 channels
+// cores busy for 0.19 of the time); 64 ragged requests in bf16 45.5 us (5.6 TB/s), 9 requests of 16 heads of 192/128 e4m3 channels
 // 58 us (6.0 TB/s).  The rest is the start (lengths, then pages, then tiles: three trips to memory) and the join, 6 to 8 us
 // together, which is also what a short context takes: 256 tokens 6 us, one request of 32768 tokens 18 us.
 // With 16 query heads per KV head a byte meets twice the arithmetic and widening V takes as long as its load: 4.1 TB/s
