@@ -633,7 +633,7 @@ struct Schedule {
     bounds_few<8>(a, b, p0, p1);
   }
 
-  // Any number, the whole block: prefix: [blockDim.x] and sums: [33] in shared memory.  Leaves a.starts for the join.
+  // Any number, the whole block: prefix: [blockDim.x] and sums: [warps] in shared memory.  Leaves a.starts for the join.
   __device__ __forceinline__ void find(const DecodeArgs& a, unsigned* prefix, unsigned* sums, bool finds, unsigned g, int* b,
                                        unsigned* tile, int* left) {
     // (code that a case does not need costs it: four requests a lane for all made short batches 0.2 us slower, eight 0.5)
@@ -889,21 +889,19 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       const bool ended = c.ends(TT);
       c.left = c.left_after(TT);
       if (c.left <= 0) break;
-      {
-        c.first = false;
-        c.t += TT;
-        if (ended) {
-          c.b = next_b;
-          c.len = next_len;
-          c.t = 0;
-          c.first = c.from_start = true;
-          pg_now = pg_next;
-          desc = desc_next;
-          look_ahead(true);
-        } else if ((c.t >> a.box_log2 & 31) == 0) {
-          pg_now = pg_next;
-          look_ahead(false);
-        }
+      c.first = false;
+      c.t += TT;
+      if (ended) {
+        c.b = next_b;
+        c.len = next_len;
+        c.t = 0;
+        c.first = c.from_start = true;
+        pg_now = pg_next;
+        desc = desc_next;
+        look_ahead(true);
+      } else if ((c.t >> a.box_log2 & 31) == 0) {
+        pg_now = pg_next;
+        look_ahead(false);
       }
       if (++stage == S) {
         stage = 0;

@@ -31,7 +31,8 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
   if (static_cast<long long>(max_pages) * cache->page_size > (1ll << 30)) return ZYFA_ERR_UNSUPPORTED;
   if (B > 65536 || H > 65536 || static_cast<long long>(B) * H > (1ll << 24)) return ZYFA_ERR_UNSUPPORTED;
   if (q_batch_stride > (1ll << 40)) return ZYFA_ERR_UNSUPPORTED;
-  if (B * ((static_cast<long long>(max_pages) * cache->page_size + 15) / 16) > 0x7fffffffll) return ZYFA_ERR_UNSUPPORTED;
+  // the schedule numbers tiles, and a gap behind each request, in 31 bits
+  if (B * ((static_cast<long long>(max_pages) * cache->page_size + 15) / 16 + kGap) > 0x7fffffffll) return ZYFA_ERR_UNSUPPORTED;
   if (B == 0) return ZYFA_OK;
   if (!q || !out || !seq_lens || (max_pages > 0 && !block_table)) return ZYFA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || (q_batch_stride * es) % 16 != 0 || !aligned(out, 16) || !aligned(seq_lens, 4) ||

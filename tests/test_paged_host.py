@@ -60,6 +60,12 @@ def test_decode_refusals(lib, kw, expect):
     assert _decode(lib, _cache(), **kw) == expect
 
 
+def test_decode_refuses_more_tiles_than_its_schedule_numbers(lib):
+    # 65536 requests of 2^15 tiles: 2^31, and just below that with what lies between the requests
+    assert _decode(lib, _cache(), B=65536, mp=1 << 15, ts=1 << 15) == 2
+    assert _decode(lib, _cache(), B=65536, mp=(1 << 15) - 1, ts=1 << 15) == 2
+
+
 def test_decode_needs_a_cache(lib):
     assert _decode(lib, None) == 1
     assert _store(lib, None) == 1
