@@ -1376,18 +1376,21 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   if (a.whole) return ZYFA_OK;
   // Few rows have many parts each; a ragged batch may have most of its parts in a few rows, whatever their average.  So a row has as
   // many warps as the GPU holds at once (53 ragged requests of 8 heads: 25.5 us with one, 22.2 with four; 6 requests of 12 heads
-  // 20.6 with four, 17.4 with 16; 32 rows 19.3 with whole rows, 18.0 with their channels spread), and of many rows, most of
+  // 20.6 with four, 17.4 with 16; 5 of 64 heads 11.9 with four, 10.8 with eight; 32 rows 19.3 with whole rows, 18.0 with their channels spread), and of many rows, most of
   // which lie in one or two groups, a warp takes one (32 short requests of 32 heads: 7.5 us, with four warps 8.4).
   const unsigned rows = static_cast<unsigned>(a.B) * a.H, sms = static_cast<unsigned>(nsm);
   const long long parts_each = a.groups / a.B;
   constexpr int V = DV / 32;
-  static std::atomic<int> set[4][kMaxDevices];
+  static std::atomic<int> set[5][kMaxDevices];
   if (rows * V <= sms) {
     if (!prepare(join_kernel<DV, 16, 1, 1, 16>, 1, dev, set[0])) return ZYFA_ERR_CUDA;
     e = launch_dependent(join_kernel<DV, 16, 1, 1, 16>, dim3(rows, V), 512, 0, stream, a);
   } else if (rows <= sms) {
     if (!prepare(join_kernel<DV, 16, 1, V, 8>, 1, dev, set[1])) return ZYFA_ERR_CUDA;
     e = launch_dependent(join_kernel<DV, 16, 1, V, 8>, dim3(rows), 512, 0, stream, a);
+  } else if (rows <= 3 * sms && parts_each > 8) {
+    if (!prepare(join_kernel<DV, 8, 1, V, 8>, 1, dev, set[4])) return ZYFA_ERR_CUDA;
+    e = launch_dependent(join_kernel<DV, 8, 1, V, 8>, dim3(rows), 256, 0, stream, a);
   } else if (rows <= 4 * sms || (rows <= 8 * sms && parts_each > 4) || parts_each > 8) {
     if (!prepare(join_kernel<DV, 4, 1, V, 8>, 1, dev, set[2])) return ZYFA_ERR_CUDA;
     e = launch_dependent(join_kernel<DV, 4, 1, V, 8>, dim3(rows), 128, 0, stream, a);

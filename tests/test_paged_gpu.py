@@ -448,6 +448,8 @@ def test_decode_long_and_ragged(kind):
     _decode_case(kind, "128", [20001], 8, 1, seed=1)
     _decode_case(kind, "64", [1, 9000, 3, 4000, 0, 0, 17], 4, 2, page=32, seed=2)
     _decode_case(kind, "mla", [5000, 1], 4, 4, page=64, seed=3)
+    _decode_case(kind, "64", [6000, 40, 2500], 64, 16, page=32, seed=4)           # joins of 192 and 384 rows
+    _decode_case(kind, "128", [900, 3000, 5, 1200, 700, 800], 64, 4, seed=5)
 
 
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
