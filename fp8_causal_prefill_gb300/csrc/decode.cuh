@@ -91,7 +91,7 @@ struct DecodeArgs {
   int q_bytes;                  // of a block's queries in shared memory
   int box_log2;                 // tokens of a TMA box, at most a tile's
   int joint_k, joint_v;         // rows of 64 (or 192) bytes lie in shared memory in 128-byte columns across heads
-  unsigned* starts;  // [B + 1], for more than kFew requests: number of each one's first tile, then the numbers of a run
+  unsigned* starts;  // [B + 1], for more than kFewJoin requests: number of each one's first tile, then the numbers of a run
   float2* ml;        // [groups][2][H]
   float* part;       // [groups][2][H][DV]
 };
@@ -562,6 +562,9 @@ __device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head,
 constexpr unsigned kGap = 2;
 // Up to kFew requests warps read all lengths themselves, else blocks do with barriers: 189 requests 20.0 us instead of 21.6.
 constexpr int kFew = 256;
+// The join reads them up to kFewJoin, else what the first kernel left (256 requests of 32 heads, 100 tokens each: 21.0 us instead of
+// 23.2; from the first request on 0.3 us more for short batches).
+constexpr int kFewJoin = 128;
 
 struct Schedule {
   unsigned total = 0, per = 0;  // numbers, and those of a run
@@ -606,8 +609,10 @@ struct Schedule {
         rest = number - start;
         here = true;
       }
+      if (N * 32 > kFewJoin && blockIdx.x == 0 && threadIdx.x < 32 && threadIdx.x * N + i < a.B) a.starts[threadIdx.x * N + i] = start;
       start += numbers(n[i]);
     }
+    if (N * 32 > kFewJoin && blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.B] = per;
     const unsigned hit = __ballot_sync(0xffffffffu, here);
     const int l = hit ? __ffs(hit) - 1 : 0;
     *b = static_cast<int>(__shfl_sync(0xffffffffu, at, l));
@@ -629,8 +634,7 @@ struct Schedule {
   }
   __device__ __forceinline__ void bounds(const DecodeArgs& a, int b, unsigned* p0, unsigned* p1) {
     if (a.B <= 32) return bounds_few<1>(a, b, p0, p1);
-    if (a.B <= 128) return bounds_few<4>(a, b, p0, p1);
-    bounds_few<8>(a, b, p0, p1);
+    bounds_few<4>(a, b, p0, p1);
   }
 
   // Any number, the whole block: prefix: [blockDim.x] and sums: [warps] in shared memory.  Leaves a.starts for the join.
@@ -1141,13 +1145,13 @@ __global__ void __launch_bounds__(W * ROWS * 32, W == 16 ? 1 : W == 4 ? 7 : 3) j
   const long long row = static_cast<long long>(blockIdx.x) * ROWS + (ROWS > 1 ? warp : 0);
   if (row >= static_cast<long long>(a.B) * a.H) return;
   const int b = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H), w = ROWS > 1 ? 0 : warp, tid = w * 32 + lane;
-  // Up to kFew requests the bounds come from their lengths, read before the first kernel has ended: it does not write them, and
+  // Up to kFewJoin requests the bounds come from their lengths, read before the first kernel has ended: it does not write them, and
   // what did had ended before that kernel let this one start.
   Schedule plan;
   unsigned p0, p1;
-  if (a.B <= kFew) plan.bounds(a, b, &p0, &p1);
+  if (a.B <= kFewJoin) plan.bounds(a, b, &p0, &p1);
   wait_for_predecessor();
-  if (a.B > kFew) {
+  if (a.B > kFewJoin) {
     p0 = a.starts[b];
     p1 = p0 + Schedule::tiles(a, b);
     plan.per = a.starts[a.B];
