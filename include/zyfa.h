@@ -340,8 +340,8 @@ zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v,
  *
  * Tokens whose page lies outside [0, num_pages) are left out of the softmax and zyfa_check_errors() returns
  * ZYFA_ERR_BAD_PAGE.  Cache rows behind a request's length do not matter, whatever they hold.
- * Scores and sums are held in fp32; the weights exp(s - max) are rounded to 16 bits before they
- * multiply V (fp16 for an e4m3 cache, whose values fp16 holds exactly, else bf16).  Bitwise reproducible
+ * Scores and sums are held in fp32; before the weights exp(s - max) multiply V they are rounded to fp16 for an e4m3
+ * cache, whose values fp16 holds exactly, else to a sum of two bf16 numbers (16 bits).  Bitwise reproducible
  * for identical inputs on one GPU model.  One or two launches, asynchronous on `stream`; allocates nothing, no host
  * synchronisation.  A kernel that gives up on a copy (about a second) records ZYFA_ERR_TIMEOUT as the prefill does.
  */
