@@ -2,7 +2,8 @@
 //
 // One pass over the keys with the running maximum m and sum l of the softmax (in units of log2):
 //   x_j = a q.k_j,  m' = max(m, max_j x_j),  l' = l 2^(m-m') + sum_j 2^(x_j-m'),  O' = O 2^(m-m') + sum_j 2^(x_j-m') v_j
-// and out = dv O / l, lse = ln2 (m + log2 l), with a = scale dq dk log2(e).
+// and out = dv O / l, lse = ln2 (m + log2 l), with a = scale dq dk log2(e).  A row is empty (0 and -inf) if l is 0, not where it
+// is not above 0: a NaN score, or one of +inf, makes NaN of l and of the row, as in the formula, however its request is split.
 //
 // Bound: the cache is read once (H_kv (D_qk + D_v) values per token) and a key costs 2 (D_qk + D_v) operations per
 // query head, so with the usual 1 to 16 heads per KV head this is far below the tensor cores and HBM is the limit.
@@ -331,7 +332,7 @@ struct Rows {
   static constexpr int kKSteps = T::kRowK / 32, kMTiles = DV / 16;
   static constexpr int kScoreKind = FP8 ? kE4m3 : kBf16, kValueKind = FP8 ? kF16 : kBf16;
   static constexpr float kLift = FP8 ? 15.0f : 0.0f;  // e4m3: weights in fp16 up to 2^15, so that light ones keep their bits
-  static constexpr float kNoKey = 3.0e38f;            // ref before the first key: lifts any score but -inf over the limit
+  static constexpr float kNoKey = 3.402823466e38f;    // ref before the first key: lifts every score above its negative over the limit
 
   uint32_t qf[kKSteps][2];      // B fragments of the queries
   float o[kMTiles][4], m[2], l[2];  // this lane's two heads
@@ -470,7 +471,7 @@ struct Rows {
       const int head = t4 * 2 + e;
       if (head < count) {
         const long long row = (direct ? static_cast<long long>(b) : slot) * a.H + first + head;
-        const float f = !direct ? dv : sum > 0.0f ? dv / sum : 0.0f;
+        const float f = !direct ? dv : sum == 0.0f ? 0.0f : dv / sum;
         if (g8 == 0) put_sums(a, row, direct, m[e], sum);
         __nv_bfloat16* out = a.out + row * DV;
         float* part = a.part + row * DV;
@@ -481,7 +482,7 @@ struct Rows {
             out[i * 16 + g8] = __float2bfloat16_rn(y0);
             out[i * 16 + g8 + 8] = __float2bfloat16_rn(y1);
           }
-        } else if (m[e] != -INFINITY) {  // without a valid key the join does not read O
+        } else {
           put_o(part, e, f, g8);
         }
       }
@@ -509,9 +510,9 @@ struct Rows {
     for (int head = sub; head < count; head += subs) {
       float M = -INFINITY, L = 0.0f, x[V] = {};
       for (int k = 0; k < subs; ++k) M = fmaxf(M, all_ml[k * stride * 8 + head].x);
-      for (int k = 0; k < subs && M != -INFINITY; ++k) {
+      for (int k = 0; k < subs; ++k) {
         const float2 ml = all_ml[k * stride * 8 + head];
-        const float e = exp2_approx(ml.x - M);  // 0 for a run without a valid key, whose O is 0
+        const float e = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - M);  // 0 for a run without a valid key, whose O is 0
         L = fmaf(ml.y, e, L);
         const float* y = all_o + (k * stride * 8 + head) * DV + lane * V;
 #pragma unroll
@@ -519,12 +520,12 @@ struct Rows {
       }
       const long long row = (direct ? static_cast<long long>(b) : slot) * a.H + first + head;
       if (lane == 0) put_sums(a, row, direct, M, L);
-      const float f = L > 0.0f ? 1.0f / L : 0.0f;
+      const float f = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
       for (int j = 0; j < V; j += 2) {
         if (direct)
           *reinterpret_cast<__nv_bfloat162*>(a.out + row * DV + lane * V + j) = __floats2bfloat162_rn(x[j] * f, x[j + 1] * f);
-        else if (M != -INFINITY)
+        else
           *reinterpret_cast<float2*>(a.part + row * DV + lane * V + j) = make_float2(x[j], x[j + 1]);
       }
     }
@@ -543,7 +544,7 @@ struct Rows {
     if (!direct)
       a.ml[row] = make_float2(top - kLift, sum);
     else if (a.lse)
-      a.lse[row] = sum > 0.0f ? (top + log2f(sum) - kLift) * 0.69314718055994531f : -INFINITY;
+      a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - kLift) * 0.69314718055994531f;
   }
   __device__ __forceinline__ void put_o(float* to, int e, float f, int g8) const {
 #pragma unroll
@@ -1203,7 +1204,7 @@ __global__ void __launch_bounds__(W * ROWS * 32, W == 16 ? 1 : W == 4 ? 7 : 3) j
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
         const float ek = __shfl_sync(0xffffffffu, e, (k0 + k) & 31);
-        if (k0 + k < count && ek > 0.0f) {  // a part without a valid key has no O
+        if (k0 + k < count) {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) o[j] = fmaf(x[k].y[j], ek, o[j]);
         }
@@ -1213,11 +1214,11 @@ __global__ void __launch_bounds__(W * ROWS * 32, W == 16 ? 1 : W == 4 ? 7 : 3) j
 #pragma unroll
   for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
   if constexpr (W == 1) {
-    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat16* out = a.out + row * DV + d0 + lane * VEC;
 #pragma unroll
     for (int j = 0; j < VEC; j += 2) *reinterpret_cast<__nv_bfloat162*>(out + j) = __floats2bfloat162_rn(o[j] * f, o[j + 1] * f);
-    if (a.lse && lane == 0 && d0 == 0) a.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (a.lse && lane == 0 && d0 == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s_o[w][lane * VEC + j] = o[j];
@@ -1239,9 +1240,9 @@ __global__ void __launch_bounds__(W * ROWS * 32, W == 16 ? 1 : W == 4 ? 7 : 3) j
       float x = 0.0f;
 #pragma unroll
       for (int j = 0; j < W; ++j) x = fmaf(s_o[j][i], e[j], x);
-      a.out[row * DV + d0 + i] = __float2bfloat16_rn(L > 0.0f ? x / L : 0.0f);
+      a.out[row * DV + d0 + i] = __float2bfloat16_rn(L == 0.0f ? 0.0f : x / L);
     }
-    if (a.lse && tid == 0 && d0 == 0) a.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+    if (a.lse && tid == 0 && d0 == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
   }
 }
 

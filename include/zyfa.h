@@ -339,7 +339,8 @@ zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v,
  *                     captured graphs) need one each.
  *
  * Tokens whose page lies outside [0, num_pages) are left out of the softmax and zyfa_check_errors() returns
- * ZYFA_ERR_BAD_PAGE.  Cache rows behind a request's length do not matter, whatever they hold.
+ * ZYFA_ERR_BAD_PAGE.  Cache rows behind a request's length do not matter, whatever they hold.  A NaN among a row's
+ * scores, or a score of +inf, makes the row and its lse NaN; a NaN or infinity of V stays in its channel.
  * Scores and sums are held in fp32; before the weights exp(s - max) multiply V they are rounded to fp16 for an e4m3
  * cache, whose values fp16 holds exactly, else to a sum of two bf16 numbers (16 bits).  Bitwise reproducible
  * for identical inputs on one GPU model.  One or two launches, asynchronous on `stream`; allocates nothing, no host

@@ -78,3 +78,66 @@ def test_decode_bf16_weights_keep_16_bits(shape, page):
         worst = max(worst, float((np.abs(out[b, h] - ref) / tol).max()))
         assert abs(lse[b, h] - ref_lse) <= lse_tol + 2.0 ** -22 * abs(ref_lse)
     assert worst <= 1.0, worst
+
+
+# ------------------------------------------------------------------------------------------------
+# values that are not finite
+
+# (requests, query heads, KV heads, tokens): rows in one block; few rows (16 warps a row, by channels and whole); 8 and 4 warps a row;
+# a warp a row
+SPLITS = [(2, 4, 2, 40), (1, 4, 2, 9000), (2, 32, 8, 9000), (6, 64, 4, 5000), (16, 32, 8, 2000), (48, 32, 8, 700)]
+
+
+@pytest.mark.parametrize("kind,what", [(kind, what) for kind in ("fp8", "bf16") for what in ("query", "key", "value")] +
+                         [("bf16", "infinite score")])                        # (e4m3 products do not overflow)
+@pytest.mark.parametrize("page", [7, 16])
+@pytest.mark.parametrize("B,H,H_kv,n", SPLITS)
+def test_decode_shows_values_that_are_not_finite(kind, B, H, H_kv, n, page, what):
+    """A NaN in a query, a key or a value, and a score of +inf, make NaN of the rows that they belong to, however these are split, and
+    change no other row."""
+    x = _Batch(kind, "128", [n + i % 3 for i in range(B)], H, H_kv, page=page, width=None if n < 100 else -(-(n + 40) // page) + 64, seed=n)
+    clean, clean_lse = x.attend()
+    assert np.isfinite(clean).all() and np.isfinite(clean_lse).all()
+    b, head, token, group = B - 1, H_kv - 1, n // 3, H // H_kv
+    nan = bits(torch.full((1,), math.nan, device="cuda").to(dtype_of(kind)))
+    rows, channels = np.zeros((B, H), dtype=bool), slice(None)
+    rows[b, head * group:] = True
+    if what == "query":
+        bits(x.q)[b, head * group, 5] = nan
+        rows[b] = False
+        rows[b, head * group] = True
+    elif what == "key":
+        bits(x.k[b])[token, head, 5] = nan
+    elif what == "infinite score":
+        x.q[b, head * group:, 5] = 4.0
+        x.k[b][token, head, 5] = 3e38
+    else:
+        bits(x.v[b])[token, head, 5] = nan
+        channels = 5
+    x.fill(b)
+    out, lse = x.attend()
+    assert np.isnan(out[rows][:, channels]).all()
+    if what == "value":
+        out[rows, 5] = clean[rows, 5]
+        assert np.array_equal(out, clean) and np.array_equal(lse, clean_lse)
+    else:
+        assert not np.isfinite(lse[rows]).any() and not (lse[rows] == -math.inf).any()
+        assert np.array_equal(out[~rows], clean[~rows]) and np.array_equal(lse[~rows], clean_lse[~rows])
+
+
+@pytest.mark.parametrize("page", [7, 16])
+@pytest.mark.parametrize("n", [40, 5000])
+def test_decode_of_scores_near_the_lowest_number(n, page):
+    """Scores between -3e38 and the lowest fp32 number, in units of log2, are scores like others: their weights go by their differences."""
+    x = _Batch("bf16", "64", [n], 1, 1, page=page, seed=n)
+    x.scale = 1.0 / math.log2(math.e)
+    x.q.zero_()
+    x.q[..., 0] = 1.0
+    x.k[0].zero_()
+    x.k[0][..., 0] = -3.2e38                                                   # one score for all: equal weights
+    x.fill(0)
+    out, lse = x.attend(softmax_scale=x.scale)
+    assert np.isfinite(lse).all()
+    v = f64(x.v[0])[:, 0]
+    # equal weights are exact powers of two; n products and weights summed in fp32, out rounded once
+    assert np.all(np.abs(out[0, 0] - v.mean(0)) <= 2.0 ** -8 * np.abs(v.mean(0)) + 2 * n * 2.0 ** -24 * np.abs(v).mean(0) * 1.01)
