@@ -10,8 +10,8 @@
 // per chunk of rows: 337 us for the 256.)  One launch: every block takes a run of token rows,
 // forms the two prefix sums over the requests itself (1024 requests at a time in shared memory; the lengths come from
 // L2 once another block has read them) rather than wait for another block, and finds the request of a row by
-// bisection.  A fresh page always begins with a new token, so the thread of that token's row writes the table entry and
-// no block depends on another's writes.
+// bisection.  A fresh page always begins with a new token, so the thread of that token's row writes the table entry (the last
+// block those of tokens that have no row) and no block depends on another's writes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   __shared__ long long s_wtok[kWarps], s_wpage[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lead = blockIdx.x == 0 && !a.cursor_only;      // writes the per-request results
-  const bool tail = blockIdx.x == gridDim.x - 1;            // takes rows behind max_tokens (their pages count) too
+  const bool tail = blockIdx.x == gridDim.x - 1;            // takes the pages that tokens behind max_tokens start, too
   zyfa::wait_for_predecessor();
   const int cursor = max(0, __ldg(a.cursor_in));
   const int cap = a.max_pages * a.page;                     // at most 2^30
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     if (tid == 0) s_tok[kChunk] = all_tok;
     __syncthreads();
     // this block's rows among the chunk's
-    const long long end = a.cursor_only ? 0 : tail ? tok + all_tok : min(r1, tok + all_tok);
+    const long long end = a.cursor_only ? 0 : min(r1, tok + all_tok);
     for (long long r = max(r0, tok) + tid; r < end; r += kThreads) {
       const long long x = r - tok;
       int lo = 0, hi = min(kChunk, a.B - b0);               // s_tok[lo] <= x < s_tok[hi]
@@ -147,9 +147,21 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         bad |= pg < 0;
         if (pg >= 0) slot = static_cast<long long>(pg) * a.page + off;
       }
-      if (r < a.max_tokens) {
-        a.positions[r] = saturated(pos);
-        a.slots[r] = slot;
+      a.positions[r] = saturated(pos);
+      a.slots[r] = slot;
+    }
+    // Tokens behind max_tokens are dropped, not the pages that they start.  (Page by page: lengths may name 2^31 tokens a request.)
+    if (tail && !a.cursor_only && tok + all_tok > a.max_tokens) {
+      for (long long x = tid; x < all_page; x += kThreads) {
+        int lo = 0, hi = min(kChunk, a.B - b0);             // s_page[lo] <= x < s_page[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_page[mid] <= x) lo = mid; else hi = mid;
+        }
+        const int c = s_cached[lo], p = pages_before(min(c, cap) + a.page - 1) + static_cast<int>(x - s_page[lo]);
+        if (tok + s_tok[lo] + static_cast<long long>(p) * a.page - c < a.max_tokens) continue;  // written with its first token's row
+        const long long f = cursor + page + x;
+        a.table[static_cast<long long>(b0 + lo) * a.table_stride + p] = f < a.num_free ? __ldg(a.free_pages + f) : -1;
       }
     }
     tok += all_tok;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from _paged_util import SHAPES, bits, decode_tolerance, dtype_of, f64, fill_tokens, make_cache, random_table, random_values
-from fp8_causal_prefill_gb300 import paged_decode_attn, zyfa_check_errors
+from fp8_causal_prefill_gb300 import paged_decode_attn, paged_plan, zyfa_check_errors
 from oracle import paged as P
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +141,45 @@ def test_decode_of_scores_near_the_lowest_number(n, page):
     v = f64(x.v[0])[:, 0]
     # equal weights are exact powers of two; n products and weights summed in fp32, out rounded once
     assert np.all(np.abs(out[0, 0] - v.mean(0)) <= 2.0 ** -8 * np.abs(v.mean(0)) + 2 * n * 2.0 ** -24 * np.abs(v).mean(0) * 1.01)
+
+
+# ------------------------------------------------------------------------------------------------
+# a step over capacity
+
+@pytest.mark.parametrize("over", [1, 5000])
+@pytest.mark.parametrize("above", [1, 300])
+def test_plan_of_more_tokens_than_rows(above, over):
+    """Tokens behind the last row are dropped, not their pages: they are in the table, whatever number of rows the blocks take."""
+    blocks = 8 * torch.cuda.get_device_properties(0).multi_processor_count      # each takes 256 rows, or more where there are more
+    rows, page, B = blocks * 256 + above, 16, 7
+    rng = np.random.default_rng(above + over)
+    cached = rng.integers(0, 100, B)
+    new = np.full(B, (rows + over) // B)
+    new[-1] += rows + over - new.sum()
+    need = int(sum(-(-int(c + n) // page) for c, n in zip(cached, new)))
+    free = rng.permutation(need + 9).astype(np.int32)
+    table = np.full((B, -(-int(max(cached + new)) // page)), 5, dtype=np.int32)
+    want = P.paged_plan(cached, new, table, free, 2, page, rows)
+    t = torch.from_numpy(table).cuda()
+    got = paged_plan(i32(cached), i32(new), t, torch.from_numpy(free).cuda(), i32([2]), page, rows)
+    assert zyfa_check_errors() == 6                                             # ZYFA_ERR_CAPACITY
+    np.testing.assert_array_equal(t.cpu().numpy(), want[0])
+    for g, w in zip(got, want[1:]):
+        np.testing.assert_array_equal(g.cpu().numpy().reshape(-1), np.atleast_1d(w))
+
+
+@pytest.mark.parametrize("B,page,width,rows", [(3, 16, 9, 500), (3, 1, 40, 0), (1500, 5, 3, 4000)])
+def test_plan_of_lengths_as_large_as_int32_holds(B, page, width, rows):
+    # lengths that no program means end in an error, at once
+    most, cap, cursor = 2 ** 31 - 1, width * page, 4
+    pool = cursor + B * width - 1                                               # the last page is missing
+    free = np.random.default_rng(B).permutation(pool).astype(np.int32)
+    table = torch.full((B, width + 2), 5, dtype=torch.int32, device="cuda")
+    got = paged_plan(i32([0] * B), i32([most] * B), table[:, :width], torch.from_numpy(free).cuda(), i32([cursor]), page, rows)
+    assert zyfa_check_errors() == 6
+    pages = np.append(free[cursor:], -1).reshape(B, width)
+    np.testing.assert_array_equal(table.cpu().numpy(), np.pad(pages, ((0, 0), (0, 2)), constant_values=5))
+    t = np.arange(rows)                                                         # all of request 0
+    slots = np.where(t < cap, pages[0, np.minimum(t // page, width - 1)].astype(np.int64) * page + t % page, -1)
+    assert got.seq_lens.tolist() == [cap] * B and got.cu_tokens.tolist() == [min(b * most, most) for b in range(B + 1)]
+    assert got.positions.tolist() == t.tolist() and got.slots.tolist() == slots.tolist() and got.cursor.tolist() == [pool]
