@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <utility>
 
 #include "paged.cuh"
 
@@ -286,6 +287,52 @@ cudaError_t launch(const StoreArgs& a, int D_qk, cudaStream_t stream) {
   return zyfa::launch_dependent(store_kernel<FP8, INTERLEAVED, 192, 128>, dim3(grid), kThreads<192>, 0, stream, a);
 }
 
+// Where the rows of a cache begin: the sums of multiples, below their extents, of three strides (elements), the largest first.
+struct CacheDims {
+  long long extent[3], stride[3];
+  CacheDims(const zyfa_paged_cache_t& c, long long page, long long token, long long head) {
+    std::pair<long long, long long> d[3] = {{page, c.num_pages}, {token, c.page_size}, {head, c.H_kv}};
+    for (auto& x : d)
+      if (x.second == 1) x.first = 0;  // a stride that is never taken
+    std::sort(d, d + 3);
+    for (int i = 0; i < 3; ++i) {
+      stride[i] = d[2 - i].first;
+      extent[i] = d[2 - i].second;
+    }
+  }
+  // The rows, of D elements, do not overlap: each stride passes over everything within it, as in any view of a dense tensor.
+  // (Strides that miss one another by their remainders alone are refused.)
+  bool apart(long long D) const {
+    long long span = D;
+    for (int i = 2; i >= 0; --i) {
+      if (extent[i] == 1) continue;
+      if (stride[i] < span) return false;
+      if (stride[i] > (1ll << 60) / extent[i]) return i == 0;  // more than any memory, and nothing may lie around it
+      span += (extent[i] - 1) * stride[i];
+    }
+    return true;
+  }
+  // A row of D elements of this cache and one of `other_D`, `offset` elements behind, overlap somewhere.  Decided for equal strides
+  // (rows apart in both); with others, as of K and V blocks side by side within a page, the caller answers for them.
+  bool meets(const CacheDims& other, long long offset, long long D, long long other_D) const {
+    for (int i = 0; i < 3; ++i)
+      if (stride[i] != other.stride[i] || extent[i] != other.extent[i]) return offset == 0;
+    return meets_from(0, offset, D, other_D);
+  }
+
+ private:
+  bool meets_from(int i, long long offset, long long D, long long other_D) const {
+    if (i == 3) return offset < D && -offset < other_D;
+    if (extent[i] == 1) return meets_from(i + 1, offset, D, other_D);
+    // what is left has to lie within this stride
+    long long n = offset / stride[i];
+    if (offset % stride[i] < 0) --n;
+    for (long long x : {n, n + 1})
+      if (x > -extent[i] && x < extent[i] && meets_from(i + 1, offset - x * stride[i], D, other_D)) return true;
+    return false;
+  }
+};
+
 }  // namespace
 
 extern "C" zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v, long long q_token_stride,
@@ -303,13 +350,9 @@ extern "C" zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, con
   if (N < 0 || H < 1 || H % H_kv != 0 || (descale_per_kv_head != 0 && descale_per_kv_head != 1)) return ZYFA_ERR_INVALID_ARG;
   if (!k != !v || (!q && !k)) return ZYFA_ERR_INVALID_ARG;
   // the cache is written here: its rows must not overlap
-  if (k) {
-    const bool apart =
-        (H_kv == 1 || (cache->k_head_stride >= D_qk && cache->v_head_stride >= D_v)) &&
-        (cache->page_size == 1 || (cache->k_token_stride >= D_qk && cache->v_token_stride >= D_v)) &&
-        (cache->num_pages == 1 || (cache->k_page_stride >= D_qk && cache->v_page_stride >= D_v));
-    if (!apart) return ZYFA_ERR_INVALID_ARG;
-  }
+  const CacheDims kdims(*cache, cache->k_page_stride, cache->k_token_stride, cache->k_head_stride);
+  const CacheDims vdims(*cache, cache->v_page_stride, cache->v_token_stride, cache->v_head_stride);
+  if (k && !(kdims.apart(D_qk) && vdims.apart(D_v))) return ZYFA_ERR_INVALID_ARG;
   if (rope && rope->rot_dim != 0) {
     const zyfa_rope_t& r = *rope;
     if (r.rot_dim < 0 || r.rot_dim % 16 != 0 || r.rot_offset < 0 || r.rot_offset % 8 != 0) return ZYFA_ERR_INVALID_ARG;
@@ -346,6 +389,7 @@ extern "C" zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, con
     if (!aligned(p, 16)) return ZYFA_ERR_MISALIGNED;
   if (!aligned(slots, 8) || !aligned(q_descale, 4) || !aligned(k_descale, 4) || !aligned(v_descale, 4))
     return ZYFA_ERR_MISALIGNED;
+  if (k && kdims.meets(vdims, (a.cache.v - a.cache.k) / zyfa::element_size(cache->dtype), D_qk, D_v)) return ZYFA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ZYFA_ERR_CUDA;
   a.status = zyfa::device_status_word(dev);

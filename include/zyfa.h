@@ -309,8 +309,9 @@ typedef struct {
  *   q/k/v_descale     e4m3 only: device pointers to one float (or H_kv floats with descale_per_kv_head = 1;
  *                     query head h uses hk = h / (H / H_kv)); NULL means 1.  Ignored for bf16.
  *
- * Outputs must not overlap one another or the inputs.  One launch, asynchronous on `stream`, allocates
- * nothing.  N == 0 returns ZYFA_OK.
+ * Outputs must not overlap one another or the inputs.  Nor may rows of the cache: of the page, token and head strides each
+ * passes over all that lies within it, as in any view of a dense tensor (else, and where a row of K and one of V of the same
+ * strides overlap, ZYFA_ERR_INVALID_ARG).  One launch, asynchronous on `stream`, allocates nothing.  N == 0 returns ZYFA_OK.
  */
 zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v, long long q_token_stride,
                                     long long k_token_stride, long long v_token_stride, void* q_out, void* k_out,

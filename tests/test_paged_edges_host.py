@@ -1,0 +1,81 @@
+"""Refusals and choices of the paged serving operators that need no GPU: caches whose rows overlap."""
+import itertools
+import random
+
+import pytest
+import torch
+
+from test_paged_host import A, _cache, _store, lib  # noqa: F401
+
+
+def _rows(strides, extents):
+    return [sum(i * s for i, s in zip(at, strides)) for at in itertools.product(*(range(n) for n in extents))]
+
+
+def _overlap(strides, extents, D):
+    rows = sorted(_rows(strides, extents))
+    return any(b - a < D for a, b in zip(rows, rows[1:]))
+
+
+# 4 pages of 16 tokens of 2 heads of 128 channels: (page, token, head) strides
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("strides,apart", [
+    ((4096, 256, 128), True), ((4096, 128, 2048), True), ((8192, 512, 256), True), ((256, 1024, 128), True), ((128, 1024, 512), True),
+    ((4160, 256, 128), True), ((256, 4096, 128), True), ((2048, 128, 8192), True), ((1 << 46, 256, 128), True),
+    ((4096, 128, 128), False), ((128, 256, 128), False), ((256, 2048, 1024), True), ((256, 512, 128), False), ((4096, 128, 256), False), ((4080, 256, 128), False),
+    ((4096, 256, 144), False), ((512, 128, 1024), False), ((4096, 1 << 46, 1 << 46), False)])
+def test_store_refuses_strides_that_overlap_together(lib, strides, apart, which):  # noqa: F811
+    assert _overlap(strides, (4, 16, 2), 128) == (not apart)
+    kw = {f"{which}_{n}_stride": s for n, s in zip(("page", "token", "head"), strides)}
+    assert _store(lib, _cache(**kw), N=0) == (0 if apart else 1)
+
+
+def test_store_accepts_views_of_dense_tensors_and_nothing_that_overlaps(lib):  # noqa: F811
+    rng = random.Random(1)
+    accepted = 0
+    for _ in range(4000):
+        extents = [rng.choice([1, 2, 3, 5]) for _ in range(3)]                  # pages, tokens, heads
+        D, D_v = rng.choice([(64, 64), (128, 128), (192, 128)])
+        order, strides, span = rng.sample(range(3), 3), [0, 0, 0], D
+        for i in order:                                                         # a view of a dense tensor, innermost dimension first
+            strides[i] = span + 64 * rng.choice([0, 0, 0, 1, 7])
+            span = strides[i] * extents[i]
+        dense = rng.random() < 0.5
+        if not dense:
+            strides[rng.randrange(3)] = 64 * rng.randrange(20)
+        kw = {f"{w}_{n}_stride": s for w in "kv" for n, s in zip(("page", "token", "head"), strides)}
+        st = _store(lib, _cache(num_pages=extents[0], page_size=extents[1], H_kv=extents[2], D_qk=D, D_v=D_v, **kw), N=0, H=extents[2])
+        assert st in (0, 1) and not (dense and st) and not (st == 0 and _overlap(strides, extents, D))
+        accepted += st == 0
+    assert 2000 < accepted < 3900
+
+
+def _in_one_place(lib, extents, strides, D, D_v, offset):  # noqa: F811
+    """The store's answer for V `offset` elements behind K, in the same strides, and whether rows of the two overlap."""
+    kw = {f"{w}_{n}_stride": s for w in "kv" for n, s in zip(("page", "token", "head"), strides)}
+    base = 1 << 30
+    c = _cache(k=base, v=base + offset, num_pages=extents[0], page_size=extents[1], H_kv=extents[2], D_qk=D, D_v=D_v, **kw)
+    rows = _rows(strides, extents)
+    return c, any(x - D_v < y < x + D for x in rows for y in (z + offset for z in rows))
+
+
+def test_store_refuses_keys_and_values_in_one_place(lib):  # noqa: F811
+    # (calls that are accepted are made only where there is no GPU to take their addresses, which are not memory)
+    rng = random.Random(2)
+    refused = 0
+    while refused < 300:
+        extents = [rng.choice([1, 2, 3, 4]) for _ in range(3)]
+        D, D_v = rng.choice([(64, 64), (128, 128), (192, 128)])
+        strides, span = [0, 0, 0], D
+        for i in rng.sample(range(3), 3):
+            strides[i] = span + 64 * rng.choice([0, 1, 2, 7])
+            span = strides[i] * extents[i]
+        offset = 16 * rng.randrange(-span // 16 - 20, span // 16 + 20)
+        c, meet = _in_one_place(lib, extents, strides, D, D_v, offset)
+        if meet:
+            assert _store(lib, c, H=extents[2], q=0, k=A, v=A, slots=A) == 1
+            refused += 1
+        elif not torch.cuda.is_available():
+            assert _store(lib, c, H=extents[2], q=0, k=A, v=A, slots=A) == 4    # past every check
+    c, _ = _in_one_place(lib, (4, 16, 2), (4096, 256, 128), 128, 128, 0)
+    assert _store(lib, c) == 1
