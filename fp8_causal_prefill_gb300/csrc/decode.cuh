@@ -301,7 +301,12 @@ struct Header {
 // first and last tile of a request's part; the part is the whole request; it begins the request; not every key is valid; the run's last tile
 enum : int { kFirst = 1, kLast = 2, kDirect = 4, kSlot1 = 8, kPartial = 16, kEnd = 32 };
 
-__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) { return max(0, min(__ldg(a.seq_lens + b), a.max_len)); }
+// EARLY: before the kernel has waited for its predecessor.
+template <bool EARLY = false>
+__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
+  const int n = EARLY ? load_relaxed(a.seq_lens + b) : a.seq_lens[b];
+  return max(0, min(n, a.max_len));
+}
 
 __device__ __forceinline__ void page_of(const DecodeArgs& a, int t, int* p, int* off) {
   *p = static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(t)) * a.page_magic) >> a.page_shift);
@@ -576,15 +581,16 @@ __device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head,
 constexpr unsigned kGap = 2;
 // Up to kFew requests warps read all lengths themselves, else blocks do with barriers: 189 requests 20.0 us instead of 21.6.
 constexpr int kFew = 256;
-// The join reads them up to kFewJoin, else what the first kernel left (256 requests of 32 heads, 100 tokens each: 21.0 us instead of
-// 23.2; from the first request on 0.3 us more for short batches).
-constexpr int kFewJoin = 128;
+// The join reads them up to kFewJoin, else what the first kernel left (from the first request on 0.2 to 0.4 us more for the shortest
+// batches; up to 128 requests read, 0.3 us more for 64 ragged ones and 1.4 for 128, whose every row reads them from L2).
+constexpr int kFewJoin = 32;
 
 struct Schedule {
   unsigned total = 0, per = 0;  // numbers, and those of a run
 
+  template <bool EARLY = false>
   static __device__ __forceinline__ unsigned tiles(const DecodeArgs& a, int b) {
-    return b < a.B ? (length_of(a, b) + a.tile_tokens - 1u) >> a.tile_log2 : 0u;
+    return b < a.B ? (length_of<EARLY>(a, b) + a.tile_tokens - 1u) >> a.tile_log2 : 0u;
   }
   static __device__ __forceinline__ unsigned numbers(unsigned tiles) { return tiles ? tiles + kGap : 0; }
   __device__ __forceinline__ void set(const DecodeArgs& a, unsigned sum) {
@@ -593,12 +599,12 @@ struct Schedule {
   }
 
   // Up to 32 N requests: every warp by itself, N requests a lane, without a barrier.  Returns the lane's first number.
-  template <int N>
+  template <int N, bool EARLY>
   __device__ __forceinline__ unsigned scan_few(const DecodeArgs& a, unsigned (&n)[N]) {
     const int lane = threadIdx.x & 31;
     unsigned sum = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) n[i] = tiles(a, lane * N + i);
+    for (int i = 0; i < N; ++i) n[i] = tiles<EARLY>(a, lane * N + i);
 #pragma unroll
     for (int i = 0; i < N; ++i) sum += numbers(n[i]);
     unsigned incl = sum;
@@ -612,7 +618,7 @@ struct Schedule {
   }
   template <int N>
   __device__ __forceinline__ void find_few(const DecodeArgs& a, unsigned g, int* b, unsigned* tile, int* left) {
-    unsigned n[N], start = scan_few<N>(a, n), at = 0, number = 0, rest = 0;
+    unsigned n[N], start = scan_few<N, false>(a, n), at = 0, number = 0, rest = 0;
     const unsigned first = g * per;
     bool here = false;
 #pragma unroll
@@ -634,21 +640,12 @@ struct Schedule {
     number = __shfl_sync(0xffffffffu, number, l);
     *left = hit ? max(0, static_cast<int>(min(first + per, total) - number)) : 0;
   }
-  // Numbers of request b's first tile and, were it one longer, of its next.
-  template <int N>
-  __device__ __forceinline__ void bounds_few(const DecodeArgs& a, int b, unsigned* p0, unsigned* p1) {
-    unsigned n[N], mine = scan_few<N>(a, n), len = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i < b % N) mine += numbers(n[i]);
-      if (i == b % N) len = n[i];
-    }
-    *p0 = __shfl_sync(0xffffffffu, mine, b / N);
-    *p1 = *p0 + __shfl_sync(0xffffffffu, len, b / N);
-  }
+  // Numbers of request b's first tile and, were it one longer, of its next, for the join, before it has waited.
   __device__ __forceinline__ void bounds(const DecodeArgs& a, int b, unsigned* p0, unsigned* p1) {
-    if (a.B <= 32) return bounds_few<1>(a, b, p0, p1);
-    bounds_few<4>(a, b, p0, p1);
+    static_assert(kFewJoin <= 32);
+    unsigned n[1], mine = scan_few<1, true>(a, n);
+    *p0 = __shfl_sync(0xffffffffu, mine, b);
+    *p1 = *p0 + __shfl_sync(0xffffffffu, n[0], b);
   }
 
   // Any number, the whole block: prefix: [blockDim.x] and sums: [warps] in shared memory.  Leaves a.starts for the join.
@@ -840,7 +837,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       if (t >= len) return -1;
       int p, off;
       page_of(a, t, &p, &off);
-      return __ldg(a.table + request * a.table_stride + p);
+      return a.table[request * a.table_stride + p];
     };
     struct Descales {
       float q, k, v;
@@ -849,9 +846,9 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
       Descales d = {1.0f, 1.0f, 1.0f};
       if (FP8 && lane < a.heads) {
         const int i = a.desc_per_head ? request * a.cache.H_kv + min(head0 + lane, a.cache.H_kv - 1) : 0;
-        if (a.q_desc) d.q = __ldg(a.q_desc + i);
-        if (a.k_desc) d.k = __ldg(a.k_desc + i);
-        if (a.v_desc) d.v = __ldg(a.v_desc + i);
+        if (a.q_desc) d.q = a.q_desc[i];
+        if (a.k_desc) d.k = a.k_desc[i];
+        if (a.v_desc) d.v = a.v_desc[i];
       }
       return d;
     };
@@ -1066,7 +1063,7 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
     if (lane < KT && c.t + lane < c.len) {
       int p;
       page_of(a, c.t + lane, &p, &off);
-      pg = __ldg(a.table + c.b * a.table_stride + p);
+      pg = a.table[c.b * a.table_stride + p];
     }
   };
   look_up();
@@ -1098,8 +1095,8 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
           float2 scale = {a.scale_log2, 1.0f};
           if (FP8) {
             const int di = a.desc_per_head ? c.b * a.cache.H_kv + hk : 0;
-            scale.x *= (a.q_desc ? __ldg(a.q_desc + di) : 1.0f) * (a.k_desc ? __ldg(a.k_desc + di) : 1.0f);
-            scale.y = a.v_desc ? __ldg(a.v_desc + di) : 1.0f;
+            scale.x *= (a.q_desc ? a.q_desc[di] : 1.0f) * (a.k_desc ? a.k_desc[di] : 1.0f);
+            scale.y = a.v_desc ? a.v_desc[di] : 1.0f;
           }
           s_scale[warp][stage] = scale;
         }
@@ -1159,8 +1156,9 @@ __global__ void __launch_bounds__(W * ROWS * 32, W == 16 ? 1 : W == 4 ? 7 : 3) j
   const long long row = static_cast<long long>(blockIdx.x) * ROWS + (ROWS > 1 ? warp : 0);
   if (row >= static_cast<long long>(a.B) * a.H) return;
   const int b = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H), w = ROWS > 1 ? 0 : warp, tid = w * 32 + lane;
-  // Up to kFewJoin requests the bounds come from their lengths, read before the first kernel has ended: it does not write them, and
-  // what did had ended before that kernel let this one start.
+  // Up to kFewJoin requests the bounds come from their lengths, read before the first kernel has ended.  It does not write them; what
+  // did had ended, and its writes were visible, when that kernel's blocks came from their own wait, after which each let this one
+  // start.  Only this SM's L1 could still hold what was there before, and these loads pass it by.
   Schedule plan;
   unsigned p0, p1;
   if (a.B <= kFewJoin) plan.bounds(a, b, &p0, &p1);

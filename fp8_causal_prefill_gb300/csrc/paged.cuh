@@ -69,7 +69,8 @@ inline zyfa_status_t check_cache(const zyfa_paged_cache_t* c, CacheView* view) {
 }
 
 // Programmatic dependent launch: the kernel may start while its predecessor on the stream still runs, and waits for it
-// on the device (wait_for_predecessor, before it touches memory), so that its launch costs the stream nothing.
+// on the device (wait_for_predecessor, before it touches memory), so that its launch costs the stream nothing.  Its inputs
+// are written within its lifetime, so it reads them by ordinary loads, which the wait orders, not as read-only data.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, int smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchAttribute attr = {};
@@ -86,6 +87,12 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned bloc
 }
 
 __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A load that sees what had been written when it was issued (from L2, not from an earlier copy in this SM's L1).
+__device__ __forceinline__ int load_relaxed(const int* p) {
+  int x;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
 __device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace zyfa

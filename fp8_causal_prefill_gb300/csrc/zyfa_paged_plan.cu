@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   const bool lead = blockIdx.x == 0 && !a.cursor_only;      // writes the per-request results
   const bool tail = blockIdx.x == gridDim.x - 1;            // takes the pages that tokens behind max_tokens start, too
   zyfa::wait_for_predecessor();
-  const int cursor = max(0, __ldg(a.cursor_in));
+  const int cursor = max(0, *a.cursor_in);
   const int cap = a.max_pages * a.page;                     // at most 2^30
   const long long r0 = static_cast<long long>(blockIdx.x) * a.rows;
   const long long r1 = min(r0 + a.rows, static_cast<long long>(a.max_tokens));
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int b = b0 + tid * kPerThread + i;
-      const int c = b < a.B ? max(0, __ldg(a.cached + b)) : 0;
-      n[i] = b < a.B ? max(0, __ldg(a.fresh + b)) : 0;
+      const int c = b < a.B ? max(0, a.cached[b]) : 0;
+      n[i] = b < a.B ? max(0, a.fresh[b]) : 0;
       const long long len = c + n[i];
       const int had = pages_before(min(c, cap) + a.page - 1), has = pages_before(min(len, static_cast<long long>(cap)) + a.page - 1);
       need[i] = has - had;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
           pg = *entry;
         } else {
           const long long f = cursor + page + s_page[lo] + (p - had);
-          pg = f < a.num_free ? __ldg(a.free_pages + f) : -1;
+          pg = f < a.num_free ? a.free_pages[f] : -1;
           if (off == 0) *entry = pg;
         }
         bad |= pg < 0;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         const int c = s_cached[lo], p = pages_before(min(c, cap) + a.page - 1) + static_cast<int>(x - s_page[lo]);
         if (tok + s_tok[lo] + static_cast<long long>(p) * a.page - c < a.max_tokens) continue;  // written with its first token's row
         const long long f = cursor + page + x;
-        a.table[static_cast<long long>(b0 + lo) * a.table_stride + p] = f < a.num_free ? __ldg(a.free_pages + f) : -1;
+        a.table[static_cast<long long>(b0 + lo) * a.table_stride + p] = f < a.num_free ? a.free_pages[f] : -1;
       }
     }
     tok += all_tok;

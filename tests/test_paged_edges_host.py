@@ -1,10 +1,13 @@
-"""Refusals and choices of the paged serving operators that need no GPU: caches whose rows overlap."""
+"""Refusals and choices of the paged serving operators that need no GPU: caches whose rows overlap, loads that
+the dependent launch does not order."""
 import itertools
+import os
 import random
 
 import pytest
 import torch
 
+from fp8_causal_prefill_gb300 import build
 from test_paged_host import A, _cache, _store, lib  # noqa: F401
 
 
@@ -79,3 +82,12 @@ def test_store_refuses_keys_and_values_in_one_place(lib):  # noqa: F811
             assert _store(lib, c, H=extents[2], q=0, k=A, v=A, slots=A) == 4    # past every check
     c, _ = _in_one_place(lib, (4, 16, 2), (4096, 256, 128), 128, 128, 0)
     assert _store(lib, c) == 1
+
+
+@pytest.mark.parametrize("name", ["paged.cuh", "decode.cuh", "zyfa_paged_plan.cu", "zyfa_rope_store.cu"])
+def test_kernels_that_start_early_read_by_ordinary_loads(name):
+    # what they read is written by the kernel before, while they may already run: never read-only data
+    text = open(os.path.join(build.CSRC, name)).read()
+    assert "launch_dependent" in text
+    for word in ("__ldg", "ld.global.nc", "ld.nc", "__restrict__", "tex."):
+        assert word not in text, word
