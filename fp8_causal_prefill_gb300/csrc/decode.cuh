@@ -26,8 +26,8 @@
 //   the other, with a gap behind each request for what its end costs, and each group of blocks (one block per chunk of heads) takes an
 //   equal run of the numbers.  A block finds its run from seq_lens on the device, so the host never needs the lengths.
 // * A request that lies in one group's run is written directly; otherwise each group leaves (m, l, O) of its
-//   part in the workspace and a second kernel joins the parts in group order.  Where the table has room for a few tiles only, a
-//   group is a request, and there is no second kernel.
+//   part in the workspace and a second kernel joins the parts in group order.  Where the table has room for a few tiles only (at
+//   most kLongest), a group is a request, and there is no second kernel.
 // * The join is launched while the first kernel still runs and waits for it on the device (programmatic dependent
 //   launch), which hides its launch.
 //
@@ -760,8 +760,11 @@ constexpr int kBoxWarps = KEY_BYTES <= 320 ? 4 : 2;
 // Tiles of a ring: the same 189 and 48 us with two, 179 and 46 with three, 187 and 49 with four.
 constexpr int kMaxStages = 3, kMaxHeads = 8;
 // A lone block takes 0.6 us a tile, the join 3 us.  With 4: 32 requests of 64 tokens (32 query heads, e4m3) 6.0 us instead of 7.9, one 5.5
-// instead of 6.5, eight (16 heads, bf16) 5.7 instead of 7.0; with 8 also one of 128 tokens 8.1 instead of 6.8.
-constexpr int kSerial = 4;
+// instead of 6.5, eight (16 heads, bf16) 5.7 instead of 7.0; with 8 also one of 128 tokens 8.1 instead of 6.8.  kLongest: 228
+// requests (32 query and 8 KV heads, e4m3) of 128 tokens, 8 tiles, 14.8 us whole and 18.1 split, and with one such request among ones of one
+// token 9.1 and 10.3; one of 256 tokens, 16 tiles, 13.2 whole and 10.2 split.  With no such bound, 228 requests of 1 to 16384 tokens took 598
+// us instead of 127, since equal ones would have filled the GPU evenly.
+constexpr int kSerial = 4, kLongest = 8;
 
 template <bool FP8, int DQK, int DV>
 __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1) * 32, 3)
@@ -1295,13 +1298,19 @@ inline int log2_of(int power) {
 // Fewest equal pieces of `n` that are at most `most`, as the size of a piece.
 inline int piece(int n, int most) { return (n + (n + most - 1) / most - 1) / ((n + most - 1) / most); }
 
-// A block of boxes_kernel: chunks of a head first (they read the same tile), then heads side by side, then runs of tokens.
+// Chunks of up to 8 query heads, as equal as they come.
+inline void set_chunks(DecodeArgs& a) {
+  a.chunks = (a.group + 7) / 8;
+  a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
+}
+
+// A block of boxes_kernel: chunks of a head first (they read the same tile), then heads side by side, then runs of tokens.  False if
+// this cache is for rows_kernel.  Shared memory: what a stage takes, and the warps' meeting.
 template <bool FP8, int DQK, int DV>
-cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream_t stream) {
+bool plan_boxes(DecodeArgs& a, int nsm, int* stage_bytes, int* meeting_bytes) {
   using T = Tile<FP8, DQK, DV>;
   const CacheView& c = a.cache;
   constexpr int kWarps = kBoxWarps<T::kKeyBytes>;
-  *done = false;
   a.chunk_warps = piece(a.chunks, kWarps);
   a.heads = piece(c.H_kv, kWarps / a.chunk_warps);
   a.subs = 1;
@@ -1317,19 +1326,15 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   a.tile_log2 = log2_of(a.tile_tokens);
   int tokens = a.tile_tokens;
   while (tokens > 1 && c.page_size % tokens != 0) tokens /= 2;
-  if (tokens < 8) return cudaSuccess;
+  if (tokens < 8) return false;
   for (long long s : {c.k_page, c.k_tok, c.k_head, c.v_page, c.v_tok, c.v_head})
-    if (s <= 0 || s >= (1ll << 40)) return cudaSuccess;
+    if (s <= 0 || s >= (1ll << 40)) return false;
   a.box_log2 = log2_of(tokens);
   auto joint = [&](int row, long long head) {
     return row % 128 != 0 && head == row && static_cast<long long>(c.H_kv) * row % 128 == 0 && a.heads * row % 128 == 0;
   };
   a.joint_k = joint(T::kRowK, c.k_head);
   a.joint_v = joint(T::kRowV, c.v_head);
-  CUtensorMap kmap, vmap;
-  if (!make_map(&kmap, c.k, FP8, T::kRowK, c, c.k_page, c.k_tok, c.k_head, tokens, a.heads, a.joint_k) ||
-      !make_map(&vmap, c.v, FP8, T::kRowV, c, c.v_page, c.v_tok, c.v_head, tokens, a.heads, a.joint_v))
-    return cudaSuccess;
   // a block's queries: whole heads, or (more chunks than warps) part of one head's
   const int nq = a.chunks > a.chunk_warps ? a.chunk_warps * a.chunk_heads : a.heads * a.group;
   a.q_bytes = static_cast<int>(round_up(nq * T::kRowK, 16));
@@ -1340,18 +1345,44 @@ cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream
   int blocks = 3;
   while (blocks > 1 && blocks * (2 * stage + meeting + kStatic) > kSmemPerSm) --blocks;
   a.stages = std::min(kMaxStages, (std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) - meeting) / stage);
-  if (a.stages < 2) return cudaSuccess;
-  // Runs that are equal whatever the lengths, and a join; or, where that is at most kSerial tiles behind the equal split for the
-  // longest lengths that the table has room for, a request a group, and no join.
+  if (a.stages < 2) return false;
+  // Runs that are equal whatever the lengths, and a join; or a request a group, and no join.  What that can cost is the tiles of the
+  // longest request that the table has room for, which one block takes alone, be the others as short as they may: kLongest of them at
+  // most; and of the tables that short, those whose blocks are at most kSerial tiles behind the equal split when all requests are as long.
   const long long most = std::max(1ll, (a.max_len + a.tile_tokens - 1ll) / a.tile_tokens), at_once = std::max(1ll, static_cast<long long>(nsm) * blocks / a.units);
   const long long turns_whole = (a.B + at_once - 1) / at_once * most, turns_split = (a.B * most + at_once - 1) / at_once;
-  a.whole = turns_whole - turns_split <= kSerial;
+  a.whole = most <= kLongest && turns_whole - turns_split <= kSerial;
   a.groups = static_cast<int>(a.whole ? a.B : std::min(at_once, a.B * most));
+  *stage_bytes = stage;
+  *meeting_bytes = meeting;
+  return true;
+}
+
+template <bool FP8, int DQK, int DV>
+cudaError_t launch_boxes(DecodeArgs& a, bool* done, int nsm, int dev, cudaStream_t stream) {
+  using T = Tile<FP8, DQK, DV>;
+  const CacheView& c = a.cache;
+  CUtensorMap kmap, vmap;
+  int stage, meeting;
+  *done = plan_boxes<FP8, DQK, DV>(a, nsm, &stage, &meeting) &&
+          make_map(&kmap, c.k, FP8, T::kRowK, c, c.k_page, c.k_tok, c.k_head, 1 << a.box_log2, a.heads, a.joint_k) &&
+          make_map(&vmap, c.v, FP8, T::kRowV, c, c.v_page, c.v_tok, c.v_head, 1 << a.box_log2, a.heads, a.joint_v);
+  if (!*done) {
+    a.whole = 0;
+    return cudaSuccess;
+  }
   static std::atomic<int> set[kMaxDevices];
   if (!prepare(boxes_kernel<FP8, DQK, DV>, 2, dev, set)) return cudaErrorUnknown;
-  *done = true;
-  return launch_dependent(boxes_kernel<FP8, DQK, DV>, dim3(static_cast<unsigned>(a.groups) * a.units), (warps + 1) * 32, a.stages * stage + meeting, stream, a, kmap,
-                          vmap);
+  return launch_dependent(boxes_kernel<FP8, DQK, DV>, dim3(static_cast<unsigned>(a.groups) * a.units), (a.heads * a.chunk_warps * a.subs + 1) * 32,
+                          a.stages * stage + meeting, stream, a, kmap, vmap);
+}
+
+// Kernels that launch() enqueues (if the driver takes the tensor maps).
+template <bool FP8, int DQK, int DV>
+int launches(DecodeArgs& a, int nsm) {
+  int stage, meeting;
+  set_chunks(a);
+  return plan_boxes<FP8, DQK, DV>(a, nsm, &stage, &meeting) && a.whole ? 1 : 2;
 }
 
 template <bool FP8, int DQK, int DV>
@@ -1382,9 +1413,7 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   a.ml = reinterpret_cast<float2*>(ws);
   ws += round_up(2 * parts * a.H * 8, 256);
   a.part = reinterpret_cast<float*>(ws);
-  // chunks of up to 8 query heads, as equal as they come
-  a.chunks = (a.group + 7) / 8;
-  a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
+  set_chunks(a);
   bool done;
   cudaError_t e = launch_boxes<FP8, DQK, DV>(a, &done, nsm, dev, stream);
   if (e == cudaSuccess && !done) e = launch_rows<FP8, DQK, DV>(a, nsm, dev, stream);
@@ -1422,5 +1451,7 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
 // Instantiated in zyfa_decode_fp8.cu and zyfa_decode_bf16.cu.
 zyfa_status_t decode_fp8(decode::DecodeArgs& a, int D_qk, int nsm, int dev, uint8_t* ws, cudaStream_t stream);
 zyfa_status_t decode_bf16(decode::DecodeArgs& a, int D_qk, int nsm, int dev, uint8_t* ws, cudaStream_t stream);
+int decode_launches_fp8(decode::DecodeArgs& a, int D_qk, int nsm);
+int decode_launches_bf16(decode::DecodeArgs& a, int D_qk, int nsm);
 
 }  // namespace zyfa

@@ -7,4 +7,9 @@ zyfa_status_t decode_bf16(decode::DecodeArgs& a, int D_qk, int nsm, int dev, uin
          : D_qk == 128 ? decode::launch<false, 128, 128>(a, nsm, dev, ws, stream)
                        : decode::launch<false, 192, 128>(a, nsm, dev, ws, stream);
 }
+int decode_launches_bf16(decode::DecodeArgs& a, int D_qk, int nsm) {
+  return D_qk == 64    ? decode::launches<false, 64, 64>(a, nsm)
+         : D_qk == 128 ? decode::launches<false, 128, 128>(a, nsm)
+                       : decode::launches<false, 192, 128>(a, nsm);
+}
 }  // namespace zyfa

@@ -360,6 +360,12 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
  * Pure host arithmetic; 0 for sizes that the call refuses. */
 size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v, long long max_len);
 
+/* zyfa_attn_decode_paged_launches - number of kernel launches one zyfa_attn_decode_paged call with this cache and these sizes
+ * enqueues on a GPU of `sms` SMs (0: the current device's): 1 where a request is one block's work (tables that name a few
+ * tiles of tokens), 2 where the work is cut into equal parts, which a second kernel joins.  0 for B == 0 and for
+ * what the call refuses.  Host arithmetic, for accounting in benchmarks. */
+int zyfa_attn_decode_paged_launches(const zyfa_paged_cache_t* cache, int max_pages, int B, int H, int sms);
+
 /*
  * zyfa_check_errors - synchronise `stream`, then read and clear the current device's status word.
  * Returns ZYFA_ERR_TIMEOUT if any kernel of this library timed out since the last check, else

@@ -183,3 +183,22 @@ def test_plan_of_lengths_as_large_as_int32_holds(B, page, width, rows):
     slots = np.where(t < cap, pages[0, np.minimum(t // page, width - 1)].astype(np.int64) * page + t % page, -1)
     assert got.seq_lens.tolist() == [cap] * B and got.cu_tokens.tolist() == [min(b * most, most) for b in range(B + 1)]
     assert got.positions.tolist() == t.tolist() and got.slots.tolist() == slots.tolist() and got.cursor.tolist() == [pool]
+
+
+# ------------------------------------------------------------------------------------------------
+# batches of every size
+
+@pytest.mark.parametrize("kind,H,H_kv,B", [("bf16", 32, 32, 28), ("bf16", 32, 8, 114), ("fp8", 32, 8, 228), ("fp8", 16, 16, 114)])
+def test_decode_of_one_long_request_where_whole_ones_would_fill_the_gpu(kind, H, H_kv, B):
+    lens = [1 + 7 * b % 30 for b in range(B)]
+    lens[B // 3], lens[5], lens[6] = 3000, 0, 0
+    x = _Batch(kind, "64" if H_kv == 16 else "128", lens, H, H_kv, seed=B)
+    out, lse = x.attend()
+    f = 1 / 64.0 if kind == "fp8" else 1.0
+    for b, h, q, k, v in x.rows():
+        ref, ref_lse, w = P.decode_attention(q, k, v * f, x.scale)
+        if lens[b] == 0:
+            assert (out[b, h] == 0).all() and lse[b, h] == -math.inf
+            continue
+        tol, lse_tol = decode_tolerance(q, k, v, x.scale, f, ref, w, kind)
+        assert np.all(np.abs(out[b, h] - ref) <= tol) and abs(lse[b, h] - ref_lse) <= lse_tol + 2.0 ** -22 * abs(ref_lse)

@@ -1,5 +1,6 @@
 """Refusals and choices of the paged serving operators that need no GPU: caches whose rows overlap, loads that
 the dependent launch does not order."""
+import ctypes
 import itertools
 import os
 import random
@@ -91,3 +92,34 @@ def test_kernels_that_start_early_read_by_ordinary_loads(name):
     assert "launch_dependent" in text
     for word in ("__ldg", "ld.global.nc", "ld.nc", "__restrict__", "tex."):
         assert word not in text, word
+
+
+# Tokens that a request may have where it is one block's work: kLongest tiles of at most 128 tokens (4 warps of 32 keys)
+SMALL_TABLE = 8 * 128
+
+
+def _launches(lib, kind, shape, H, H_kv, page, tokens, B):  # noqa: F811
+    D, D_v = shape
+    c = _cache(dtype=kind, page_size=page, num_pages=1000, H_kv=H_kv, D_qk=D, D_v=D_v, k_page_stride=page * H_kv * D, k_token_stride=H_kv * D,
+               k_head_stride=D, v_page_stride=page * H_kv * D_v, v_token_stride=H_kv * D_v, v_head_stride=D_v)
+    return lib.zyfa_attn_decode_paged_launches(ctypes.byref(c), -(-tokens // page), B, H, 152)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("shape,H,H_kv", [((64, 64), 16, 16), ((64, 64), 2, 2), ((128, 128), 32, 8), ((128, 128), 32, 32), ((128, 128), 40, 40),
+                                          ((128, 128), 64, 4), ((128, 128), 32, 1), ((192, 128), 16, 16), ((192, 128), 128, 128)])
+def test_requests_of_wide_tables_are_split_whatever_their_number(lib, kind, shape, H, H_kv):  # noqa: F811
+    """Lengths are not known where the work is divided.  A table of many tokens may hold one long request among short ones at every
+    number of requests, also where whole requests would fill the GPU evenly were all as long."""
+    for page in (16, 64):
+        for tokens in (2 * SMALL_TABLE, 4096, 8192, 32768, 131072):
+            assert {_launches(lib, kind, shape, H, H_kv, page, tokens, B) for B in range(1, 513)} == {2}
+    # a few tokens are one block's work
+    assert _launches(lib, kind, shape, H, H_kv, 16, 16, 1) == 1 and _launches(lib, kind, shape, H, H_kv, 16, 32, 100) == 1
+
+
+def test_launch_counts_of_refused_calls_and_odd_pages(lib):  # noqa: F811
+    assert _launches(lib, 0, (128, 128), 32, 8, 16, 64, 32) == 1 and _launches(lib, 0, (128, 128), 32, 8, 7, 64, 32) == 2
+    assert _launches(lib, 0, (128, 128), 32, 8, 16, 64, 0) == 0 and _launches(lib, 0, (128, 96), 32, 8, 16, 64, 1) == 0
+    assert _launches(lib, 0, (128, 128), 31, 8, 16, 64, 1) == 0 and lib.zyfa_attn_decode_paged_launches(None, 4, 1, 8, 152) == 0
+    assert lib.zyfa_attn_decode_paged_launches(ctypes.byref(_cache()), 4, 1, 4, -1) == 0
