@@ -1,14 +1,19 @@
 """GPU tests of the paged serving operators where their numbers, checks or choices could go wrong beside the ordinary cases:
 the bits that the weights keep, values that are not finite, steps over capacity, batches of every size."""
+import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
 import torch
 
 from _paged_util import SHAPES, bits, decode_tolerance, dtype_of, f64, fill_tokens, make_cache, random_table, random_values
-from fp8_causal_prefill_gb300 import paged_decode_attn, paged_plan, zyfa_check_errors
+from fp8_causal_prefill_gb300 import api, paged_decode_attn, paged_plan, zyfa_check_errors
 from oracle import paged as P
+from test_paged_gpu import _FIRST_IN_CAPTURE, _Server
 
 pytestmark = pytest.mark.gpu
 
@@ -193,6 +198,87 @@ def test_decode_of_one_long_request_where_whole_ones_would_fill_the_gpu(kind, H,
     lens = [1 + 7 * b % 30 for b in range(B)]
     lens[B // 3], lens[5], lens[6] = 3000, 0, 0
     x = _Batch(kind, "64" if H_kv == 16 else "128", lens, H, H_kv, seed=B)
+    out, lse = x.attend()
+    f = 1 / 64.0 if kind == "fp8" else 1.0
+    for b, h, q, k, v in x.rows():
+        ref, ref_lse, w = P.decode_attention(q, k, v * f, x.scale)
+        if lens[b] == 0:
+            assert (out[b, h] == 0).all() and lse[b, h] == -math.inf
+            continue
+        tol, lse_tol = decode_tolerance(q, k, v, x.scale, f, ref, w, kind)
+        assert np.all(np.abs(out[b, h] - ref) <= tol) and abs(lse[b, h] - ref_lse) <= lse_tol + 2.0 ** -22 * abs(ref_lse)
+
+
+# ------------------------------------------------------------------------------------------------
+# steps whose attention is split and joined, captured
+
+def _launches(kc, vc, width, B, H):
+    c = api.PagedCache(kc.data_ptr(), vc.data_ptr(), 0 if kc.element_size() == 1 else 1, kc.shape[1], kc.shape[0], kc.shape[2], kc.shape[3], vc.shape[3],
+                       *kc.stride()[:3], *vc.stride()[:3])
+    return api.load_library().zyfa_attn_decode_paged_launches(ctypes.byref(c), width, B, H, 0)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("B", [5, 40, 140, 300])
+def test_captured_step_of_wide_tables_replays(kind, B):
+    """A captured token step over a table of 800 tokens a request, some of them idle, replayed equals eager steps: the join finds the lengths
+    that the step's plan has written, at every number of requests that reads them in a way of its own."""
+    H, H_kv, page, width, steps = 4, 2, 8, 100, 6
+    rng = np.random.default_rng(B)
+    prompts = rng.integers(0, 60, B)
+    prompts[0], prompts[B // 2], prompts[B - 1] = 500, 0, 0
+    new = np.ones(B, dtype=int)
+    new[rng.permutation(B)[: B // 4]] = 0
+    pages = int(sum(-(-(p + steps) // page) for p in prompts)) + 8
+    a, b = (_Server(kind, B, H, H_kv, "128", page, pages, width, seed=B) for _ in range(2))
+    assert _launches(a.kc, a.vc, width, B, H) == 2
+    for s in (a, b):
+        s.store(s.tokens(int(prompts.sum())), s.plan(i32(prompts), int(prompts.sum())))
+    new_t = i32(new)
+    static = [torch.zeros_like(t) for t in a.tokens(B)]
+
+    def step(s, x):
+        plan = s.plan(new_t, B)
+        q, _ = s.store(x, plan)
+        rows = plan.cu_tokens[:B].long().clamp(max=int(new.sum()) - 1)          # an idle request takes any row
+        return s.attend(q[rows]), plan
+
+    step(_Server(kind, B, H, H_kv, "128", page, pages, width, seed=1), static)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, plan = step(b, static)
+    for _ in range(steps):
+        x = a.tokens(B)
+        want, want_plan = step(a, x)
+        for t, v in zip(static, x):
+            t.copy_(v)
+        out.fill_(math.nan)
+        graph.replay()
+        assert all(torch.equal(p, w) for p, w in zip(plan, want_plan))
+        assert torch.equal(out, want) and bool(torch.isfinite(want).all())
+    assert torch.equal(bits(a.kc), bits(b.kc)) and torch.equal(a.table, b.table) and zyfa_check_errors() == 0
+    assert a.lens.tolist() == (prompts + steps * new).tolist()
+
+
+def test_first_calls_of_a_process_inside_a_capture_of_a_wide_table():
+    # kernel attributes of both kernels and the dependent launch of the join are set up within the capture
+    text = _FIRST_IN_CAPTURE.replace("[[-1] * 4]", "[[-1] * 64]")
+    assert text != _FIRST_IN_CAPTURE
+    assert _launches(torch.empty((6, 16, 2, 128), dtype=torch.bfloat16), torch.empty((6, 16, 2, 128), dtype=torch.bfloat16), 64, 1, 8) == 2
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", text], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("B", [256, 257, 700, 1100])
+def test_decode_of_many_requests_is_split(kind, B):
+    # up to 256 requests warps form the schedule, beyond that blocks, beyond a block's threads in several passes
+    lens = [b * 37 % 90 if b % 4 else 0 for b in range(B)]
+    lens[3], lens[B - 1] = 800, 5
+    x = _Batch(kind, "64", lens, 2, 1, page=16, width=200, seed=B)
+    assert _launches(x.kc, x.vc, 200, B, 2) == 2
     out, lse = x.attend()
     f = 1 / 64.0 if kind == "fp8" else 1.0
     for b, h, q, k, v in x.rows():
