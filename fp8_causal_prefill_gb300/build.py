@@ -19,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzyfa.so")
 BINDING = os.path.join(PKG, "_paged.so")
+BINDING_STAMP = "paged_binding.for"
 SOURCES = ["zyfa_api.cu", "zyfa_kernels_fp8.cu", "zyfa_kernels_fp8_exact.cu", "zyfa_kernels_bf16.cu",
            "zyfa_hadamard.cu", "zyfa_probe.cu", "zyfa_paged_plan.cu", "zyfa_rope_store.cu", "zyfa_decode.cu",
            "zyfa_decode_fp8.cu", "zyfa_decode_bf16.cu"]
@@ -69,6 +70,21 @@ def _torch_dir() -> str:
     return os.path.dirname(os.path.abspath(torch.__file__))
 
 
+def _binding_target() -> str:
+    """What the tensor binding is compiled against beside this package: its C++ ABI is that of one torch and one Python."""
+    import torch
+    return f"torch {torch.__version__} python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def binding_built_for() -> str | None:
+    """The ``_binding_target`` of the binding that was built last, if that is known."""
+    stamp = os.path.join(BUILD, BINDING_STAMP)
+    if not os.path.exists(stamp):
+        return None
+    with open(stamp) as f:
+        return f.read()
+
+
 def _cxx() -> str:
     for cand in (os.environ.get("CXX"), shutil.which("g++")):
         if cand and shutil.which(cand):
@@ -98,11 +114,15 @@ def link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of the tensor binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, BINDING_STAMP), "w") as f:
+        f.write(_binding_target())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if any source is newer than the library or its binding) and return the library path."""
-    if not force and not _inputs_newer(LIB) and not _inputs_newer(BINDING):
+    """Compile (if any source is newer than the library or its binding, or the binding was made for another torch) and
+    return the library path.  The library does not need the binding: it is linked also where the binding cannot be made, whose
+    error is raised then."""
+    if not force and not _inputs_newer(LIB) and not _inputs_newer(BINDING) and binding_built_for() == _binding_target():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -121,13 +141,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    link_binding(binding_obj)
+    link_binding(binding.result())
     return LIB
 
 

@@ -37,9 +37,13 @@ class PagedPlan(NamedTuple):
 
 
 def _load():
-    """The native binding; raises if it has not been built (there is no fallback path)."""
+    """The native binding; raises if it has not been built, or for another torch (there is no fallback path)."""
     global _native
+    from . import build
     load_library()
+    made_for = build.binding_built_for()
+    if made_for not in (None, build._binding_target()):
+        raise ZyfaError(4, f"the tensor binding was built for {made_for}; build it anew with `python -m fp8_causal_prefill_gb300.build`")
     path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_paged.so")
     if not os.path.exists(path):
         raise ZyfaError(4, f"{path} is missing; build it with `python -m fp8_causal_prefill_gb300.build`")
