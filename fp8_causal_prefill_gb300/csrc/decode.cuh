@@ -81,7 +81,7 @@ struct DecodeArgs {
   const float *q_desc, *k_desc, *v_desc;
   int* status;
   float scale_log2;
-  int desc_per_head;
+  int desc_per_head, desc_request;  // one value a KV head; values from a request to the next (0: all take the same)
   int max_len;  // max_pages * page_size
   int B, H, group;
   uint32_t page_magic;  // floor(t / page_size) = t * page_magic >> page_shift for t < 2^30
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     auto descales = [&](int request) {
       Descales d = {1.0f, 1.0f, 1.0f};
       if (FP8 && lane < a.heads) {
-        const int i = a.desc_per_head ? request * a.cache.H_kv + min(head0 + lane, a.cache.H_kv - 1) : 0;
+        const int i = a.desc_per_head ? request * a.desc_request + min(head0 + lane, a.cache.H_kv - 1) : 0;
         if (a.q_desc) d.q = a.q_desc[i];
         if (a.k_desc) d.k = a.k_desc[i];
         if (a.v_desc) d.v = a.v_desc[i];
@@ -1097,7 +1097,7 @@ __global__ void __launch_bounds__((kRowWarps<Tile<FP8, DQK, DV>::kKeyBytes>) * 3
         if (c.first) {
           float2 scale = {a.scale_log2, 1.0f};
           if (FP8) {
-            const int di = a.desc_per_head ? c.b * a.cache.H_kv + hk : 0;
+            const int di = a.desc_per_head ? c.b * a.desc_request + hk : 0;
             scale.x *= (a.q_desc ? a.q_desc[di] : 1.0f) * (a.k_desc ? a.k_desc[di] : 1.0f);
             scale.y = a.v_desc ? a.v_desc[di] : 1.0f;
           }

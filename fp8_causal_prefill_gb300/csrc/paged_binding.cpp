@@ -116,11 +116,11 @@ Table table_of(PyObject* o, int64_t B, int dev) {
 
 struct Descales {
   const float* p[3] = {nullptr, nullptr, nullptr};
-  int per_head = 0;
+  int per_head = 0;  // 0, 1 or 3, as the attention takes them
 };
 
-// Three descales, all per tensor or all per head.
-Descales descales_of(PyObject* const* o, int64_t per_head, int dev) {
+// Three descales, all per tensor, all of `heads` values or all of `requests` times as many.
+Descales descales_of(PyObject* const* o, int64_t heads, int64_t requests, int dev) {
   static const char* const names[3] = {"q_descale", "k_descale", "v_descale"};
   Descales d;
   int form = -1;
@@ -130,13 +130,13 @@ Descales descales_of(PyObject* const* o, int64_t per_head, int dev) {
     NEED_TYPE(t->scalar_type() == at::kFloat && t->is_contiguous(), names[i], " must be a contiguous float32 CUDA tensor or None");
     NEED_VALUE(cuda_index(*t) == dev, names[i], " must be on the same CUDA device as the other tensors");
     const int64_t n = t->numel();
-    NEED_VALUE(n == 1 || n == per_head, names[i], " must hold 1 or ", per_head, " values, got ", n);
-    const int mine = n == 1 ? 0 : 1;
-    NEED_VALUE(form < 0 || form == mine, "descales must all be per tensor or all per head");
+    NEED_VALUE(n == 1 || n == heads || n == requests * heads, names[i], " must hold 1, ", heads, " or ", requests * heads, " values, got ", n);
+    const int mine = n == 1 ? 0 : n == heads ? 3 : 1;
+    NEED_VALUE(form < 0 || form == mine, "descales must all be per tensor, all per head or all per request and head");
     form = mine;
     d.p[i] = static_cast<const float*>(t->data_ptr());
   }
-  d.per_head = form == 1;
+  d.per_head = form < 0 ? 0 : form;
   return d;
 }
 
@@ -332,12 +332,12 @@ PyObject* store(PyObject* const* a, Py_ssize_t n) {
     stride = axes > 1 ? pos->stride(0) : N;
     NEED_VALUE(stride >= N, "positions rows must not overlap");
   }
-  const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 8, H_kv, dev) : Descales();
+  const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 8, H_kv, 1, dev) : Descales();
   // (an empty tensor has no address, which the C call would take for one that is not given)
   if (N > 0)
     succeed(zyfa_rope_paged_store(q ? q->data_ptr() : nullptr, k ? k->data_ptr() : nullptr, v ? v->data_ptr() : nullptr, qs, ks, vs, qop,
                                 kop, vop, positions, stride, static_cast<const long long*>(slots), N, static_cast<int>(H), &cache.c,
-                                turns ? &spec : nullptr, d.p[0], d.p[1], d.p[2], d.per_head, stream_of(dev)),
+                                turns ? &spec : nullptr, d.p[0], d.p[1], d.p[2], d.per_head != 0, stream_of(dev)),
           "zyfa_rope_paged_store");
   return made ? THPVariable_Wrap(std::move(*made)) : keep(a[11]);
 }
@@ -363,7 +363,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw python_error();
     NEED_VALUE(scale == 0.0 || static_cast<float>(scale) != 0.0f, "softmax_scale is below the smallest float32");  // 0: the default
   }
-  const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 6, B * H_kv, dev) : Descales();
+  const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 6, H_kv, B, dev) : Descales();
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   const Tensor* given = optional(a[9], "out");
   std::optional<Tensor> made, lse;

@@ -55,7 +55,7 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
   const bool fp8 = cache->dtype == ZYFA_DTYPE_E4M3;
   const int es = zyfa::element_size(cache->dtype);
   if (table_stride < max_pages) return ZYFA_ERR_INVALID_ARG;
-  if (descale_per_kv_head != 0 && descale_per_kv_head != 1) return ZYFA_ERR_INVALID_ARG;
+  if (descale_per_kv_head != 0 && descale_per_kv_head != 1 && descale_per_kv_head != 3) return ZYFA_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale) || softmax_scale < 0.0f) return ZYFA_ERR_INVALID_ARG;
   if (q_batch_stride < 0) return ZYFA_ERR_INVALID_ARG;
   if (q_batch_stride > (1ll << 40)) return ZYFA_ERR_UNSUPPORTED;
@@ -85,7 +85,8 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
   a.q_desc = q_descale;
   a.k_desc = k_descale;
   a.v_desc = v_descale;
-  a.desc_per_head = descale_per_kv_head;
+  a.desc_per_head = descale_per_kv_head != 0;
+  a.desc_request = descale_per_kv_head == 1 ? H_kv : 0;
   // t / page_size for t < 2^30: with s = ceil(log2 page_size) and M = floor(2^(30+s) / page_size) + 1 the error of
   // t M / 2^(30+s) is below 1 / page_size
   int s = 0;

@@ -116,7 +116,8 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     ``seq_lens[b]`` tokens (int32 [B]) of the pages that ``block_table`` (int32 [B, max_pages]) names.
 
     Returns bfloat16 [B, H, D_v] (0 for a request without tokens), and with ``return_lse`` also the float32
-    log-sum-exp [B, H] (-inf without tokens).  e4m3 descales hold one value or B * H_kv values ([request][KV head]).
+    log-sum-exp [B, H] (-inf without tokens).  e4m3 descales hold one value, H_kv values, as ``rope_paged_store`` takes
+    them, or B * H_kv values ([request][KV head]).
     ``workspace`` (uint8 CUDA, ``paged_decode_workspace_bytes``) is allocated per call if not given; calls that
     may overlap on the GPU need one each.
     """

@@ -333,7 +333,8 @@ zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v,
  *   out               [B][H][D_v] bf16 dense, written in full: 0 for a request without tokens.
  *   lse               NULL, or [B][H] floats: ln sum_j exp(scale q.k) in real units, -inf without tokens.
  *   softmax_scale     0 selects 1/sqrt(D_qk); negative, NaN or infinite values are rejected.
- *   q/k/v_descale     e4m3 only: one float, or [B][H_kv] floats with descale_per_kv_head = 1; NULL means 1.
+ *   q/k/v_descale     e4m3 only: one float, or with descale_per_kv_head = 1 [B][H_kv] floats, with 3 [H_kv] floats that
+ *                     all requests share, as zyfa_rope_paged_store takes them; NULL means 1.
  *                     out and lse must not overlap the inputs or the workspace.
  *   workspace         device scratch of zyfa_attn_decode_paged_workspace_bytes() bytes, 16-byte aligned; its
  *                     contents on entry do not matter.  Calls that may overlap on the GPU (other streams, two

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from _paged_util import SHAPES, bits, decode_tolerance, dtype_of, f64, fill_tokens, make_cache, random_table, random_values
-from fp8_causal_prefill_gb300 import api, paged_decode_attn, paged_plan, zyfa_check_errors
+from fp8_causal_prefill_gb300 import api, paged_decode_attn, paged_plan, rope_paged_store, zyfa_check_errors
 from oracle import paged as P
 from test_paged_gpu import _FIRST_IN_CAPTURE, _Server
 
@@ -288,3 +288,37 @@ def test_decode_of_many_requests_is_split(kind, B):
             continue
         tol, lse_tol = decode_tolerance(q, k, v, x.scale, f, ref, w, kind)
         assert np.all(np.abs(out[b, h] - ref) <= tol) and abs(lse[b, h] - ref_lse) <= lse_tol + 2.0 ** -22 * abs(ref_lse)
+
+
+# ------------------------------------------------------------------------------------------------
+# descales per head through the whole step
+
+@pytest.mark.parametrize("page", [7, 16])
+@pytest.mark.parametrize("width", [None, 90])
+def test_descales_of_a_head_serve_the_store_and_the_attention(page, width):
+    """The H_kv values that the store divides by are those that the attention multiplies by, for any number of requests."""
+    B, H, H_kv, d, n = 3, 8, 4, 128, 41
+    rng = np.random.default_rng(page)
+    table, pages = random_table([n] * B, page, rng, width)
+    kc, vc = make_cache(pages, page, H_kv, "128", "fp8")
+    ds = [torch.from_numpy((rng.random(H_kv) + 0.5) / 64).float().cuda() for _ in range(3)]
+    q, k, v = (torch.from_numpy(rng.standard_normal((B * n, h, d))).to(torch.bfloat16).cuda() for h in (H, H_kv, H_kv))
+    t = np.arange(n)
+    slots = torch.from_numpy(np.concatenate([table[b, t // page].astype(np.int64) * page + t % page for b in range(B)])).cuda()
+    kw = dict(q_descale=ds[0], k_descale=ds[1], v_descale=ds[2])
+    q8 = rope_paged_store(q, k, v, kc, vc, slots, **kw)[n - 1:: n]
+    lens, table_t = i32([n] * B), torch.from_numpy(table).cuda()
+    out = paged_decode_attn(q8, kc, vc, table_t, lens, **kw)
+    wide = {name: x.repeat(B) for name, x in kw.items()}
+    assert torch.equal(out, paged_decode_attn(q8, kc, vc, table_t, lens, **wide)) and zyfa_check_errors() == 0
+    for b in range(B):                                                          # one request by itself
+        one = paged_decode_attn(q8[b: b + 1], kc, vc, table_t[b: b + 1], lens[:1], **kw)
+        ref = [P.decode_attention(f64(q8)[b, h] * f64(ds[0])[h // 2], f64(kc)[table[b, t // page], t % page, h // 2] * f64(ds[1])[h // 2],
+                                  f64(vc)[table[b, t // page], t % page, h // 2] * f64(ds[2])[h // 2], d ** -0.5)[0] for h in range(H)]
+        for got in (out[b], one[0]):
+            # within the tolerance of the weights and the output's rounding (2^-11 and 2^-8), with |v| of some units
+            assert np.all(np.abs(f64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * np.abs(f64(v)[b * n: (b + 1) * n]).max())
+    with pytest.raises(ValueError):                                             # two forms at once
+        paged_decode_attn(q8, kc, vc, table_t, lens, q_descale=ds[0], k_descale=wide["k_descale"])
+    with pytest.raises(ValueError):
+        paged_decode_attn(q8, kc, vc, table_t, lens, q_descale=ds[0][:2])

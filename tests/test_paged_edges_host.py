@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from fp8_causal_prefill_gb300 import build
-from test_paged_host import A, _cache, _store, lib  # noqa: F401
+from test_paged_host import A, _cache, _decode, _store, lib  # noqa: F401
 
 
 def _rows(strides, extents):
@@ -123,3 +123,9 @@ def test_launch_counts_of_refused_calls_and_odd_pages(lib):  # noqa: F811
     assert _launches(lib, 0, (128, 128), 32, 8, 16, 64, 0) == 0 and _launches(lib, 0, (128, 96), 32, 8, 16, 64, 1) == 0
     assert _launches(lib, 0, (128, 128), 31, 8, 16, 64, 1) == 0 and lib.zyfa_attn_decode_paged_launches(None, 4, 1, 8, 152) == 0
     assert lib.zyfa_attn_decode_paged_launches(ctypes.byref(_cache()), 4, 1, 4, -1) == 0
+
+
+def test_decode_forms_of_descales(lib):  # noqa: F811
+    # one value, one a request and head (1), one a head for all requests (3); for no requests, since addresses are not memory
+    assert [_decode(lib, _cache(), B=0, per=per) for per in (0, 1, 3)] == [0, 0, 0]
+    assert [_decode(lib, _cache(), B=0, per=per) for per in (2, 4, -1)] == [1, 1, 1]
