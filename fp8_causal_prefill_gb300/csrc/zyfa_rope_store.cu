@@ -2,8 +2,8 @@
 //
 // Pair i of a token turns by angle = position[axis(i)] * inv_freq[i].  Far positions need more than the 24
 // bits of an fp32 product, so the angle is taken in turns as a 64-bit fixed-point fraction: inv_freq is an
-// fp32 number m * 2^e, turns-per-position = m * 2^e / (2 pi) is formed once from the integer m and 2^66 / (2 pi)
-// to within 2^-64 of a turn, and position * fraction mod 2^64 is the exact reduction.  Its top 32 bits,
+// fp32 number m * 2^e, turns-per-position = m * 2^e / (2 pi) is formed once from the integer m and 2^66 / (2 pi),
+// off by at most (1 + |inv_freq| / 4) 2^-64, and position * fraction mod 2^64 is the exact reduction.  Its top 32 bits,
 // read as signed, are the angle in half turns within [-1, 1).
 //
 // Bound: HBM.  Each value is read once (bf16) and written once or twice (cache, dense copy).  A block takes a few
@@ -210,8 +210,15 @@ __global__ void __launch_bounds__(kThreads<DQK>) store_kernel(const __grid_const
     if (t0 < min(at_once, here)) {
       const int axis = (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]);
       const int* position = a.positions + axis * a.pos_stride + n0;
-      const uint64_t fraction = turn_fraction(a.inv_freq[p]);
-      for (int t = t0; t < here; t += at_once) angle_sincos(fraction, position[t], &s_sin[t][p], &s_cos[t][p]);
+      const float frequency = a.inv_freq[p];
+      const uint64_t fraction = turn_fraction(frequency);
+      const bool finite = isfinite(frequency);  // an infinity or NaN has no turns
+      for (int t = t0; t < here; t += at_once) {
+        float s, c;
+        angle_sincos(fraction, position[t], &s, &c);
+        s_sin[t][p] = finite ? s : NAN;
+        s_cos[t][p] = finite ? c : NAN;
+      }
     }
   }
   __syncthreads();

@@ -277,7 +277,8 @@ zyfa_status_t zyfa_paged_plan(const int* cached_lens, const int* new_lens, int B
 
 /* Rotary positions with one to four axes (for example time, height and width of an image or video patch). */
 typedef struct {
-  const float* inv_freq; /* device, [rot_dim / 2]: radians per unit of position, magnitude below 2^24    */
+  const float* inv_freq; /* device, [rot_dim / 2]: radians per unit of position, magnitude below 2^24;   */
+                         /* an infinity or NaN makes its pair NaN                                        */
   int rot_dim;           /* rotated channels, a multiple of 16 (0: no rotation)                          */
   int rot_offset;        /* first rotated channel, a multiple of 8; rot_offset + rot_dim <= D_qk         */
   int interleaved;       /* pair i of the rotated channels: 0: (i, i + rot_dim/2); 1: (2i, 2i + 1)       */

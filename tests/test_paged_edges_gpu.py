@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from _paged_util import SHAPES, bits, decode_tolerance, dtype_of, f64, fill_tokens, make_cache, random_table, random_values
-from fp8_causal_prefill_gb300 import api, paged_decode_attn, paged_plan, rope_paged_store, zyfa_check_errors
+from fp8_causal_prefill_gb300 import Rope, api, paged_decode_attn, paged_plan, rope_paged_store, zyfa_check_errors
 from oracle import paged as P
 from test_paged_gpu import _FIRST_IN_CAPTURE, _Server
 
@@ -322,3 +322,27 @@ def test_descales_of_a_head_serve_the_store_and_the_attention(page, width):
         paged_decode_attn(q8, kc, vc, table_t, lens, q_descale=ds[0], k_descale=wide["k_descale"])
     with pytest.raises(ValueError):
         paged_decode_attn(q8, kc, vc, table_t, lens, q_descale=ds[0][:2])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_store_shows_frequencies_that_are_not_finite(kind, interleaved):
+    """A pair whose frequency is infinite or NaN is NaN, as its angle is; every other channel is as with finite ones."""
+    n, H, H_kv, d = 40, 4, 2, 128
+    rng = np.random.default_rng(11)
+    q, k, v = (torch.from_numpy(rng.standard_normal((n, h, d))).to(torch.bfloat16).cuda() for h in (H, H_kv, H_kv))
+    inv = torch.from_numpy((10000.0 ** (-np.arange(0, d, 2) / d)).astype(np.float32)).cuda()
+    bad = inv.clone()
+    bad[3], bad[17], bad[63] = math.inf, math.nan, -math.inf
+    slots, positions = torch.arange(n, device="cuda"), i32(np.arange(n))
+    got = []
+    for f in (inv, bad):
+        kc, vc = make_cache(3, 16, H_kv, "128", kind)
+        out = rope_paged_store(q, k, v, kc, vc, slots, positions, Rope(f, interleaved=interleaved))
+        got.append([f64(t) for t in (out, kc.flatten(0, 1)[:n], vc.flatten(0, 1)[:n])])
+    lost = np.zeros(d, dtype=bool)
+    for i in (3, 17, 63):
+        lost[[2 * i, 2 * i + 1] if interleaved else [i, i + 64]] = True
+    for clean, x in zip(*got):
+        assert np.isfinite(clean).all() and np.array_equal(x[..., ~lost], clean[..., ~lost])
+    assert np.isnan(got[1][0][..., lost]).all() and np.isnan(got[1][1][..., lost]).all() and np.array_equal(got[1][2], got[0][2])
