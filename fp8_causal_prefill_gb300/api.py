@@ -28,7 +28,8 @@ EXPORTED = ("zyfa_attn_fwd_causal", "zyfa_attn_fwd_causal_ex", "zyfa_attn_fwd_ca
             "zyfa_probe_mma_rate",
             "zyfa_probe_mma_flops_per_iter", "zyfa_probe_mma_form_rate", "zyfa_probe_mma_form_flops_per_iter",
             "zyfa_paged_plan", "zyfa_rope_paged_store", "zyfa_attn_decode_paged",
-            "zyfa_attn_decode_paged_workspace_bytes", "zyfa_attn_decode_paged_launches")
+            "zyfa_attn_decode_paged_workspace_bytes", "zyfa_attn_decode_paged_launches",
+            "zyfa_selftest_stalled_decode")
 ZYFA_P_LEAN = 0
 ZYFA_P_EXACT = 1
 ZYFA_P_EXACT_NO_BLOCK_SCALE = 2
@@ -119,6 +120,8 @@ def load_library() -> ctypes.CDLL:
         lib.zyfa_attn_decode_paged.restype = ci
         lib.zyfa_attn_decode_paged_workspace_bytes.argtypes = [ci, ci, ci, ci, ll]
         lib.zyfa_attn_decode_paged_workspace_bytes.restype = sz
+        lib.zyfa_selftest_stalled_decode.argtypes = [vp, ll, cache, vp, ll, ci, vp, vp, ci, ci, vp, sz, vp]
+        lib.zyfa_selftest_stalled_decode.restype = ci
         lib.zyfa_attn_decode_paged_launches.argtypes = [cache, ci, ci, ci, ci]
         lib.zyfa_attn_decode_paged_launches.restype = ci
         _lib = lib

@@ -67,7 +67,7 @@ constexpr int kMaxSms = 160;          // the workspace is sized for at most this
 constexpr int kMaxWarpsPerSm = 16;    // ... of this many compute warps
 constexpr int kMaxDevices = 64;
 constexpr int kSmemPerBlock = 232448, kSmemPerSm = 233472;
-constexpr long long kWaitClocks = 1ll << 31;  // bound of every wait, about a second
+constexpr long long kWaitClocks = 1ll << 31, kShortWaitClocks = 1ll << 22;  // bound of every wait, about a second; that of the self-test
 
 struct DecodeArgs {
   const uint8_t* q;
@@ -86,6 +86,8 @@ struct DecodeArgs {
   int B, H, group;
   uint32_t page_magic;  // floor(t / page_size) = t * page_magic >> page_shift for t < 2^30
   int page_shift;
+  long long wait_clocks;
+  int stalled;  // self-test: nothing is loaded
   // schedule and workspace
   int whole;                    // a group is a request; no join
   int groups, units;            // `units` blocks (boxes_kernel) or warps (rows_kernel) make a group
@@ -107,13 +109,13 @@ struct DecodeArgs {
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// Waits for a phase, for at most kWaitClocks; the whole warp gets the same answer.
-__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity) {
+// Waits for a phase, for at most `clocks`; the whole warp gets the same answer.
+__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, long long clocks) {
   bool done = ptx::mbar_try_wait(bar, parity);
   if (!done) {
     const long long t0 = clock64();
     do done = ptx::mbar_try_wait(bar, parity);
-    while (!done && clock64() - t0 < kWaitClocks);
+    while (!done && clock64() - t0 < clocks);
   }
   return __all_sync(0xffffffffu, done);
 }
@@ -826,6 +828,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   }
 
   if (warp == warps) {
+    if (a.stalled) return;
     Cursor c;
     c.start(a, b, tile0, left);
     const int box = 1 << a.box_log2, row = lane << a.box_log2;  // this lane's box of a tile: its first token
@@ -874,7 +877,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
     uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
     bool begun = false;
     while (true) {
-      if (!mbar_wait_bounded(empty_s + 8 * stage, parity)) {
+      if (!mbar_wait_bounded(empty_s + 8 * stage, parity, a.wait_clocks)) {
         if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
         break;
       }
@@ -951,7 +954,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
         st = 0;
         par ^= 1;
       }
-      mbar_wait_bounded(full_s + 8 * st, par);
+      mbar_wait_bounded(full_s + 8 * st, par, a.wait_clocks);
     }
     if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
   };
@@ -959,7 +962,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
   int stage = 0;
   uint32_t parity = 0;
   while (true) {
-    if (!mbar_wait_bounded(full_s + 8 * stage, parity)) {
+    if (!mbar_wait_bounded(full_s + 8 * stage, parity, a.wait_clocks)) {
       give_up(stage, parity);
       return;
     }
@@ -1002,7 +1005,7 @@ __global__ void __launch_bounds__((kBoxWarps<Tile<FP8, DQK, DV>::kKeyBytes> + 1)
           const bool met = rows.finish_shared(a, h.b, q0, nq, direct, slot, lane, sub, a.subs, peers, all_ml, all_o, [&]() {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(meet_s);
-            const bool ok = mbar_wait_bounded(meet_s, meet_parity);
+            const bool ok = mbar_wait_bounded(meet_s, meet_parity, a.wait_clocks);
             meet_parity ^= 1;
             return ok;
           });

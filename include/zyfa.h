@@ -347,7 +347,8 @@ zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v,
  * Scores and sums are held in fp32; before the weights exp(s - max) multiply V they are rounded to fp16 for an e4m3
  * cache, whose values fp16 holds exactly, else to a sum of two bf16 numbers (16 bits).  Bitwise reproducible
  * for identical inputs on one GPU model.  One or two launches, asynchronous on `stream`; allocates nothing, no host
- * synchronisation.  A kernel that gives up on a copy (about a second) records ZYFA_ERR_TIMEOUT as the prefill does.
+ * synchronisation.  A kernel that gives up on a copy (about a second) records ZYFA_ERR_TIMEOUT as the prefill does; what
+ * its call writes is then unspecified.
  */
 zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache,
                                      const int* block_table, long long table_stride, int max_pages,
@@ -391,6 +392,17 @@ zyfa_status_t zyfa_check_errors(cudaStream_t stream);
 zyfa_status_t zyfa_selftest_stalled_pipeline(const void* q, const void* k, const void* v, void* out, int B, int S,
                                              int H, int H_kv, int D_qk, int D_v, zyfa_dtype_t dtype,
                                              cudaStream_t stream);
+
+/*
+ * zyfa_selftest_stalled_decode - the same for the attention over a paged cache: enqueues the kernels of
+ * zyfa_attn_decode_paged (same arguments and errors, default scale, no descales or lse) with nothing loaded and waits of
+ * about two milliseconds, which all run out.  Only caches whose pages are loaded as a whole (page sizes that are multiples of 8, no
+ * stride of 0) have such waits.  What `out` holds then is unspecified; zyfa_check_errors() returns ZYFA_ERR_TIMEOUT.
+ */
+zyfa_status_t zyfa_selftest_stalled_decode(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache,
+                                           const int* block_table, long long table_stride, int max_pages,
+                                           const int* seq_lens, void* out, int B, int H, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream);
 
 /* zyfa_status_string - static, human-readable name of a status code (never NULL). */
 const char* zyfa_status_string(zyfa_status_t status);

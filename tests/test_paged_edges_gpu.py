@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from _paged_util import SHAPES, bits, decode_tolerance, dtype_of, f64, fill_tokens, make_cache, random_table, random_values
-from fp8_causal_prefill_gb300 import Rope, api, paged_decode_attn, paged_plan, rope_paged_store, zyfa_check_errors
+from fp8_causal_prefill_gb300 import Rope, api, paged_decode_attn, paged_decode_workspace_bytes, paged_plan, rope_paged_store, zyfa_check_errors
 from oracle import paged as P
 from test_paged_gpu import _FIRST_IN_CAPTURE, _Server
 
@@ -212,10 +212,13 @@ def test_decode_of_one_long_request_where_whole_ones_would_fill_the_gpu(kind, H,
 # ------------------------------------------------------------------------------------------------
 # steps whose attention is split and joined, captured
 
+def _cache_of(kc, vc):
+    return api.PagedCache(kc.data_ptr(), vc.data_ptr(), 0 if kc.element_size() == 1 else 1, kc.shape[1], kc.shape[0], kc.shape[2], kc.shape[3],
+                          vc.shape[3], *kc.stride()[:3], *vc.stride()[:3])
+
+
 def _launches(kc, vc, width, B, H):
-    c = api.PagedCache(kc.data_ptr(), vc.data_ptr(), 0 if kc.element_size() == 1 else 1, kc.shape[1], kc.shape[0], kc.shape[2], kc.shape[3], vc.shape[3],
-                       *kc.stride()[:3], *vc.stride()[:3])
-    return api.load_library().zyfa_attn_decode_paged_launches(ctypes.byref(c), width, B, H, 0)
+    return api.load_library().zyfa_attn_decode_paged_launches(ctypes.byref(_cache_of(kc, vc)), width, B, H, 0)
 
 
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
@@ -346,3 +349,30 @@ def test_store_shows_frequencies_that_are_not_finite(kind, interleaved):
     for clean, x in zip(*got):
         assert np.isfinite(clean).all() and np.array_equal(x[..., ~lost], clean[..., ~lost])
     assert np.isnan(got[1][0][..., lost]).all() and np.isnan(got[1][1][..., lost]).all() and np.array_equal(got[1][2], got[0][2])
+
+
+# ------------------------------------------------------------------------------------------------
+# waits that run out
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("shape,H,H_kv,lens,width", [
+    ("128", 32, 8, [64, 0, 17], 4),                                             # a request a block, no join
+    ("128", 32, 8, [900, 0, 17, 400], 64),                                      # split and joined
+    ("64", 2, 1, [900, 5], 64),                                                 # warps that share a head's tokens and would meet
+    ("mla", 20, 2, [300], 64)])
+def test_decode_without_its_loads_times_out_and_the_next_call_is_right(kind, shape, H, H_kv, lens, width):
+    """Every wait of the kernel is bounded: without a load it ends, with a status that the host reads once, and the context, the status
+    word and the workspace serve the next call as ever."""
+    x = _Batch(kind, shape, lens, H, H_kv, width=width, seed=3)
+    B, d_v = len(lens), x.vc.shape[3]
+    ws = torch.empty(paged_decode_workspace_bytes(B, H, H_kv, d_v, width * x.page), dtype=torch.uint8, device="cuda")
+    want, want_lse = x.attend(workspace=ws)
+    out = torch.empty((B, H, d_v), dtype=torch.bfloat16, device="cuda")
+    table, lens_t, c = torch.from_numpy(x.table).cuda(), i32(lens), _cache_of(x.kc, x.vc)
+    stream = torch.cuda.current_stream().cuda_stream
+    st = api.load_library().zyfa_selftest_stalled_decode(x.q.data_ptr(), x.q.stride(0), ctypes.byref(c), table.data_ptr(), width, width,
+                                                         lens_t.data_ptr(), out.data_ptr(), B, H, ws.data_ptr(), ws.numel(), stream)
+    assert st == 0
+    assert zyfa_check_errors(stream) == 5 and zyfa_check_errors(stream) == 0    # ZYFA_ERR_TIMEOUT, read and cleared
+    got, got_lse = x.attend(workspace=ws)
+    assert np.array_equal(got, want) and np.array_equal(got_lse, want_lse)

@@ -129,3 +129,10 @@ def test_decode_forms_of_descales(lib):  # noqa: F811
     # one value, one a request and head (1), one a head for all requests (3); for no requests, since addresses are not memory
     assert [_decode(lib, _cache(), B=0, per=per) for per in (0, 1, 3)] == [0, 0, 0]
     assert [_decode(lib, _cache(), B=0, per=per) for per in (2, 4, -1)] == [1, 1, 1]
+
+
+def test_stalled_self_test_validates_its_arguments_like_the_call(lib):  # noqa: F811
+    def call(B=3, H=4, ws=A, q=A, page=16):
+        return lib.zyfa_selftest_stalled_decode(q or None, 512, ctypes.byref(_cache(page_size=page)), A, 8, 8, A, A, B, H, ws or None, 1 << 40, None)
+
+    assert [call(B=0), call(B=-1), call(H=3), call(ws=0), call(q=0), call(q=A + 8), call(page=0), call(B=65537)] == [0, 1, 1, 1, 1, 3, 1, 2]
