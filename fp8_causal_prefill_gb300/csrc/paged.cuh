@@ -33,6 +33,26 @@ struct CacheView {
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// `rows` runs of `bytes` bytes, `stride` bytes apart (none for a null pointer).
+struct Span {
+  uintptr_t begin, end;
+  long long bytes, rows, stride;
+  Span(const void* p, long long bytes_, long long rows_ = 1, long long stride_ = 0) : bytes(bytes_), rows(rows_), stride(stride_) {
+    const bool any = p && bytes > 0 && rows > 0;
+    begin = any ? reinterpret_cast<uintptr_t>(p) : 0;
+    end = any ? begin + static_cast<uintptr_t>((rows - 1) * stride + bytes) : 0;
+  }
+};
+
+// A dense output and `x` have a byte in common.
+inline bool overlap(const Span& out, const Span& x) {
+  if (out.end <= x.begin || x.end <= out.begin) return false;
+  if (x.rows == 1 || out.begin < x.begin + x.bytes) return true;
+  if (x.stride <= 0) return false;
+  const uintptr_t i = (out.begin - x.begin - x.bytes) / x.stride + 1;  // the first run that ends behind out's beginning
+  return x.begin + i * x.stride < out.end;
+}
+
 inline int element_size(zyfa_dtype_t t) { return t == ZYFA_DTYPE_E4M3 ? 1 : 2; }
 
 inline zyfa_status_t check_cache(const zyfa_paged_cache_t* c, CacheView* view) {

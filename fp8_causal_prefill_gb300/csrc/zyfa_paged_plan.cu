@@ -200,8 +200,17 @@ extern "C" zyfa_status_t zyfa_paged_plan(const int* cached_lens, const int* new_
   for (const void* p : ints)
     if (!aligned(p, 4)) return ZYFA_ERR_MISALIGNED;
   if (!aligned(slots, 8)) return ZYFA_ERR_MISALIGNED;
-  // every block reads the lengths, at its own time
-  if (B > 0 && (seq_lens == cached_lens || seq_lens == new_lens || cu_tokens == cached_lens || cu_tokens == new_lens)) return ZYFA_ERR_INVALID_ARG;
+  // Every block reads the lengths, the pool and the table, at its own time.  (Of the cursors, which may be one, see below.)
+  const long long n = B;
+  const zyfa::Span outs[5] = {{seq_lens, n * 4}, {cu_tokens, n * 4 + 4}, {positions, max_tokens * 4ll}, {slots, max_tokens * 8ll}, {cursor_out, 4}};
+  const zyfa::Span ins[5] = {{cached_lens, n * 4}, {new_lens, n * 4}, {free_pages, num_free * 4ll}, {block_table, max_pages * 4ll, n, table_stride * 4},
+                             {cursor_in != cursor_out ? cursor_in : nullptr, 4}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (zyfa::overlap(outs[i], outs[j])) return ZYFA_ERR_INVALID_ARG;
+    for (const zyfa::Span& x : ins)
+      if (zyfa::overlap(outs[i], x)) return ZYFA_ERR_INVALID_ARG;
+  }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ZYFA_ERR_CUDA;
   int* status = zyfa::device_status_word(dev);

@@ -396,6 +396,16 @@ extern "C" zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, con
     if (!aligned(p, 16)) return ZYFA_ERR_MISALIGNED;
   if (!aligned(slots, 8) || !aligned(q_descale, 4) || !aligned(k_descale, 4) || !aligned(v_descale, 4))
     return ZYFA_ERR_MISALIGNED;
+  const long long es = zyfa::element_size(cache->dtype), heads[3] = {static_cast<long long>(H) * D_qk, static_cast<long long>(H_kv) * D_qk,
+                                                                     static_cast<long long>(H_kv) * D_v};
+  const zyfa::Span outs[3] = {{q ? q_out : nullptr, N * heads[0] * es}, {k ? k_out : nullptr, N * heads[1] * es}, {k ? v_out : nullptr, N * heads[2] * es}};
+  const void* ins[3] = {q, k, v};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (zyfa::overlap(outs[i], outs[j])) return ZYFA_ERR_INVALID_ARG;
+    for (int j = 0; j < 3; ++j)
+      if (zyfa::overlap(outs[i], {ins[j], heads[j] * 2, N, strides[j] * 2})) return ZYFA_ERR_INVALID_ARG;
+  }
   if (k && kdims.meets(vdims, (a.cache.v - a.cache.k) / zyfa::element_size(cache->dtype), D_qk, D_v)) return ZYFA_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ZYFA_ERR_CUDA;

@@ -265,8 +265,7 @@ typedef struct {
  * ZYFA_ERR_CAPACITY, as it does when the tokens are more than max_tokens (the rows behind are dropped).
  * Asynchronous on `stream`, one launch (two for many rows with the cursor updated in place), allocates
  * nothing.  The outputs must not overlap one another or the inputs (cursors excepted).  Errors: ZYFA_ERR_INVALID_ARG (null pointers; B, max_tokens,
- * num_free or max_pages < 0, table_stride < max_pages, page_size outside 1 .. 65536, seq_lens or cu_tokens
- * in the place of cached_lens or new_lens),
+ * num_free or max_pages < 0, table_stride < max_pages, page_size outside 1 .. 65536, outputs that overlap),
  * ZYFA_ERR_UNSUPPORTED (max_pages * page_size beyond 2^30, B beyond 65536), ZYFA_ERR_MISALIGNED
  * (pointers not aligned to their type), ZYFA_ERR_CUDA.  B == 0 still writes cu_tokens[0], the cursor and the rows.
  */
@@ -310,7 +309,8 @@ typedef struct {
  *   q/k/v_descale     e4m3 only: device pointers to one float (or H_kv floats with descale_per_kv_head = 1;
  *                     query head h uses hk = h / (H / H_kv)); NULL means 1.  Ignored for bf16.
  *
- * Outputs must not overlap one another or the inputs.  Nor may rows of the cache: of the page, token and head strides each
+ * Outputs must not overlap one another or the inputs (q_out, k_out and v_out among themselves or with q, k or v:
+ * ZYFA_ERR_INVALID_ARG).  Nor may rows of the cache: of the page, token and head strides each
  * passes over all that lies within it, as in any view of a dense tensor (else, and where a row of K and one of V of the same
  * strides overlap, ZYFA_ERR_INVALID_ARG).  One launch, asynchronous on `stream`, allocates nothing.  N == 0 returns ZYFA_OK.
  */

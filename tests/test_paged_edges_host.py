@@ -1,4 +1,4 @@
-"""Refusals and choices of the paged serving operators that need no GPU: caches whose rows overlap, loads that
+"""Refusals and choices of the paged serving operators that need no GPU: memory that two would write, loads that
 the dependent launch does not order."""
 import ctypes
 import itertools
@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from fp8_causal_prefill_gb300 import build
-from test_paged_host import A, _cache, _decode, _store, lib  # noqa: F401
+from test_paged_host import A, _cache, _decode, _plan, _store, lib  # noqa: F401
 
 
 def _rows(strides, extents):
@@ -136,3 +136,42 @@ def test_stalled_self_test_validates_its_arguments_like_the_call(lib):  # noqa: 
         return lib.zyfa_selftest_stalled_decode(q or None, 512, ctypes.byref(_cache(page_size=page)), A, 8, 8, A, A, B, H, ws or None, 1 << 40, None)
 
     assert [call(B=0), call(B=-1), call(H=3), call(ws=0), call(q=0), call(q=A + 8), call(page=0), call(B=65537)] == [0, 1, 1, 1, 1, 3, 1, 2]
+
+
+# Buffers far apart, none of which is memory: calls that are accepted are made only where there is no GPU
+FAR = {name: (i + 1) << 32 for i, name in enumerate(("q", "k", "v", "qo", "ko", "vo", "kc", "vc", "c", "n", "t", "free", "ci", "co", "sl", "cu", "pos", "slots"))}
+
+
+def _accepted(call):
+    return torch.cuda.is_available() or call() == 4
+
+
+# 10 tokens of 4 and 2 heads of 128 channels, bf16; an e4m3 cache: q_out has 5120 bytes, k_out and v_out 2560
+STORE = dict(qs=1024, ks=1024, vs=1024, H=4, **{x: FAR[x] for x in ("q", "k", "v", "qo", "ko", "vo", "slots")})
+
+
+@pytest.mark.parametrize("kw,apart", [
+    ({}, True), (dict(k=FAR["q"] + 1024, v=FAR["q"] + 1536), True),             # slices of one projection
+    (dict(ko=FAR["qo"] + 5120), True), (dict(ko=FAR["qo"] - 2560), True), (dict(vo=FAR["ko"] + 2560), True),
+    (dict(qo=FAR["q"] + 9 * 2048 + 1024), True), (dict(qo=FAR["q"] - 5120), True), (dict(ko=FAR["q"], q=0), True),
+    (dict(ko=FAR["qo"]), False), (dict(ko=FAR["qo"] + 5104), False), (dict(ko=FAR["qo"] - 2544), False), (dict(vo=FAR["ko"]), False),
+    (dict(vo=FAR["qo"] + 16), False), (dict(qo=FAR["q"]), False), (dict(qo=FAR["q"] + 9 * 2048 + 1008), False), (dict(qo=FAR["q"] - 5104), False),
+    (dict(ko=FAR["k"] + 2048), False), (dict(vo=FAR["q"] + 1040), False), (dict(qo=FAR["v"] + 9 * 2048), False)])
+def test_store_refuses_outputs_that_overlap(lib, kw, apart):  # noqa: F811
+    call = lambda: _store(lib, _cache(k=FAR["kc"], v=FAR["vc"]), **{**STORE, **kw})  # noqa: E731
+    assert _accepted(call) if apart else call() == 1
+
+
+PLAN = dict(B=4, mp=8, ts=10, nf=10, mt=32, **{x: FAR[x] for x in ("c", "n", "t", "free", "ci", "co", "sl", "cu", "pos", "slots")})
+
+
+@pytest.mark.parametrize("kw,apart", [
+    ({}, True), (dict(co=FAR["ci"]), True), (dict(cu=FAR["sl"] + 16), True), (dict(sl=FAR["cu"] + 20), True), (dict(n=FAR["c"] + 16), True),
+    (dict(c=FAR["t"] + 32, B=1), True), (dict(co=FAR["t"] + 32), True), (dict(pos=FAR["slots"] + 256), True), (dict(sl=FAR["c"], B=0), True),
+    (dict(sl=FAR["c"] + 12), False), (dict(sl=FAR["n"] - 12), False), (dict(cu=FAR["c"] - 16), False), (dict(cu=FAR["sl"] + 12), False),
+    (dict(pos=FAR["slots"] + 252), False), (dict(slots=FAR["pos"] + 120), False), (dict(co=FAR["sl"] + 12), False), (dict(co=FAR["free"] + 36), False),
+    (dict(co=FAR["t"] + 28), False), (dict(co=FAR["t"] + 3 * 40), False), (dict(pos=FAR["free"] + 36), False), (dict(slots=FAR["ci"] - 248), False),
+    (dict(sl=FAR["t"] + 32), False)])
+def test_plan_refuses_results_that_overlap(lib, kw, apart):  # noqa: F811
+    call = lambda: _plan(lib, **{**PLAN, **kw})  # noqa: E731
+    assert _accepted(call) if apart else call() == 1
