@@ -40,7 +40,7 @@ struct Span {
   Span(const void* p, long long bytes_, long long rows_ = 1, long long stride_ = 0) : bytes(bytes_), rows(rows_), stride(stride_) {
     const bool any = p && bytes > 0 && rows > 0;
     begin = any ? reinterpret_cast<uintptr_t>(p) : 0;
-    end = any ? begin + static_cast<uintptr_t>((rows - 1) * stride + bytes) : 0;
+    end = any ? begin + static_cast<uintptr_t>(rows - 1) * static_cast<uintptr_t>(stride) + static_cast<uintptr_t>(bytes) : 0;
   }
 };
 

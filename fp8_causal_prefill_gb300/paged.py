@@ -60,8 +60,8 @@ def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     Pages that the new tokens start are taken from ``free_pages`` (int32) at ``cursor`` (int32, one value)
     and written into ``block_table`` (int32 [B, max_pages]; other entries stay as they are).  Token rows are
     numbered request after request; rows from the last token up to ``max_tokens`` get position 0 and slot -1.
-    ``out`` gives the result's tensors (for captured graphs); ``out.cursor`` may be ``cursor`` itself.  Without it they
-    are made in one allocation.
+    ``out`` gives the result's tensors (for captured graphs), none in the place of another or of an input, but
+    ``out.cursor`` may be ``cursor`` itself.  Without it they are made in one allocation.
     """
     return (_native or _load()).plan(cached_lens, new_lens, block_table, free_pages, cursor, page_size, max_tokens, out, PagedPlan)
 
@@ -89,14 +89,15 @@ def rope_paged_store(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Te
                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
                      v_out: torch.Tensor | None = None) -> torch.Tensor | None:
     """Rotate a step's bf16 queries [N, H, D_qk] and keys [N, H_kv, D_qk] by their positions, write keys and values
-    [N, H_kv, D_v] into cache slots ``slots`` (int64 [N]; below 0: a padding row, for which nothing is written),
+    [N, H_kv, D_v] into cache slots ``slots`` (int64 [N], distinct; below 0: a padding row, for which nothing is written),
     and return the queries in the cache's type.
 
     ``q``, ``k`` and ``v`` may be slices of one projection (dense heads, any token stride that is a multiple
     of 8).  ``positions`` is int32 [N], or [axes, N] for a ``rope`` with several axes; without ``rope`` nothing is
     rotated.  For an e4m3 cache the descales (float32, one value or H_kv values) divide what is stored.
-    ``k_out`` and ``v_out`` [N, H_kv, D] receive dense copies, as ``flash_attn_func`` reads them.  ``q`` may be None (keys and
-    values only), or ``k`` and ``v`` (queries only).
+    For a bf16 cache they are not used, as in the prefill.  ``k_out`` and ``v_out`` [N, H_kv, D] receive dense copies, as
+    ``flash_attn_func`` reads them.  ``q`` may be None (keys and values only), or ``k`` and ``v`` (queries only).  What is
+    written must not overlap what is read, nor rows of the cache one another.
     """
     return (_native or _load()).store(q, k, v, k_cache, v_cache, slots, positions, None if rope is None else rope._spec,
                                       q_descale, k_descale, v_descale, q_out, k_out, v_out)
@@ -117,9 +118,9 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 
     Returns bfloat16 [B, H, D_v] (0 for a request without tokens), and with ``return_lse`` also the float32
     log-sum-exp [B, H] (-inf without tokens).  e4m3 descales hold one value, H_kv values, as ``rope_paged_store`` takes
-    them, or B * H_kv values ([request][KV head]).
+    them, or B * H_kv values ([request][KV head]); for a bf16 cache they are not used.
     ``workspace`` (uint8 CUDA, ``paged_decode_workspace_bytes``) is allocated per call if not given; calls that
-    may overlap on the GPU need one each.
+    may overlap on the GPU need one each.  A NaN among a row's scores makes the row NaN.
     """
     return (_native or _load()).decode(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, q_descale, k_descale,
                                        v_descale, out, return_lse, workspace)

@@ -5,6 +5,7 @@ import math
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
 import pytest
@@ -376,3 +377,29 @@ def test_decode_without_its_loads_times_out_and_the_next_call_is_right(kind, sha
     assert zyfa_check_errors(stream) == 5 and zyfa_check_errors(stream) == 0    # ZYFA_ERR_TIMEOUT, read and cleared
     got, got_lse = x.attend(workspace=ws)
     assert np.array_equal(got, want) and np.array_equal(got_lse, want_lse)
+
+
+# ------------------------------------------------------------------------------------------------
+# several callers
+
+def test_steps_of_several_threads_and_streams():
+    """Threads that each run their own steps on their own stream get what they get alone."""
+    def run(seed, stream):
+        with torch.cuda.stream(stream):
+            s = _Server("fp8" if seed % 2 else "bf16", 40, 8, 2, "128", 16, 400, 100, seed=seed)
+            outs = []
+            for step in range(12):
+                new = [(37 * b + step) % 60 if step == 0 else 1 for b in range(40)]
+                plan = s.plan(i32(new), sum(new))
+                q, _ = s.store(s.tokens(sum(new)), plan)
+                if step:
+                    outs.append(s.attend(q))
+            stream.synchronize()
+            return outs
+
+    alone = [run(seed, torch.cuda.Stream()) for seed in range(4)]
+    with ThreadPoolExecutor(4) as pool:
+        for _ in range(3):
+            together = list(pool.map(run, range(4), [torch.cuda.Stream() for _ in range(4)]))
+            assert all(torch.equal(x, y) for a, b in zip(alone, together) for x, y in zip(a, b))
+    assert zyfa_check_errors() == 0
