@@ -36,13 +36,14 @@
 // 950 clocks per tile on it, as long as on the tile.)  rows_kernel: any page size and stride, by cp.async; each warp
 // loads its own tiles row by row into a ring of its own.
 //
-// Measured, with the bytes of the caches over the time, against 6.78 TB/s of a copy: 128 requests of 513 to 16384 tokens,
-// 8 KV heads of 128 e4m3 channels and 32 query heads, 178 us (6.8 TB/s; 0.86 of the DRAM's cycles, the tensor
-// cores busy for 0.19 of the time); 64 ragged requests in bf16 45.5 us (5.6 TB/s), 9 requests of 16 heads of 192/128 e4m3 channels
-// 58 us (6.0 TB/s).  The rest is the start (lengths, then pages, then tiles: three trips to memory) and the join, 6 to 8 us
-// together, which is also what a short context takes: 256 tokens 6 us, one request of 32768 tokens 18 us.
-// With 16 query heads per KV head a byte meets twice the arithmetic and widening V takes as long as its load: 4.1 TB/s
-// in e4m3, 5.8 in bf16.  (ldmatrix transposes bytes, so widening is one conversion per two values; with pairs of bytes and a
+// Measured on the GPU, in captured graphs, with the bytes of the caches over the time, against 6.78 TB/s of a copy: 128 requests of 513
+// to 16384 tokens, 8 KV heads of 128 e4m3 channels and 32 query heads, 178 to 180 us (6.7 TB/s; 0.87 of the DRAM's cycles, the tensor
+// cores busy for 0.19 of the time); 64 ragged requests in bf16 46.5 us (5.4 TB/s), 9 requests of 16 heads of 192/128 e4m3 channels
+// 59 us (6.0 TB/s).  The rest is the start (lengths, then pages, then tiles: three trips to memory) and the join, 6 to 8 us
+// together, which is also what a short context takes: 256 tokens 6 us, one request of 32768 tokens 18 us.  (The call of the 256 tokens, with
+// nothing else to do, takes the host 8 to 10.)
+// With 16 query heads per KV head a byte meets twice the arithmetic and widening V takes as long as its load: 4.2 TB/s
+// in e4m3, 5.7 in bf16.  (ldmatrix transposes bytes, so widening is one conversion per two values; with pairs of bytes and a
 // permutation before it, 48.4 us instead of 45.9.)  Two column groups that share the fragments of K and V take 168 registers a
 // thread, and with a third fewer warps the same time (48.7 to 47.6 us, 32 heads 37 to 41): chunks of 8 heads have a warp each.
 #pragma once

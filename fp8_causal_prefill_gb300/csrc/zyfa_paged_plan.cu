@@ -5,8 +5,8 @@
 // has position c_b + i, and slot page * P + position % P, where the page is a fresh one or the one of the
 // table that the last cached token lies in.
 //
-// Bound: latency (the tables of a step are a few KB to a MB): 2.2 us for one request, 2.9 us for 256 with one token each
-// and 3.1 us for 96 with 48 prompt chunks of up to 2048 tokens, of which an empty launch is about 2 us.  (One block with a barrier
+// Bound: latency (the tables of a step are a few KB to a MB): 2.4 us for one request, 3.1 us for 256 with one token each
+// and 3.1 us for 96 with 48 prompt chunks of up to 2048 tokens (on the GPU, in captured graphs), of which an empty launch is about 2 us.  (One block with a barrier
 // per chunk of rows: 337 us for the 256.)  One launch: every block takes a run of token rows,
 // forms the two prefix sums over the requests itself (1024 requests at a time in shared memory; the lengths come from
 // L2 once another block has read them) rather than wait for another block, and finds the request of a row by

@@ -262,7 +262,7 @@ typedef struct {
  *
  * A token that gets no slot (no free page left, a page beyond max_pages, a table entry below 0) has slot
  * -1, the page it would have started is -1 in the table, and zyfa_check_errors() then returns
- * ZYFA_ERR_CAPACITY, as it does when the tokens are more than max_tokens (the rows behind are dropped).
+ * ZYFA_ERR_CAPACITY, as it does when the tokens are more than max_tokens (the rows behind are dropped, their pages taken).
  * Asynchronous on `stream`, one launch (two for many rows with the cursor updated in place), allocates
  * nothing.  The outputs must not overlap one another or the inputs (cursors excepted).  Errors: ZYFA_ERR_INVALID_ARG (null pointers; B, max_tokens,
  * num_free or max_pages < 0, table_stride < max_pages, page_size outside 1 .. 65536, outputs that overlap),
