@@ -304,12 +304,7 @@ struct Header {
 // first and last tile of a request's part; the part is the whole request; it begins the request; not every key is valid; the run's last tile
 enum : int { kFirst = 1, kLast = 2, kDirect = 4, kSlot1 = 8, kPartial = 16, kEnd = 32 };
 
-// EARLY: before the kernel has waited for its predecessor.
-template <bool EARLY = false>
-__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
-  const int n = EARLY ? load_relaxed(a.seq_lens + b) : a.seq_lens[b];
-  return max(0, min(n, a.max_len));
-}
+__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) { return max(0, min(a.seq_lens[b], a.max_len)); }
 
 __device__ __forceinline__ void page_of(const DecodeArgs& a, int t, int* p, int* off) {
   *p = static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(t)) * a.page_magic) >> a.page_shift);
@@ -584,30 +579,26 @@ __device__ __forceinline__ void set_readers(int lane, int tokens_log2, int head,
 constexpr unsigned kGap = 2;
 // Up to kFew requests warps read all lengths themselves, else blocks do with barriers: 189 requests 20.0 us instead of 21.6.
 constexpr int kFew = 256;
-// The join reads them up to kFewJoin, else what the first kernel left (from the first request on 0.2 to 0.4 us more for the shortest
-// batches; up to 128 requests read, 0.3 us more for 64 ragged ones and 1.4 for 128, whose every row reads them from L2).
-constexpr int kFewJoin = 32;
+// The join reads them up to kFewJoin, else what the first kernel left (from the first request on 0.2 to 0.4 us more for short
+// batches; 256 requests of 32 heads, 100 tokens each: 21.0 us instead of 23.2).
+constexpr int kFewJoin = 128;  // four a lane
 
 struct Schedule {
   unsigned total = 0, per = 0;  // numbers, and those of a run
 
-  template <bool EARLY = false>
-  static __device__ __forceinline__ unsigned tiles(const DecodeArgs& a, int b) {
-    return b < a.B ? (length_of<EARLY>(a, b) + a.tile_tokens - 1u) >> a.tile_log2 : 0u;
-  }
+  static __device__ __forceinline__ unsigned tiles_of(const DecodeArgs& a, int length) { return (length + a.tile_tokens - 1u) >> a.tile_log2; }
+  static __device__ __forceinline__ unsigned tiles(const DecodeArgs& a, int b) { return b < a.B ? tiles_of(a, length_of(a, b)) : 0u; }
   static __device__ __forceinline__ unsigned numbers(unsigned tiles) { return tiles ? tiles + kGap : 0; }
   __device__ __forceinline__ void set(const DecodeArgs& a, unsigned sum) {
     total = sum ? sum - kGap : 0;
     per = (total + a.groups - 1) / a.groups;
   }
 
-  // Up to 32 N requests: every warp by itself, N requests a lane, without a barrier.  Returns the lane's first number.
-  template <int N, bool EARLY>
-  __device__ __forceinline__ unsigned scan_few(const DecodeArgs& a, unsigned (&n)[N]) {
+  // Up to 32 N requests: every warp by itself, N requests a lane, whose tiles n are, without a barrier.  Returns the lane's first number.
+  template <int N>
+  __device__ __forceinline__ unsigned scan_few(const DecodeArgs& a, const unsigned (&n)[N]) {
     const int lane = threadIdx.x & 31;
     unsigned sum = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) n[i] = tiles<EARLY>(a, lane * N + i);
 #pragma unroll
     for (int i = 0; i < N; ++i) sum += numbers(n[i]);
     unsigned incl = sum;
@@ -621,7 +612,10 @@ struct Schedule {
   }
   template <int N>
   __device__ __forceinline__ void find_few(const DecodeArgs& a, unsigned g, int* b, unsigned* tile, int* left) {
-    unsigned n[N], start = scan_few<N, false>(a, n), at = 0, number = 0, rest = 0;
+    unsigned n[N], at = 0, number = 0, rest = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n[i] = tiles(a, (threadIdx.x & 31) * N + i);
+    unsigned start = scan_few<N>(a, n);
     const unsigned first = g * per;
     bool here = false;
 #pragma unroll
@@ -643,12 +637,20 @@ struct Schedule {
     number = __shfl_sync(0xffffffffu, number, l);
     *left = hit ? max(0, static_cast<int>(min(first + per, total) - number)) : 0;
   }
-  // Numbers of request b's first tile and, were it one longer, of its next, for the join, before it has waited.
-  __device__ __forceinline__ void bounds(const DecodeArgs& a, int b, unsigned* p0, unsigned* p1) {
-    static_assert(kFewJoin <= 32);
-    unsigned n[1], mine = scan_few<1, true>(a, n);
-    *p0 = __shfl_sync(0xffffffffu, mine, b);
-    *p1 = *p0 + __shfl_sync(0xffffffffu, n[0], b);
+  // Numbers of request b's first tile and, were it one longer, of its next, from this lane's N lengths (behind the last one: 0).
+  template <int N>
+  __device__ __forceinline__ void bounds_few(const DecodeArgs& a, const int (&lengths)[N], int b, unsigned* p0, unsigned* p1) {
+    unsigned n[N], len = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n[i] = tiles_of(a, lengths[i]);
+    unsigned mine = scan_few<N>(a, n);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i < b % N) mine += numbers(n[i]);
+      if (i == b % N) len = n[i];
+    }
+    *p0 = __shfl_sync(0xffffffffu, mine, b / N);
+    *p1 = *p0 + __shfl_sync(0xffffffffu, len, b / N);
   }
 
   // Any number, the whole block: prefix: [blockDim.x] and sums: [warps] in shared memory.  Leaves a.starts for the join.
@@ -1160,15 +1162,28 @@ __global__ void __launch_bounds__(W * ROWS * 32, W == 16 ? 1 : W == 4 ? 7 : 3) j
   };
   __shared__ float s_o[W][D], s_m[W], s_l[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = blockIdx.y * D;
+  // Up to kFewJoin requests the bounds come from their lengths, read before the first kernel has ended.  It does not write them; what
+  // did had ended, and its writes were visible, when that kernel's blocks came from their own wait, after which each let this one
+  // start.  Only this SM's L1 could still hold what was there before, and these loads pass it by; of more than 32 requests a block
+  // makes them once.
+  __shared__ __align__(16) int s_length[kFewJoin];
+  auto early = [&](int i) { return i < a.B ? max(0, min(load_relaxed(a.seq_lens + i), a.max_len)) : 0; };
+  if (a.B > 32 && a.B <= kFewJoin) {
+    for (int i = threadIdx.x; i < kFewJoin; i += W * ROWS * 32) s_length[i] = early(i);
+    __syncthreads();
+  }
   const long long row = static_cast<long long>(blockIdx.x) * ROWS + (ROWS > 1 ? warp : 0);
   if (row >= static_cast<long long>(a.B) * a.H) return;
   const int b = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H), w = ROWS > 1 ? 0 : warp, tid = w * 32 + lane;
-  // Up to kFewJoin requests the bounds come from their lengths, read before the first kernel has ended.  It does not write them; what
-  // did had ended, and its writes were visible, when that kernel's blocks came from their own wait, after which each let this one
-  // start.  Only this SM's L1 could still hold what was there before, and these loads pass it by.
   Schedule plan;
   unsigned p0, p1;
-  if (a.B <= kFewJoin) plan.bounds(a, b, &p0, &p1);
+  if (a.B <= 32) {
+    const int n[1] = {early(lane)};
+    plan.bounds_few<1>(a, n, b, &p0, &p1);
+  } else if (a.B <= kFewJoin) {
+    const int4 n = reinterpret_cast<const int4*>(s_length)[lane];
+    plan.bounds_few<4>(a, {n.x, n.y, n.z, n.w}, b, &p0, &p1);
+  }
   wait_for_predecessor();
   if (a.B > kFewJoin) {
     p0 = a.starts[b];
