@@ -9,4 +9,4 @@ from .api import (ZyfaError, flash_attn_func, hadamard_quantize_e4m3, hadamard_q
                   library_path, load_library, zyfa_attn_fwd_causal, zyfa_attn_fwd_causal_ex, zyfa_check_errors,
                   zyfa_kernel_launches)
 from .paged import (PagedPlan, Rope, paged_decode_attn, paged_decode_workspace_bytes, paged_plan,  # noqa: F401
-                    rope_paged_store)
+                    paged_read, rope_paged_store)

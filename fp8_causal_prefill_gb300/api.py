@@ -19,6 +19,7 @@ _lock = threading.Lock()
 
 ZYFA_DTYPE_E4M3 = 0
 ZYFA_DTYPE_BF16 = 1
+ZYFA_DTYPE_E2M1 = 2  # paged caches only
 STATUS = {0: "ZYFA_OK", 1: "ZYFA_ERR_INVALID_ARG", 2: "ZYFA_ERR_UNSUPPORTED", 3: "ZYFA_ERR_MISALIGNED",
           4: "ZYFA_ERR_CUDA", 5: "ZYFA_ERR_TIMEOUT", 6: "ZYFA_ERR_CAPACITY", 7: "ZYFA_ERR_BAD_PAGE"}
 EXPORTED = ("zyfa_attn_fwd_causal", "zyfa_attn_fwd_causal_ex", "zyfa_attn_fwd_causal_host", "zyfa_check_errors",
@@ -29,7 +30,8 @@ EXPORTED = ("zyfa_attn_fwd_causal", "zyfa_attn_fwd_causal_ex", "zyfa_attn_fwd_ca
             "zyfa_probe_mma_flops_per_iter", "zyfa_probe_mma_form_rate", "zyfa_probe_mma_form_flops_per_iter",
             "zyfa_paged_plan", "zyfa_rope_paged_store", "zyfa_attn_decode_paged",
             "zyfa_attn_decode_paged_workspace_bytes", "zyfa_attn_decode_paged_launches",
-            "zyfa_selftest_stalled_decode")
+            "zyfa_selftest_stalled_decode", "zyfa_rope_paged_store_e2m1", "zyfa_paged_read",
+            "zyfa_attn_decode_paged_e2m1", "zyfa_selftest_stalled_decode_e2m1")
 ZYFA_P_LEAN = 0
 ZYFA_P_EXACT = 1
 ZYFA_P_EXACT_NO_BLOCK_SCALE = 2
@@ -47,6 +49,13 @@ class PagedCache(ctypes.Structure):
                 ("num_pages", ctypes.c_longlong), ("H_kv", ctypes.c_int), ("D_qk", ctypes.c_int), ("D_v", ctypes.c_int),
                 ("k_page_stride", ctypes.c_longlong), ("k_token_stride", ctypes.c_longlong),
                 ("k_head_stride", ctypes.c_longlong), ("v_page_stride", ctypes.c_longlong),
+                ("v_token_stride", ctypes.c_longlong), ("v_head_stride", ctypes.c_longlong)]
+
+
+class PagedScales(ctypes.Structure):
+    """zyfa_paged_scales_t: addresses and byte strides of a 4-bit cache's scales."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_page_stride", ctypes.c_longlong),
+                ("k_token_stride", ctypes.c_longlong), ("k_head_stride", ctypes.c_longlong), ("v_page_stride", ctypes.c_longlong),
                 ("v_token_stride", ctypes.c_longlong), ("v_head_stride", ctypes.c_longlong)]
 
 
@@ -124,6 +133,17 @@ def load_library() -> ctypes.CDLL:
         lib.zyfa_selftest_stalled_decode.restype = ci
         lib.zyfa_attn_decode_paged_launches.argtypes = [cache, ci, ci, ci, ci]
         lib.zyfa_attn_decode_paged_launches.restype = ci
+        scales = ctypes.POINTER(PagedScales)
+        lib.zyfa_rope_paged_store_e2m1.argtypes = [vp, vp, vp, ll, ll, ll, vp, vp, vp, vp, ll, vp, ll, ci, cache, scales, rope,
+                                                   vp, vp, ci, vp]
+        lib.zyfa_rope_paged_store_e2m1.restype = ci
+        lib.zyfa_paged_read.argtypes = [cache, scales, vp, ll, ci, vp, vp, ci, vp, vp, ll, ci, vp, vp, ci, vp, vp, ci, vp]
+        lib.zyfa_paged_read.restype = ci
+        lib.zyfa_attn_decode_paged_e2m1.argtypes = [vp, ll, cache, scales, vp, ll, ci, vp, vp, vp, ci, ci, cf, vp, vp, ci, vp,
+                                                    sz, vp]
+        lib.zyfa_attn_decode_paged_e2m1.restype = ci
+        lib.zyfa_selftest_stalled_decode_e2m1.argtypes = [vp, ll, cache, scales, vp, ll, ci, vp, vp, ci, ci, vp, sz, vp]
+        lib.zyfa_selftest_stalled_decode_e2m1.restype = ci
         _lib = lib
         return lib
 

@@ -22,7 +22,7 @@ BINDING = os.path.join(PKG, "_paged.so")
 BINDING_STAMP = "paged_binding.for"
 SOURCES = ["zyfa_api.cu", "zyfa_kernels_fp8.cu", "zyfa_kernels_fp8_exact.cu", "zyfa_kernels_bf16.cu",
            "zyfa_hadamard.cu", "zyfa_probe.cu", "zyfa_paged_plan.cu", "zyfa_rope_store.cu", "zyfa_decode.cu",
-           "zyfa_decode_fp8.cu", "zyfa_decode_bf16.cu"]
+           "zyfa_decode_fp8.cu", "zyfa_decode_bf16.cu", "zyfa_decode_e2m1.cu", "zyfa_rope_store_e2m1.cu", "zyfa_paged_read.cu"]
 # The attention kernel splits its registers between warpgroups at run time (setmaxnreg); the split is
 # sized for exactly this many registers per thread at launch, which every instantiation must get.
 KERNEL_REGS = 168

@@ -1423,21 +1423,9 @@ cudaError_t launch_rows(DecodeArgs& a, int nsm, int dev, cudaStream_t stream) {
   return launch_dependent(rows_kernel<FP8, DQK, DV>, dim3(grid), warps * 32, ring * warps, stream, a);
 }
 
-template <bool FP8, int DQK, int DV>
-zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t stream) {
-  // workspace: plan, (m, l), O
-  const long long parts = parts_at_most(a.B, a.H, a.cache.H_kv, a.max_len);
-  a.starts = reinterpret_cast<unsigned*>(ws);
-  ws += round_up((a.B + 2ll) * 4, 256);
-  a.ml = reinterpret_cast<float2*>(ws);
-  ws += round_up(2 * parts * a.H * 8, 256);
-  a.part = reinterpret_cast<float*>(ws);
-  set_chunks(a);
-  bool done;
-  cudaError_t e = launch_boxes<FP8, DQK, DV>(a, &done, nsm, dev, stream);
-  if (e == cudaSuccess && !done) e = launch_rows<FP8, DQK, DV>(a, nsm, dev, stream);
-  if (e != cudaSuccess) return ZYFA_ERR_CUDA;
-  if (a.whole) return ZYFA_OK;
+// The join, behind the kernel that left the parts.
+template <int DV>
+zyfa_status_t launch_join(DecodeArgs& a, int nsm, int dev, cudaStream_t stream) {
   // Few rows have many parts each; a ragged batch may have most of its parts in a few rows, whatever their average.  So a row has as
   // many warps as the GPU holds at once (53 ragged requests of 8 heads: 25.5 us with one, 22.2 with four; 6 requests of 12 heads
   // 20.6 with four, 17.4 with 16; 5 of 64 heads 11.9 with four, 10.8 with eight; 32 rows 19.3 with whole rows, 18.0 with their channels spread), and of many rows, most of
@@ -1446,6 +1434,7 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
   const long long parts_each = a.groups / a.B;
   constexpr int V = DV / 32;
   static std::atomic<int> set[5][kMaxDevices];
+  cudaError_t e;
   if (rows * V <= sms) {
     if (!prepare(join_kernel<DV, 16, 1, 1, 16>, 1, dev, set[0])) return ZYFA_ERR_CUDA;
     e = launch_dependent(join_kernel<DV, 16, 1, 1, 16>, dim3(rows, V), 512, 0, stream, a);
@@ -1463,6 +1452,94 @@ zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t 
     e = launch_dependent(join_kernel<DV, 1, 8, V, 8>, dim3((rows + 7) / 8), 256, 0, stream, a);
   }
   return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
+}
+
+// Workspace: plan, (m, l), O.
+inline void set_workspace(DecodeArgs& a, uint8_t* ws) {
+  const long long parts = parts_at_most(a.B, a.H, a.cache.H_kv, a.max_len);
+  a.starts = reinterpret_cast<unsigned*>(ws);
+  ws += round_up((a.B + 2ll) * 4, 256);
+  a.ml = reinterpret_cast<float2*>(ws);
+  ws += round_up(2 * parts * a.H * 8, 256);
+  a.part = reinterpret_cast<float*>(ws);
+}
+
+template <bool FP8, int DQK, int DV>
+zyfa_status_t launch(DecodeArgs& a, int nsm, int dev, uint8_t* ws, cudaStream_t stream) {
+  set_workspace(a, ws);
+  set_chunks(a);
+  bool done;
+  cudaError_t e = launch_boxes<FP8, DQK, DV>(a, &done, nsm, dev, stream);
+  if (e == cudaSuccess && !done) e = launch_rows<FP8, DQK, DV>(a, nsm, dev, stream);
+  if (e != cudaSuccess) return ZYFA_ERR_CUDA;
+  return a.whole ? ZYFA_OK : launch_join<DV>(a, nsm, dev, stream);
+}
+
+// ------------------------------------------------------------------------------------------------
+// checks that the caches' entry points share
+
+// What the call's sizes decide, checked.
+inline zyfa_status_t set_sizes(DecodeArgs* a, const zyfa_paged_cache_t* cache, int max_pages, int B, int H, unsigned types = kWideCaches) {
+  const zyfa_status_t st = check_cache(cache, &a->cache, types);
+  if (st != ZYFA_OK) return st;
+  if (B < 0 || H < 1 || H % cache->H_kv != 0 || max_pages < 0) return ZYFA_ERR_INVALID_ARG;
+  const long long max_len = static_cast<long long>(max_pages) * cache->page_size;
+  if (max_len > (1ll << 30)) return ZYFA_ERR_UNSUPPORTED;
+  if (B > 65536 || H > 65536 || static_cast<long long>(B) * H > (1ll << 24)) return ZYFA_ERR_UNSUPPORTED;
+  // the schedule numbers tiles, and a gap behind each request, in 31 bits
+  if (B * ((max_len + 15) / 16 + kGap) > 0x7fffffffll) return ZYFA_ERR_UNSUPPORTED;
+  a->max_len = static_cast<int>(max_len);
+  a->B = B;
+  a->H = H;
+  a->group = H / cache->H_kv;
+  return ZYFA_OK;
+}
+
+// A call's other arguments (sizes set), checked and filled in but for the device's; es: bytes of a query's value.
+inline zyfa_status_t set_call(DecodeArgs& a, const void* q, long long q_batch_stride, int es, const zyfa_paged_cache_t* cache, const int* block_table,
+                              long long table_stride, int max_pages, const int* seq_lens, void* out, float* lse, float softmax_scale,
+                              const float* q_descale, const float* k_descale, const float* v_descale, int descale_per_kv_head, void* workspace,
+                              size_t workspace_bytes, bool stalled) {
+  const int H_kv = cache->H_kv;
+  if (table_stride < max_pages) return ZYFA_ERR_INVALID_ARG;
+  if (descale_per_kv_head != 0 && descale_per_kv_head != 1 && descale_per_kv_head != 3) return ZYFA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || softmax_scale < 0.0f) return ZYFA_ERR_INVALID_ARG;
+  if (q_batch_stride < 0) return ZYFA_ERR_INVALID_ARG;
+  if (q_batch_stride > (1ll << 40)) return ZYFA_ERR_UNSUPPORTED;
+  if (a.B == 0) return ZYFA_OK;
+  if (!q || !out || !seq_lens || (max_pages > 0 && !block_table)) return ZYFA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || (q_batch_stride * es) % 16 != 0 || !aligned(out, 16) || !aligned(seq_lens, 4) ||
+      !aligned(block_table, 4) || !aligned(lse, 4) || !aligned(q_descale, 4) || !aligned(k_descale, 4) ||
+      !aligned(v_descale, 4))
+    return ZYFA_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < zyfa_attn_decode_paged_workspace_bytes(a.B, a.H, H_kv, cache->D_v, a.max_len))
+    return ZYFA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16)) return ZYFA_ERR_MISALIGNED;
+  if (softmax_scale == 0.0f) softmax_scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(cache->D_qk)));
+  a.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  a.q = static_cast<const uint8_t*>(q);
+  a.q_batch = q_batch_stride * es;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.seq_lens = seq_lens;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.q_desc = q_descale;
+  a.k_desc = k_descale;
+  a.v_desc = v_descale;
+  a.desc_per_head = descale_per_kv_head != 0;
+  a.desc_request = descale_per_kv_head == 1 ? H_kv : 0;
+  division_by(cache->page_size, 30, &a.page_magic, &a.page_shift);
+  a.wait_clocks = stalled ? kShortWaitClocks : kWaitClocks;
+  a.stalled = stalled;
+  return ZYFA_OK;
+}
+
+inline zyfa_status_t set_device(DecodeArgs& a, int* dev, int* nsm) {
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return ZYFA_ERR_CUDA;
+  a.status = device_status_word(*dev);
+  *nsm = std::min(device_sm_count(*dev), kMaxSms);
+  return a.status && *nsm > 0 ? ZYFA_OK : ZYFA_ERR_CUDA;
 }
 
 }  // namespace decode

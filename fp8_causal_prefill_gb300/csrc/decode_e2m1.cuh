@@ -1,0 +1,757 @@
+// Attention of one new token per request over a 4-bit paged cache: device code.
+//
+// The mathematics, the split of the work over requests, its schedule and the join are those of the e4m3 and bf16 caches
+// (decode.cuh): one pass with the running maximum and sum, tiles of all requests numbered one after the other and dealt evenly, parts
+// joined in order.  What differs is a tile: codes and scales come in, and are widened where they are used.
+//
+// * Products run with keys (or channels of V) as the rows of mma.sync.m16n8k16 and query heads as its 8 columns, in fp16: a code
+//   times its scale has 6 bits and is exact there, and a bf16 query is, over a power of two near its row's largest.
+// * K: the contraction may take the channels in any order, so lane 4g + t keeps 32 neighbouring channels of key g (16 bytes: one
+//   wide read of shared memory, conversions two values at a time in place, two scales) and the same channels of the queries.
+// * V: the contraction runs over keys, two of which share a register, while the two codes of a byte are channels.  ldmatrix
+//   transposes 16-bit elements, four channels of a key, so that a register holds them for two keys; each byte is converted and
+//   halves of pairs exchanged: 3 operations for 2 values, with the scale's product.
+// * Codes are numbers whatever their bits, so what lies in shared memory behind a request's end only needs scales of 0.
+//
+// Bound: HBM, 9/16 byte a value, and next to it the ALU that converts: a key and head of 128 channels takes some 8 of its
+// warp instructions for 144 bytes.
+#pragma once
+#include "decode.cuh"
+
+namespace zyfa {
+namespace decode4 {
+
+using namespace decode;
+
+constexpr int kKeys = 32;         // of a warp's turn
+constexpr int kWarps = 4;         // compute warps of a block at most
+constexpr int kStages = 3;        // of the ring at most
+constexpr int kMaxTokens = kWarps * kKeys;
+
+struct Args : DecodeArgs {
+  ScaleView scales;
+  int k_log2, v_log2;    // tokens whose rows share 128 bytes of shared memory (log2), where a block's heads take less
+  int scale8;            // scales of 8 bytes, copied as such
+  uint32_t order;        // the key within 8 that row g of the scores is: nibble g
+};
+
+template <int DQK, int DV>
+struct Tile4 {
+  static constexpr int kRowK = DQK / 2, kRowV = DV / 2, kScaleK = DQK / 16, kScaleV = DV / 16;
+  static constexpr int kKeyBytes = kRowK + kRowV + kScaleK + kScaleV;
+};
+
+// Codes of a tile lie in shared memory by token, a token's heads one after the other, in columns of 128 bytes [token][128] with the
+// 16-byte pieces of a row exchanged by its number, as TMA's 128-byte swizzle does; rows of 32 or 64 bytes share 128 (`log2`).
+__device__ __forceinline__ uint32_t place4(int token, int byte, int log2, uint32_t column) {
+  const int row = token >> log2, inner = ((token & ((1 << log2) - 1)) << (7 - log2)) + byte;
+  return (inner >> 7) * column + row * 128 + ((((inner >> 4) ^ row) & 7) << 4) + (inner & 15);
+}
+__host__ __device__ inline uint32_t column4(int tokens, int log2) { return static_cast<uint32_t>(tokens >> log2) * 128u; }
+__host__ __device__ inline uint32_t region4(int tokens, int pitch, int log2) { return column4(tokens, log2) * ((pitch + 127) / 128); }
+inline int share_log2(int pitch) { return pitch == 32 ? 2 : pitch == 64 ? 1 : 0; }
+
+__device__ __forceinline__ int key4(uint32_t order, int g) { return order >> (4 * g) & 7; }
+
+// 4 or 8 bytes global -> shared; `bytes` 0 writes zeros without reading.
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+// The barrier counts this lane once all its copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+  uint2 x;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t addr) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t lds2(uint32_t addr) {
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t addr) {
+  uint32_t x;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t halves(float lo, float hi) { return pack2<true>(lo, hi); }
+
+// Where a lane reads a warp's run of 32 keys, relative to the run's first key (a multiple of 32): K of keys 8u + row, V of 16 keys.
+template <int DQK, int DV>
+struct Reader4 {
+  static constexpr bool kWideK = DQK >= 128, kRestK = DQK % 128 != 0;  // 64 bytes of a row by 16, 32 by 8
+  static constexpr int kPairsV = DV / 64;                              // 32-channel pieces of V, two at a time
+  uint32_t wide[kWideK ? 4 : 1], rest[kRestK ? 4 : 1], value[2][kPairsV];
+  uint32_t k_scale, v_scale;
+
+  __device__ __forceinline__ void set(const Args& a, int lane, int head, int first) {
+    using T = Tile4<DQK, DV>;
+    const int g = lane >> 2, t = lane & 3, TT = a.tile_tokens;
+    const uint32_t kc = column4(TT, a.k_log2), vc = column4(TT, a.v_log2);
+    const int kb = head * T::kRowK, vb = head * T::kRowV;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int key = first + 8 * u + key4(a.order, g);
+      if (kWideK) wide[u] = place4(key, kb + 16 * t, a.k_log2, kc);
+      if (kRestK) rest[u] = place4(key, kb + (kWideK ? 64 : 0) + 8 * t, a.k_log2, kc);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int p = 0; p < kPairsV; ++p)
+        value[n][p] = place4(first + 16 * n + (lane >> 3 & 1) * 8 + key4(a.order, lane & 7), vb + 32 * p + (lane >> 4) * 16, a.v_log2, vc);
+    k_scale = (head * TT + first) * T::kScaleK;
+    v_scale = (head * TT + first) * T::kScaleV;
+  }
+};
+
+// Shared memory of a stage: K, V, their scales, queries.
+struct Stage4 {
+  uint32_t k, v, ks, vs, q;
+};
+
+// ------------------------------------------------------------------------------------------------
+// the state of a compute warp: up to 8 NC query heads against its tiles
+
+template <int DQK, int DV, int NC>
+struct Rows4 {
+  using T = Tile4<DQK, DV>;
+  using R = Reader4<DQK, DV>;
+  static constexpr int KB = kKeys / 16, kKSteps = DQK / 16, kPieces = DV / 32;
+  static constexpr float kLift = 15.0f;             // weights in fp16 up to 2^15, so that light ones keep their bits
+  static constexpr float kNoKey = 3.402823466e38f;  // ref before the first key: lifts every score above its negative over the limit
+
+  uint32_t qf[NC][kKSteps][2];  // B fragments of the queries
+  float o[NC][kPieces][2][4], m[NC][2], l[NC][2];  // this lane's two heads of each 8
+  F2 ref[NC], scale[NC];
+  float dv;
+
+  // A query's 16 neighbouring channels as B fragments; they are bits of two bf16 values a word.
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t top, uint32_t w) { return max(top, max(w & 0x7fff0000u, (w << 16) & 0x7fff0000u)); }
+
+  // Begins a request's part: its queries from shared memory, `count` dense bf16 rows.
+  __device__ __forceinline__ void begin(uint32_t queries, int count, float scale_, float dv_, int lane) {
+    const int t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      // rows behind the last head repeat it: their columns are computed and never written
+      const uint32_t row = queries + min(8 * c + (lane >> 2), count - 1) * (DQK * 2);
+      uint32_t w[DQK / 8];  // this lane's channels, two a word
+      if constexpr (R::kWideK) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = lds16(row + 64 * t + 16 * i);
+          w[4 * i] = x.x;
+          w[4 * i + 1] = x.y;
+          w[4 * i + 2] = x.z;
+          w[4 * i + 3] = x.w;
+        }
+      }
+      if constexpr (R::kRestK) {
+        constexpr int at = R::kWideK ? 16 : 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = lds16(row + (R::kWideK ? 256 : 0) + 32 * t + 16 * i);
+          w[at + 4 * i] = x.x;
+          w[at + 4 * i + 1] = x.y;
+          w[at + 4 * i + 2] = x.z;
+          w[at + 4 * i + 3] = x.w;
+        }
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < DQK / 8; ++i) top = top_bits(top, w[i]);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the largest magnitude to [2^14, 2^15), which an infinity or NaN stays beyond
+      const int shift = min(127, 141 - static_cast<int>(top >> 23));
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+#pragma unroll
+      for (int i = 0; i < kKSteps; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t x = w[2 * i + j];
+          qf[c][i][j] = halves(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+        }
+      const float undo = ldexpf(scale_, -shift);
+      scale[c] = {__shfl_sync(0xffffffffu, undo, 8 * t), __shfl_sync(0xffffffffu, undo, 8 * t + 4)};
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) o[c][i][j][0] = o[c][i][j][1] = o[c][i][j][2] = o[c][i][j][3] = 0.0f;
+      m[c][0] = m[c][1] = -INFINITY;
+      ref[c] = {kNoKey, kNoKey};
+      l[c][0] = l[c][1] = 0.0f;
+    }
+    dv = dv_;
+  }
+
+  // Two steps of the contraction: a word of key g and one of key g + 8, of one scale each.
+  __device__ __forceinline__ void two_steps(float (&x)[NC][4], int step, uint32_t a, uint32_t b, uint32_t sa, uint32_t sb) {
+    const uint32_t a0 = mul_f16x2(widen_e2m1<0>(a), sa), a1 = mul_f16x2(widen_e2m1<0>(b), sb);
+    const uint32_t a2 = mul_f16x2(widen_e2m1<1>(a), sa), a3 = mul_f16x2(widen_e2m1<1>(b), sb);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) mma<kF16>(x[c], a0, a1, a2, a3, qf[c][step][0], qf[c][step][1]);
+    const uint32_t b0 = mul_f16x2(widen_e2m1<2>(a), sa), b1 = mul_f16x2(widen_e2m1<2>(b), sb);
+    const uint32_t b2 = mul_f16x2(widen_e2m1<3>(a), sa), b3 = mul_f16x2(widen_e2m1<3>(b), sb);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) mma<kF16>(x[c], b0, b1, b2, b3, qf[c][step + 1][0], qf[c][step + 1][1]);
+  }
+
+  // One run of 32 keys.  k, v, ks, vs: where the run's first key lies in each region of the stage.  mask: the keys that count.
+  __device__ __forceinline__ void tile(const Stage4& s, const R& at, uint32_t order, uint32_t mask, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    // S^T: rows are keys, columns heads; then scores in units of log2
+    F2 x[NC][KB][2];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      float acc[NC][4];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.0f;
+      const uint32_t scales = s.ks + at.k_scale + (16 * kb + key4(order, g)) * T::kScaleK;
+      if constexpr (R::kWideK) {
+        const uint4 ka = lds16(s.k + at.wide[2 * kb]), kc = lds16(s.k + at.wide[2 * kb + 1]);
+        // the scales of this lane's two blocks of channels, of both keys
+        const uint32_t sa = widen_e4m3(lds2(scales + 2 * t)), sc = widen_e4m3(lds2(scales + 8 * T::kScaleK + 2 * t));
+        const uint32_t sa0 = prmt(sa, sa, 0x1010), sa1 = prmt(sa, sa, 0x3232), sc0 = prmt(sc, sc, 0x1010), sc1 = prmt(sc, sc, 0x3232);
+        two_steps(acc, 0, ka.x, kc.x, sa0, sc0);
+        two_steps(acc, 2, ka.y, kc.y, sa0, sc0);
+        two_steps(acc, 4, ka.z, kc.z, sa1, sc1);
+        two_steps(acc, 6, ka.w, kc.w, sa1, sc1);
+      }
+      if constexpr (R::kRestK) {
+        constexpr int first = R::kWideK ? 8 : 0;
+        const uint2 ka = lds8(s.k + at.rest[2 * kb]), kc = lds8(s.k + at.rest[2 * kb + 1]);
+        const uint32_t sa = widen_e4m3(lds1(scales + first + t) * 0x101u), sc = widen_e4m3(lds1(scales + 8 * T::kScaleK + first + t) * 0x101u);
+        two_steps(acc, first, ka.x, kc.x, sa, sc);
+        two_steps(acc, first + 2, ka.y, kc.y, sa, sc);
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        x[c][kb][0] = mul2({acc[c][0], acc[c][1]}, scale[c]);
+        x[c][kb][1] = mul2({acc[c][2], acc[c][3]}, scale[c]);
+      }
+    }
+    if (mask != 0xffffffffu) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (!((mask >> (kb * 16 + j * 8 + key4(order, g))) & 1))
+#pragma unroll
+            for (int c = 0; c < NC; ++c) x[c][kb][j] = {-INFINITY, -INFINITY};
+    }
+    uint32_t pf[NC][KB][2];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      // The reference m moves only when a key exceeds it: log2 of a weight is then above the lift.
+      F2 y[KB][2];
+      float over = -INFINITY;
+      auto weigh = [&]() {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            y[kb][j] = add2(x[c][kb][j], ref[c]);
+            over = fmaxf(over, fmaxf(y[kb][j].x, y[kb][j].y));
+          }
+      };
+      weigh();
+      if (__any_sync(0xffffffffu, over > kLift)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = m[c][e];
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+            top = e ? fmaxf(top, fmaxf(x[c][kb][0].y, x[c][kb][1].y)) : fmaxf(top, fmaxf(x[c][kb][0].x, x[c][kb][1].x));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const bool none = top == -INFINITY;
+          const float f = none ? 1.0f : exp2_approx(m[c][e] - top);
+          m[c][e] = top;
+          (e ? ref[c].y : ref[c].x) = none ? kNoKey : kLift - top;
+          l[c][e] *= f;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              o[c][i][j][e] *= f;
+              o[c][i][j][e + 2] *= f;
+            }
+        }
+        weigh();
+      }
+      // weights, transposed into the B operand (keys are now the contraction)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const F2 w = {exp2_approx(y[kb][j].x), exp2_approx(y[kb][j].y)};
+          const F2 sum = add2({l[c][0], l[c][1]}, w);
+          l[c][0] = sum.x;
+          l[c][1] = sum.y;
+          pf[c][kb][j] = transpose8x8(halves(w.x, w.y));
+        }
+    }
+    // O^T += V^T P^T: rows are channels of V, the contraction keys 2t, 2t + 1 of each 8 (in the scores' order)
+    const uint32_t pick = g < 4 ? 0x6240u : 0x7351u;  // of two keys' scales: those of this lane's block of every 32 channels
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      uint32_t sv[2][kPieces];  // scales of keys 2t, 2t + 1 of the first 8 and of the second
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t base = s.vs + at.v_scale + (16 * kb + 8 * j) * T::kScaleV;
+        const uint32_t first = base + key4(order, 2 * t) * T::kScaleV, second = base + key4(order, 2 * t + 1) * T::kScaleV;
+        if constexpr (DV == 128) {
+          const uint2 a = lds8(first), b = lds8(second);
+          const uint32_t lo = prmt(a.x, b.x, pick), hi = prmt(a.y, b.y, pick);
+          sv[j][0] = widen_e4m3(lo);
+          sv[j][1] = widen_e4m3_hi(lo);
+          sv[j][2] = widen_e4m3(hi);
+          sv[j][3] = widen_e4m3_hi(hi);
+        } else {
+          const uint32_t lo = prmt(lds4(first), lds4(second), pick);
+          sv[j][0] = widen_e4m3(lo);
+          sv[j][1] = widen_e4m3_hi(lo);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        uint32_t r[4];
+        if (p % 2 == 0) {
+          ldsm4t(s.v + at.value[kb][p / 2], r);
+          two_pieces[0] = r[2];
+          two_pieces[1] = r[3];
+        } else {
+          r[0] = two_pieces[0];
+          r[1] = two_pieces[1];
+        }
+        uint32_t f[2][4];  // [8 keys][channel]: keys 2t and 2t + 1
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t c0 = widen_e2m1<0>(r[j]), c1 = widen_e2m1<1>(r[j]), c2 = widen_e2m1<2>(r[j]), c3 = widen_e2m1<3>(r[j]);
+          f[j][0] = mul_f16x2(prmt(c0, c2, 0x5410), sv[j][p]);
+          f[j][1] = mul_f16x2(prmt(c0, c2, 0x7632), sv[j][p]);
+          f[j][2] = mul_f16x2(prmt(c1, c3, 0x5410), sv[j][p]);
+          f[j][3] = mul_f16x2(prmt(c1, c3, 0x7632), sv[j][p]);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          mma<kF16>(o[c][p][0], f[0][0], f[0][1], f[1][0], f[1][1], pf[c][kb][0], pf[c][kb][1]);
+          mma<kF16>(o[c][p][1], f[0][2], f[0][3], f[1][2], f[1][3], pf[c][kb][0], pf[c][kb][1]);
+        }
+      }
+    }
+  }
+
+  // Ends a request's part: writes its rows (`count` query heads from `first`), or (m, l, O) to part `slot` of the workspace.
+  __device__ __forceinline__ void finish(const DecodeArgs& a, int b, int first, int count, bool direct, long long slot, int lane) {
+    const int g = lane >> 2;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sum = total(c, e);
+        const int head = 8 * c + (lane & 3) * 2 + e;
+        if (head < count) {
+          const long long row = (direct ? static_cast<long long>(b) : slot) * a.H + first + head;
+          const float f = !direct ? dv : sum == 0.0f ? 0.0f : dv / sum;
+          if (g == 0) put_sums(a, row, direct, m[c][e], sum);
+          if (direct) {
+            __nv_bfloat16* out = a.out + row * DV + 4 * g;
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p)
+              *reinterpret_cast<uint2*>(out + 32 * p) = make_uint2(pack2<false>(o[c][p][0][e] * f, o[c][p][0][e + 2] * f),
+                                                                   pack2<false>(o[c][p][1][e] * f, o[c][p][1][e + 2] * f));
+          } else {
+            put_o(a.part + row * DV, c, e, f, g);
+          }
+        }
+      }
+  }
+
+  // The same for a request's part whose tiles' token runs `subs` warps shared (this one the sub-th): they leave (m, l, O) in
+  // shared memory, meet, join them in order, each warp some of the heads, and meet again before the memory is used anew.
+  // all_ml, all_o: [subs][8 NC] and [subs][8 NC][DV], `stride` warps from one sub's to the next; meet() is false if it gave up.
+  template <typename F>
+  __device__ __forceinline__ bool finish_shared(const DecodeArgs& a, int b, int first, int count, bool direct, long long slot, int lane, int sub,
+                                                int subs, int stride, float2* all_ml, float* all_o, F meet) {
+    constexpr int kHeads = 8 * NC;
+    const int g = lane >> 2;
+    float2* my_ml = all_ml + sub * stride * kHeads;
+    float* my_o = all_o + sub * stride * kHeads * DV;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sum = total(c, e);
+        const int head = 8 * c + (lane & 3) * 2 + e;
+        if (g == 0) my_ml[head] = make_float2(m[c][e], sum);
+        put_o(my_o + head * DV, c, e, dv, g);
+      }
+    if (!meet()) return false;
+    constexpr int V = DV / 32;
+    for (int head = sub; head < count; head += subs) {
+      float M = -INFINITY, L = 0.0f, x[V] = {};
+      for (int k = 0; k < subs; ++k) M = fmaxf(M, all_ml[k * stride * kHeads + head].x);
+      for (int k = 0; k < subs; ++k) {
+        const float2 ml = all_ml[k * stride * kHeads + head];
+        const float e = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - M);  // 0 for a run without a valid key, whose O is 0
+        L = fmaf(ml.y, e, L);
+        const float* y = all_o + (k * stride * kHeads + head) * DV + lane * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = fmaf(y[j], e, x[j]);
+      }
+      const long long row = (direct ? static_cast<long long>(b) : slot) * a.H + first + head;
+      if (lane == 0) put_sums(a, row, direct, M, L);
+      const float f = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        if (direct)
+          *reinterpret_cast<__nv_bfloat162*>(a.out + row * DV + lane * V + j) = __floats2bfloat162_rn(x[j] * f, x[j + 1] * f);
+        else
+          *reinterpret_cast<float2*>(a.part + row * DV + lane * V + j) = make_float2(x[j], x[j + 1]);
+      }
+    }
+    return meet();
+  }
+
+ private:
+  uint32_t two_pieces[2];  // the second piece of a pair that one ldmatrix read
+
+  __device__ __forceinline__ float total(int c, int e) const {
+    float sum = l[c][e];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    return sum;
+  }
+  static __device__ __forceinline__ void put_sums(const DecodeArgs& a, long long row, bool direct, float top, float sum) {
+    if (!direct)
+      a.ml[row] = make_float2(top - kLift, sum);
+    else if (a.lse)
+      a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum) - kLift) * 0.69314718055994531f;
+  }
+  // channels 4g to 4g + 3 of each 32
+  __device__ __forceinline__ void put_o(float* to, int c, int e, float f, int g) const {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      *reinterpret_cast<float4*>(to + 32 * p + 4 * g) = make_float4(o[c][p][0][e] * f, o[c][p][0][e + 2] * f, o[c][p][1][e] * f, o[c][p][1][e + 2] * f);
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+
+template <int DQK, int DV, int NC>
+__global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_kernel(const __grid_constant__ Args a) {
+  using T = Tile4<DQK, DV>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ unsigned s_prefix[(kWarps + 1) * 32], s_sums[kWarps + 1];
+  __shared__ __align__(16) Header s_header[kStages];
+  __shared__ float2 s_scale[kStages][kWarps];  // of the scores, and of V
+  __shared__ long long s_row[4][kMaxTokens];   // where a tile's tokens lie in the cache: K, V, their scales; below 0: nowhere
+  __shared__ unsigned s_mask[kStages][kWarps]; // its keys that count, 32 a word
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_meet[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x >> 5) - 1;  // compute warps; the next one loads
+  const int S = a.stages, TT = a.tile_tokens, k_pitch = a.heads * T::kRowK, v_pitch = a.heads * T::kRowV;
+  // a stage: K, V, scales of K, scales of V, queries
+  const uint32_t k_bytes = region4(TT, k_pitch, a.k_log2), v_bytes = region4(TT, v_pitch, a.v_log2);
+  const uint32_t ks_at = k_bytes + v_bytes, vs_at = ks_at + a.heads * TT * T::kScaleK, q_at = vs_at + a.heads * TT * T::kScaleV;
+  const uint32_t stage_bytes = q_at + a.q_bytes;
+  const uint32_t tiles_s = smem_addr(smem), full_s = smem_addr(s_full), empty_s = smem_addr(s_empty);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      ptx::mbar_init(full_s + 8 * i, 33);  // each lane's copies, and the header
+      ptx::mbar_init(empty_s + 8 * i, warps);
+    }
+    for (int i = 0; i < a.heads * a.chunk_warps; ++i) ptx::mbar_init(smem_addr(s_meet + i), a.subs);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  wait_for_predecessor();
+  if (!a.whole) let_successor_start();  // to the join
+
+  // this block: group g, KV heads from head0, chunks of query heads from chunk0
+  const unsigned g = blockIdx.x / a.units;
+  const int unit = blockIdx.x % a.units, chunk_units = (a.chunks + a.chunk_warps - 1) / a.chunk_warps;
+  const int head0 = unit / chunk_units * a.heads, chunk0 = unit % chunk_units * a.chunk_warps;
+  Schedule plan;
+  int b, left;
+  unsigned tile0;
+  if (a.whole) {
+    b = static_cast<int>(g);
+    tile0 = 0;
+    left = static_cast<int>(Schedule::tiles(a, b));
+  } else {
+    plan.find(a, s_prefix, s_sums, true, g, &b, &tile0, &left);
+  }
+  // a compute warp: a run of keys, a KV head, a chunk of its query heads
+  const int head = warp % a.heads, chunk = chunk0 + warp / a.heads % a.chunk_warps, sub = warp / (a.heads * a.chunk_warps);
+  const int hk = head0 + head, q0 = hk * a.group + chunk * a.chunk_heads, nq = min(a.chunk_heads, a.group - chunk * a.chunk_heads);
+  const bool idle = hk >= a.cache.H_kv || nq <= 0;  // the last block of a group may have heads or chunks too many
+  if (left == 0) {
+    if (a.whole && sub == 0 && !idle) {  // a request without tokens (the warp that loads has a larger sub)
+      const long long row = static_cast<long long>(b) * a.H + q0;
+      for (int i = lane; i < nq * DV / 2; i += 32) reinterpret_cast<__nv_bfloat162*>(a.out + row * DV)[i] = __floats2bfloat162_rn(0.0f, 0.0f);
+      if (a.lse)
+        for (int i = lane; i < nq; i += 32) a.lse[row + i] = -INFINITY;
+    }
+    return;
+  }
+
+  if (warp == warps) {
+    if (a.stalled) return;
+    const int heads = min(a.heads, a.cache.H_kv - head0);
+    Cursor c;
+    c.start(a, b, tile0, left);
+    // the block's query rows: whole heads, or (more chunks than warps) part of one head's
+    const int first_q = head0 * a.group + chunk0 * a.chunk_heads;
+    const int queries = chunk_units > 1 ? min(a.chunk_warps * a.chunk_heads, a.group - chunk0 * a.chunk_heads) : heads * a.group;
+    const uint8_t *k = a.cache.k + head0 * a.cache.k_head, *v = a.cache.v + head0 * a.cache.v_head;
+    const uint8_t *ks = a.scales.k + head0 * a.scales.k_head, *vs = a.scales.v + head0 * a.scales.v_head;
+    constexpr int kSets = kMaxTokens / 32;
+    int pg[kSets], off[kSets];  // page and place in it of tokens c.t + 32 i + lane
+    auto look_up = [&]() {
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        const int t = c.t + 32 * i + lane;
+        pg[i] = -1;
+        off[i] = 0;
+        if (32 * i < TT && t < c.len) {
+          int p;
+          page_of(a, t, &p, &off[i]);
+          pg[i] = a.table[c.b * a.table_stride + p];
+        }
+      }
+    };
+    look_up();
+    bool bad = false;
+    int stage = 0;
+    uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
+    while (true) {
+      if (!mbar_wait_bounded(empty_s + 8 * stage, parity, a.wait_clocks)) {
+        if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+        break;
+      }
+      const uint32_t base = tiles_s + stage * stage_bytes, bar = full_s + 8 * stage;
+      const int valid = min(TT, c.len - c.t);
+      bool whole = valid == TT;
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        if (32 * i >= TT) break;
+        const bool inside = 32 * i + lane < valid, ok = inside && pg[i] >= 0 && pg[i] < a.cache.num_pages;
+        bad |= inside && !ok;
+        const unsigned mask = __ballot_sync(0xffffffffu, ok);
+        whole = whole && mask == 0xffffffffu;
+        const long long page = pg[i], at = off[i];
+        s_row[0][32 * i + lane] = ok ? page * a.cache.k_page + at * a.cache.k_tok : -1;
+        s_row[1][32 * i + lane] = ok ? page * a.cache.v_page + at * a.cache.v_tok : -1;
+        s_row[2][32 * i + lane] = ok ? page * a.scales.k_page + at * a.scales.k_tok : -1;
+        s_row[3][32 * i + lane] = ok ? page * a.scales.v_page + at * a.scales.v_tok : -1;
+        if (lane == 0) s_mask[stage][i] = mask;
+      }
+      __syncwarp();
+      // codes: the pieces of a token's heads, 32 at a time
+      auto codes = [&](auto pieces, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to, int log2) {
+        constexpr int kPieces = decltype(pieces)::value;
+        const int all = heads * kPieces, step = 32 / all, rest = 32 % all;
+        const uint32_t column = column4(TT, log2);
+        int r = lane / all, p = lane % all;
+        while (r < valid) {
+          const long long row = rows[r];
+          if (row >= 0) copy16(to + place4(r, p * 16, log2, column), from + row + p / kPieces * head_stride + p % kPieces * 16, 16);
+          r += step;
+          p += rest;
+          if (p >= all) {
+            p -= all;
+            ++r;
+          }
+        }
+      };
+      codes(std::integral_constant<int, T::kRowK / 16>(), s_row[0], k, a.cache.k_head, base, a.k_log2);
+      codes(std::integral_constant<int, T::kRowV / 16>(), s_row[1], v, a.cache.v_head, base + k_bytes, a.v_log2);
+      // scales: zeros where there is no token
+      auto scales = [&](auto bytes, auto unit, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to) {
+        constexpr int kBytes = decltype(bytes)::value, kUnit = decltype(unit)::value, kUnits = kBytes / kUnit;
+        for (int h = 0; h < heads; ++h)
+          for (int x = lane; x < TT * kUnits; x += 32) {
+            const long long row = rows[x / kUnits];
+            copy_small<kUnit>(to + h * TT * kBytes + x * kUnit, from + (row < 0 ? 0 : row) + h * head_stride + x % kUnits * kUnit, row < 0 ? 0 : kUnit);
+          }
+      };
+      if (T::kScaleK == 8 && a.scale8)
+        scales(std::integral_constant<int, T::kScaleK>(), std::integral_constant<int, T::kScaleK == 8 ? 8 : 4>(), s_row[2], ks, a.scales.k_head, base + ks_at);
+      else
+        scales(std::integral_constant<int, T::kScaleK>(), std::integral_constant<int, 4>(), s_row[2], ks, a.scales.k_head, base + ks_at);
+      if (T::kScaleV == 8 && a.scale8)
+        scales(std::integral_constant<int, T::kScaleV>(), std::integral_constant<int, T::kScaleV == 8 ? 8 : 4>(), s_row[3], vs, a.scales.v_head, base + vs_at);
+      else
+        scales(std::integral_constant<int, T::kScaleV>(), std::integral_constant<int, 4>(), s_row[3], vs, a.scales.v_head, base + vs_at);
+      if (c.first) {
+        const uint8_t* q = a.q + c.b * a.q_batch + static_cast<long long>(first_q) * (DQK * 2);
+        for (int x = lane; x < queries * (DQK / 8); x += 32) copy16(base + q_at + x * 16, q + x * 16, 16);
+        if (lane < heads) {
+          const int i = a.desc_per_head ? c.b * a.desc_request + head0 + lane : 0;
+          s_scale[stage][lane] = {a.scale_log2 * (a.k_desc ? a.k_desc[i] : 1.0f), a.v_desc ? a.v_desc[i] : 1.0f};
+        }
+      }
+      arrive_after_copies(bar);
+      __syncwarp();
+      if (lane == 0) {
+        s_header[stage] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, 0};
+        ptx::mbar_arrive(bar);
+      }
+      c.left = c.left_after(TT);
+      if (c.left <= 0) break;
+      c.advance(a, TT);
+      look_up();
+      if (++stage == S) {
+        stage = 0;
+        parity ^= 1;
+      }
+    }
+    if (bad) atomicOr(a.status, kStatusBadPageBit);
+    copy_commit();
+    copy_wait<0>();
+    return;
+  }
+
+  Reader4<DQK, DV> reader;
+  const int run_keys = a.turns * kKeys;
+  reader.set(a, lane, head, sub * run_keys);
+  const uint32_t k_turn = column4(kKeys, a.k_log2), v_turn = column4(kKeys, a.v_log2);
+  const uint32_t my_query = q_at + (head * a.group + (chunk - chunk0) * a.chunk_heads) * (DQK * 2);
+  // where warps that share a head's tokens meet
+  const int peers = a.heads * a.chunk_warps, peer = warp % peers;
+  uint8_t* meeting = smem + S * stage_bytes;
+  float2* all_ml = reinterpret_cast<float2*>(meeting) + peer * 8 * NC;
+  float* all_o = reinterpret_cast<float*>(meeting + warps * 64 * NC) + peer * 8 * NC * DV;
+  const uint32_t meet_s = smem_addr(s_meet + peer);
+  uint32_t meet_parity = 0;
+  Rows4<DQK, DV, NC> rows;
+  int stage = 0;
+  uint32_t parity = 0;
+  while (true) {
+    if (!mbar_wait_bounded(full_s + 8 * stage, parity, a.wait_clocks)) {
+      if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+      return;
+    }
+    const Header h = s_header[stage];
+    const uint32_t base = tiles_s + stage * stage_bytes;
+    if (!idle) {
+      if (h.flags & kFirst) rows.begin(base + my_query, nq, s_scale[stage][head].x, s_scale[stage][head].y, lane);
+      for (int turn = 0; turn < a.turns; ++turn) {
+        const uint32_t mask = h.flags & kPartial ? s_mask[stage][sub * a.turns + turn] : 0xffffffffu;
+        if (mask == 0) continue;
+        const Stage4 s = {base + turn * k_turn, base + k_bytes + turn * v_turn, base + ks_at + turn * kKeys * T::kScaleK,
+                          base + vs_at + turn * kKeys * T::kScaleV, 0};
+        rows.tile(s, reader, a.order, mask, lane);
+      }
+      if (h.flags & kLast) {
+        const bool direct = h.flags & kDirect;
+        const long long slot = static_cast<long long>(g) * 2 + (h.flags & kSlot1 ? 1 : 0);
+        if (a.subs == 1) {
+          rows.finish(a, h.b, q0, nq, direct, slot, lane);
+        } else {
+          const bool met = rows.finish_shared(a, h.b, q0, nq, direct, slot, lane, sub, a.subs, peers, all_ml, all_o, [&]() {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(meet_s);
+            const bool ok = mbar_wait_bounded(meet_s, meet_parity, a.wait_clocks);
+            meet_parity ^= 1;
+            return ok;
+          });
+          if (!met) {
+            if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+            return;
+          }
+        }
+      }
+    }
+    if (h.flags & kEnd) return;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(empty_s + 8 * stage);
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// host side
+
+// Blocks as for the wider caches: chunks of a head first (they read the same tile), then heads side by side, then runs of tokens.
+template <int DQK, int DV, int NC>
+bool plan4(Args& a, int nsm, int* smem) {
+  using T = Tile4<DQK, DV>;
+  a.chunks = (a.group + 8 * NC - 1) / (8 * NC);
+  a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
+  a.chunk_warps = piece(a.chunks, kWarps);
+  a.heads = piece(a.cache.H_kv, kWarps / a.chunk_warps);
+  a.subs = 1;
+  while (a.subs * 2 * a.heads * a.chunk_warps <= kWarps) a.subs *= 2;
+  a.turns = 1;
+  while (a.turns * 2 * a.subs * a.heads <= kWarps) a.turns *= 2;
+  a.tile_tokens = a.subs * a.turns * kKeys;
+  a.tile_log2 = log2_of(a.tile_tokens);
+  a.units = (a.cache.H_kv + a.heads - 1) / a.heads * ((a.chunks + a.chunk_warps - 1) / a.chunk_warps);
+  const int k_pitch = a.heads * T::kRowK, v_pitch = a.heads * T::kRowV;
+  a.k_log2 = share_log2(k_pitch);
+  a.v_log2 = share_log2(v_pitch);
+  // Keys in the order in which the rows that one phase of the reads of K takes lie in different banks: two of 64 bytes, four of 32.
+  a.order = DQK >= 128 ? (a.k_log2 == 0 ? 0x73625140u : 0x76543210u) : a.k_log2 == 0 ? 0x75316420u : a.k_log2 == 1 ? 0x76325410u : 0x76543210u;
+  const ScaleView& s = a.scales;
+  a.scale8 = aligned(s.k, 8) && aligned(s.v, 8) && ((s.k_page | s.k_tok | s.k_head | s.v_page | s.v_tok | s.v_head) & 7) == 0;
+  const int nq = a.chunks > a.chunk_warps ? a.chunk_warps * a.chunk_heads : a.heads * a.group;
+  a.q_bytes = static_cast<int>(round_up(nq * DQK * 2, 16));
+  const int warps = a.heads * a.chunk_warps * a.subs;
+  const int stage = static_cast<int>(region4(a.tile_tokens, k_pitch, a.k_log2) + region4(a.tile_tokens, v_pitch, a.v_log2)) +
+                    a.heads * a.tile_tokens * (T::kScaleK + T::kScaleV) + a.q_bytes;
+  const int meeting = a.subs > 1 ? warps * 8 * NC * (DV + 2) * 4 : 0;  // (m, l, O) of the warps that share a head's tokens
+  constexpr int kStatic = 8192;  // the schedule's tables, headers and rows, with the 1 KiB that each block takes
+  int blocks = NC == 1 ? 3 : 2;
+  while (blocks > 1 && blocks * (2 * stage + meeting + kStatic) > kSmemPerSm) --blocks;
+  a.stages = std::min(kStages, (std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) - meeting) / stage);
+  if (a.stages < 2) return false;
+  const long long most = std::max(1ll, (a.max_len + a.tile_tokens - 1ll) / a.tile_tokens), at_once = std::max(1ll, static_cast<long long>(nsm) * blocks / a.units);
+  const long long turns_whole = (a.B + at_once - 1) / at_once * most, turns_split = (a.B * most + at_once - 1) / at_once;
+  a.whole = most <= kLongest && turns_whole - turns_split <= kSerial;
+  a.groups = static_cast<int>(a.whole ? a.B : std::min({at_once, a.B * most, parts_at_most(a.B, a.H, a.cache.H_kv, a.max_len)}));
+  *smem = a.stages * stage + meeting;
+  return true;
+}
+
+template <int DQK, int DV, int NC>
+zyfa_status_t launch4(Args& a, int nsm, int dev, uint8_t* ws, cudaStream_t stream) {
+  int smem;
+  set_workspace(a, ws);
+  if (!plan4<DQK, DV, NC>(a, nsm, &smem)) return ZYFA_ERR_UNSUPPORTED;
+  static std::atomic<int> set[kMaxDevices];
+  if (!prepare(decode4_kernel<DQK, DV, NC>, 2, dev, set)) return ZYFA_ERR_CUDA;
+  if (launch_dependent(decode4_kernel<DQK, DV, NC>, dim3(static_cast<unsigned>(a.groups) * a.units), (a.heads * a.chunk_warps * a.subs + 1) * 32, smem, stream,
+                       a) != cudaSuccess)
+    return ZYFA_ERR_CUDA;
+  return a.whole ? ZYFA_OK : launch_join<DV>(a, nsm, dev, stream);
+}
+
+}  // namespace decode4
+}  // namespace zyfa

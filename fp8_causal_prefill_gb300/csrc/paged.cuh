@@ -31,6 +31,13 @@ struct CacheView {
   int page_size, H_kv;
 };
 
+// Of the scales of a 4-bit cache, in bytes.
+struct ScaleView {
+  uint8_t* k;
+  uint8_t* v;
+  long long k_page, k_tok, k_head, v_page, v_tok, v_head;
+};
+
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // `rows` runs of `bytes` bytes, `stride` bytes apart (none for a null pointer).
@@ -53,11 +60,15 @@ inline bool overlap(const Span& out, const Span& x) {
   return x.begin + i * x.stride < out.end;
 }
 
-inline int element_size(zyfa_dtype_t t) { return t == ZYFA_DTYPE_E4M3 ? 1 : 2; }
+// Of what strides count: values, or bytes of two e2m1 codes.
+inline int element_size(zyfa_dtype_t t) { return t == ZYFA_DTYPE_BF16 ? 2 : 1; }
+inline long long row_bytes(zyfa_dtype_t t, int D) { return t == ZYFA_DTYPE_E2M1 ? D / 2 : static_cast<long long>(D) * element_size(t); }
 
-inline zyfa_status_t check_cache(const zyfa_paged_cache_t* c, CacheView* view) {
+enum : unsigned { kWideCaches = 1u << ZYFA_DTYPE_E4M3 | 1u << ZYFA_DTYPE_BF16, k4BitCaches = 1u << ZYFA_DTYPE_E2M1 };
+
+inline zyfa_status_t check_cache(const zyfa_paged_cache_t* c, CacheView* view, unsigned types = kWideCaches) {
   if (!c) return ZYFA_ERR_INVALID_ARG;
-  if (c->dtype != ZYFA_DTYPE_E4M3 && c->dtype != ZYFA_DTYPE_BF16) return ZYFA_ERR_INVALID_ARG;
+  if (static_cast<unsigned>(c->dtype) > 2u || !((types >> c->dtype) & 1)) return ZYFA_ERR_INVALID_ARG;
   if (c->page_size < 1 || c->page_size > 65536 || c->num_pages < 1 || c->H_kv < 1) return ZYFA_ERR_INVALID_ARG;
   const bool shape_ok = (c->D_qk == 64 && c->D_v == 64) || (c->D_qk == 128 && c->D_v == 128) ||
                         (c->D_qk == 192 && c->D_v == 128);
@@ -88,6 +99,29 @@ inline zyfa_status_t check_cache(const zyfa_paged_cache_t* c, CacheView* view) {
   return ZYFA_OK;
 }
 
+inline zyfa_status_t check_scales(const zyfa_paged_scales_t* s, ScaleView* view) {
+  if (!s || !s->k || !s->v) return ZYFA_ERR_INVALID_ARG;
+  bool whole = aligned(s->k, 4) && aligned(s->v, 4);
+  for (long long x : {s->k_page_stride, s->k_token_stride, s->k_head_stride, s->v_page_stride, s->v_token_stride, s->v_head_stride}) {
+    if (x < 0) return ZYFA_ERR_INVALID_ARG;
+    if (x > (1ll << 46)) return ZYFA_ERR_UNSUPPORTED;
+    whole = whole && x % 4 == 0;
+  }
+  if (!whole) return ZYFA_ERR_MISALIGNED;
+  *view = {static_cast<uint8_t*>(s->k), static_cast<uint8_t*>(s->v), s->k_page_stride, s->k_token_stride, s->k_head_stride,
+           s->v_page_stride, s->v_token_stride, s->v_head_stride};
+  return ZYFA_OK;
+}
+
+// floor(t / size) = t * magic >> shift for t < 2^bits (bits at most 31) and size of 1 to 65536: with s = ceil(log2 size) and
+// magic = floor(2^(bits + s) / size) + 1 the error of t * magic / 2^(bits + s) is below 1 / size.
+inline void division_by(int size, int bits, uint32_t* magic, int* shift) {
+  int s = 0;
+  while ((1 << s) < size) ++s;
+  *shift = bits + s;
+  *magic = static_cast<uint32_t>((1ull << (bits + s)) / static_cast<unsigned>(size) + 1);
+}
+
 // Programmatic dependent launch: the kernel may start while its predecessor on the stream still runs, and waits for it
 // on the device (wait_for_predecessor, before it touches memory), so that its launch costs the stream nothing.  Its inputs
 // are written within its lifetime, so it reads them by ordinary loads, which the wait orders, not as read-only data.
@@ -104,6 +138,38 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned bloc
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The two e2m1 codes of byte I of `x`, the lower one first, as fp16 (exact).
+template <int I>
+__device__ __forceinline__ uint32_t widen_e2m1(uint32_t x) {
+  uint32_t d;
+  if constexpr (I == 0)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(d) : "r"(x));
+  else if constexpr (I == 1)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(d) : "r"(x));
+  else if constexpr (I == 2)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(d) : "r"(x));
+  else
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(d) : "r"(x));
+  return d;
+}
+// Two e4m3 codes (low half of `x`) as fp16 (exact).
+__device__ __forceinline__ uint32_t widen_e4m3(uint32_t x) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t widen_e4m3_hi(uint32_t x) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(d) : "r"(x));
+  return d;
+}
+// An e2m1 code times an e4m3 scale has 6 bits and lies between 2^-10 and 2688: exact in fp16.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

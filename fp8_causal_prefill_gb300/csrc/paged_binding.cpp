@@ -69,12 +69,48 @@ int code_of(at::ScalarType t) {
 
 struct Cache {
   zyfa_paged_cache_t c;
+  zyfa_paged_scales_t scales;  // of a 4-bit cache
   int dev;
-  at::ScalarType type;
+  at::ScalarType type;  // of queries and dense rows: the cache's, or bfloat16 beside a 4-bit one
+  bool four;
 };
 
-Cache cache_of(PyObject* ko, PyObject* vo) {
+// A dimension of one element may carry any stride.
+int64_t stride_of(const Tensor& t, int i) { return t.size(i) > 1 ? t.stride(i) : t.size(3); }
+
+// Codes, two channels a byte, and the scales of 16 channels each.
+Cache cache4_of(const Tensor& k, const Tensor& v, PyObject* kso, PyObject* vso) {
+  const Tensor &ks = tensor(kso, "k_scales"), &vs = tensor(vso, "v_scales");
+  const Tensor* const all[4] = {&k, &v, &ks, &vs};
+  static const char* const names[4] = {"k_cache", "v_cache", "k_scales", "v_scales"};
+  const int dev = cuda_index(k);
+  for (int i = 0; i < 4; ++i) {
+    const at::ScalarType t = all[i]->scalar_type();
+    NEED_TYPE((t == at::kByte || t == (i < 2 ? at::ScalarType::Float4_e2m1fn_x2 : at::kFloat8_e4m3fn)) && all[i]->dim() == 4, names[i],
+              i < 2 ? " must be a float4_e2m1fn_x2 (or uint8) CUDA tensor [num_pages, page_size, H_kv, D / 2] beside k_scales and v_scales"
+                    : " must be a float8_e4m3fn (or uint8) CUDA tensor [num_pages, page_size, H_kv, D / 16]");
+    NEED_VALUE(dev >= 0 && cuda_index(*all[i]) == dev && all[i]->sizes().slice(0, 3) == k.sizes().slice(0, 3),
+               "k_cache, v_cache, k_scales and v_scales must agree in pages, page size, heads and CUDA device");
+    NEED_VALUE(all[i]->stride(3) == 1 || all[i]->size(3) == 1, "the last dimension of ", names[i], " must be contiguous");
+    NEED_VALUE(all[i]->size(3) < (1 << 28), names[i], " is too large in a dimension");
+  }
+  NEED_VALUE(ks.size(3) * 8 == k.size(3) && vs.size(3) * 8 == v.size(3), "k_scales and v_scales must hold one value for 16 channels (8 bytes of codes)");
+  NEED_VALUE(k.size(1) < (1 << 30) && k.size(2) < (1 << 30), "k_cache and v_cache are too large in a dimension");
+  Cache r;
+  r.dev = dev;
+  r.type = at::kBFloat16;
+  r.four = true;
+  r.c = {k.data_ptr(), v.data_ptr(), ZYFA_DTYPE_E2M1, static_cast<int>(k.size(1)), k.size(0), static_cast<int>(k.size(2)),
+         static_cast<int>(2 * k.size(3)), static_cast<int>(2 * v.size(3)), stride_of(k, 0), stride_of(k, 1), stride_of(k, 2),
+         stride_of(v, 0), stride_of(v, 1), stride_of(v, 2)};
+  r.scales = {ks.data_ptr(), vs.data_ptr(), stride_of(ks, 0), stride_of(ks, 1), stride_of(ks, 2), stride_of(vs, 0), stride_of(vs, 1), stride_of(vs, 2)};
+  return r;
+}
+
+Cache cache_of(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso) {
   const Tensor &k = tensor(ko, "k_cache"), &v = tensor(vo, "v_cache");
+  NEED_TYPE((kso == Py_None) == (vso == Py_None), "k_scales and v_scales go together");
+  if (kso != Py_None) return cache4_of(k, v, kso, vso);
   const int code = code_of(k.scalar_type());
   NEED_TYPE(code >= 0 && v.scalar_type() == k.scalar_type() && k.dim() == 4 && v.dim() == 4,
             "k_cache and v_cache must be e4m3 or bfloat16 CUDA tensors [num_pages, page_size, H_kv, D] of one type");
@@ -85,13 +121,13 @@ Cache cache_of(PyObject* ko, PyObject* vo) {
   NEED_VALUE(k.size(1) < (1 << 30) && k.size(2) < (1 << 30) && k.size(3) < (1 << 30) && v.size(3) < (1 << 30),
              "k_cache and v_cache are too large in a dimension");
   Cache r;
+  r.scales = {};
+  r.four = false;
   r.dev = dev;
   r.type = k.scalar_type();
   r.c = {k.data_ptr(), v.data_ptr(), static_cast<zyfa_dtype_t>(code), static_cast<int>(k.size(1)), k.size(0),
          static_cast<int>(k.size(2)), static_cast<int>(k.size(3)), static_cast<int>(v.size(3)),
-         // a dimension of one element may carry any stride
-         k.size(0) > 1 ? k.stride(0) : k.size(3), k.size(1) > 1 ? k.stride(1) : k.size(3), k.size(2) > 1 ? k.stride(2) : k.size(3),
-         v.size(0) > 1 ? v.stride(0) : v.size(3), v.size(1) > 1 ? v.stride(1) : v.size(3), v.size(2) > 1 ? v.stride(2) : v.size(3)};
+         stride_of(k, 0), stride_of(k, 1), stride_of(k, 2), stride_of(v, 0), stride_of(v, 1), stride_of(v, 2)};
   return r;
 }
 
@@ -271,11 +307,12 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
 }
 
 // store(q, k, v, k_cache, v_cache, slots, positions, (inv_freq, axis_pairs, offset, interleaved) or None, q_descale, k_descale,
-//       v_descale, q_out, k_out, v_out) -> q_out or None
+//       v_descale, q_out, k_out, v_out, k_scales, v_scales) -> q_out or None
 PyObject* store(PyObject* const* a, Py_ssize_t n) {
-  count(n, 14);
-  const Cache cache = cache_of(a[3], a[4]);
-  const int dev = cache.dev, code = cache.c.dtype;
+  count(n, 16);
+  const Cache cache = cache_of(a[3], a[4], a[14], a[15]);
+  const int dev = cache.dev, code = code_of(cache.type);
+  NEED_VALUE(!cache.four || a[8] == Py_None, "q_descale without an e4m3 query: queries of a 4-bit cache are bfloat16");
   const int64_t H_kv = cache.c.H_kv, D_qk = cache.c.D_qk, D_v = cache.c.D_v;
   const Tensor *q = optional(a[0], "q"), *k = optional(a[1], "k"), *v = optional(a[2], "v");
   const Tensor* some = q ? q : k;
@@ -332,9 +369,14 @@ PyObject* store(PyObject* const* a, Py_ssize_t n) {
     stride = axes > 1 ? pos->stride(0) : N;
     NEED_VALUE(stride >= N, "positions rows must not overlap");
   }
-  const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 8, H_kv, 1, dev) : Descales();
+  const Descales d = code == ZYFA_DTYPE_E4M3 || cache.four ? descales_of(a + 8, H_kv, 1, dev) : Descales();
   // (an empty tensor has no address, which the C call would take for one that is not given)
-  if (N > 0)
+  if (N > 0 && cache.four)
+    succeed(zyfa_rope_paged_store_e2m1(q ? q->data_ptr() : nullptr, k ? k->data_ptr() : nullptr, v ? v->data_ptr() : nullptr, qs, ks, vs, qop, kop,
+                                       vop, positions, stride, static_cast<const long long*>(slots), N, static_cast<int>(H), &cache.c, &cache.scales,
+                                       turns ? &spec : nullptr, d.p[1], d.p[2], d.per_head != 0, stream_of(dev)),
+            "zyfa_rope_paged_store_e2m1");
+  else if (N > 0)
     succeed(zyfa_rope_paged_store(q ? q->data_ptr() : nullptr, k ? k->data_ptr() : nullptr, v ? v->data_ptr() : nullptr, qs, ks, vs, qop,
                                 kop, vop, positions, stride, static_cast<const long long*>(slots), N, static_cast<int>(H), &cache.c,
                                 turns ? &spec : nullptr, d.p[0], d.p[1], d.p[2], d.per_head != 0, stream_of(dev)),
@@ -342,14 +384,16 @@ PyObject* store(PyObject* const* a, Py_ssize_t n) {
   return made ? THPVariable_Wrap(std::move(*made)) : keep(a[11]);
 }
 
-// decode(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, q_descale, k_descale, v_descale, out, return_lse, workspace)
+// decode(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, q_descale, k_descale, v_descale, out, return_lse, workspace,
+//        k_scales, v_scales)
 PyObject* decode(PyObject* const* a, Py_ssize_t n) {
-  count(n, 12);
-  const Cache cache = cache_of(a[1], a[2]);
-  const int dev = cache.dev, code = cache.c.dtype;
+  count(n, 14);
+  const Cache cache = cache_of(a[1], a[2], a[12], a[13]);
+  const int dev = cache.dev, code = code_of(cache.type);
   const int64_t H_kv = cache.c.H_kv, D_qk = cache.c.D_qk, D_v = cache.c.D_v;
   const Tensor& q = tensor(a[0], "q");
-  NEED_TYPE(code_of(q.scalar_type()) == code && q.dim() == 3, "q must be a CUDA tensor [B, H, D_qk] of the cache's type");
+  NEED_TYPE(code_of(q.scalar_type()) == code && q.dim() == 3, "q must be a CUDA tensor [B, H, D_qk] of the cache's type (bfloat16 for a 4-bit cache)");
+  NEED_VALUE(!cache.four || a[6] == Py_None, "q_descale without an e4m3 query: queries of a 4-bit cache are bfloat16");
   const int64_t B = q.size(0), H = q.size(1);
   NEED_VALUE(q.size(2) == D_qk && cuda_index(q) == dev, "q must have ", D_qk, " channels, on the cache's device");
   NEED_VALUE(H >= 1 && H < (1 << 30) && B < (1 << 30) && H_kv >= 1 && H % H_kv == 0, "the number of query heads must be a multiple of ",
@@ -363,7 +407,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw python_error();
     NEED_VALUE(scale == 0.0 || static_cast<float>(scale) != 0.0f, "softmax_scale is below the smallest float32");  // 0: the default
   }
-  const Descales d = code == ZYFA_DTYPE_E4M3 ? descales_of(a + 6, H_kv, B, dev) : Descales();
+  const Descales d = code == ZYFA_DTYPE_E4M3 || cache.four ? descales_of(a + 6, H_kv, B, dev) : Descales();
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   const Tensor* given = optional(a[9], "out");
   std::optional<Tensor> made, lse;
@@ -383,13 +427,71 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     scratch = fresh({static_cast<int64_t>(bytes)}, at::kByte, dev);
     ws = &*scratch;
   }
-  succeed(zyfa_attn_decode_paged(q.data_ptr(), B > 1 ? q.stride(0) : H * D_qk, &cache.c, t.p, t.stride, t.width,
+  if (cache.four)
+    succeed(zyfa_attn_decode_paged_e2m1(q.data_ptr(), B > 1 ? q.stride(0) : H * D_qk, &cache.c, &cache.scales, t.p, t.stride, t.width,
+                                        static_cast<const int*>(lens), out, lse ? static_cast<float*>(lse->data_ptr()) : nullptr,
+                                        static_cast<int>(B), static_cast<int>(H), static_cast<float>(scale), d.p[1], d.p[2], d.per_head,
+                                        ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(dev)),
+            "zyfa_attn_decode_paged_e2m1");
+  else
+    succeed(zyfa_attn_decode_paged(q.data_ptr(), B > 1 ? q.stride(0) : H * D_qk, &cache.c, t.p, t.stride, t.width,
                                  static_cast<const int*>(lens), out, lse ? static_cast<float*>(lse->data_ptr()) : nullptr,
                                  static_cast<int>(B), static_cast<int>(H), static_cast<float>(scale), d.p[0], d.p[1], d.p[2], d.per_head,
                                  ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(dev)),
           "zyfa_attn_decode_paged");
   PyObject* result = made ? THPVariable_Wrap(std::move(*made)) : keep(a[9]);
   return lse ? pack({result, THPVariable_Wrap(std::move(*lse))}) : result;
+}
+
+// read(k_cache, v_cache, block_table, cu_tokens, max_tokens or None, starts or None, type of the rows (a zyfa_dtype_t) or None, k_descale,
+//      v_descale, k_out_descale, v_out_descale, k_out, v_out, k_scales, v_scales) -> (k_out, v_out)
+PyObject* read(PyObject* const* a, Py_ssize_t n) {
+  count(n, 15);
+  const Cache cache = cache_of(a[0], a[1], a[13], a[14]);
+  const int dev = cache.dev;
+  const int64_t H_kv = cache.c.H_kv, D_qk = cache.c.D_qk, D_v = cache.c.D_v;
+  const Tensor& cu = tensor(a[3], "cu_tokens");
+  NEED_TYPE(cu.dim() == 1, "cu_tokens must be a contiguous int32 CUDA tensor [B + 1]");
+  NEED_VALUE(cu.size(0) >= 1 && cu.size(0) <= (1 << 30), "cu_tokens must hold one value more than there are requests");
+  const int64_t B = cu.size(0) - 1;
+  void* c = exact(cu, "cu_tokens", at::kInt, dev, {B + 1});
+  const Table t = table_of(a[2], B, dev);
+  void* starts = a[5] == Py_None ? nullptr : exact(tensor(a[5], "starts"), "starts", at::kInt, dev, {B});
+  const Tensor *ko = optional(a[11], "k_out"), *vo = optional(a[12], "v_out");
+  NEED_TYPE(!ko == !vo, "k_out and v_out go together");
+  NEED_VALUE(!ko || ko->dim() == 3, "k_out must be [max_tokens, H_kv, D_qk]");
+  NEED_VALUE(ko || a[4] != Py_None, "max_tokens or k_out and v_out must be given");
+  const int64_t rows = a[4] == Py_None ? ko->size(0) : integer(a[4], "max_tokens");
+  NEED_VALUE(rows >= 0 && (!ko || ko->size(0) == rows), "max_tokens must not be negative, and k_out and v_out must have that many rows");
+  int code = a[6] == Py_None ? (ko ? code_of(ko->scalar_type()) : ZYFA_DTYPE_BF16) : static_cast<int>(integer(a[6], "dtype"));
+  NEED_TYPE(code == ZYFA_DTYPE_E4M3 || code == ZYFA_DTYPE_BF16, "rows are bfloat16 or float8_e4m3fn");
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+  std::optional<Tensor> made[2];
+  void* out[2];
+  const int64_t width[2] = {D_qk, D_v};
+  for (int i = 0; i < 2; ++i) {
+    const Tensor* given = i ? vo : ko;
+    const char* const name = i ? "v_out" : "k_out";
+    if (given) {
+      NEED_TYPE(code_of(given->scalar_type()) == code && given->is_contiguous(), name, " must be a contiguous CUDA tensor of the rows' type");
+      NEED_VALUE(given->sizes() == at::IntArrayRef({rows, H_kv, width[i]}) && cuda_index(*given) == dev, name, " must have shape [", rows, ", ", H_kv, ", ",
+                 width[i], "] on the cache's device, got ", given->sizes());
+    } else {
+      made[i] = fresh({rows, H_kv, width[i]}, code == ZYFA_DTYPE_E4M3 ? at::kFloat8_e4m3fn : at::kBFloat16, dev);
+    }
+    out[i] = given ? given->data_ptr() : made[i]->data_ptr();
+  }
+  PyObject* const of_cache[3] = {Py_None, a[7], a[8]};
+  PyObject* const of_rows[3] = {Py_None, a[9], a[10]};
+  const Descales d = cache.c.dtype != ZYFA_DTYPE_BF16 ? descales_of(of_cache, H_kv, B, dev) : Descales();
+  NEED_VALUE(code == ZYFA_DTYPE_E4M3 || (a[9] == Py_None && a[10] == Py_None), "k_out_descale and v_out_descale are for float8_e4m3fn rows");
+  const Descales o = descales_of(of_rows, H_kv, 1, dev);
+  if (rows > 0 && B > 0)
+    succeed(zyfa_paged_read(&cache.c, cache.four ? &cache.scales : nullptr, t.p, t.stride, t.width, static_cast<const int*>(c),
+                            static_cast<const int*>(starts), static_cast<int>(B), out[0], out[1], rows, static_cast<zyfa_dtype_t>(code), d.p[1],
+                            d.p[2], d.per_head, o.p[1], o.p[2], o.per_head != 0, stream_of(dev)),
+            "zyfa_paged_read");
+  return pack({made[0] ? THPVariable_Wrap(std::move(*made[0])) : keep(a[11]), made[1] ? THPVariable_Wrap(std::move(*made[1])) : keep(a[12])});
 }
 
 // No C++ exception leaves a C entry: each becomes a Python one.
@@ -414,6 +516,7 @@ PyMethodDef g_methods[] = {
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<rope>)), METH_FASTCALL, nullptr},
     {"store", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<store>)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<decode>)), METH_FASTCALL, nullptr},
+    {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<read>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

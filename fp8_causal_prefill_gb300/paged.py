@@ -5,9 +5,14 @@ A serving step runs ``paged_plan`` (pages, slots and positions of its tokens fro
 ``paged_decode_attn`` (one query token per request attends over its pages); prompts go through
 ``flash_attn_func`` on the dense copies that ``rope_paged_store`` can write in the same pass.
 
+``paged_read`` reads tokens back as dense rows, for a prompt whose beginning is cached.
+
 A paged cache is a pair of CUDA tensors [num_pages, page_size, H_kv, D]: ``torch.float8_e4m3fn`` (or
 ``torch.uint8`` holding e4m3 codes) or ``torch.bfloat16``.  Only D has to be contiguous, so permuted views
-of [num_pages, H_kv, page_size, D] tensors and halves of a combined tensor work too.  Every call runs
+of [num_pages, H_kv, page_size, D] tensors and halves of a combined tensor work too.  A 4-bit cache is two such pairs: e2m1 codes
+[num_pages, page_size, H_kv, D / 2] (``torch.float4_e2m1fn_x2``, or ``torch.uint8``), channel 2i in the low half of byte i, and
+``k_scales`` and ``v_scales`` [num_pages, page_size, H_kv, D / 16] (``torch.float8_e4m3fn``, or ``torch.uint8``), one scale for 16
+channels of a token and head; a value is code * scale * descale.  Queries beside it are bfloat16.  Every call runs
 on the current CUDA stream of its tensors' device, allocates through PyTorch's allocator only, and does
 not synchronise; what a kernel meets (no page left, a bad page) is reported by ``zyfa_check_errors``.
 
@@ -22,7 +27,7 @@ from typing import NamedTuple
 
 import torch
 
-from .api import ZyfaError, load_library
+from .api import ZYFA_DTYPE_BF16, ZYFA_DTYPE_E4M3, ZyfaError, load_library
 
 _native = None
 
@@ -87,7 +92,8 @@ def rope_paged_store(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Te
                      v_cache: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor | None = None,
                      rope: Rope | None = None, *, q_descale=None, k_descale=None, v_descale=None,
                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
-                     v_out: torch.Tensor | None = None) -> torch.Tensor | None:
+                     v_out: torch.Tensor | None = None, k_scales: torch.Tensor | None = None,
+                     v_scales: torch.Tensor | None = None) -> torch.Tensor | None:
     """Rotate a step's bf16 queries [N, H, D_qk] and keys [N, H_kv, D_qk] by their positions, write keys and values
     [N, H_kv, D_v] into cache slots ``slots`` (int64 [N], distinct; below 0: a padding row, for which nothing is written),
     and return the queries in the cache's type.
@@ -98,9 +104,38 @@ def rope_paged_store(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Te
     For a bf16 cache they are not used, as in the prefill.  ``k_out`` and ``v_out`` [N, H_kv, D] receive dense copies, as
     ``flash_attn_func`` reads them.  ``q`` may be None (keys and values only), or ``k`` and ``v`` (queries only).  What is
     written must not overlap what is read, nor rows of the cache one another.
+
+    With ``k_scales`` and ``v_scales`` the cache holds 4 bits: each 16 channels, over the descale, get the scale of their largest
+    magnitude over 6, rounded to e4m3, and codes rounded to the nearest.  Queries come back in bfloat16, and ``k_out`` and ``v_out`` are
+    bfloat16 copies from before that rounding, as the bfloat16 prefill reads them.
     """
     return (_native or _load()).store(q, k, v, k_cache, v_cache, slots, positions, None if rope is None else rope._spec,
-                                      q_descale, k_descale, v_descale, q_out, k_out, v_out)
+                                      q_descale, k_descale, v_descale, q_out, k_out, v_out, k_scales, v_scales)
+
+
+_ROW_TYPES = {None: None, torch.float8_e4m3fn: ZYFA_DTYPE_E4M3, torch.bfloat16: ZYFA_DTYPE_BF16}
+
+
+def paged_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, cu_tokens: torch.Tensor,
+               max_tokens: int | None = None, *, starts: torch.Tensor | None = None, dtype: torch.dtype | None = None, k_descale=None,
+               v_descale=None, k_out_descale=None, v_out_descale=None, k_out: torch.Tensor | None = None,
+               v_out: torch.Tensor | None = None, k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None):
+    """Read tokens of a paged cache of any type back as dense rows, keys [max_tokens, H_kv, D_qk] and values [max_tokens, H_kv, D_v],
+    as ``flash_attn_func`` reads them.
+
+    Request b's rows are ``cu_tokens[b]`` up to ``cu_tokens[b + 1]`` (int32 [B + 1], not decreasing, as ``paged_plan`` numbers them); they
+    hold its tokens from ``starts[b]`` on (int32 [B]; 0 without it), from the pages that ``block_table`` (int32 [B, max_pages]) names.
+    Rows that no request has, such as those behind the last one, stay as they were in ``k_out`` and ``v_out``, and hold anything where
+    the call makes its results.  A token without a page is a row of zeros, and ``zyfa_check_errors`` reports it.
+
+    ``dtype`` is ``torch.bfloat16`` (the default) or ``torch.float8_e4m3fn``, whose values are divided by ``k_out_descale`` and
+    ``v_out_descale`` (one value or H_kv values).  The cache's own descales are as ``paged_decode_attn`` takes them; for a bf16 cache they
+    are not used.  Without descales the rows of an e4m3 cache read as e4m3 are its codes.
+    """
+    if dtype not in _ROW_TYPES:
+        raise TypeError("dtype must be torch.bfloat16 or torch.float8_e4m3fn")
+    return (_native or _load()).read(k_cache, v_cache, block_table, cu_tokens, max_tokens, starts, _ROW_TYPES[dtype], k_descale, v_descale,
+                                     k_out_descale, v_out_descale, k_out, v_out, k_scales, v_scales)
 
 
 def paged_decode_workspace_bytes(B: int, H: int, H_kv: int, D_v: int, max_len: int) -> int:
@@ -112,8 +147,10 @@ def paged_decode_workspace_bytes(B: int, H: int, H_kv: int, D_v: int, max_len: i
 def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                       seq_lens: torch.Tensor, softmax_scale: float | None = None, *, q_descale=None, k_descale=None,
                       v_descale=None, out: torch.Tensor | None = None, return_lse: bool = False,
-                      workspace: torch.Tensor | None = None):
-    """Attention of one query token per request, ``q`` [B, H, D_qk] in the cache's type, over the first
+                      workspace: torch.Tensor | None = None, k_scales: torch.Tensor | None = None,
+                      v_scales: torch.Tensor | None = None):
+    """Attention of one query token per request, ``q`` [B, H, D_qk] in the cache's type (bfloat16 for a 4-bit cache, which is given
+    with ``k_scales`` and ``v_scales``), over the first
     ``seq_lens[b]`` tokens (int32 [B]) of the pages that ``block_table`` (int32 [B, max_pages]) names.
 
     Returns bfloat16 [B, H, D_v] (0 for a request without tokens), and with ``return_lse`` also the float32
@@ -123,4 +160,4 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     may overlap on the GPU need one each.  A NaN among a row's scores makes the row NaN.
     """
     return (_native or _load()).decode(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, q_descale, k_descale,
-                                       v_descale, out, return_lse, workspace)
+                                       v_descale, out, return_lse, workspace, k_scales, v_scales)

@@ -46,7 +46,8 @@ extern "C" {
 
 typedef enum {
   ZYFA_DTYPE_E4M3 = 0, /* OCP FP8 e4m3 ("fn"): q, k, v hold bit patterns, one byte each */
-  ZYFA_DTYPE_BF16 = 1
+  ZYFA_DTYPE_BF16 = 1,
+  ZYFA_DTYPE_E2M1 = 2  /* paged caches only: OCP FP4 e2m1 codes, two channels a byte, with zyfa_paged_scales_t */
 } zyfa_dtype_t;
 
 typedef enum {
@@ -243,6 +244,18 @@ typedef struct {
 } zyfa_paged_cache_t;
 
 /*
+ * The scales of a 4-bit cache.  Its zyfa_paged_cache_t has dtype ZYFA_DTYPE_E2M1 and strides in bytes; byte i of a token and head
+ * holds the e2m1 codes of channels 2i (low half) and 2i + 1, so its D / 2 bytes are contiguous.  Each 16 channels share one e4m3
+ * scale, whose D / 16 bytes are contiguous too, and a value is code * scale * descale.  A NaN scale makes its 16 values NaN.
+ */
+typedef struct {
+  void* k;               /* device pointers, 4-byte aligned: e4m3 bytes                                */
+  void* v;
+  long long k_page_stride, k_token_stride, k_head_stride;  /* bytes, >= 0, multiples of 4              */
+  long long v_page_stride, v_token_stride, v_head_stride;
+} zyfa_paged_scales_t;
+
+/*
  * zyfa_paged_plan - pages, slots and positions of one serving step, from request lengths on the device.
  *
  * Request b holds cached_lens[b] tokens and adds new_lens[b] (negative lengths count as 0).  Its tokens
@@ -322,6 +335,55 @@ zyfa_status_t zyfa_rope_paged_store(const void* q, const void* k, const void* v,
                                     const float* v_descale, int descale_per_kv_head, cudaStream_t stream);
 
 /*
+ * zyfa_rope_paged_store_e2m1 - zyfa_rope_paged_store into a 4-bit cache: arguments, layouts, padding, refusals and errors as there, but
+ *
+ *   cache, scales     dtype ZYFA_DTYPE_E2M1 and the scales that belong to it.  Neither's rows may overlap, nor those of two of the four
+ *                     tensors where their strides are the same (else ZYFA_ERR_INVALID_ARG).
+ *   q_out             bf16, as zyfa_attn_decode_paged_e2m1 and the bf16 prefill read it.
+ *   k_out, v_out      NULL, or dense bf16 copies of the rotated keys and of the values, before they are quantised.
+ *   k/v_descale       device pointers to one float (or H_kv floats with descale_per_kv_head = 1); NULL means 1.
+ *
+ * Of 16 neighbouring channels of a token and head, z = fl32(y * fl32(1 / descale)): scale = rne_satfinite(fl32(max|z| * fl32(1/6)))
+ * in e4m3, code = rne_satfinite(fl32(z * fl32(1 / scale))) in e2m1, and 0 where the scale is 0.  A NaN among them makes the scale
+ * NaN; an infinity is the largest value that the cache holds, 6 * 448 * descale, and leaves of the others what that scale holds.
+ */
+zyfa_status_t zyfa_rope_paged_store_e2m1(const void* q, const void* k, const void* v, long long q_token_stride,
+                                         long long k_token_stride, long long v_token_stride, void* q_out, void* k_out,
+                                         void* v_out, const int* positions, long long position_stride,
+                                         const long long* slots, long long N, int H, const zyfa_paged_cache_t* cache,
+                                         const zyfa_paged_scales_t* scales, const zyfa_rope_t* rope,
+                                         const float* k_descale, const float* v_descale, int descale_per_kv_head,
+                                         cudaStream_t stream);
+
+/*
+ * zyfa_paged_read - read tokens of a paged cache back as dense rows, as zyfa_attn_fwd_causal reads keys and values (a prompt
+ * whose beginning is cached, a cache that moves).
+ *
+ * Row n holds token starts[b] + n - cu_tokens[b] of the request b with cu_tokens[b] <= n < cu_tokens[b + 1]:
+ *
+ *   cache, scales       a cache of any type; scales is NULL unless that is ZYFA_DTYPE_E2M1.
+ *   block_table         [B][table_stride >= max_pages] int32; only entries of tokens that are read are looked at.
+ *   cu_tokens           [B + 1] int32, not decreasing.  Rows that no request has (before cu_tokens[0], from cu_tokens[B] on) are
+ *                       left as they were; tokens that N has no row for are not read.
+ *   starts              [B] int32, or NULL: every run begins with token 0.
+ *   k_out, v_out, N     dense [N][H_kv][D_qk] and [N][H_kv][D_v] of out_dtype, ZYFA_DTYPE_BF16 or ZYFA_DTYPE_E4M3, 16-byte
+ *                       aligned; one of the two may be NULL.  They must not overlap one another, the inputs or the cache.
+ *   k/v_descale         of the cache, not used if that is bf16: device pointers to one float, to [B][H_kv] floats with
+ *                       descale_per_kv_head = 1, to [H_kv] floats with 3; NULL means 1.
+ *   k/v_out_descale     of what is written, e4m3 only: one float, or [H_kv] floats with out_descale_per_kv_head = 1; NULL means 1.
+ *
+ * A value is fl32(x * fl32(descale * fl32(1 / out_descale))) with x = code * scale, exact, rounded once to out_dtype (e4m3: nearest even,
+ * saturating, a NaN stays one).  A token outside the table's pages, or whose page lies outside the cache, is a row of zeros, and
+ * zyfa_check_errors() returns ZYFA_ERR_BAD_PAGE.  One launch, asynchronous on `stream`, allocates nothing.  N == 0 or B == 0
+ * returns ZYFA_OK.
+ */
+zyfa_status_t zyfa_paged_read(const zyfa_paged_cache_t* cache, const zyfa_paged_scales_t* scales, const int* block_table,
+                              long long table_stride, int max_pages, const int* cu_tokens, const int* starts, int B,
+                              void* k_out, void* v_out, long long N, zyfa_dtype_t out_dtype, const float* k_descale,
+                              const float* v_descale, int descale_per_kv_head, const float* k_out_descale,
+                              const float* v_out_descale, int out_descale_per_kv_head, cudaStream_t stream);
+
+/*
  * zyfa_attn_decode_paged - attention of one new token per request over a paged cache:
  *
  *     out[b, h, :] = sum_{j < seq_lens[b]} softmax_j(scale * q[b,h,:] . k[slot(b,j), hk, :]) * v[slot(b,j), hk, :]
@@ -357,7 +419,21 @@ zyfa_status_t zyfa_attn_decode_paged(const void* q, long long q_batch_stride, co
                                      int descale_per_kv_head, void* workspace, size_t workspace_bytes,
                                      cudaStream_t stream);
 
-/* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged for these sizes, with max_len =
+/*
+ * zyfa_attn_decode_paged_e2m1 - zyfa_attn_decode_paged over a 4-bit cache: arguments, workspace, edges and errors as there, but
+ * cache and scales as for zyfa_rope_paged_store_e2m1 and q in bf16 (q_batch_stride in elements, a multiple of 8), without a descale.
+ * Keys and values are taken exactly; a query's channels are rounded to 11 bits of fp16 over a power of two near its largest (bf16
+ * has 8, so only those below 2^-28 of it lose any), scores and sums are held in fp32, and the weights exp(s - max) are rounded
+ * to fp16 before they multiply V.
+ */
+zyfa_status_t zyfa_attn_decode_paged_e2m1(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache,
+                                          const zyfa_paged_scales_t* scales, const int* block_table,
+                                          long long table_stride, int max_pages, const int* seq_lens, void* out,
+                                          float* lse, int B, int H, float softmax_scale, const float* k_descale,
+                                          const float* v_descale, int descale_per_kv_head, void* workspace,
+                                          size_t workspace_bytes, cudaStream_t stream);
+
+/* zyfa_attn_decode_paged_workspace_bytes - workspace of zyfa_attn_decode_paged (of any cache type) for these sizes, with max_len =
  * max_pages * page_size; the same whatever the lengths are: 2 * H * (D_v + 2) floats for each group that the
  * work may be cut into, of which there are at most 2560 / (H_kv * ceil(H / H_kv / 8)), and one per 16 tokens.
  * Pure host arithmetic; 0 for sizes that the call refuses. */
@@ -403,6 +479,13 @@ zyfa_status_t zyfa_selftest_stalled_decode(const void* q, long long q_batch_stri
                                            const int* block_table, long long table_stride, int max_pages,
                                            const int* seq_lens, void* out, int B, int H, void* workspace,
                                            size_t workspace_bytes, cudaStream_t stream);
+
+/* zyfa_selftest_stalled_decode_e2m1 - the same for zyfa_attn_decode_paged_e2m1, whatever the page size and strides. */
+zyfa_status_t zyfa_selftest_stalled_decode_e2m1(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache,
+                                                const zyfa_paged_scales_t* scales, const int* block_table,
+                                                long long table_stride, int max_pages, const int* seq_lens, void* out,
+                                                int B, int H, void* workspace, size_t workspace_bytes,
+                                                cudaStream_t stream);
 
 /* zyfa_status_string - static, human-readable name of a status code (never NULL). */
 const char* zyfa_status_string(zyfa_status_t status);
