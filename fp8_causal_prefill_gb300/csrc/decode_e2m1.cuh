@@ -30,8 +30,9 @@ constexpr int kMaxTokens = kWarps * kKeys;
 
 struct Args : DecodeArgs {
   ScaleView scales;
+  int boxes;             // codes come by TMA, box by box (1 << box_log2 tokens of a page); else piece by piece, and box_log2 is the tile's
   int k_log2, v_log2;    // tokens whose rows share 128 bytes of shared memory (log2), where a block's heads take less
-  int scale8;            // scales of 8 bytes, copied as such
+  int k_unit, v_unit;    // bytes of scales copied at a time: 4, 8, or 16 across heads
   uint32_t order;        // the key within 8 that row g of the scores is: nibble g
 };
 
@@ -41,14 +42,21 @@ struct Tile4 {
   static constexpr int kKeyBytes = kRowK + kRowV + kScaleK + kScaleV;
 };
 
-// Codes of a tile lie in shared memory by token, a token's heads one after the other, in columns of 128 bytes [token][128] with the
-// 16-byte pieces of a row exchanged by its number, as TMA's 128-byte swizzle does; rows of 32 or 64 bytes share 128 (`log2`).
-__device__ __forceinline__ uint32_t place4(int token, int byte, int log2, uint32_t column) {
-  const int row = token >> log2, inner = ((token & ((1 << log2) - 1)) << (7 - log2)) + byte;
-  return (inner >> 7) * column + row * 128 + ((((inner >> 4) ^ row) & 7) << 4) + (inner & 15);
-}
-__host__ __device__ inline uint32_t column4(int tokens, int log2) { return static_cast<uint32_t>(tokens >> log2) * 128u; }
-__host__ __device__ inline uint32_t region4(int tokens, int pitch, int log2) { return column4(tokens, log2) * ((pitch + 127) / 128); }
+// Codes of a tile lie in shared memory box by box, a token's heads one after the other, in columns of 128 bytes [token][128] with
+// the 16-byte pieces of a row exchanged by its number, as TMA's 128-byte swizzle does; rows of 32 or 64 bytes share 128 (`log2`).
+struct Place {
+  int log2, box_log2;
+  uint32_t box_bytes;
+  __device__ __forceinline__ uint32_t operator()(int token, int byte) const {
+    const int in = token & ((1 << box_log2) - 1), row = in >> log2, inner = ((in & ((1 << log2) - 1)) << (7 - log2)) + byte;
+    return (token >> box_log2) * box_bytes + (inner >> 7) * (128u << (box_log2 - log2)) + row * 128 + ((((inner >> 4) ^ row) & 7) << 4) + (inner & 15);
+  }
+  // of a multiple of 16 tokens, from token 0
+  __device__ __forceinline__ uint32_t step(int token) const {
+    return (token >> box_log2) * box_bytes + ((token & ((1 << box_log2) - 1)) >> log2) * 128;
+  }
+};
+__host__ __device__ inline uint32_t bytes4(int tokens, int pitch, int log2) { return static_cast<uint32_t>(tokens >> log2) * 128u * ((pitch + 127) / 128); }
 inline int share_log2(int pitch) { return pitch == 32 ? 2 : pitch == 64 ? 1 : 0; }
 
 __device__ __forceinline__ int key4(uint32_t order, int g) { return order >> (4 * g) & 7; }
@@ -95,37 +103,49 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 __device__ __forceinline__ uint32_t halves(float lo, float hi) { return pack2<true>(lo, hi); }
 
 // Where a lane reads a warp's run of 32 keys, relative to the run's first key (a multiple of 32): K of keys 8u + row, V of 16 keys.
+// 16 keys on, the exchange of pieces is the same unless four tokens share a row (64 channels, one head).
 template <int DQK, int DV>
 struct Reader4 {
   static constexpr bool kWideK = DQK >= 128, kRestK = DQK % 128 != 0;  // 64 bytes of a row by 16, 32 by 8
   static constexpr int kPairsV = DV / 64;                              // 32-channel pieces of V, two at a time
-  uint32_t wide[kWideK ? 4 : 1], rest[kRestK ? 4 : 1], value[2][kPairsV];
-  uint32_t k_scale, v_scale;
+  uint32_t wide[2], rest[kWideK ? 1 : 4], value[kPairsV == 1 ? 2 : 1][kPairsV];
+  uint32_t k_16, v_16;               // from 16 keys to the next
+  uint32_t k_scale, v_scale[2];      // of key g, and of keys 2t and 2t + 1 (of each 8)
+  uint32_t k_scale_8, v_scale_8;     // from 8 keys to the next
 
-  __device__ __forceinline__ void set(const Args& a, int lane, int head, int first) {
+  __device__ __forceinline__ void set(const Args& a, int lane, int head, int first, const Place& kp, const Place& vp) {
     using T = Tile4<DQK, DV>;
-    const int g = lane >> 2, t = lane & 3, TT = a.tile_tokens;
-    const uint32_t kc = column4(TT, a.k_log2), vc = column4(TT, a.v_log2);
+    const int g = lane >> 2, t = lane & 3;
     const int kb = head * T::kRowK, vb = head * T::kRowV;
+    k_16 = kp.step(16);
+    v_16 = vp.step(16);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int key = first + 8 * u + key4(a.order, g);
-      if (kWideK) wide[u] = place4(key, kb + 16 * t, a.k_log2, kc);
-      if (kRestK) rest[u] = place4(key, kb + (kWideK ? 64 : 0) + 8 * t, a.k_log2, kc);
+      if (kWideK && u < 2) wide[u] = kp(key, kb + 16 * t);
+      if (kRestK && u < (kWideK ? 1 : 4)) rest[u] = kp(key, kb + (kWideK ? 64 : 0) + 8 * t);
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < (kPairsV == 1 ? 2 : 1); ++n)
 #pragma unroll
       for (int p = 0; p < kPairsV; ++p)
-        value[n][p] = place4(first + 16 * n + (lane >> 3 & 1) * 8 + key4(a.order, lane & 7), vb + 32 * p + (lane >> 4) * 16, a.v_log2, vc);
-    k_scale = (head * TT + first) * T::kScaleK;
-    v_scale = (head * TT + first) * T::kScaleV;
+        value[n][p] = vp(first + 16 * n + (lane >> 3 & 1) * 8 + key4(a.order, lane & 7), vb + 32 * p + (lane >> 4) * 16);
+    const int ks = a.heads * T::kScaleK, vs = a.heads * T::kScaleV;
+    k_scale = (first + key4(a.order, g)) * ks + head * T::kScaleK;
+    v_scale[0] = (first + key4(a.order, 2 * t)) * vs + head * T::kScaleV;
+    v_scale[1] = (first + key4(a.order, 2 * t + 1)) * vs + head * T::kScaleV;
+    k_scale_8 = 8 * ks;
+    v_scale_8 = 8 * vs;
   }
+  __device__ __forceinline__ uint32_t wide_at(int u) const { return wide[u & 1] + (u >> 1) * k_16; }
+  // (192 channels: rows of 96 bytes share nothing, and 8 keys on is 1 KiB)
+  __device__ __forceinline__ uint32_t rest_at(int u) const { return kWideK ? rest[0] + (u & 1) * 1024 + (u >> 1) * k_16 : rest[kWideK ? 0 : u]; }
+  __device__ __forceinline__ uint32_t value_at(int n, int p) const { return kPairsV == 1 ? value[kPairsV == 1 ? n : 0][p] : value[0][p] + n * v_16; }
 };
 
-// Shared memory of a stage: K, V, their scales, queries.
-struct Stage4 {
-  uint32_t k, v, ks, vs, q;
+// Where a run's first key lies in a stage's K, V and their scales.
+struct Run4 {
+  uint32_t k, v, ks, vs;
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -216,8 +236,8 @@ struct Rows4 {
     for (int c = 0; c < NC; ++c) mma<kF16>(x[c], b0, b1, b2, b3, qf[c][step + 1][0], qf[c][step + 1][1]);
   }
 
-  // One run of 32 keys.  k, v, ks, vs: where the run's first key lies in each region of the stage.  mask: the keys that count.
-  __device__ __forceinline__ void tile(const Stage4& s, const R& at, uint32_t order, uint32_t mask, int lane) {
+  // One run of 32 keys.  mask: those that count.
+  __device__ __forceinline__ void tile(const Run4& s, const R& at, uint32_t order, uint32_t mask, int lane) {
     const int g = lane >> 2, t = lane & 3;
     // S^T: rows are keys, columns heads; then scores in units of log2
     F2 x[NC][KB][2];
@@ -226,11 +246,11 @@ struct Rows4 {
       float acc[NC][4];
 #pragma unroll
       for (int c = 0; c < NC; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.0f;
-      const uint32_t scales = s.ks + at.k_scale + (16 * kb + key4(order, g)) * T::kScaleK;
+      const uint32_t scales = s.ks + at.k_scale + 2 * kb * at.k_scale_8, scales_8 = scales + at.k_scale_8;
       if constexpr (R::kWideK) {
-        const uint4 ka = lds16(s.k + at.wide[2 * kb]), kc = lds16(s.k + at.wide[2 * kb + 1]);
+        const uint4 ka = lds16(s.k + at.wide_at(2 * kb)), kc = lds16(s.k + at.wide_at(2 * kb + 1));
         // the scales of this lane's two blocks of channels, of both keys
-        const uint32_t sa = widen_e4m3(lds2(scales + 2 * t)), sc = widen_e4m3(lds2(scales + 8 * T::kScaleK + 2 * t));
+        const uint32_t sa = widen_e4m3(lds2(scales + 2 * t)), sc = widen_e4m3(lds2(scales_8 + 2 * t));
         const uint32_t sa0 = prmt(sa, sa, 0x1010), sa1 = prmt(sa, sa, 0x3232), sc0 = prmt(sc, sc, 0x1010), sc1 = prmt(sc, sc, 0x3232);
         two_steps(acc, 0, ka.x, kc.x, sa0, sc0);
         two_steps(acc, 2, ka.y, kc.y, sa0, sc0);
@@ -239,8 +259,8 @@ struct Rows4 {
       }
       if constexpr (R::kRestK) {
         constexpr int first = R::kWideK ? 8 : 0;
-        const uint2 ka = lds8(s.k + at.rest[2 * kb]), kc = lds8(s.k + at.rest[2 * kb + 1]);
-        const uint32_t sa = widen_e4m3(lds1(scales + first + t) * 0x101u), sc = widen_e4m3(lds1(scales + 8 * T::kScaleK + first + t) * 0x101u);
+        const uint2 ka = lds8(s.k + at.rest_at(2 * kb)), kc = lds8(s.k + at.rest_at(2 * kb + 1));
+        const uint32_t sa = widen_e4m3(lds1(scales + first + t) * 0x101u), sc = widen_e4m3(lds1(scales_8 + first + t) * 0x101u);
         two_steps(acc, first, ka.x, kc.x, sa, sc);
         two_steps(acc, first + 2, ka.y, kc.y, sa, sc);
       }
@@ -319,8 +339,7 @@ struct Rows4 {
       uint32_t sv[2][kPieces];  // scales of keys 2t, 2t + 1 of the first 8 and of the second
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t base = s.vs + at.v_scale + (16 * kb + 8 * j) * T::kScaleV;
-        const uint32_t first = base + key4(order, 2 * t) * T::kScaleV, second = base + key4(order, 2 * t + 1) * T::kScaleV;
+        const uint32_t base = s.vs + (2 * kb + j) * at.v_scale_8, first = base + at.v_scale[0], second = base + at.v_scale[1];
         if constexpr (DV == 128) {
           const uint2 a = lds8(first), b = lds8(second);
           const uint32_t lo = prmt(a.x, b.x, pick), hi = prmt(a.y, b.y, pick);
@@ -338,7 +357,7 @@ struct Rows4 {
       for (int p = 0; p < kPieces; ++p) {
         uint32_t r[4];
         if (p % 2 == 0) {
-          ldsm4t(s.v + at.value[kb][p / 2], r);
+          ldsm4t(s.v + at.value_at(kb, p / 2), r);
           two_pieces[0] = r[2];
           two_pieces[1] = r[3];
         } else {
@@ -462,21 +481,23 @@ struct Rows4 {
 // ------------------------------------------------------------------------------------------------
 
 template <int DQK, int DV, int NC>
-__global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using T = Tile4<DQK, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ unsigned s_prefix[(kWarps + 1) * 32], s_sums[kWarps + 1];
   __shared__ __align__(16) Header s_header[kStages];
   __shared__ float2 s_scale[kStages][kWarps];  // of the scores, and of V
-  __shared__ long long s_row[4][kMaxTokens];   // where a tile's tokens lie in the cache: K, V, their scales; below 0: nowhere
+  __shared__ long long s_row[4][kMaxTokens];   // where a tile's tokens lie in the scales of K and V, and (no boxes) in K and V; below 0: nowhere
   __shared__ unsigned s_mask[kStages][kWarps]; // its keys that count, 32 a word
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_meet[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x >> 5) - 1;  // compute warps; the next one loads
   const int S = a.stages, TT = a.tile_tokens, k_pitch = a.heads * T::kRowK, v_pitch = a.heads * T::kRowV;
   // a stage: K, V, scales of K, scales of V, queries
-  const uint32_t k_bytes = region4(TT, k_pitch, a.k_log2), v_bytes = region4(TT, v_pitch, a.v_log2);
+  const uint32_t k_bytes = bytes4(TT, k_pitch, a.k_log2), v_bytes = bytes4(TT, v_pitch, a.v_log2);
   const uint32_t ks_at = k_bytes + v_bytes, vs_at = ks_at + a.heads * TT * T::kScaleK, q_at = vs_at + a.heads * TT * T::kScaleV;
-  const uint32_t stage_bytes = q_at + a.q_bytes;
+  const uint32_t stage_bytes = (q_at + a.q_bytes + 1023) & ~1023u;
+  const Place k_place = {a.k_log2, a.box_log2, bytes4(1 << a.box_log2, k_pitch, a.k_log2)};
+  const Place v_place = {a.v_log2, a.box_log2, bytes4(1 << a.box_log2, v_pitch, a.v_log2)};
   const uint32_t tiles_s = smem_addr(smem), full_s = smem_addr(s_full), empty_s = smem_addr(s_empty);
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -485,6 +506,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
     }
     for (int i = 0; i < a.heads * a.chunk_warps; ++i) ptx::mbar_init(smem_addr(s_meet + i), a.subs);
     ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (a.boxes && threadIdx.x == 32) {
+    ptx::tma_prefetch_desc(&kmap);
+    ptx::tma_prefetch_desc(&vmap);
   }
   __syncthreads();
   wait_for_predecessor();
@@ -529,6 +555,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
     const uint8_t *k = a.cache.k + head0 * a.cache.k_head, *v = a.cache.v + head0 * a.cache.v_head;
     const uint8_t *ks = a.scales.k + head0 * a.scales.k_head, *vs = a.scales.v + head0 * a.scales.v_head;
     constexpr int kSets = kMaxTokens / 32;
+    const int box = 1 << a.box_log2;
+    const unsigned firsts = box == 16 ? 0x10001u : 1u;  // lanes whose token begins a box, of the sets where one does
     int pg[kSets], off[kSets];  // page and place in it of tokens c.t + 32 i + lane
     auto look_up = [&]() {
 #pragma unroll
@@ -555,6 +583,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
       const uint32_t base = tiles_s + stage * stage_bytes, bar = full_s + 8 * stage;
       const int valid = min(TT, c.len - c.t);
       bool whole = valid == TT;
+      uint32_t bytes = 0;
 #pragma unroll
       for (int i = 0; i < kSets; ++i) {
         if (32 * i >= TT) break;
@@ -563,22 +592,56 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
         const unsigned mask = __ballot_sync(0xffffffffu, ok);
         whole = whole && mask == 0xffffffffu;
         const long long page = pg[i], at = off[i];
-        s_row[0][32 * i + lane] = ok ? page * a.cache.k_page + at * a.cache.k_tok : -1;
-        s_row[1][32 * i + lane] = ok ? page * a.cache.v_page + at * a.cache.v_tok : -1;
-        s_row[2][32 * i + lane] = ok ? page * a.scales.k_page + at * a.scales.k_tok : -1;
-        s_row[3][32 * i + lane] = ok ? page * a.scales.v_page + at * a.scales.v_tok : -1;
+        if (a.boxes) {  // the first token of each box issues its copies, before the barrier's phase can end by the arrivals below
+          if (ok && ((32 * i + lane) & (box - 1)) == 0) {
+            const int n = (32 * i + lane) >> a.box_log2;
+            tma_load_5d(base + n * k_place.box_bytes, &kmap, bar, 0, off[i] >> a.k_log2, a.k_log2 ? 0 : head0 * T::kRowK / 128, 0, pg[i]);
+            tma_load_5d(base + k_bytes + n * v_place.box_bytes, &vmap, bar, 0, off[i] >> a.v_log2, a.v_log2 ? 0 : head0 * T::kRowV / 128, 0, pg[i]);
+          }
+          // (a box's tokens share a page, so if its first one has none, neither do the others; and the first is inside if any is)
+          bytes += __popc(mask & firsts) * (box >= 32 && ((32 * i) & (box - 1)) ? 0u : k_place.box_bytes + v_place.box_bytes);
+        } else {
+          s_row[2][32 * i + lane] = ok ? page * a.cache.k_page + at * a.cache.k_tok : -1;
+          s_row[3][32 * i + lane] = ok ? page * a.cache.v_page + at * a.cache.v_tok : -1;
+        }
+        s_row[0][32 * i + lane] = ok ? page * a.scales.k_page + at * a.scales.k_tok : -1;
+        s_row[1][32 * i + lane] = ok ? page * a.scales.v_page + at * a.scales.v_tok : -1;
         if (lane == 0) s_mask[stage][i] = mask;
       }
       __syncwarp();
-      // codes: the pieces of a token's heads, 32 at a time
-      auto codes = [&](auto pieces, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to, int log2) {
-        constexpr int kPieces = decltype(pieces)::value;
-        const int all = heads * kPieces, step = 32 / all, rest = 32 % all;
-        const uint32_t column = column4(TT, log2);
+      if (!a.boxes) {
+        // codes: the pieces of a token's heads, 32 at a time
+        auto codes = [&](auto pieces, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to, const Place& place) {
+          constexpr int kPieces = decltype(pieces)::value;
+          const int all = heads * kPieces, step = 32 / all, rest = 32 % all;
+          int r = lane / all, p = lane % all;
+          while (r < valid) {
+            const long long row = rows[r];
+            if (row >= 0) copy16(to + place(r, p * 16), from + row + p / kPieces * head_stride + p % kPieces * 16, 16);
+            r += step;
+            p += rest;
+            if (p >= all) {
+              p -= all;
+              ++r;
+            }
+          }
+        };
+        codes(std::integral_constant<int, T::kRowK / 16>(), s_row[2], k, a.cache.k_head, base, k_place);
+        codes(std::integral_constant<int, T::kRowV / 16>(), s_row[3], v, a.cache.v_head, base + k_bytes, v_place);
+      }
+      // scales [token][head]: zeros where there is no token
+      auto scales = [&](auto unit, int head_bytes, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to) {
+        constexpr int kUnit = decltype(unit)::value;
+        const int each = kUnit == 16 ? 1 : head_bytes / kUnit, all = kUnit == 16 ? heads * head_bytes / 16 : heads * each, pitch = a.heads * head_bytes;
+        const int step = 32 / all, rest = 32 % all;
         int r = lane / all, p = lane % all;
-        while (r < valid) {
+        while (r < TT) {
           const long long row = rows[r];
-          if (row >= 0) copy16(to + place4(r, p * 16, log2, column), from + row + p / kPieces * head_stride + p % kPieces * 16, 16);
+          const uint8_t* src = from + (row < 0 ? 0 : row) + (kUnit == 16 ? p * 16ll : p / each * head_stride + p % each * kUnit);
+          if constexpr (kUnit == 16)
+            copy16(to + r * pitch + p * 16, src, row < 0 ? 0 : 16);
+          else
+            copy_small<kUnit>(to + r * pitch + p * kUnit, src, row < 0 ? 0 : kUnit);
           r += step;
           p += rest;
           if (p >= all) {
@@ -587,38 +650,29 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
           }
         }
       };
-      codes(std::integral_constant<int, T::kRowK / 16>(), s_row[0], k, a.cache.k_head, base, a.k_log2);
-      codes(std::integral_constant<int, T::kRowV / 16>(), s_row[1], v, a.cache.v_head, base + k_bytes, a.v_log2);
-      // scales: zeros where there is no token
-      auto scales = [&](auto bytes, auto unit, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to) {
-        constexpr int kBytes = decltype(bytes)::value, kUnit = decltype(unit)::value, kUnits = kBytes / kUnit;
-        for (int h = 0; h < heads; ++h)
-          for (int x = lane; x < TT * kUnits; x += 32) {
-            const long long row = rows[x / kUnits];
-            copy_small<kUnit>(to + h * TT * kBytes + x * kUnit, from + (row < 0 ? 0 : row) + h * head_stride + x % kUnits * kUnit, row < 0 ? 0 : kUnit);
-          }
+      auto scales_by = [&](int unit, int head_bytes, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to) {
+        if (unit == 16)
+          scales(std::integral_constant<int, 16>(), head_bytes, rows, from, head_stride, to);
+        else if (unit == 8)
+          scales(std::integral_constant<int, 8>(), head_bytes, rows, from, head_stride, to);
+        else
+          scales(std::integral_constant<int, 4>(), head_bytes, rows, from, head_stride, to);
       };
-      if (T::kScaleK == 8 && a.scale8)
-        scales(std::integral_constant<int, T::kScaleK>(), std::integral_constant<int, T::kScaleK == 8 ? 8 : 4>(), s_row[2], ks, a.scales.k_head, base + ks_at);
-      else
-        scales(std::integral_constant<int, T::kScaleK>(), std::integral_constant<int, 4>(), s_row[2], ks, a.scales.k_head, base + ks_at);
-      if (T::kScaleV == 8 && a.scale8)
-        scales(std::integral_constant<int, T::kScaleV>(), std::integral_constant<int, T::kScaleV == 8 ? 8 : 4>(), s_row[3], vs, a.scales.v_head, base + vs_at);
-      else
-        scales(std::integral_constant<int, T::kScaleV>(), std::integral_constant<int, 4>(), s_row[3], vs, a.scales.v_head, base + vs_at);
-      if (c.first) {
-        const uint8_t* q = a.q + c.b * a.q_batch + static_cast<long long>(first_q) * (DQK * 2);
-        for (int x = lane; x < queries * (DQK / 8); x += 32) copy16(base + q_at + x * 16, q + x * 16, 16);
-        if (lane < heads) {
-          const int i = a.desc_per_head ? c.b * a.desc_request + head0 + lane : 0;
-          s_scale[stage][lane] = {a.scale_log2 * (a.k_desc ? a.k_desc[i] : 1.0f), a.v_desc ? a.v_desc[i] : 1.0f};
-        }
+      scales_by(a.k_unit, T::kScaleK, s_row[0], ks, a.scales.k_head, base + ks_at);
+      scales_by(a.v_unit, T::kScaleV, s_row[1], vs, a.scales.v_head, base + vs_at);
+      if (c.first && lane < heads) {
+        const int i = a.desc_per_head ? c.b * a.desc_request + head0 + lane : 0;
+        s_scale[stage][lane] = {a.scale_log2 * (a.k_desc ? a.k_desc[i] : 1.0f), a.v_desc ? a.v_desc[i] : 1.0f};
       }
       arrive_after_copies(bar);
       __syncwarp();
       if (lane == 0) {
         s_header[stage] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, 0};
-        ptx::mbar_arrive(bar);
+        if (c.first) {
+          bytes += queries * (DQK * 2);
+          bulk_load(base + q_at, a.q + c.b * a.q_batch + static_cast<long long>(first_q) * (DQK * 2), queries * (DQK * 2), bar);
+        }
+        ptx::mbar_arrive_expect_tx(bar, bytes);
       }
       c.left = c.left_after(TT);
       if (c.left <= 0) break;
@@ -637,8 +691,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
 
   Reader4<DQK, DV> reader;
   const int run_keys = a.turns * kKeys;
-  reader.set(a, lane, head, sub * run_keys);
-  const uint32_t k_turn = column4(kKeys, a.k_log2), v_turn = column4(kKeys, a.v_log2);
+  reader.set(a, lane, head, sub * run_keys, k_place, v_place);
   const uint32_t my_query = q_at + (head * a.group + (chunk - chunk0) * a.chunk_heads) * (DQK * 2);
   // where warps that share a head's tokens meet
   const int peers = a.heads * a.chunk_warps, peer = warp % peers;
@@ -647,12 +700,23 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
   float* all_o = reinterpret_cast<float*>(meeting + warps * 64 * NC) + peer * 8 * NC * DV;
   const uint32_t meet_s = smem_addr(s_meet + peer);
   uint32_t meet_parity = 0;
+  // Copies still in flight write to this block's shared memory: waits for them, again for a bounded time.
+  auto give_up = [&](int st, uint32_t par) {
+    for (int j = 1; j < S; ++j) {
+      if (++st == S) {
+        st = 0;
+        par ^= 1;
+      }
+      mbar_wait_bounded(full_s + 8 * st, par, a.wait_clocks);
+    }
+    if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+  };
   Rows4<DQK, DV, NC> rows;
   int stage = 0;
   uint32_t parity = 0;
   while (true) {
     if (!mbar_wait_bounded(full_s + 8 * stage, parity, a.wait_clocks)) {
-      if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+      give_up(stage, parity);
       return;
     }
     const Header h = s_header[stage];
@@ -662,8 +726,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
       for (int turn = 0; turn < a.turns; ++turn) {
         const uint32_t mask = h.flags & kPartial ? s_mask[stage][sub * a.turns + turn] : 0xffffffffu;
         if (mask == 0) continue;
-        const Stage4 s = {base + turn * k_turn, base + k_bytes + turn * v_turn, base + ks_at + turn * kKeys * T::kScaleK,
-                          base + vs_at + turn * kKeys * T::kScaleV, 0};
+        const Run4 s = {base + k_place.step(turn * kKeys), base + k_bytes + v_place.step(turn * kKeys), base + ks_at + turn * 4 * reader.k_scale_8,
+                        base + vs_at + turn * 4 * reader.v_scale_8};
         rows.tile(s, reader, a.order, mask, lane);
       }
       if (h.flags & kLast) {
@@ -680,7 +744,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
             return ok;
           });
           if (!met) {
-            if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+            give_up(stage, parity);
             return;
           }
         }
@@ -698,6 +762,37 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
 
 // ------------------------------------------------------------------------------------------------
 // host side
+
+// A cache's codes (strides in bytes) as boxes of `box` tokens of a block's heads.
+inline bool boxable(const Args& a, long long page, long long tok, long long head, int row, int log2, int box) {
+  const int H_kv = a.cache.H_kv, pitch = a.heads * row;
+  for (long long s : {page, tok, head})
+    if (s <= 0 || s >= (1ll << 40)) return false;
+  if (H_kv > 1 && head != row) return false;
+  if (log2 > 0) return a.heads == H_kv && tok == pitch && box * pitch % 1024 == 0;  // tokens one after the other
+  return pitch % 128 == 0 && H_kv * row % 128 == 0;
+}
+
+// The map of such boxes: [page][128-byte column][token][128], or of rows of 128 bytes that several tokens share.
+inline bool make_map4(CUtensorMap* m, const uint8_t* base, const Args& a, long long page, long long tok, int row, int log2) {
+  using u64 = cuuint64_t;
+  using u32 = cuuint32_t;
+  const CacheView& c = a.cache;
+  const u64 dims[5] = {128, u64(c.page_size >> log2), u64(log2 ? 1 : c.H_kv * row / 128), 1, u64(c.num_pages)};
+  const u64 strides[4] = {u64(log2 ? 128 : tok), 128, u64(log2 ? 128 : tok), u64(page)};
+  const u32 box[5] = {128, u32(1) << (a.box_log2 - log2), u32(log2 ? 1 : a.heads * row / 128), 1, 1};
+  const u32 estr[5] = {1, 1, 1, 1, 1};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t*>(base), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Bytes of scales that can be copied at a time: 16 where a block's heads follow one another and rows are aligned.
+inline int scale_unit(const Args& a, const uint8_t* base, long long page, long long tok, long long head, int bytes) {
+  const int H_kv = a.cache.H_kv, last = (H_kv - 1) % a.heads + 1;
+  if (H_kv == 1) head = bytes;
+  const long long all = page | tok;
+  if (head == bytes && aligned(base, 16) && all % 16 == 0 && a.heads * bytes % 16 == 0 && last * bytes % 16 == 0) return 16;
+  return bytes == 8 && aligned(base, 8) && (all | head) % 8 == 0 ? 8 : 4;
+}
 
 // Blocks as for the wider caches: chunks of a head first (they read the same tile), then heads side by side, then runs of tokens.
 template <int DQK, int DV, int NC>
@@ -719,13 +814,21 @@ bool plan4(Args& a, int nsm, int* smem) {
   a.v_log2 = share_log2(v_pitch);
   // Keys in the order in which the rows that one phase of the reads of K takes lie in different banks: two of 64 bytes, four of 32.
   a.order = DQK >= 128 ? (a.k_log2 == 0 ? 0x73625140u : 0x76543210u) : a.k_log2 == 0 ? 0x75316420u : a.k_log2 == 1 ? 0x76325410u : 0x76543210u;
+  // Boxes: as many tokens of a page as divide both the page and the tile, in whole swizzle patterns of 1 KiB.  Heads that do not
+  // follow one another, rows of other widths and smaller pages come piece by piece.
+  int box = a.tile_tokens;
+  while (box > 1 && a.cache.page_size % box != 0) box /= 2;
+  const CacheView& c = a.cache;
+  a.boxes = box >= 16 && boxable(a, c.k_page, c.k_tok, c.k_head, T::kRowK, a.k_log2, box) && boxable(a, c.v_page, c.v_tok, c.v_head, T::kRowV, a.v_log2, box);
+  a.box_log2 = a.boxes ? log2_of(box) : a.tile_log2;
   const ScaleView& s = a.scales;
-  a.scale8 = aligned(s.k, 8) && aligned(s.v, 8) && ((s.k_page | s.k_tok | s.k_head | s.v_page | s.v_tok | s.v_head) & 7) == 0;
+  a.k_unit = scale_unit(a, s.k, s.k_page, s.k_tok, s.k_head, T::kScaleK);
+  a.v_unit = scale_unit(a, s.v, s.v_page, s.v_tok, s.v_head, T::kScaleV);
   const int nq = a.chunks > a.chunk_warps ? a.chunk_warps * a.chunk_heads : a.heads * a.group;
   a.q_bytes = static_cast<int>(round_up(nq * DQK * 2, 16));
   const int warps = a.heads * a.chunk_warps * a.subs;
-  const int stage = static_cast<int>(region4(a.tile_tokens, k_pitch, a.k_log2) + region4(a.tile_tokens, v_pitch, a.v_log2)) +
-                    a.heads * a.tile_tokens * (T::kScaleK + T::kScaleV) + a.q_bytes;
+  const int stage = static_cast<int>(round_up(bytes4(a.tile_tokens, k_pitch, a.k_log2) + bytes4(a.tile_tokens, v_pitch, a.v_log2) +
+                                                  a.heads * a.tile_tokens * (T::kScaleK + T::kScaleV) + a.q_bytes, 1024));
   const int meeting = a.subs > 1 ? warps * 8 * NC * (DV + 2) * 4 : 0;  // (m, l, O) of the warps that share a head's tokens
   constexpr int kStatic = 8192;  // the schedule's tables, headers and rows, with the 1 KiB that each block takes
   int blocks = NC == 1 ? 3 : 2;
@@ -745,10 +848,17 @@ zyfa_status_t launch4(Args& a, int nsm, int dev, uint8_t* ws, cudaStream_t strea
   int smem;
   set_workspace(a, ws);
   if (!plan4<DQK, DV, NC>(a, nsm, &smem)) return ZYFA_ERR_UNSUPPORTED;
+  CUtensorMap kmap = {}, vmap = {};
+  const CacheView& c = a.cache;
+  if (a.boxes && !(make_map4(&kmap, c.k, a, c.k_page, c.k_tok, Tile4<DQK, DV>::kRowK, a.k_log2) &&
+                   make_map4(&vmap, c.v, a, c.v_page, c.v_tok, Tile4<DQK, DV>::kRowV, a.v_log2))) {
+    a.boxes = 0;
+    a.box_log2 = a.tile_log2;
+  }
   static std::atomic<int> set[kMaxDevices];
   if (!prepare(decode4_kernel<DQK, DV, NC>, 2, dev, set)) return ZYFA_ERR_CUDA;
   if (launch_dependent(decode4_kernel<DQK, DV, NC>, dim3(static_cast<unsigned>(a.groups) * a.units), (a.heads * a.chunk_warps * a.subs + 1) * 32, smem, stream,
-                       a) != cudaSuccess)
+                       a, kmap, vmap) != cudaSuccess)
     return ZYFA_ERR_CUDA;
   return a.whole ? ZYFA_OK : launch_join<DV>(a, nsm, dev, stream);
 }
