@@ -100,6 +100,27 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
   return d;
 }
+// (a.lo s, b.lo s') and (a.hi s, b.hi s') from s0 = (s, 0) and s1 = (0, s'): exact, since one of the two products in each half is 0.
+__device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b, uint32_t s0, uint32_t s1) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 x, y;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 x, {l, l};\n\tmov.b32 {l, h}, %2;\n\tmov.b32 y, {l, l};\n\t"
+      "mul.rn.f16x2 y, y, %4;\n\tfma.rn.f16x2 %0, x, %3, y;\n\t}"
+      : "=r"(d)
+      : "r"(a), "r"(b), "r"(s0), "r"(s1));
+  return d;
+}
+__device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b, uint32_t s0, uint32_t s1) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 x, y;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 x, {h, h};\n\tmov.b32 {l, h}, %2;\n\tmov.b32 y, {h, h};\n\t"
+      "mul.rn.f16x2 y, y, %4;\n\tfma.rn.f16x2 %0, x, %3, y;\n\t}"
+      : "=r"(d)
+      : "r"(a), "r"(b), "r"(s0), "r"(s1));
+  return d;
+}
+__device__ __forceinline__ void apart(uint32_t s, uint32_t (&d)[2]) {
+  d[0] = s & 0xffffu;
+  d[1] = s & 0xffff0000u;
+}
 __device__ __forceinline__ uint32_t halves(float lo, float hi) { return pack2<true>(lo, hi); }
 
 // Where a lane reads a warp's run of 32 keys, relative to the run's first key (a multiple of 32): K of keys 8u + row, V of 16 keys.
@@ -146,6 +167,55 @@ struct Reader4 {
 // Where a run's first key lies in a stage's K, V and their scales.
 struct Run4 {
   uint32_t k, v, ks, vs;
+};
+
+// A lane's share of a tile's scales, [token][head] in shared memory: `unit` bytes at a time, the pieces of a token's heads one after the other.
+struct ScaleCopy {
+  int unit, first, piece, step, rest, all, each, pitch;
+  const uint8_t* from;
+  long long head_stride, offset;
+  __device__ __forceinline__ ScaleCopy(int unit_, int heads, int heads_apart, int bytes, const uint8_t* from_, long long head_stride_, int lane)
+      : unit(unit_), pitch(heads_apart * bytes), from(from_), head_stride(head_stride_) {
+    all = heads * bytes / unit;
+    each = unit == 16 ? all : bytes / unit;  // 16 bytes only where heads follow one another
+    first = lane / all;
+    piece = lane - first * all;
+    step = 32 / all;
+    rest = 32 - step * all;
+    offset = at(piece);
+  }
+  __device__ __forceinline__ long long at(int p) const { return p / each * head_stride + p % each * unit; }
+  template <int UNIT>
+  __device__ __forceinline__ void copy_by(const long long* rows, int tokens, uint32_t to) const {
+    int r = first, p = piece;
+    long long off = offset;
+    while (r < tokens) {
+      const long long row = rows[r];
+      const uint8_t* src = from + off + (row < 0 ? 0 : row);
+      const uint32_t dst = to + r * pitch + p * UNIT;
+      if constexpr (UNIT == 16)
+        copy16(dst, src, row < 0 ? 0 : 16);
+      else
+        copy_small<UNIT>(dst, src, row < 0 ? 0 : UNIT);
+      r += step;
+      if (rest) {
+        p += rest;
+        if (p >= all) {
+          p -= all;
+          ++r;
+        }
+        off = at(p);
+      }
+    }
+  }
+  __device__ __forceinline__ void copy(const long long* rows, int tokens, uint32_t to) const {
+    if (unit == 16)
+      copy_by<16>(rows, tokens, to);
+    else if (unit == 8)
+      copy_by<8>(rows, tokens, to);
+    else
+      copy_by<4>(rows, tokens, to);
+  }
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -336,21 +406,21 @@ struct Rows4 {
     const uint32_t pick = g < 4 ? 0x6240u : 0x7351u;  // of two keys' scales: those of this lane's block of every 32 channels
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      uint32_t sv[2][kPieces];  // scales of keys 2t, 2t + 1 of the first 8 and of the second
+      uint32_t sv[2][kPieces][2];  // scales of keys 2t, 2t + 1 of the first 8 and of the second: (s, 0) and (0, s)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t base = s.vs + (2 * kb + j) * at.v_scale_8, first = base + at.v_scale[0], second = base + at.v_scale[1];
         if constexpr (DV == 128) {
           const uint2 a = lds8(first), b = lds8(second);
           const uint32_t lo = prmt(a.x, b.x, pick), hi = prmt(a.y, b.y, pick);
-          sv[j][0] = widen_e4m3(lo);
-          sv[j][1] = widen_e4m3_hi(lo);
-          sv[j][2] = widen_e4m3(hi);
-          sv[j][3] = widen_e4m3_hi(hi);
+          apart(widen_e4m3(lo), sv[j][0]);
+          apart(widen_e4m3_hi(lo), sv[j][1]);
+          apart(widen_e4m3(hi), sv[j][2]);
+          apart(widen_e4m3_hi(hi), sv[j][3]);
         } else {
           const uint32_t lo = prmt(lds4(first), lds4(second), pick);
-          sv[j][0] = widen_e4m3(lo);
-          sv[j][1] = widen_e4m3_hi(lo);
+          apart(widen_e4m3(lo), sv[j][0]);
+          apart(widen_e4m3_hi(lo), sv[j][1]);
         }
       }
 #pragma unroll
@@ -368,10 +438,10 @@ struct Rows4 {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t c0 = widen_e2m1<0>(r[j]), c1 = widen_e2m1<1>(r[j]), c2 = widen_e2m1<2>(r[j]), c3 = widen_e2m1<3>(r[j]);
-          f[j][0] = mul_f16x2(prmt(c0, c2, 0x5410), sv[j][p]);
-          f[j][1] = mul_f16x2(prmt(c0, c2, 0x7632), sv[j][p]);
-          f[j][2] = mul_f16x2(prmt(c1, c3, 0x5410), sv[j][p]);
-          f[j][3] = mul_f16x2(prmt(c1, c3, 0x7632), sv[j][p]);
+          f[j][0] = pair_lo(c0, c2, sv[j][p][0], sv[j][p][1]);
+          f[j][1] = pair_hi(c0, c2, sv[j][p][0], sv[j][p][1]);
+          f[j][2] = pair_lo(c1, c3, sv[j][p][0], sv[j][p][1]);
+          f[j][3] = pair_hi(c1, c3, sv[j][p][0], sv[j][p][1]);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -554,6 +624,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
     const int queries = chunk_units > 1 ? min(a.chunk_warps * a.chunk_heads, a.group - chunk0 * a.chunk_heads) : heads * a.group;
     const uint8_t *k = a.cache.k + head0 * a.cache.k_head, *v = a.cache.v + head0 * a.cache.v_head;
     const uint8_t *ks = a.scales.k + head0 * a.scales.k_head, *vs = a.scales.v + head0 * a.scales.v_head;
+    const ScaleCopy k_scales(a.k_unit, heads, a.heads, T::kScaleK, ks, a.scales.k_head, lane), v_scales(a.v_unit, heads, a.heads, T::kScaleV, vs, a.scales.v_head, lane);
     constexpr int kSets = kMaxTokens / 32;
     const int box = 1 << a.box_log2;
     const unsigned firsts = box == 16 ? 0x10001u : 1u;  // lanes whose token begins a box, of the sets where one does
@@ -630,36 +701,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
         codes(std::integral_constant<int, T::kRowV / 16>(), s_row[3], v, a.cache.v_head, base + k_bytes, v_place);
       }
       // scales [token][head]: zeros where there is no token
-      auto scales = [&](auto unit, int head_bytes, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to) {
-        constexpr int kUnit = decltype(unit)::value;
-        const int each = kUnit == 16 ? 1 : head_bytes / kUnit, all = kUnit == 16 ? heads * head_bytes / 16 : heads * each, pitch = a.heads * head_bytes;
-        const int step = 32 / all, rest = 32 % all;
-        int r = lane / all, p = lane % all;
-        while (r < TT) {
-          const long long row = rows[r];
-          const uint8_t* src = from + (row < 0 ? 0 : row) + (kUnit == 16 ? p * 16ll : p / each * head_stride + p % each * kUnit);
-          if constexpr (kUnit == 16)
-            copy16(to + r * pitch + p * 16, src, row < 0 ? 0 : 16);
-          else
-            copy_small<kUnit>(to + r * pitch + p * kUnit, src, row < 0 ? 0 : kUnit);
-          r += step;
-          p += rest;
-          if (p >= all) {
-            p -= all;
-            ++r;
-          }
-        }
-      };
-      auto scales_by = [&](int unit, int head_bytes, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to) {
-        if (unit == 16)
-          scales(std::integral_constant<int, 16>(), head_bytes, rows, from, head_stride, to);
-        else if (unit == 8)
-          scales(std::integral_constant<int, 8>(), head_bytes, rows, from, head_stride, to);
-        else
-          scales(std::integral_constant<int, 4>(), head_bytes, rows, from, head_stride, to);
-      };
-      scales_by(a.k_unit, T::kScaleK, s_row[0], ks, a.scales.k_head, base + ks_at);
-      scales_by(a.v_unit, T::kScaleV, s_row[1], vs, a.scales.v_head, base + vs_at);
+      k_scales.copy(s_row[0], TT, base + ks_at);
+      v_scales.copy(s_row[1], TT, base + vs_at);
       if (c.first && lane < heads) {
         const int i = a.desc_per_head ? c.b * a.desc_request + head0 + lane : 0;
         s_scale[stage][lane] = {a.scale_log2 * (a.k_desc ? a.k_desc[i] : 1.0f), a.v_desc ? a.v_desc[i] : 1.0f};
