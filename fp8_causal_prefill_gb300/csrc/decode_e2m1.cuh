@@ -30,10 +30,15 @@ constexpr int kMaxTokens = kWarps * kKeys;
 
 struct Args : DecodeArgs {
   ScaleView scales;
-  int boxes;             // codes come by TMA, box by box (1 << box_log2 tokens of a page); else piece by piece, and box_log2 is the tile's
+  int boxes;             // codes and scales come by TMA, box by box (1 << box_log2 tokens of a page); else piece by piece, and box_log2 is the tile's
+  int dense;             // the scales of a box are one run of bytes
   int k_log2, v_log2;    // tokens whose rows share 128 bytes of shared memory (log2), where a block's heads take less
   int k_unit, v_unit;    // bytes of scales copied at a time: 4, 8, or 16 across heads
   uint32_t order;        // the key within 8 that row g of the scores is: nibble g
+};
+
+struct Maps4 {
+  CUtensorMap k, v, ks, vs;
 };
 
 template <int DQK, int DV>
@@ -65,6 +70,11 @@ __device__ __forceinline__ int key4(uint32_t order, int g) { return order >> (4 
 template <int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+               : "memory");
 }
 // The barrier counts this lane once all its copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
@@ -551,7 +561,7 @@ struct Rows4 {
 // ------------------------------------------------------------------------------------------------
 
 template <int DQK, int DV, int NC>
-__global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+__global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps4 maps) {
   using T = Tile4<DQK, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ unsigned s_prefix[(kWarps + 1) * 32], s_sums[kWarps + 1];
@@ -571,7 +581,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
   const uint32_t tiles_s = smem_addr(smem), full_s = smem_addr(s_full), empty_s = smem_addr(s_empty);
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      ptx::mbar_init(full_s + 8 * i, 33);  // each lane's copies, and the header
+      ptx::mbar_init(full_s + 8 * i, a.boxes ? 1 : 33);  // the header, and (piece by piece) each lane's copies
       ptx::mbar_init(empty_s + 8 * i, warps);
     }
     for (int i = 0; i < a.heads * a.chunk_warps; ++i) ptx::mbar_init(smem_addr(s_meet + i), a.subs);
@@ -579,8 +589,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
     ptx::fence_proxy_async_smem();
   }
   if (a.boxes && threadIdx.x == 32) {
-    ptx::tma_prefetch_desc(&kmap);
-    ptx::tma_prefetch_desc(&vmap);
+    ptx::tma_prefetch_desc(&maps.k);
+    ptx::tma_prefetch_desc(&maps.v);
+    if (!a.dense) {
+      ptx::tma_prefetch_desc(&maps.ks);
+      ptx::tma_prefetch_desc(&maps.vs);
+    }
   }
   __syncthreads();
   wait_for_predecessor();
@@ -624,10 +638,87 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
     const int queries = chunk_units > 1 ? min(a.chunk_warps * a.chunk_heads, a.group - chunk0 * a.chunk_heads) : heads * a.group;
     const uint8_t *k = a.cache.k + head0 * a.cache.k_head, *v = a.cache.v + head0 * a.cache.v_head;
     const uint8_t *ks = a.scales.k + head0 * a.scales.k_head, *vs = a.scales.v + head0 * a.scales.v_head;
+    bool bad = false;
+    int stage = 0;
+    uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
+    auto descales = [&](int st) {  // of a request that begins with this tile
+      if (c.first && lane < heads) {
+        const int i = a.desc_per_head ? c.b * a.desc_request + head0 + lane : 0;
+        s_scale[st][lane] = {a.scale_log2 * (a.k_desc ? a.k_desc[i] : 1.0f), a.v_desc ? a.v_desc[i] : 1.0f};
+      }
+    };
+    // What the compute warps need to know of a tile, and its queries; `bytes` of other copies count on the barrier.
+    auto publish = [&](int st, uint32_t base, uint32_t bar, int valid, bool whole, uint32_t bytes) {
+      s_header[st] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, 0};
+      if (c.first) {
+        bytes += queries * (DQK * 2);
+        bulk_load(base + q_at, a.q + c.b * a.q_batch + static_cast<long long>(first_q) * (DQK * 2), queries * (DQK * 2), bar);
+      }
+      ptx::mbar_arrive_expect_tx(bar, bytes);
+    };
+    if (a.boxes) {
+      // a lane: a box of the tile
+      const int boxes = TT >> a.box_log2, row = lane << a.box_log2;
+      const uint32_t ks_bytes = a.heads * T::kScaleK << a.box_log2, vs_bytes = a.heads * T::kScaleV << a.box_log2;
+      const uint32_t k_to = lane * k_place.box_bytes, v_to = k_bytes + lane * v_place.box_bytes, ks_to = ks_at + lane * ks_bytes, vs_to = vs_at + lane * vs_bytes;
+      const uint32_t box_bytes = k_place.box_bytes + v_place.box_bytes + ks_bytes + vs_bytes;
+      const int k_column = a.k_log2 ? 0 : head0 * T::kRowK / 128, v_column = a.v_log2 ? 0 : head0 * T::kRowV / 128;
+      int pg, off;
+      auto look_up = [&]() {
+        pg = -1;
+        off = 0;
+        if (lane < boxes && c.t + row < c.len) {
+          int p;
+          page_of(a, c.t + row, &p, &off);
+          pg = a.table[c.b * a.table_stride + p];
+        }
+      };
+      look_up();
+      while (true) {
+        if (!mbar_wait_bounded(empty_s + 8 * stage, parity, a.wait_clocks)) {
+          if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
+          break;
+        }
+        const uint32_t base = tiles_s + stage * stage_bytes, bar = full_s + 8 * stage;
+        const int valid = min(TT, c.len - c.t);
+        const bool inside = lane < boxes && row < valid, ok = inside && pg >= 0 && pg < a.cache.num_pages;
+        bad |= inside && !ok;
+        const unsigned there = __ballot_sync(0xffffffffu, ok);
+        if (ok) {  // (the barrier's phase cannot end before the arrival below)
+          tma_load_5d(base + k_to, &maps.k, bar, 0, off >> a.k_log2, k_column, 0, pg);
+          tma_load_5d(base + v_to, &maps.v, bar, 0, off >> a.v_log2, v_column, 0, pg);
+          if (a.dense) {
+            bulk_load(base + ks_to, ks + pg * a.scales.k_page + off * a.scales.k_tok, ks_bytes, bar);
+            bulk_load(base + vs_to, vs + pg * a.scales.v_page + off * a.scales.v_tok, vs_bytes, bar);
+          } else {
+            tma_load_3d(base + ks_to, &maps.ks, bar, head0 * T::kScaleK, off, pg);
+            tma_load_3d(base + vs_to, &maps.vs, bar, head0 * T::kScaleV, off, pg);
+          }
+        }
+        const bool whole = valid == TT && there == 0xffffffffu >> (32 - boxes);
+        if (!whole)
+          for (int i = 0; i < TT / 32; ++i) {
+            const int r = 32 * i + lane;
+            const unsigned mask = __ballot_sync(0xffffffffu, r < valid && (there >> (r >> a.box_log2) & 1));
+            if (lane == 0) s_mask[stage][i] = mask;
+          }
+        descales(stage);
+        __syncwarp();
+        if (lane == 0) publish(stage, base, bar, valid, whole, __popc(there) * box_bytes);
+        c.left = c.left_after(TT);
+        if (c.left <= 0) break;
+        c.advance(a, TT);
+        look_up();
+        if (++stage == S) {
+          stage = 0;
+          parity ^= 1;
+        }
+      }
+      if (bad) atomicOr(a.status, kStatusBadPageBit);
+      return;
+    }
     const ScaleCopy k_scales(a.k_unit, heads, a.heads, T::kScaleK, ks, a.scales.k_head, lane), v_scales(a.v_unit, heads, a.heads, T::kScaleV, vs, a.scales.v_head, lane);
     constexpr int kSets = kMaxTokens / 32;
-    const int box = 1 << a.box_log2;
-    const unsigned firsts = box == 16 ? 0x10001u : 1u;  // lanes whose token begins a box, of the sets where one does
     int pg[kSets], off[kSets];  // page and place in it of tokens c.t + 32 i + lane
     auto look_up = [&]() {
 #pragma unroll
@@ -643,9 +734,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
       }
     };
     look_up();
-    bool bad = false;
-    int stage = 0;
-    uint32_t parity = 1;  // a new barrier counts as one whose phase before its first has ended
     while (true) {
       if (!mbar_wait_bounded(empty_s + 8 * stage, parity, a.wait_clocks)) {
         if (lane == 0) atomicOr(a.status, kStatusTimeoutBit);
@@ -654,7 +742,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
       const uint32_t base = tiles_s + stage * stage_bytes, bar = full_s + 8 * stage;
       const int valid = min(TT, c.len - c.t);
       bool whole = valid == TT;
-      uint32_t bytes = 0;
 #pragma unroll
       for (int i = 0; i < kSets; ++i) {
         if (32 * i >= TT) break;
@@ -663,60 +750,38 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
         const unsigned mask = __ballot_sync(0xffffffffu, ok);
         whole = whole && mask == 0xffffffffu;
         const long long page = pg[i], at = off[i];
-        if (a.boxes) {  // the first token of each box issues its copies, before the barrier's phase can end by the arrivals below
-          if (ok && ((32 * i + lane) & (box - 1)) == 0) {
-            const int n = (32 * i + lane) >> a.box_log2;
-            tma_load_5d(base + n * k_place.box_bytes, &kmap, bar, 0, off[i] >> a.k_log2, a.k_log2 ? 0 : head0 * T::kRowK / 128, 0, pg[i]);
-            tma_load_5d(base + k_bytes + n * v_place.box_bytes, &vmap, bar, 0, off[i] >> a.v_log2, a.v_log2 ? 0 : head0 * T::kRowV / 128, 0, pg[i]);
-          }
-          // (a box's tokens share a page, so if its first one has none, neither do the others; and the first is inside if any is)
-          bytes += __popc(mask & firsts) * (box >= 32 && ((32 * i) & (box - 1)) ? 0u : k_place.box_bytes + v_place.box_bytes);
-        } else {
-          s_row[2][32 * i + lane] = ok ? page * a.cache.k_page + at * a.cache.k_tok : -1;
-          s_row[3][32 * i + lane] = ok ? page * a.cache.v_page + at * a.cache.v_tok : -1;
-        }
+        s_row[2][32 * i + lane] = ok ? page * a.cache.k_page + at * a.cache.k_tok : -1;
+        s_row[3][32 * i + lane] = ok ? page * a.cache.v_page + at * a.cache.v_tok : -1;
         s_row[0][32 * i + lane] = ok ? page * a.scales.k_page + at * a.scales.k_tok : -1;
         s_row[1][32 * i + lane] = ok ? page * a.scales.v_page + at * a.scales.v_tok : -1;
         if (lane == 0) s_mask[stage][i] = mask;
       }
       __syncwarp();
-      if (!a.boxes) {
-        // codes: the pieces of a token's heads, 32 at a time
-        auto codes = [&](auto pieces, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to, const Place& place) {
-          constexpr int kPieces = decltype(pieces)::value;
-          const int all = heads * kPieces, step = 32 / all, rest = 32 % all;
-          int r = lane / all, p = lane % all;
-          while (r < valid) {
-            const long long row = rows[r];
-            if (row >= 0) copy16(to + place(r, p * 16), from + row + p / kPieces * head_stride + p % kPieces * 16, 16);
-            r += step;
-            p += rest;
-            if (p >= all) {
-              p -= all;
-              ++r;
-            }
+      // codes: the pieces of a token's heads, 32 at a time
+      auto codes = [&](auto pieces, const long long* rows, const uint8_t* from, long long head_stride, uint32_t to, const Place& place) {
+        constexpr int kPieces = decltype(pieces)::value;
+        const int all = heads * kPieces, step = 32 / all, rest = 32 % all;
+        int r = lane / all, p = lane % all;
+        while (r < valid) {
+          const long long row = rows[r];
+          if (row >= 0) copy16(to + place(r, p * 16), from + row + p / kPieces * head_stride + p % kPieces * 16, 16);
+          r += step;
+          p += rest;
+          if (p >= all) {
+            p -= all;
+            ++r;
           }
-        };
-        codes(std::integral_constant<int, T::kRowK / 16>(), s_row[2], k, a.cache.k_head, base, k_place);
-        codes(std::integral_constant<int, T::kRowV / 16>(), s_row[3], v, a.cache.v_head, base + k_bytes, v_place);
-      }
+        }
+      };
+      codes(std::integral_constant<int, T::kRowK / 16>(), s_row[2], k, a.cache.k_head, base, k_place);
+      codes(std::integral_constant<int, T::kRowV / 16>(), s_row[3], v, a.cache.v_head, base + k_bytes, v_place);
       // scales [token][head]: zeros where there is no token
       k_scales.copy(s_row[0], TT, base + ks_at);
       v_scales.copy(s_row[1], TT, base + vs_at);
-      if (c.first && lane < heads) {
-        const int i = a.desc_per_head ? c.b * a.desc_request + head0 + lane : 0;
-        s_scale[stage][lane] = {a.scale_log2 * (a.k_desc ? a.k_desc[i] : 1.0f), a.v_desc ? a.v_desc[i] : 1.0f};
-      }
+      descales(stage);
       arrive_after_copies(bar);
       __syncwarp();
-      if (lane == 0) {
-        s_header[stage] = {c.b, c.flags(TT) | (whole ? 0 : kPartial), valid, 0};
-        if (c.first) {
-          bytes += queries * (DQK * 2);
-          bulk_load(base + q_at, a.q + c.b * a.q_batch + static_cast<long long>(first_q) * (DQK * 2), queries * (DQK * 2), bar);
-        }
-        ptx::mbar_arrive_expect_tx(bar, bytes);
-      }
+      if (lane == 0) publish(stage, base, bar, valid, whole, 0);
       c.left = c.left_after(TT);
       if (c.left <= 0) break;
       c.advance(a, TT);
@@ -769,8 +834,22 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, NC == 1 ? 3 : 2) decode4_ke
       for (int turn = 0; turn < a.turns; ++turn) {
         const uint32_t mask = h.flags & kPartial ? s_mask[stage][sub * a.turns + turn] : 0xffffffffu;
         if (mask == 0) continue;
-        const Run4 s = {base + k_place.step(turn * kKeys), base + k_bytes + v_place.step(turn * kKeys), base + ks_at + turn * 4 * reader.k_scale_8,
-                        base + vs_at + turn * 4 * reader.v_scale_8};
+        Run4 s = {base, base + k_bytes, base + ks_at, base + vs_at};
+        if (turn) {
+          s.k += k_place.step(turn * kKeys);
+          s.v += v_place.step(turn * kKeys);
+          s.ks += turn * 4 * reader.k_scale_8;
+          s.vs += turn * 4 * reader.v_scale_8;
+        }
+        if (mask != 0xffffffffu && a.boxes) {
+          // whatever the scales of keys that do not count hold is no number to multiply by 0
+          const uint32_t mine = s.vs + (sub * run_keys + lane) * a.heads * T::kScaleV + head * T::kScaleV;
+          if (!((mask >> lane) & 1))
+#pragma unroll
+            for (int i = 0; i < T::kScaleV; i += 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(mine + i), "r"(0) : "memory");
+          ptx::fence_proxy_async_smem();  // before a later TMA load into this stage
+          __syncwarp();
+        }
         rows.tile(s, reader, a.order, mask, lane);
       }
       if (h.flags & kLast) {
@@ -828,6 +907,15 @@ inline bool make_map4(CUtensorMap* m, const uint8_t* base, const Args& a, long l
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t*>(base), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The map of a box's scales: [page][token][heads].
+inline bool make_scale_map(CUtensorMap* m, const uint8_t* base, const Args& a, long long page, long long tok, int bytes) {
+  using u64 = cuuint64_t;
+  using u32 = cuuint32_t;
+  const u64 dims[3] = {u64(a.cache.H_kv) * bytes, u64(a.cache.page_size), u64(a.cache.num_pages)}, strides[2] = {u64(tok), u64(page)};
+  const u32 box[3] = {u32(a.heads * bytes), u32(1) << a.box_log2, 1}, estr[3] = {1, 1, 1};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 // Bytes of scales that can be copied at a time: 16 where a block's heads follow one another and rows are aligned.
 inline int scale_unit(const Args& a, const uint8_t* base, long long page, long long tok, long long head, int bytes) {
   const int H_kv = a.cache.H_kv, last = (H_kv - 1) % a.heads + 1;
@@ -863,10 +951,17 @@ bool plan4(Args& a, int nsm, int* smem) {
   while (box > 1 && a.cache.page_size % box != 0) box /= 2;
   const CacheView& c = a.cache;
   a.boxes = box >= 16 && boxable(a, c.k_page, c.k_tok, c.k_head, T::kRowK, a.k_log2, box) && boxable(a, c.v_page, c.v_tok, c.v_head, T::kRowV, a.v_log2, box);
-  a.box_log2 = a.boxes ? log2_of(box) : a.tile_log2;
   const ScaleView& s = a.scales;
   a.k_unit = scale_unit(a, s.k, s.k_page, s.k_tok, s.k_head, T::kScaleK);
   a.v_unit = scale_unit(a, s.v, s.v_page, s.v_tok, s.v_head, T::kScaleV);
+  // The scales of a box: one run of bytes where a block takes all heads, else rows of a multiple of 16 bytes.
+  auto run = [&](const uint8_t* base, long long page, long long tok, long long head, int bytes) {
+    return a.heads == c.H_kv && tok == a.heads * bytes && (c.H_kv == 1 || head == bytes) && aligned(base, 16) && page % 16 == 0;
+  };
+  a.dense = run(s.k, s.k_page, s.k_tok, s.k_head, T::kScaleK) && run(s.v, s.v_page, s.v_tok, s.v_head, T::kScaleV);
+  auto spaced = [](long long page, long long tok) { return page > 0 && tok > 0 && page < (1ll << 40) && tok < (1ll << 40); };
+  a.boxes = a.boxes && (a.dense || (a.k_unit == 16 && a.v_unit == 16 && spaced(s.k_page, s.k_tok) && spaced(s.v_page, s.v_tok)));
+  a.box_log2 = a.boxes ? log2_of(box) : a.tile_log2;
   const int nq = a.chunks > a.chunk_warps ? a.chunk_warps * a.chunk_heads : a.heads * a.group;
   a.q_bytes = static_cast<int>(round_up(nq * DQK * 2, 16));
   const int warps = a.heads * a.chunk_warps * a.subs;
@@ -891,17 +986,19 @@ zyfa_status_t launch4(Args& a, int nsm, int dev, uint8_t* ws, cudaStream_t strea
   int smem;
   set_workspace(a, ws);
   if (!plan4<DQK, DV, NC>(a, nsm, &smem)) return ZYFA_ERR_UNSUPPORTED;
-  CUtensorMap kmap = {}, vmap = {};
+  Maps4 maps = {};
   const CacheView& c = a.cache;
-  if (a.boxes && !(make_map4(&kmap, c.k, a, c.k_page, c.k_tok, Tile4<DQK, DV>::kRowK, a.k_log2) &&
-                   make_map4(&vmap, c.v, a, c.v_page, c.v_tok, Tile4<DQK, DV>::kRowV, a.v_log2))) {
+  using T = Tile4<DQK, DV>;
+  if (a.boxes && !(make_map4(&maps.k, c.k, a, c.k_page, c.k_tok, T::kRowK, a.k_log2) && make_map4(&maps.v, c.v, a, c.v_page, c.v_tok, T::kRowV, a.v_log2) &&
+                   (a.dense || (make_scale_map(&maps.ks, a.scales.k, a, a.scales.k_page, a.scales.k_tok, T::kScaleK) &&
+                                make_scale_map(&maps.vs, a.scales.v, a, a.scales.v_page, a.scales.v_tok, T::kScaleV))))) {
     a.boxes = 0;
     a.box_log2 = a.tile_log2;
   }
   static std::atomic<int> set[kMaxDevices];
   if (!prepare(decode4_kernel<DQK, DV, NC>, 2, dev, set)) return ZYFA_ERR_CUDA;
   if (launch_dependent(decode4_kernel<DQK, DV, NC>, dim3(static_cast<unsigned>(a.groups) * a.units), (a.heads * a.chunk_warps * a.subs + 1) * 32, smem, stream,
-                       a, kmap, vmap) != cudaSuccess)
+                       a, maps) != cudaSuccess)
     return ZYFA_ERR_CUDA;
   return a.whole ? ZYFA_OK : launch_join<DV>(a, nsm, dev, stream);
 }
