@@ -19,9 +19,9 @@ zyfa_status_t attend(const void* q, long long q_batch_stride, const zyfa_paged_c
   st = set_device(a, &dev, &nsm);
   if (st != ZYFA_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  return cache->D_qk == 64    ? launch4<64, 64, 1>(a, nsm, dev, ws, stream)
-         : cache->D_qk == 128 ? launch4<128, 128, 1>(a, nsm, dev, ws, stream)
-                              : launch4<192, 128, 1>(a, nsm, dev, ws, stream);
+  return cache->D_qk == 64    ? launch4<64, 64>(a, nsm, dev, ws, stream)
+         : cache->D_qk == 128 ? launch4<128, 128>(a, nsm, dev, ws, stream)
+                              : launch4<192, 128>(a, nsm, dev, ws, stream);
 }
 
 }  // namespace
