@@ -17,8 +17,8 @@
 
 namespace {
 
-constexpr int kMaxRows = 32;  // rows per block at most
-constexpr int kBatch = 4;     // of a thread's loads on their way
+constexpr int kMaxRows = 128;  // rows per block at most
+constexpr int kBatch = 4;      // of a thread's pieces on their way
 
 struct ReadArgs {
   zyfa::CacheView cache;
@@ -31,6 +31,7 @@ struct ReadArgs {
   int* status;
   long long table_stride, N, max_len;
   int B, rows;  // rows per block
+  int wide;     // bf16 rows are aligned to 32 bytes
   int desc_per_head, desc_request, out_per_head;
   uint32_t page_magic;
   int page_shift;
@@ -38,22 +39,20 @@ struct ReadArgs {
 };
 
 template <int DQK>
-constexpr int kReadThreads = DQK == 192 ? 192 : 256;
+constexpr int kReadThreads = 256;
 
-// What a thread reads of a head: VEC values of a cache type, and their scale.
-template <int KIND, int VEC>
+// What a thread reads of a head: 16 values of a cache type, and their scale.
+template <int KIND>
 struct Piece {
-  static constexpr int kBytes = KIND == ZYFA_DTYPE_E2M1 ? VEC / 2 : KIND == ZYFA_DTYPE_E4M3 ? VEC : 2 * VEC;
+  static constexpr int kBytes = KIND == ZYFA_DTYPE_E2M1 ? 8 : KIND == ZYFA_DTYPE_E4M3 ? 16 : 32;
   static constexpr int kWords = kBytes / 4;
-  uint32_t w[kWords];
-  uint32_t scale;
+  uint32_t w[kWords], scale;
   __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* s) {
-    if constexpr (kWords == 1) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (kWords == 2) {
+    if constexpr (KIND == ZYFA_DTYPE_E2M1) {
       const uint2 x = *reinterpret_cast<const uint2*>(p);
       w[0] = x.x;
       w[1] = x.y;
+      scale = *s;
     } else {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
@@ -64,7 +63,6 @@ struct Piece {
         w[i + 3] = x.w;
       }
     }
-    if constexpr (KIND == ZYFA_DTYPE_E2M1) scale = *s;
   }
   static __device__ __forceinline__ void two(uint32_t f16, float* y) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f16));
@@ -72,7 +70,7 @@ struct Piece {
     y[1] = v.y;
   }
   // the values over their descale
-  __device__ __forceinline__ void values(float (&y)[VEC]) const {
+  __device__ __forceinline__ void values(float (&y)[16]) const {
     if constexpr (KIND == ZYFA_DTYPE_E2M1) {
       const uint32_t s = zyfa::widen_e4m3(scale * 0x101u);  // in both halves
 #pragma unroll
@@ -98,12 +96,25 @@ struct Piece {
   }
 };
 
-template <bool OUT_FP8, int VEC>
-__device__ __forceinline__ void put(uint8_t* to, const float (&y)[VEC], float f) {
-  uint32_t w[4];
-  static_assert(VEC == (OUT_FP8 ? 16 : 8));
+// 16 bytes, or 32, at once where the rows are aligned to them (`wide`).
+template <bool OUT_FP8>
+__device__ __forceinline__ void put_words(uint8_t* to, const uint32_t (&w)[OUT_FP8 ? 4 : 8], bool wide) {
+  if (OUT_FP8 || !wide) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < (OUT_FP8 ? 4 : 8); i += 4) reinterpret_cast<uint4*>(to)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else if constexpr (!OUT_FP8) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                 "r"(w[6]), "r"(w[7])
+                 : "memory");
+  }
+}
+
+template <bool OUT_FP8>
+__device__ __forceinline__ void put(uint8_t* to, const float (&y)[16], float f, bool wide) {
+  constexpr int kWords = OUT_FP8 ? 4 : 8;
+  uint32_t w[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
     if constexpr (OUT_FP8)
       asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
           "mov.b32 %0, {lo, hi};\n\t}"
@@ -112,63 +123,60 @@ __device__ __forceinline__ void put(uint8_t* to, const float (&y)[VEC], float f)
     else
       asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(y[2 * i + 1] * f), "f"(y[2 * i] * f));
   }
-  *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+  put_words<OUT_FP8>(to, w, wide);
 }
 
-// Where a block's rows are: request (-2: none's, left as it is; -1: no page, zeros), page and place in it.
+// Where a block's rows are: request (-2: none's, left as it is; -1: no page, zeros), and the token's bytes in the cache and in the scales.
 struct Places {
-  long long page[kMaxRows];
-  int off[kMaxRows], request[kMaxRows];
+  long long row[2][kMaxRows], scales[2][kMaxRows];  // K, V
+  int request[kMaxRows];
 };
 
-template <int KIND, bool OUT_FP8, int D, int THREADS>
-__device__ __forceinline__ void copy_rows(const ReadArgs& a, const Places& at, long long n0, int here, const uint8_t* cache, long long page, long long tok,
-                                          long long head, const uint8_t* scales, long long s_page, long long s_tok, long long s_head, const float* desc,
-                                          const float* out_desc, uint8_t* out) {
-  constexpr int VEC = OUT_FP8 ? 16 : 8, kPieces = D / VEC, kLanes = THREADS / kPieces;
-  static_assert(THREADS % kPieces == 0);
-  using P = Piece<KIND, VEC>;
-  const int H_kv = a.cache.H_kv, piece = threadIdx.x % kPieces, c = piece * VEC;
-  int row = 0, h = threadIdx.x / kPieces;
-  auto settle = [&]() {
-    while (h >= H_kv) {
-      h -= H_kv;
-      ++row;
-    }
-  };
-  settle();
-  while (row < here) {
-    P p[kBatch];
-    int rows[kBatch], heads[kBatch], n = 0;
+// K (WHICH 0) or V (1) of the block's rows.  A thread keeps its 16 channels of a head while rows pass, several rows of few heads at a time.
+template <int WHICH, int KIND, bool OUT_FP8, int D, int THREADS>
+__device__ __forceinline__ void copy_rows(const ReadArgs& a, const Places& at, long long n0, int here) {
+  constexpr int kPieces = D / 16, kOut = 16 * (OUT_FP8 ? 1 : 2);
+  using P = Piece<KIND>;
+  const int H_kv = a.cache.H_kv, all = H_kv * kPieces;
+  const uint8_t *cache = WHICH ? a.cache.v : a.cache.k, *scales = WHICH ? a.scales.v : a.scales.k;
+  const long long head_stride = WHICH ? a.cache.v_head : a.cache.k_head, scale_stride = WHICH ? a.scales.v_head : a.scales.k_head;
+  const float *desc = WHICH ? a.v_desc : a.k_desc, *out_desc = WHICH ? a.v_out_desc : a.k_out_desc;
+  uint8_t* const out = WHICH ? a.v_out : a.k_out;
+  if (!out) return;
+  const int step = all < THREADS ? THREADS / all : 1, first = all < THREADS ? static_cast<int>(threadIdx.x) / all : 0;
+  if (first >= step) return;
+  for (int item = threadIdx.x - first * all; item < all; item += THREADS) {
+    const int h = item / kPieces, c = item % kPieces;
+    const uint8_t* from = cache + h * head_stride + c * P::kBytes;
+    const uint8_t* from_scales = scales + h * scale_stride + c;
+    uint8_t* to = out + ((n0 + first) * all + item) * kOut;
+    float inv = 1.0f, f = 1.0f;
+    if (OUT_FP8 && out_desc) inv = __frcp_rn(out_desc[a.out_per_head ? h : 0]);
+    const bool by_request = KIND != ZYFA_DTYPE_BF16 && desc && a.desc_request;
+    if (KIND != ZYFA_DTYPE_BF16 && desc && !by_request) f = desc[a.desc_per_head ? h : 0];
+    f *= inv;
+    for (int r0 = first; r0 < here; r0 += kBatch * step) {
+      P p[kBatch];
+      int request[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      rows[i] = row;
-      heads[i] = h;
-      if (row < here) {
-        n = i + 1;
-        if (at.request[row] >= 0)
-          p[i].load(cache + at.page[row] * page + at.off[row] * tok + h * head + c * P::kBytes / VEC,
-                    KIND == ZYFA_DTYPE_E2M1 ? scales + at.page[row] * s_page + at.off[row] * s_tok + h * s_head + c / 16 : nullptr);
-        h += kLanes;
-        settle();
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * step;
+        request[i] = r < here ? at.request[r] : -2;
+        if (request[i] >= 0) p[i].load(from + at.row[WHICH][r], KIND == ZYFA_DTYPE_E2M1 ? from_scales + at.scales[WHICH][r] : nullptr);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (i >= n) break;
-      const int b = at.request[rows[i]];
-      if (b == -2) continue;
-      uint8_t* to = out + (((n0 + rows[i]) * H_kv + heads[i]) * D + c) * (OUT_FP8 ? 1 : 2);
-      if (b < 0) {
-        *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
-        continue;
+      for (int i = 0; i < kBatch; ++i) {
+        if (request[i] >= 0) {
+          if (by_request) f = desc[request[i] * a.desc_request + h] * inv;
+          float y[16];
+          p[i].values(y);
+          put<OUT_FP8>(to, y, f, a.wide);
+        } else if (request[i] == -1) {
+          const uint32_t none[OUT_FP8 ? 4 : 8] = {};
+          put_words<OUT_FP8>(to, none, a.wide);
+        }
+        to += static_cast<long long>(step) * all * kOut;
       }
-      float f = 1.0f;
-      if (KIND != ZYFA_DTYPE_BF16 && desc) f = desc[a.desc_per_head ? b * a.desc_request + heads[i] : 0];
-      if (OUT_FP8 && out_desc) f *= __frcp_rn(out_desc[a.out_per_head ? heads[i] : 0]);
-      float y[VEC];
-      p[i].values(y);
-      put<OUT_FP8, VEC>(to, y, f);
     }
   }
 }
@@ -214,19 +222,17 @@ __global__ void __launch_bounds__(kReadThreads<DQK>) read_kernel(const __grid_co
         if (request < 0) atomicOr(a.status, zyfa::kStatusBadPageBit);
       }
     }
-    s_at.page[tid] = page;
-    s_at.off[tid] = off;
+    const zyfa::CacheView& c = a.cache;
+    const zyfa::ScaleView& s = a.scales;
+    s_at.row[0][tid] = page * c.k_page + off * c.k_tok;
+    s_at.row[1][tid] = page * c.v_page + off * c.v_tok;
+    s_at.scales[0][tid] = page * s.k_page + off * s.k_tok;
+    s_at.scales[1][tid] = page * s.v_page + off * s.v_tok;
     s_at.request[tid] = request;
   }
   __syncthreads();
-  const zyfa::CacheView& c = a.cache;
-  const zyfa::ScaleView& s = a.scales;
-  if (a.k_out)
-    copy_rows<KIND, OUT_FP8, DQK, kN>(a, s_at, n0, here, c.k, c.k_page, c.k_tok, c.k_head, s.k, s.k_page, s.k_tok, s.k_head, a.k_desc, a.k_out_desc,
-                                      a.k_out);
-  if (a.v_out)
-    copy_rows<KIND, OUT_FP8, DV, kN>(a, s_at, n0, here, c.v, c.v_page, c.v_tok, c.v_head, s.v, s.v_page, s.v_tok, s.v_head, a.v_desc, a.v_out_desc,
-                                     a.v_out);
+  copy_rows<0, KIND, OUT_FP8, DQK, kN>(a, s_at, n0, here);
+  copy_rows<1, KIND, OUT_FP8, DV, kN>(a, s_at, n0, here);
 }
 
 template <int KIND, bool OUT_FP8>
@@ -306,6 +312,7 @@ extern "C" zyfa_status_t zyfa_paged_read(const zyfa_paged_cache_t* cache, const 
   a.k_out = static_cast<uint8_t*>(k_out);
   a.v_out = static_cast<uint8_t*>(v_out);
   a.N = N;
+  a.wide = aligned(k_out, 32) && aligned(v_out, 32);
   const bool fp8 = out_dtype == ZYFA_DTYPE_E4M3;
   a.k_desc = k_descale;
   a.v_desc = v_descale;
@@ -317,8 +324,11 @@ extern "C" zyfa_status_t zyfa_paged_read(const zyfa_paged_cache_t* cache, const 
   zyfa::division_by(cache->page_size, 30, &a.page_magic, &a.page_shift);
   const int threads = cache->D_qk == 192 ? kReadThreads<192> : kReadThreads<64>;
   a.step = (B + threads - 1) / threads;
-  const long long most = std::min<long long>(kMaxRows, std::max(1ll, 8192 / (heads * (cache->D_qk + cache->D_v) * es / 4)));
-  a.rows = static_cast<int>(std::max(1ll, std::min(most, (N + 4ll * nsm - 1) / (4ll * nsm))));
+  // Rows of a block: whole passes of its threads, 64 KiB to write (96 in e4m3, where the start counts more), but blocks for every SM four
+  // times over.  131072 tokens of 8 heads of 128 as bf16: 105.6 us, with 96 KiB 107.2; 32768 as e4m3 22.0 with 96 KiB, 24.2 with 64.
+  const long long bytes = heads * (cache->D_qk + cache->D_v) * es, pass = std::max(1ll, threads / std::max(1ll, heads * cache->D_qk / 16));
+  const long long most = std::max(pass, (es == 2 ? 65536 : 98304) / bytes / pass * pass), wanted = (N + 4ll * nsm - 1) / (4ll * nsm);
+  a.rows = static_cast<int>(std::min<long long>(kMaxRows, std::min(most, (wanted + pass - 1) / pass * pass)));
   cudaError_t e;
   if (four)
     e = launch<ZYFA_DTYPE_E2M1>(a, fp8, cache->D_qk, stream);

@@ -55,34 +55,39 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
   return r;
 }
 
-// 16 values as codes and their scale.
-__device__ __forceinline__ void quantise(const float (&y)[16], float inv, uint2* codes, uint8_t* scale) {
-  float z[16];
+// The largest magnitude among 8 values, as bits, whose order is that of magnitudes, with NaN above all.
+__device__ __forceinline__ uint32_t top_of(const float* z) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    z[i] = y[i] * inv;
-    top = max(top, __float_as_uint(z[i]) & 0x7fffffffu);  // magnitudes in the order of their bits, NaN above all
-  }
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(z[i]) & 0x7fffffffu);
+  return top;
+}
+// The scale of a block with this largest magnitude; *r: what its values are multiplied by.
+__device__ __forceinline__ uint8_t scale_of(uint32_t top, float* r) {
   uint16_t s8;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.0f), "f"(__uint_as_float(top) * (1.0f / 6.0f)));
   float s;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(s) : "r"(zyfa::widen_e4m3(s8)));
-  const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-  uint32_t w[2];
+  *r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  return static_cast<uint8_t>(s8);
+}
+__device__ __forceinline__ uint32_t codes8(const float* z, float r) {
+  return codes2(z[0] * r, z[1] * r) | codes2(z[2] * r, z[3] * r) << 8 | codes2(z[4] * r, z[5] * r) << 16 | codes2(z[6] * r, z[7] * r) << 24;
+}
+// 16 values as codes and their scale.
+__device__ __forceinline__ void quantise(float (&y)[16], float inv, uint2* codes, uint8_t* scale) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = codes2(z[8 * i + 2 * j] * r, z[8 * i + 2 * j + 1] * r);
-    w[i] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-  }
-  *codes = make_uint2(w[0], w[1]);
-  *scale = static_cast<uint8_t>(s8);
+  for (int i = 0; i < 16; ++i) y[i] *= inv;
+  float r;
+  *scale = scale_of(max(top_of(y), top_of(y + 8)), &r);
+  *codes = make_uint2(codes8(y, r), codes8(y + 8, r));
 }
 
-template <bool INTERLEAVED, int DQK, int DV>
-__global__ void __launch_bounds__(kThreads<DQK>) store4_kernel(const __grid_constant__ Store4Args a) {
+// NEAT: blocks of 16 key channels turn as a whole (they begin and end where the rotation's halves do), and a block of a key is in one thread,
+// or halves in two lanes that tell one another their largest magnitude: keys go the way of queries.  Else a thread has a block of a key
+// and reads its partners a second time.
+template <bool INTERLEAVED, bool NEAT, int DQK, int DV>
+__global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1) store4_kernel(const __grid_constant__ Store4Args a) {
   constexpr int kN = kThreads<DQK>, kPieces = DQK / 16, kBlocksK = DQK / 16, kBlocksV = DV / 16, kHalf = DQK / 2;
   static_assert(kN % kPieces == 0 && kN % kBlocksV == 0);
   __shared__ __align__(16) float s_cos[kMaxTokens][kHalf], s_sin[kMaxTokens][kHalf];
@@ -105,17 +110,18 @@ __global__ void __launch_bounds__(kThreads<DQK>) store4_kernel(const __grid_cons
     d0 = d < a.offset ? d : d + a.rot;
     d1 = d + 8 < a.offset ? d + 8 : d + 8 + a.rot;
   }
-  Walk w = {0, tid / kPieces, a.H, kN / kPieces};
-  w.settle();
-  if (!a.q) w.token = here;
+  const int heads_q = a.q ? a.H : 0;
+  Walk w = {0, tid / kPieces, heads_q + (NEAT && a.k ? H_kv : 0), kN / kPieces};
+  if (w.heads) w.settle(); else w.token = here;
   uint4 x0, x1;
   auto fetch = [&]() {
     if (w.token >= here) return;
-    const __nv_bfloat16* x = a.q + (n0 + w.token) * a.q_tok + w.head * DQK;
+    const long long n = n0 + w.token;
+    const __nv_bfloat16* x = w.head < heads_q ? a.q + n * a.q_tok + w.head * DQK : a.k + n * a.k_tok + (w.head - heads_q) * DQK;
     x0 = *reinterpret_cast<const uint4*>(x + d0);
     x1 = *reinterpret_cast<const uint4*>(x + d1);
   };
-  // keys: this thread's block of 16 channels, two halves of 8 that turn alike; from: the channel of a half's partners (its own: none)
+  // keys (not NEAT): this thread's block of 16 channels, two halves of 8 that turn alike; from: the channel of a half's partners (its own: none)
   const int kd = tid % kBlocksK * 16;
   int from[2], first_pair[2];
   bool second[2];
@@ -143,7 +149,8 @@ __global__ void __launch_bounds__(kThreads<DQK>) store4_kernel(const __grid_cons
   const int vd = tid % kBlocksV * 16;
   Walk wv = {0, tid / kBlocksV, H_kv, kN / kBlocksV};
   wv.settle();
-  if (!a.k) wk.token = wv.token = here;
+  if (!a.k) wv.token = here;
+  if (!a.k || NEAT) wk.token = here;
   uint4 v0, v1;
   auto fetch_v = [&]() {
     if (wv.token >= here) return;
@@ -154,7 +161,7 @@ __global__ void __launch_bounds__(kThreads<DQK>) store4_kernel(const __grid_cons
   zyfa::wait_for_predecessor();
   // the first loads run while the tables are made
   fetch();
-  fetch_k();
+  if (!NEAT) fetch_k();
   fetch_v();
   if (tid < here) {
     const long long slot = a.slots[n0 + tid];
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(kThreads<DQK>) store4_kernel(const __grid_cons
     *reinterpret_cast<uint2*>(a.cache.v + at * a.cache.v_page + s_off[token] * a.cache.v_tok + head * a.cache.v_head + vd / 2) = codes;
     a.scales.v[at * a.scales.v_page + s_off[token] * a.scales.v_tok + head * a.scales.v_head + vd / 16] = scale;
   }
-  while (wk.token < here) {
+  while (!NEAT && wk.token < here) {
     const int token = wk.token, head = wk.head;
     float y[16], p[16];
     widen8(k0, *reinterpret_cast<float(*)[8]>(y));
@@ -249,7 +256,8 @@ __global__ void __launch_bounds__(kThreads<DQK>) store4_kernel(const __grid_cons
     w.head += w.lanes;
     w.settle();
     fetch();
-    if (s_page[token] == -2) continue;
+    const long long at = s_page[token];
+    if (at == -2) continue;
     if (pair >= 0) {
       float c[8], s[8];
       *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&s_cos[token][pair]);
@@ -266,18 +274,59 @@ __global__ void __launch_bounds__(kThreads<DQK>) store4_kernel(const __grid_cons
         }
       }
     }
-    __nv_bfloat16* row = a.q_out + ((n0 + token) * a.H + head) * DQK;
-    *reinterpret_cast<uint4*>(row + d0) = bf16x8(u);
-    *reinterpret_cast<uint4*>(row + d1) = bf16x8(v);
+    const long long n = n0 + token;
+    if (!NEAT || head < heads_q) {
+      __nv_bfloat16* row = a.q_out + (n * a.H + head) * DQK;
+      *reinterpret_cast<uint4*>(row + d0) = bf16x8(u);
+      *reinterpret_cast<uint4*>(row + d1) = bf16x8(v);
+    } else {
+      const int hk = head - heads_q;
+      if (a.k_out) {
+        __nv_bfloat16* row = a.k_out + (n * H_kv + hk) * DQK;
+        *reinterpret_cast<uint4*>(row + d0) = bf16x8(u);
+        *reinterpret_cast<uint4*>(row + d1) = bf16x8(v);
+      }
+      if (at < 0) continue;
+      const float inv = inverse(a.k_desc, a.desc_per_head ? hk : 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        u[i] *= inv;
+        v[i] *= inv;
+      }
+      uint32_t tu = top_of(u), tv = top_of(v);
+      const bool apart = !INTERLEAVED && pair >= 0;  // u and v are halves of two blocks, whose others the next lane has
+      if (apart) {
+        const unsigned both = 3u << (tid & 30);
+        tu = max(tu, __shfl_xor_sync(both, tu, 1));
+        tv = max(tv, __shfl_xor_sync(both, tv, 1));
+      } else {
+        tu = tv = max(tu, tv);
+      }
+      float ru, rv;
+      const uint8_t su = scale_of(tu, &ru), sv = scale_of(tv, &rv);
+      uint8_t* codes = a.cache.k + at * a.cache.k_page + s_off[token] * a.cache.k_tok + hk * a.cache.k_head;
+      uint8_t* scales = a.scales.k + at * a.scales.k_page + s_off[token] * a.scales.k_tok + hk * a.scales.k_head;
+      *reinterpret_cast<uint32_t*>(codes + d0 / 2) = codes8(u, ru);
+      *reinterpret_cast<uint32_t*>(codes + d1 / 2) = codes8(v, rv);
+      if (!apart || !(d0 & 8)) {
+        scales[d0 / 16] = su;
+        if (apart) scales[d1 / 16] = sv;
+      }
+    }
   }
 }
 
-template <bool INTERLEAVED>
+template <bool INTERLEAVED, bool NEAT>
 cudaError_t launch(const Store4Args& a, int D_qk, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.N + a.tokens - 1) / a.tokens));
-  if (D_qk == 64) return zyfa::launch_dependent(store4_kernel<INTERLEAVED, 64, 64>, grid, kThreads<64>, 0, stream, a);
-  if (D_qk == 128) return zyfa::launch_dependent(store4_kernel<INTERLEAVED, 128, 128>, grid, kThreads<128>, 0, stream, a);
-  return zyfa::launch_dependent(store4_kernel<INTERLEAVED, 192, 128>, grid, kThreads<192>, 0, stream, a);
+  if (D_qk == 64) return zyfa::launch_dependent(store4_kernel<INTERLEAVED, NEAT, 64, 64>, grid, kThreads<64>, 0, stream, a);
+  if (D_qk == 128) return zyfa::launch_dependent(store4_kernel<INTERLEAVED, NEAT, 128, 128>, grid, kThreads<128>, 0, stream, a);
+  return zyfa::launch_dependent(store4_kernel<INTERLEAVED, NEAT, 192, 128>, grid, kThreads<192>, 0, stream, a);
+}
+
+template <bool INTERLEAVED>
+cudaError_t launch(const Store4Args& a, bool neat, int D_qk, cudaStream_t stream) {
+  return neat ? launch<INTERLEAVED, true>(a, D_qk, stream) : launch<INTERLEAVED, false>(a, D_qk, stream);
 }
 
 }  // namespace
@@ -358,6 +407,7 @@ extern "C" zyfa_status_t zyfa_rope_paged_store_e2m1(const void* q, const void* k
   const long long most = std::min(kMaxTokens, std::max(12, 320 / (H + 2 * H_kv)));
   const long long waves = (N + most * slots_gpu - 1) / (most * slots_gpu);
   a.tokens = static_cast<int>((N + slots_gpu * waves - 1) / (slots_gpu * waves));
-  const cudaError_t e = rope && rope->interleaved ? launch<true>(a, D_qk, stream) : launch<false>(a, D_qk, stream);
+  const bool interleaved = rope && rope->interleaved, neat = a.offset % 16 == 0 && (interleaved || a.rot % 32 == 0);
+  const cudaError_t e = interleaved ? launch<true>(a, neat, D_qk, stream) : launch<false>(a, neat, D_qk, stream);
   return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
 }
