@@ -6,15 +6,19 @@
 //
 // * Products run with keys (or channels of V) as the rows of mma.sync.m16n8k16 and query heads as its 8 columns, in fp16: a code
 //   times its scale has 6 bits and is exact there, and a bf16 query is, over a power of two near its row's largest.
-// * K: the contraction may take the channels in any order, so lane 4g + t keeps 32 neighbouring channels of key g (16 bytes: one
-//   wide read of shared memory, conversions two values at a time in place, two scales) and the same channels of the queries.
+// * K: ldmatrix hands a lane 4 bytes of a key, 8 neighbouring channels.  The contraction may take channels in any order, as long as the
+//   queries' fragments do: each byte, converted and multiplied by its scale both channels at a time, is an operand.
 // * V: the contraction runs over keys, two of which share a register, while the two codes of a byte are channels.  ldmatrix
-//   transposes 16-bit elements, four channels of a key, so that a register holds them for two keys; each byte is converted and
-//   halves of pairs exchanged: 3 operations for 2 values, with the scale's product.
+//   transposes 16-bit elements, four channels of a key, so that a register holds them for two keys; each byte is converted, halves of
+//   pairs exchanged and the products with the two keys' scales taken: 3 operations for 2 values.
 // * Codes are numbers whatever their bits, so what lies in shared memory behind a request's end only needs scales of 0.
 //
-// Bound: HBM, 9/16 byte a value, and next to it the ALU that converts: a key and head of 128 channels takes some 8 of its
-// warp instructions for 144 bytes.
+// Bound: HBM, 9/16 byte a value, and next to it the SM's issue: 16 keys of a head of 128 channels take 142 clocks of an SM for 2304 bytes.
+// 128 requests of up to 16384 tokens, 8 KV heads of 128: 147 us, where the bytes take 101, the loads alone 111 and the arithmetic alone 141.
+// What converts (a conversion, a product, an exchange) and mma.sync pass at 2.3 to 2.5 instructions a clock together at most when nothing
+// else runs, and the kernel reaches 2.2.  Products with the scales taken outside the matrix product, on weights and scores, cost as many
+// instructions where a key has 8 scales for a few heads; tcgen05 would read the widened operands from shared memory, twice the bytes that
+// its bandwidth holds there.
 #pragma once
 #include "decode.cuh"
 
@@ -1101,7 +1105,7 @@ bool plan4(Args& a, int nsm, int* smem) {
                                                   a.heads * a.tile_tokens * (T::kScaleK + T::kScaleV) + a.q_bytes, 1024));
   a.meeting_bytes = a.subs > 1 ? warps * Rows::kHeads * (DV + 2) * 4 : 0;  // (m, l, O)
   const int more = a.meeting_bytes + warps * static_cast<int>(Rows::kQueryBytes);
-  const int kStatic = a.boxes ? 3072 : 8192;  // the schedule's tables, headers and rows, with the 1 KiB that each block takes
+  const int kStatic = a.boxes ? 2560 : 8192;  // the schedule's tables, headers and rows, with the 1 KiB that each block takes
   int blocks = kBlocks<NS>;
   while (blocks > 1 && blocks * (2 * stage + more + kStatic) > kSmemPerSm) --blocks;
   a.stages = std::min(kStages, (std::min(kSmemPerSm / blocks - kStatic, kSmemPerBlock - 8192) - more) / stage);

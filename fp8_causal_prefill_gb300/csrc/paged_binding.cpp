@@ -89,6 +89,8 @@ Cache cache4_of(const Tensor& k, const Tensor& v, PyObject* kso, PyObject* vso) 
     NEED_TYPE((t == at::kByte || t == (i < 2 ? at::ScalarType::Float4_e2m1fn_x2 : at::kFloat8_e4m3fn)) && all[i]->dim() == 4, names[i],
               i < 2 ? " must be a float4_e2m1fn_x2 (or uint8) CUDA tensor [num_pages, page_size, H_kv, D / 2] beside k_scales and v_scales"
                     : " must be a float8_e4m3fn (or uint8) CUDA tensor [num_pages, page_size, H_kv, D / 16]");
+  }
+  for (int i = 0; i < 4; ++i) {
     NEED_VALUE(dev >= 0 && cuda_index(*all[i]) == dev && all[i]->sizes().slice(0, 3) == k.sizes().slice(0, 3),
                "k_cache, v_cache, k_scales and v_scales must agree in pages, page size, heads and CUDA device");
     NEED_VALUE(all[i]->stride(3) == 1 || all[i]->size(3) == 1, "the last dimension of ", names[i], " must be contiguous");
