@@ -9,8 +9,8 @@
 // * K: ldmatrix hands a lane 4 bytes of a key, 8 neighbouring channels.  The contraction may take channels in any order, as long as the
 //   queries' fragments do: each byte, converted and multiplied by its scale both channels at a time, is an operand.
 // * V: the contraction runs over keys, two of which share a register, while the two codes of a byte are channels.  ldmatrix
-//   transposes 16-bit elements, four channels of a key, so that a register holds them for two keys; each byte is converted, halves of
-//   pairs exchanged and the products with the two keys' scales taken: 3 operations for 2 values.
+//   transposes 16-bit elements, four channels of a key.  Two registers with the same channels of other keys exchange nibbles (4 operations
+//   for 16 values), so that a byte is one channel of two keys: converted and multiplied by their scales, it is an operand.
 // * Codes are numbers whatever their bits, so what lies in shared memory behind a request's end only needs scales of 0.
 //
 // Bound: HBM, 9/16 byte a value, and next to it the SM's issue: 16 keys of a head of 128 channels take 142 clocks of an SM for 2304 bytes.
@@ -121,7 +121,13 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 __device__ __forceinline__ uint32_t halves(float lo, float hi) { return pack2<true>(lo, hi); }
 
-// Where a lane's ldmatrix reads of a run of 32 keys go, relative to the run's first key (a multiple of 32): key (lane & 7), 8 on for the
+// The order of 16 keys in V's matrices and in K's.  A register of V's first matrix and the one of its second pair nibble by nibble: rows 2t of
+// both, and rows 2t + 1.  Weights leave the scores' rows in pairs 2t, 2t + 1, so K's rows are these keys: those of V's two matrices in turn.
+// Keys of a matrix are apart mod 8 in both, which keeps its rows in different banks.
+__host__ __device__ constexpr int key_of_v(int row) { return row < 8 ? row : 8 + (row + 1) % 8; }
+__host__ __device__ constexpr int key_of_k(int row) { return key_of_v((row & 1) * 8 + (row & 6) + (row >> 3)); }
+
+// Where a lane's ldmatrix reads of a run of 32 keys go, relative to the run's first key (a multiple of 32): row (lane & 7), 8 on for the
 // odd matrices, and of its 16-byte pieces one, or the next for the last two matrices.  16 keys on, the exchange of pieces is the same
 // unless four tokens share a row (64 channels, one head).
 template <int DQK, int DV>
@@ -129,30 +135,37 @@ struct Reader4 {
   static constexpr int kPairsK = DQK / 64, kPairsV = DV / 64;  // of 16-byte pieces, 32 channels each
   uint32_t key[DQK == 64 ? 2 : 1][kPairsK], value[DV == 64 ? 2 : 1][kPairsV];
   uint32_t k_16, v_16;               // from 16 keys to the next
-  uint32_t k_scale, v_scale;         // of key g, and of key 2t (of each 8)
+  uint32_t k_scale[2];               // of rows g and g + 8 of K
+  uint32_t v_scale, v_last;          // of row 2t of V's first matrix, and row 2t + 1 of its second
   uint32_t k_scales, v_scales;       // from a key's scales to the next's
   uint32_t v_zero;                   // of key `lane`
 
   __device__ __forceinline__ void set(const Args& a, int lane, int head, int first, const Place& kp, const Place& vp) {
     using T = Tile4<DQK, DV>;
-    const int row = first + (lane >> 3 & 1) * 8 + (lane & 7), piece = (lane >> 4) * 16;
+    const int row = lane & 15, piece = (lane >> 4) * 16, k_row = first + key_of_k(row), v_row = first + key_of_v(row);
     k_16 = kp.step(16);
     v_16 = vp.step(16);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
 #pragma unroll
       for (int i = 0; i < kPairsK; ++i)
-        if (n == 0 || DQK == 64) key[n][i] = kp(row + 16 * n, head, 32 * i + piece) - n * k_16;
+        if (n == 0 || DQK == 64) key[n][i] = kp(k_row + 16 * n, head, 32 * i + piece) - n * k_16;
 #pragma unroll
       for (int i = 0; i < kPairsV; ++i)
-        if (n == 0 || DV == 64) value[n][i] = vp(row + 16 * n, head, 32 * i + piece) - n * v_16;
+        if (n == 0 || DV == 64) value[n][i] = vp(v_row + 16 * n, head, 32 * i + piece) - n * v_16;
     }
     const bool k_each = a.boxes && a.ks_mode == kRunEach, v_each = a.boxes && a.vs_mode == kRunEach;
     k_scales = (k_each ? 1 : a.heads) * T::kScaleK;
     v_scales = (v_each ? 1 : a.heads) * T::kScaleV;
     v_zero = (first + lane) * v_scales + head * T::kScaleV * (v_each ? a.tile_tokens : 1);
-    k_scale = (first + (lane >> 2)) * k_scales + head * T::kScaleK * (k_each ? a.tile_tokens : 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) k_scale[j] = (first + key_of_k((lane >> 2) + 8 * j)) * k_scales + head * T::kScaleK * (k_each ? a.tile_tokens : 1);
     v_scale = v_zero + (2 * (lane & 3) - lane) * v_scales;
+    v_last = v_zero + (key_of_v(2 * (lane & 3) + 9) - lane) * v_scales;
+  }
+  // row 2t (2t + 1) of V's first matrix (its second)
+  __device__ __forceinline__ uint32_t value_scale(bool odd, bool second) const {
+    return !second ? v_scale + odd * v_scales : odd ? v_last : v_scale + key_of_v(8) * v_scales;
   }
   __device__ __forceinline__ uint32_t key_at(int i, bool second) const { return DQK == 64 && second ? key[DQK == 64][i] : key[0][i]; }
   __device__ __forceinline__ uint32_t value_at(int i, bool second) const { return DV == 64 && second ? value[DV == 64][i] : value[0][i]; }
@@ -283,22 +296,31 @@ struct Rows4 {
     if (!kQueriesInRegisters) __syncwarp();
   }
 
-  // The e4m3 scales of one key (of D channels) for this lane's block of each 32 channels: two a register, as bytes.
+  // The scales of one key (of D channels) for this lane's block of each 32 channels, widened: two a register.
   template <int D>
   static __device__ __forceinline__ void scales_of(uint32_t at, bool second, uint32_t (&s)[(D / 32 + 1) / 2]) {
     if constexpr (D == 64) {
-      s[0] = prmt(lds4(at), 0, second ? 0x31 : 0x20);
+      s[0] = widen_e4m3(prmt(lds4(at), 0, second ? 0x31 : 0x20));
     } else if constexpr (D == 128) {
       const uint2 w = lds8(at);
       const uint32_t x = prmt(w.x, w.y, second ? 0x7531 : 0x6420);
-      s[0] = x;
-      s[1] = x >> 16;
+      s[0] = widen_e4m3(x);
+      s[1] = widen_e4m3_hi(x);
     } else {
       const uint32_t x = prmt(lds4(at), lds4(at + 4), second ? 0x7531 : 0x6420);
-      s[0] = x;
-      s[1] = x >> 16;
-      s[2] = prmt(lds4(at + 8), 0, second ? 0x31 : 0x20);
+      s[0] = widen_e4m3(x);
+      s[1] = widen_e4m3_hi(x);
+      s[2] = widen_e4m3(prmt(lds4(at + 8), 0, second ? 0x31 : 0x20));
     }
+  }
+  // One of two fp16 numbers in both places (which a product takes as it is).
+  static __device__ __forceinline__ uint32_t both(uint32_t x, int which) {
+    uint32_t d;
+    if (which)
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tmov.b32 %0, {hi, hi};\n\t}" : "=r"(d) : "r"(x));
+    else
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tmov.b32 %0, {lo, lo};\n\t}" : "=r"(d) : "r"(x));
+    return d;
   }
   static __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     F2 d;
@@ -312,15 +334,15 @@ struct Rows4 {
   template <bool FULL>
   __device__ __forceinline__ void keys16(const Run4& s, const R& at, uint32_t mask, bool second, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    // S^T: rows are keys g and g + 8, columns heads; two chains of products
+    // S^T: rows are keys, columns heads; two chains of products
     float acc[2][NS][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int c = 0; c < NS; ++c) acc[j][c][0] = acc[j][c][1] = acc[j][c][2] = acc[j][c][3] = 0.0f;
     uint32_t sa[(kPiecesK + 1) / 2], sb[(kPiecesK + 1) / 2];
-    scales_of<DQK>(s.ks + at.k_scale, t >= 2, sa);
-    scales_of<DQK>(s.ks + at.k_scale + 8 * at.k_scales, t >= 2, sb);
+    scales_of<DQK>(s.ks + at.k_scale[0], t >= 2, sa);
+    scales_of<DQK>(s.ks + at.k_scale[1], t >= 2, sb);
 #pragma unroll
     for (int i = 0; i < kPiecesK / 2; ++i) {
       uint32_t r[4];
@@ -328,7 +350,7 @@ struct Rows4 {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t ka = r[2 * j], kb = r[2 * j + 1];
-        const uint32_t fa = widen_e4m3(prmt(sa[i], 0, j ? 0x11 : 0x00)), fb = widen_e4m3(prmt(sb[i], 0, j ? 0x11 : 0x00));
+        const uint32_t fa = both(sa[i], j), fb = both(sb[i], j);
         const uint32_t a0 = mul_f16x2(widen_e2m1<0>(ka), fa), a1 = mul_f16x2(widen_e2m1<0>(kb), fb);
         const uint32_t a2 = mul_f16x2(widen_e2m1<1>(ka), fa), a3 = mul_f16x2(widen_e2m1<1>(kb), fb);
         const uint32_t b0 = mul_f16x2(widen_e2m1<2>(ka), fa), b1 = mul_f16x2(widen_e2m1<2>(kb), fb);
@@ -349,7 +371,7 @@ struct Rows4 {
         x[c][j] = add2({acc[0][c][2 * j], acc[0][c][2 * j + 1]}, {acc[1][c][2 * j], acc[1][c][2 * j + 1]});
         if (!FULL) {
           x[c][j] = mul2(x[c][j], scale[c]);
-          if (!((mask >> (j * 8 + g)) & 1)) x[c][j] = {-INFINITY, -INFINITY};
+          if (!((mask >> key_of_k(j * 8 + g)) & 1)) x[c][j] = {-INFINITY, -INFINITY};
         }
       }
     uint32_t pf[NS][2];
@@ -398,12 +420,12 @@ struct Rows4 {
         pf[c][j] = transpose8x8(halves(w.x, w.y));
       }
     }
-    // O^T += V^T P^T: rows are channels of V, the contraction keys 2t, 2t + 1 of each 8
-    uint32_t sv[2][kPieces];  // scales of keys 2t, 2t + 1 of the first 8 and of the second, of this lane's block of every 32 channels
+    // O^T += V^T P^T: rows are channels of V, the contraction keys
+    uint32_t sv[2][kPieces];  // scales of rows 2t (2t + 1) of V's two matrices, of this lane's block of every 32 channels
     const uint32_t pick = g < 4 ? 0x6240u : 0x7351u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint32_t first = s.vs + at.v_scale + 8 * j * at.v_scales, other = first + at.v_scales;
+      const uint32_t first = s.vs + at.value_scale(j, false), other = s.vs + at.value_scale(j, true);
       if constexpr (DV == 128) {
         const uint2 a = lds8(first), b = lds8(other);
         const uint32_t lo = prmt(a.x, b.x, pick), hi = prmt(a.y, b.y, pick);
@@ -423,16 +445,13 @@ struct Rows4 {
       ldsm4t(s.v + at.value_at(p / 2, second), r);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint32_t f[2][4];  // [8 keys][channel]: keys 2t and 2t + 1
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t v = r[2 * i + j];
-          const uint32_t c0 = widen_e2m1<0>(v), c1 = widen_e2m1<1>(v), c2 = widen_e2m1<2>(v), c3 = widen_e2m1<3>(v);
-          f[j][0] = mul_f16x2(prmt(c0, c2, 0x5410), sv[j][p + i]);
-          f[j][1] = mul_f16x2(prmt(c0, c2, 0x7632), sv[j][p + i]);
-          f[j][2] = mul_f16x2(prmt(c1, c3, 0x5410), sv[j][p + i]);
-          f[j][3] = mul_f16x2(prmt(c1, c3, 0x7632), sv[j][p + i]);
-        }
+        // two keys a byte: even channels, and odd ones
+        const uint32_t v = r[2 * i], w = r[2 * i + 1], even = (v & 0x0f0f0f0fu) | (w << 4 & 0xf0f0f0f0u), odd = (v >> 4 & 0x0f0f0f0fu) | (w & 0xf0f0f0f0u);
+        const uint32_t s0 = sv[0][p + i], s1 = sv[1][p + i];
+        const uint32_t f[2][4] = {{mul_f16x2(widen_e2m1<0>(even), s0), mul_f16x2(widen_e2m1<0>(odd), s0), mul_f16x2(widen_e2m1<1>(even), s0),
+                                   mul_f16x2(widen_e2m1<1>(odd), s0)},
+                                  {mul_f16x2(widen_e2m1<2>(even), s1), mul_f16x2(widen_e2m1<2>(odd), s1), mul_f16x2(widen_e2m1<3>(even), s1),
+                                   mul_f16x2(widen_e2m1<3>(odd), s1)}};
 #pragma unroll
         for (int c = 0; c < NS; ++c) {
           mma<kF16>(o[c][p + i][0], f[0][0], f[0][1], f[1][0], f[1][1], pf[c][0], pf[c][1]);
