@@ -13,12 +13,12 @@
 //   for 16 values), so that a byte is one channel of two keys: converted and multiplied by their scales, it is an operand.
 // * Codes are numbers whatever their bits, so what lies in shared memory behind a request's end only needs scales of 0.
 //
-// Bound: HBM, 9/16 byte a value, and next to it the SM's issue: 16 keys of a head of 128 channels take 142 clocks of an SM for 2304 bytes.
-// 128 requests of up to 16384 tokens, 8 KV heads of 128: 147 us, where the bytes take 101, the loads alone 111 and the arithmetic alone 141.
-// What converts (a conversion, a product, an exchange) and mma.sync pass at 2.3 to 2.5 instructions a clock together at most when nothing
-// else runs, and the kernel reaches 2.2.  Products with the scales taken outside the matrix product, on weights and scores, cost as many
-// instructions where a key has 8 scales for a few heads; tcgen05 would read the widened operands from shared memory, twice the bytes that
-// its bandwidth holds there.
+// Bound: HBM, 9/16 byte a value, and next to it the SM's issue: 16 keys of a head of 128 channels are some 310 warp instructions for 2304
+// bytes, 64 of which convert, 64 multiply by scales and 16 are matrix products.  128 requests of up to 16384 tokens, 8 KV heads of 128: 136 us,
+// where the bytes take 101 and the loads alone 111; 2.4 instructions a clock and SM, the ALU at half its rate, matrix instructions at a
+// quarter of theirs.  More warps an SM would fill the gaps, but 96 registers a thread spill (177 us with 16 compute warps), and V's loads
+// ahead of the weights spill as well (142 us).  Scales taken outside the matrix products, on weights and scores, cost as many instructions;
+// tcgen05 would read widened operands from shared memory, which takes longer than the whole kernel.
 #pragma once
 #include "decode.cuh"
 
@@ -236,6 +236,9 @@ struct Rows4 {
   static constexpr int kHeads = 8 * NS, kPiecesK = DQK / 32, kPieces = DV / 32;
   static constexpr bool kQueriesInRegisters = NS == 1;
   static constexpr uint32_t kQueryBytes = kQueriesInRegisters ? 0 : NS * kPiecesK * 512;  // else B fragments in shared memory, a lane's of a piece in 16 bytes
+  // Runs of 16 keys whose scores are weighed together: both of a turn where registers hold them (128 requests 136 us, one by one 138; two
+  // sets of 64 channels 31.1 and 33.7; two sets of 128 would spill 144 bytes a thread: 51 instead of 45).
+  static constexpr int kTogether = NS == 1 || DV == 64 ? 2 : 1;
   static constexpr float kLift = 15.0f;             // weights in fp16 up to 2^15, so that light ones keep their bits
   static constexpr float kNoKey = 3.402823466e38f;  // ref before the first key: lifts every score above its negative over the limit
 
@@ -330,23 +333,21 @@ struct Rows4 {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
   }
-  // 16 keys.  FULL: all count; else mask: those that do.  second: of the run of 32, the second 16.
-  template <bool FULL>
-  __device__ __forceinline__ void keys16(const Run4& s, const R& at, uint32_t mask, bool second, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    // S^T: rows are keys, columns heads; two chains of products
+  // The scores of 16 keys (second: of the run of 32, the second 16), over scale: rows are keys, columns heads; two chains of products.
+  __device__ __forceinline__ void scores(const Run4& s, const R& at, bool second, int t, F2 (&x)[NS][2]) {
     float acc[2][NS][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int c = 0; c < NS; ++c) acc[j][c][0] = acc[j][c][1] = acc[j][c][2] = acc[j][c][3] = 0.0f;
+    const uint32_t ks = s.ks + (second ? 16 * at.k_scales : 0), k = s.k + (second ? at.k_16 : 0);
     uint32_t sa[(kPiecesK + 1) / 2], sb[(kPiecesK + 1) / 2];
-    scales_of<DQK>(s.ks + at.k_scale[0], t >= 2, sa);
-    scales_of<DQK>(s.ks + at.k_scale[1], t >= 2, sb);
+    scales_of<DQK>(ks + at.k_scale[0], t >= 2, sa);
+    scales_of<DQK>(ks + at.k_scale[1], t >= 2, sb);
 #pragma unroll
     for (int i = 0; i < kPiecesK / 2; ++i) {
       uint32_t r[4];
-      ldsm4(s.k + at.key_at(i, second), r);
+      ldsm4(k + at.key_at(i, second), r);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t ka = r[2 * j], kb = r[2 * j + 1];
@@ -363,69 +364,19 @@ struct Rows4 {
         }
       }
     }
-    F2 x[NS][2];
 #pragma unroll
     for (int c = 0; c < NS; ++c)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        x[c][j] = add2({acc[0][c][2 * j], acc[0][c][2 * j + 1]}, {acc[1][c][2 * j], acc[1][c][2 * j + 1]});
-        if (!FULL) {
-          x[c][j] = mul2(x[c][j], scale[c]);
-          if (!((mask >> key_of_k(j * 8 + g)) & 1)) x[c][j] = {-INFINITY, -INFINITY};
-        }
-      }
-    uint32_t pf[NS][2];
-#pragma unroll
-    for (int c = 0; c < NS; ++c) {
-      // log2 of the weights: scores in units of log2 over the reference m, which moves only when a key exceeds it: log2 of a weight is then
-      // above the lift.
-      F2 y[2];
-      float over;
-      auto weigh = [&]() {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) y[j] = FULL ? fma2(scale[c], x[c][j], ref[c]) : add2(x[c][j], ref[c]);
-        over = fmaxf(fmaxf(y[0].x, y[0].y), fmaxf(y[1].x, y[1].y));
-      };
-      weigh();
-      if (__any_sync(0xffffffffu, over > kLift)) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float by = !FULL ? 1.0f : e ? scale[c].y : scale[c].x;
-          float top = fmaxf(m[c][e], by * (e ? fmaxf(x[c][0].y, x[c][1].y) : fmaxf(x[c][0].x, x[c][1].x)));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const bool none = top == -INFINITY;
-          const float f = none ? 1.0f : exp2_approx(m[c][e] - top);
-          m[c][e] = top;
-          (e ? ref[c].y : ref[c].x) = none ? kNoKey : kLift - top;
-          l[c][e] *= f;
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              o[c][i][j][e] *= f;
-              o[c][i][j][e + 2] *= f;
-            }
-        }
-        weigh();
-      }
-      // weights, transposed into the B operand (keys are now the contraction)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const F2 w = {exp2_approx(y[j].x), exp2_approx(y[j].y)};
-        const F2 sum = add2({l[c][0], l[c][1]}, w);
-        l[c][0] = sum.x;
-        l[c][1] = sum.y;
-        pf[c][j] = transpose8x8(halves(w.x, w.y));
-      }
-    }
-    // O^T += V^T P^T: rows are channels of V, the contraction keys
+      for (int j = 0; j < 2; ++j) x[c][j] = add2({acc[0][c][2 * j], acc[0][c][2 * j + 1]}, {acc[1][c][2 * j], acc[1][c][2 * j + 1]});
+  }
+  // O^T += V^T P^T of 16 keys: rows are channels of V, the contraction keys.
+  __device__ __forceinline__ void values(const Run4& s, const R& at, bool second, int g, const uint32_t (&pf)[NS][2]) {
+    const uint32_t vs = s.vs + (second ? 16 * at.v_scales : 0), v0 = s.v + (second ? at.v_16 : 0);
     uint32_t sv[2][kPieces];  // scales of rows 2t (2t + 1) of V's two matrices, of this lane's block of every 32 channels
     const uint32_t pick = g < 4 ? 0x6240u : 0x7351u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint32_t first = s.vs + at.value_scale(j, false), other = s.vs + at.value_scale(j, true);
+      const uint32_t first = vs + at.value_scale(j, false), other = vs + at.value_scale(j, true);
       if constexpr (DV == 128) {
         const uint2 a = lds8(first), b = lds8(other);
         const uint32_t lo = prmt(a.x, b.x, pick), hi = prmt(a.y, b.y, pick);
@@ -442,7 +393,7 @@ struct Rows4 {
 #pragma unroll
     for (int p = 0; p < kPieces; p += 2) {
       uint32_t r[4];
-      ldsm4t(s.v + at.value_at(p / 2, second), r);
+      ldsm4t(v0 + at.value_at(p / 2, second), r);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         // two keys a byte: even channels, and odd ones
@@ -463,17 +414,88 @@ struct Rows4 {
 
   // One run of 32 keys.  FULL: all count; else mask: those that do, at least one.
   template <bool FULL>
-  __device__ __forceinline__ void tile(Run4 s, const R& at, uint32_t mask, int lane) {
+  __device__ __forceinline__ void tile(const Run4& s, const R& at, uint32_t mask, int lane) {
+    if constexpr (kTogether == 2) {
+      weigh<FULL>(s, at, 0, mask, lane);
+    } else {
 #pragma unroll 1
-    for (int i = 0;; ++i) {
-      if (FULL || (mask & 0xffffu)) keys16<FULL>(s, at, mask & 0xffffu, i, lane);
-      mask >>= 16;
-      if (i) return;
-      s.k += at.k_16;
-      s.v += at.v_16;
-      s.ks += 16 * at.k_scales;
-      s.vs += 16 * at.v_scales;
+      for (int i = 0; i < 2; ++i) weigh<FULL>(s, at, i, mask >> (16 * i), lane);
     }
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void weigh(const Run4& s, const R& at, int from, uint32_t mask, int lane) {
+    constexpr int H = kTogether;
+    const int g = lane >> 2, t = lane & 3;
+    F2 x[H][NS][2];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      scores(s, at, from + h, t, x[h]);
+      if (!FULL)
+#pragma unroll
+        for (int c = 0; c < NS; ++c)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            x[h][c][j] = mul2(x[h][c][j], scale[c]);
+            if (!((mask >> (16 * h + key_of_k(j * 8 + g))) & 1)) x[h][c][j] = {-INFINITY, -INFINITY};
+          }
+    }
+    uint32_t pf[H][NS][2];
+#pragma unroll
+    for (int c = 0; c < NS; ++c) {
+      // log2 of the weights: scores in units of log2 over the reference m, which moves only when a key exceeds it: log2 of a weight is then
+      // above the lift.
+      F2 y[H][2];
+      float over;
+      auto log2_weights = [&]() {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            y[h][j] = FULL ? fma2(scale[c], x[h][c][j], ref[c]) : add2(x[h][c][j], ref[c]);
+            const float top = fmaxf(y[h][j].x, y[h][j].y);
+            over = h + j ? fmaxf(over, top) : top;
+          }
+      };
+      log2_weights();
+      if (__any_sync(0xffffffffu, over > kLift)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float by = !FULL ? 1.0f : e ? scale[c].y : scale[c].x;
+          float top = m[c][e];
+#pragma unroll
+          for (int h = 0; h < H; ++h) top = fmaxf(top, by * (e ? fmaxf(x[h][c][0].y, x[h][c][1].y) : fmaxf(x[h][c][0].x, x[h][c][1].x)));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const bool none = top == -INFINITY;
+          const float f = none ? 1.0f : exp2_approx(m[c][e] - top);
+          m[c][e] = top;
+          (e ? ref[c].y : ref[c].x) = none ? kNoKey : kLift - top;
+          l[c][e] *= f;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              o[c][i][j][e] *= f;
+              o[c][i][j][e + 2] *= f;
+            }
+        }
+        log2_weights();
+      }
+      // weights, transposed into the B operand (keys are now the contraction)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const F2 w = {exp2_approx(y[h][j].x), exp2_approx(y[h][j].y)};
+          const F2 sum = add2({l[c][0], l[c][1]}, w);
+          l[c][0] = sum.x;
+          l[c][1] = sum.y;
+          pf[h][c][j] = transpose8x8(halves(w.x, w.y));
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) values(s, at, from + h, g, pf[h]);
   }
 
   // Ends a request's part: writes its rows (`count` query heads from `first`), or (m, l, O) to part `slot` of the workspace.
