@@ -1191,7 +1191,7 @@ zyfa_status_t launch4_as(Args& a, int nsm, int dev, uint8_t* ws, cudaStream_t st
 }
 
 // By the query heads of a KV head: up to 8 are a warp's; more come in chunks of up to 16, two sets that share the widened codes and whose
-// registers leave room for two blocks an SM instead of three (64 requests of 500 to 8000 tokens, 4 KV heads of 16: 46 us; in chunks of 8 54).
+// registers leave room for two blocks an SM instead of three (64 requests of 500 to 8000 tokens, 4 KV heads of 16: 45 us, in chunks of 8 49; of 64 channels, 31 and 59).
 template <int DQK, int DV>
 zyfa_status_t launch4(Args& a, int nsm, int dev, uint8_t* ws, cudaStream_t stream) {
   return a.group <= 8 ? launch4_as<DQK, DV, 1>(a, nsm, dev, ws, stream) : launch4_as<DQK, DV, 2>(a, nsm, dev, ws, stream);
