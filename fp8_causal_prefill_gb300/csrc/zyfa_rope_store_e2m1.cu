@@ -53,35 +53,58 @@ __device__ __forceinline__ uint4 bf16x8(const float* y) {
 
 // The largest magnitude among 8 values, as bits, whose order is that of magnitudes, with NaN above all.
 __device__ __forceinline__ uint32_t top_of(const float* z) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(z[i]) & 0x7fffffffu);
-  return top;
+  float top;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(z[0]), "f"(z[1]), "f"(z[2]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(top), "f"(z[3]), "f"(z[4]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(top), "f"(z[5]), "f"(z[6]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(top) : "f"(top), "f"(z[7]), "f"(z[7]));
+  return __float_as_uint(top);
 }
-// The scale of a block with this largest magnitude; *r: what its values are multiplied by.
-__device__ __forceinline__ uint8_t scale_of(uint32_t top, float* r) {
-  uint16_t s8;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.0f), "f"(__uint_as_float(top) * (1.0f / 6.0f)));
+// What values are multiplied by under a scale; 0 under 0 and NaN.
+__device__ __forceinline__ float reciprocal(uint32_t s8) {
   float s;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(s) : "r"(zyfa::widen_e4m3(s8)));
-  *r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  return s > 0.0f ? __frcp_rn(s) : 0.0f;
+}
+// The scale of a block with this largest magnitude; *r: what its values are multiplied by, of those in shared memory for each scale.
+__device__ __forceinline__ uint8_t scale_of(uint32_t top, const float* reciprocals, float* r) {
+  uint16_t s8;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.0f), "f"(__uint_as_float(top) * (1.0f / 6.0f)));
+  *r = reciprocals[s8 & 0x7f];
   return static_cast<uint8_t>(s8);
+}
+// Two products by one instruction.
+__device__ __forceinline__ float2 times(float a, float b, float f) {
+  float2 d;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a), "f"(b), "f"(f));
+  return d;
+}
+__device__ __forceinline__ void times8(float* z, float f) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 p = times(z[i], z[i + 1], f);
+    z[i] = p.x;
+    z[i + 1] = p.y;
+  }
 }
 // Eight e2m1 codes, the first in the lowest bits.
 __device__ __forceinline__ uint32_t codes8(const float* z, float r) {
   uint32_t d;
+  const float2 x = times(z[0], z[1], r), y = times(z[2], z[3], r), u = times(z[4], z[5], r), v = times(z[6], z[7], r);
   asm("{\n\t.reg .b8 a, b, c, e;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 e, %8, %7;\n\tmov.b32 %0, {a, b, c, e};\n\t}"
       : "=r"(d)
-      : "f"(z[0] * r), "f"(z[1] * r), "f"(z[2] * r), "f"(z[3] * r), "f"(z[4] * r), "f"(z[5] * r), "f"(z[6] * r), "f"(z[7] * r));
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(u.x), "f"(u.y), "f"(v.x), "f"(v.y));
   return d;
 }
 // 16 values as codes and their scale.
-__device__ __forceinline__ void quantise(float (&y)[16], float inv, uint2* codes, uint8_t* scale) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] *= inv;
+__device__ __forceinline__ void quantise(float (&y)[16], float inv, const float* reciprocals, uint2* codes, uint8_t* scale) {
+  times8(y, inv);
+  times8(y + 8, inv);
   float r;
-  *scale = scale_of(max(top_of(y), top_of(y + 8)), &r);
+  *scale = scale_of(max(top_of(y), top_of(y + 8)), reciprocals, &r);
   *codes = make_uint2(codes8(y, r), codes8(y + 8, r));
 }
 
@@ -94,6 +117,7 @@ __global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1
   __shared__ __align__(16) float s_cos[kMaxTokens][kHalf], s_sin[kMaxTokens][kHalf];
   __shared__ long long s_page[kMaxTokens];  // -1: outside the cache, -2: padding
   __shared__ int s_off[kMaxTokens];
+  __shared__ float s_reciprocal[128];
   const int tid = threadIdx.x;
   const long long n0 = static_cast<long long>(blockIdx.x) * a.tokens;
   const int here = static_cast<int>(min(static_cast<long long>(a.tokens), a.N - n0));
@@ -177,7 +201,9 @@ __global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1
     s_page[tid] = at;
     s_off[tid] = static_cast<int>(off);
   }
+  if (tid < 128 && a.k) s_reciprocal[tid] = reciprocal(tid);
   fill_turns<kN>(a, n0, here, s_cos, s_sin);
+  const float inv_k = a.desc_per_head ? 0.0f : inverse(a.k_desc, 0), inv_v = a.desc_per_head ? 0.0f : inverse(a.v_desc, 0);
   __syncthreads();
 
   while (wv.token < here) {
@@ -199,7 +225,7 @@ __global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1
     widen8(c1, *reinterpret_cast<float(*)[8]>(y + 8));
     uint2 codes;
     uint8_t scale;
-    quantise(y, inverse(a.v_desc, a.desc_per_head ? head : 0), &codes, &scale);
+    quantise(y, a.desc_per_head ? inverse(a.v_desc, head) : inv_v, s_reciprocal, &codes, &scale);
     *reinterpret_cast<uint2*>(a.cache.v + at * a.cache.v_page + s_off[token] * a.cache.v_tok + head * a.cache.v_head + vd / 2) = codes;
     a.scales.v[at * a.scales.v_page + s_off[token] * a.scales.v_tok + head * a.scales.v_head + vd / 16] = scale;
   }
@@ -245,7 +271,7 @@ __global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1
     if (at < 0) continue;
     uint2 codes;
     uint8_t scale;
-    quantise(y, inverse(a.k_desc, a.desc_per_head ? head : 0), &codes, &scale);
+    quantise(y, a.desc_per_head ? inverse(a.k_desc, head) : inv_k, s_reciprocal, &codes, &scale);
     *reinterpret_cast<uint2*>(a.cache.k + at * a.cache.k_page + s_off[token] * a.cache.k_tok + head * a.cache.k_head + kd / 2) = codes;
     a.scales.k[at * a.scales.k_page + s_off[token] * a.scales.k_tok + head * a.scales.k_head + kd / 16] = scale;
   }
@@ -288,12 +314,9 @@ __global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1
         *reinterpret_cast<uint4*>(row + d1) = bf16x8(v);
       }
       if (at < 0) continue;
-      const float inv = inverse(a.k_desc, a.desc_per_head ? hk : 0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        u[i] *= inv;
-        v[i] *= inv;
-      }
+      const float inv = a.desc_per_head ? inverse(a.k_desc, hk) : inv_k;
+      times8(u, inv);
+      times8(v, inv);
       uint32_t tu = top_of(u), tv = top_of(v);
       const bool apart = !INTERLEAVED && pair >= 0;  // u and v are halves of two blocks, whose others the next lane has
       if (apart) {
@@ -304,7 +327,7 @@ __global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1
         tu = tv = max(tu, tv);
       }
       float ru, rv;
-      const uint8_t su = scale_of(tu, &ru), sv = scale_of(tv, &rv);
+      const uint8_t su = scale_of(tu, s_reciprocal, &ru), sv = scale_of(tv, s_reciprocal, &rv);
       uint8_t* codes = a.cache.k + at * a.cache.k_page + s_off[token] * a.cache.k_tok + hk * a.cache.k_head;
       uint8_t* scales = a.scales.k + at * a.scales.k_page + s_off[token] * a.scales.k_tok + hk * a.scales.k_head;
       *reinterpret_cast<uint32_t*>(codes + d0 / 2) = codes8(u, ru);
