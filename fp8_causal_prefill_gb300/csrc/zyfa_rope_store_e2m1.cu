@@ -8,9 +8,9 @@
 // their partners half the rotated width away (or 16 neighbours, where pairs are neighbours), of queries and then of keys.  A block of 16
 // keys' channels is then in one thread, or its halves are in two lanes, which tell one another their largest magnitude: nothing is read
 // twice.  Where a rotated part begins or ends inside such a block a thread has a block of a key and reads its partners again, by the line
-// that its neighbour also reads.  32768 tokens of 32 query and 8 KV heads of 128 channels, dense rows written as well: 130 us, 96% of what
-// their bytes take; 192 us by second reads.  Few heads a token leave the angles' work in sight: 8000 tokens of 8 heads of 192/128 take
-// 27 us where their bytes take 15.
+// that its neighbour also reads.  32768 tokens of 32 query and 8 KV heads of 128 channels, dense rows written as well: 129 us, 96% of what
+// their bytes take; 173 us by second reads.  Few query heads leave the arithmetic of blocks and angles in sight: 20000 tokens of 8 and 8
+// heads take 38 us where their bytes take 28.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,6 +24,9 @@
 namespace {
 
 using namespace zyfa::rope;
+
+// Blocks an SM holds of 256 (192 for 192 channels) threads of 64 registers, below which they spill
+constexpr int kBlocks = 4, kBlocksOf192 = 5;
 
 struct Store4Args {
   const __nv_bfloat16 *q, *k, *v;
@@ -109,9 +112,9 @@ __device__ __forceinline__ void quantise(float (&y)[16], float inv, const float*
 }
 
 // NEAT: no block of 16 key channels is rotated in part, or lies in both halves of the rotated part: keys go the way of queries.  Else a
-// thread has a block of a key and reads its partners a second time.  Blocks an SM (at least): 64 registers a thread, below which it spills.
+// thread has a block of a key and reads its partners a second time.
 template <bool INTERLEAVED, bool NEAT, int DQK, int DV>
-__global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? 5 : 4) : 1) store4_kernel(const __grid_constant__ Store4Args a) {
+__global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? kBlocksOf192 : kBlocks) : 1) store4_kernel(const __grid_constant__ Store4Args a) {
   constexpr int kN = kThreads<DQK>, kPieces = DQK / 16, kBlocksK = DQK / 16, kBlocksV = DV / 16, kHalf = DQK / 2;
   static_assert(kN % kPieces == 0 && kN % kBlocksV == 0);
   __shared__ __align__(16) float s_cos[kMaxTokens][kHalf], s_sin[kMaxTokens][kHalf];
@@ -427,7 +430,9 @@ extern "C" zyfa_status_t zyfa_rope_paged_store_e2m1(const void* q, const void* k
   a.desc_per_head = descale_per_kv_head;
   a.N = N;
   a.H = H;
-  const long long slots_gpu = (D_qk == 192 ? 6ll : 4ll) * std::max(1, zyfa::device_sm_count(dev));
+  // Tokens a block: so many that all blocks run at once, in as few such waves as 12 to 32 tokens of a few or more heads allow (8000 tokens of 8
+  // heads of 192/128: 21.2 us in one wave, 26.1 where an eighth of the blocks waits).
+  const long long slots_gpu = static_cast<long long>(D_qk == 192 ? kBlocksOf192 : kBlocks) * std::max(1, zyfa::device_sm_count(dev));
   const long long most = std::min(kMaxTokens, std::max(12, 320 / (H + 2 * H_kv)));
   const long long waves = (N + most * slots_gpu - 1) / (most * slots_gpu);
   a.tokens = static_cast<int>((N + slots_gpu * waves - 1) / (slots_gpu * waves));
