@@ -234,32 +234,25 @@ struct Rows4 {
   using T = Tile4<DQK, DV>;
   using R = Reader4<DQK, DV>;
   static constexpr int kHeads = 8 * NS, kPiecesK = DQK / 32, kPieces = DV / 32;
-  static constexpr bool kQueriesInRegisters = NS == 1;
-  static constexpr uint32_t kQueryBytes = kQueriesInRegisters ? 0 : NS * kPiecesK * 512;  // else B fragments in shared memory, a lane's of a piece in 16 bytes
+  static constexpr uint32_t kQueryBytes = NS * kPiecesK * 512;  // B fragments in shared memory, a lane's of two steps of the contraction in 16 bytes
   // Runs of 16 keys whose scores are weighed together: both of a turn where registers hold them (128 requests 136 us, one by one 138; two
   // sets of 64 channels 31.1 and 33.7; two sets of 128 would spill 144 bytes a thread: 51 instead of 45).
   static constexpr int kTogether = NS == 1 || DV == 64 ? 2 : 1;
   static constexpr float kLift = 15.0f;             // weights in fp16 up to 2^15, so that light ones keep their bits
   static constexpr float kNoKey = 3.402823466e38f;  // ref before the first key: lifts every score above its negative over the limit
 
-  uint4 qf[kQueriesInRegisters ? kPiecesK : 1];  // B fragments of the queries, two steps of the contraction a piece
   uint32_t queries;
   float o[NS][kPieces][2][4], m[NS][2], l[NS][2];  // this lane's two heads of each set
   F2 ref[NS], scale[NS];
   float dv;
 
-  __device__ __forceinline__ uint4 query(int c, int p) const {
-    if constexpr (kQueriesInRegisters)
-      return qf[p];
-    else
-      return lds16(queries + (c * kPiecesK + p) * 512);
-  }
+  __device__ __forceinline__ uint4 query(int c, int p) const { return lds16(queries + (c * kPiecesK + p) * 512); }
   static __device__ __forceinline__ uint32_t top_bits(uint32_t top, uint32_t w) { return max(top, max(w & 0x7fff0000u, (w << 16) & 0x7fff0000u)); }
 
   // Begins a request's part: its queries from shared memory, `count` dense bf16 rows.
   __device__ __forceinline__ void begin(uint32_t rows, int count, float scale_, float dv_, int lane) {
     const int t = lane & 3;
-    if (!kQueriesInRegisters) __syncwarp();  // the last part's fragments have been read
+    __syncwarp();  // the last part's fragments have been read
 #pragma unroll
     for (int c = 0; c < NS; ++c) {
       // rows behind the last head repeat it: their columns are computed and never written
@@ -280,10 +273,7 @@ struct Rows4 {
         const uint4 w = lds16(row + 64 * p);
         auto two = [&](uint32_t x) { return halves(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
         const uint4 q = make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
-        if constexpr (kQueriesInRegisters)
-          qf[p] = q;
-        else
-          ptx::st_shared_v4(queries + (c * kPiecesK + p) * 512, q.x, q.y, q.z, q.w);
+        ptx::st_shared_v4(queries + (c * kPiecesK + p) * 512, q.x, q.y, q.z, q.w);
       }
       const float undo = ldexpf(scale_, -shift);
       scale[c] = {__shfl_sync(0xffffffffu, undo, 8 * t), __shfl_sync(0xffffffffu, undo, 8 * t + 4)};
@@ -296,7 +286,7 @@ struct Rows4 {
       l[c][0] = l[c][1] = 0.0f;
     }
     dv = dv_;
-    if (!kQueriesInRegisters) __syncwarp();
+    __syncwarp();
   }
 
   // The scales of one key (of D channels) for this lane's block of each 32 channels, widened: two a register.
@@ -369,35 +359,44 @@ struct Rows4 {
 #pragma unroll
       for (int j = 0; j < 2; ++j) x[c][j] = add2({acc[0][c][2 * j], acc[0][c][2 * j + 1]}, {acc[1][c][2 * j], acc[1][c][2 * j + 1]});
   }
-  // O^T += V^T P^T of 16 keys: rows are channels of V, the contraction keys.
-  __device__ __forceinline__ void values(const Run4& s, const R& at, bool second, int g, const uint32_t (&pf)[NS][2]) {
+  // V's matrices of 16 keys and the scales of rows 2t and 2t + 1 of both, as they lie in shared memory.
+  struct Raw {
+    uint32_t r[kPieces / 2][4];
+    uint2 first[2], other[2];
+  };
+  __device__ __forceinline__ void load_values(const Run4& s, const R& at, bool second, Raw& v) const {
     const uint32_t vs = s.vs + (second ? 16 * at.v_scales : 0), v0 = s.v + (second ? at.v_16 : 0);
-    uint32_t sv[2][kPieces];  // scales of rows 2t (2t + 1) of V's two matrices, of this lane's block of every 32 channels
-    const uint32_t pick = g < 4 ? 0x6240u : 0x7351u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t first = vs + at.value_scale(j, false), other = vs + at.value_scale(j, true);
+      v.first[j] = DV == 128 ? lds8(first) : make_uint2(lds4(first), 0);
+      v.other[j] = DV == 128 ? lds8(other) : make_uint2(lds4(other), 0);
+    }
+#pragma unroll
+    for (int p = 0; p < kPieces / 2; ++p) ldsm4t(v0 + at.value_at(p, second), v.r[p]);
+  }
+  // O^T += V^T P^T of 16 keys: rows are channels of V, the contraction keys.
+  __device__ __forceinline__ void values(const Raw& raw, int g, const uint32_t (&pf)[NS][2]) {
+    uint32_t sv[2][kPieces];  // scales of this lane's block of every 32 channels
+    const uint32_t pick = g < 4 ? 0x6240u : 0x7351u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t lo = prmt(raw.first[j].x, raw.other[j].x, pick);
+      sv[j][0] = widen_e4m3(lo);
+      sv[j][1] = widen_e4m3_hi(lo);
       if constexpr (DV == 128) {
-        const uint2 a = lds8(first), b = lds8(other);
-        const uint32_t lo = prmt(a.x, b.x, pick), hi = prmt(a.y, b.y, pick);
-        sv[j][0] = widen_e4m3(lo);
-        sv[j][1] = widen_e4m3_hi(lo);
+        const uint32_t hi = prmt(raw.first[j].y, raw.other[j].y, pick);
         sv[j][2] = widen_e4m3(hi);
         sv[j][3] = widen_e4m3_hi(hi);
-      } else {
-        const uint32_t lo = prmt(lds4(first), lds4(other), pick);
-        sv[j][0] = widen_e4m3(lo);
-        sv[j][1] = widen_e4m3_hi(lo);
       }
     }
 #pragma unroll
     for (int p = 0; p < kPieces; p += 2) {
-      uint32_t r[4];
-      ldsm4t(v0 + at.value_at(p / 2, second), r);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         // two keys a byte: even channels, and odd ones
-        const uint32_t v = r[2 * i], w = r[2 * i + 1], even = (v & 0x0f0f0f0fu) | (w << 4 & 0xf0f0f0f0u), odd = (v >> 4 & 0x0f0f0f0fu) | (w & 0xf0f0f0f0u);
+        const uint32_t v = raw.r[p / 2][2 * i], w = raw.r[p / 2][2 * i + 1];
+        const uint32_t even = (v & 0x0f0f0f0fu) | (w << 4 & 0xf0f0f0f0u), odd = (v >> 4 & 0x0f0f0f0fu) | (w & 0xf0f0f0f0u);
         const uint32_t s0 = sv[0][p + i], s1 = sv[1][p + i];
         const uint32_t f[2][4] = {{mul_f16x2(widen_e2m1<0>(even), s0), mul_f16x2(widen_e2m1<0>(odd), s0), mul_f16x2(widen_e2m1<1>(even), s0),
                                    mul_f16x2(widen_e2m1<1>(odd), s0)},
@@ -439,6 +438,8 @@ struct Rows4 {
             if (!((mask >> (16 * h + key_of_k(j * 8 + g))) & 1)) x[h][c][j] = {-INFINITY, -INFINITY};
           }
     }
+    Raw raw;  // on its way while scores become weights
+    load_values(s, at, from, raw);
     uint32_t pf[H][NS][2];
 #pragma unroll
     for (int c = 0; c < NS; ++c) {
@@ -495,7 +496,11 @@ struct Rows4 {
         }
     }
 #pragma unroll
-    for (int h = 0; h < H; ++h) values(s, at, from + h, g, pf[h]);
+    for (int h = 0; h < H; ++h) {
+      const Raw now = raw;
+      if (h + 1 < H) load_values(s, at, from + h + 1, raw);
+      values(now, g, pf[h]);
+    }
   }
 
   // Ends a request's part: writes its rows (`count` query heads from `first`), or (m, l, O) to part `slot` of the workspace.
