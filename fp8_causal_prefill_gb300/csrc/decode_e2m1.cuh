@@ -13,11 +13,12 @@
 //   for 16 values), so that a byte is one channel of two keys: converted and multiplied by their scales, it is an operand.
 // * Codes are numbers whatever their bits, so what lies in shared memory behind a request's end only needs scales of 0.
 //
-// Bound: HBM, 9/16 byte a value, and next to it the SM's issue: 16 keys of a head of 128 channels are some 310 warp instructions for 2304
-// bytes, 64 of which convert, 64 multiply by scales and 16 are matrix products.  128 requests of up to 16384 tokens, 8 KV heads of 128: 136 us,
+// Bound: HBM, 9/16 byte a value, and next to it the SM's issue: 16 keys of a head of 128 channels are some 318 warp instructions for 2304
+// bytes, 64 of which convert, 64 multiply by scales and 16 are matrix products.  128 requests of up to 16384 tokens, 8 KV heads of 128: 135 us,
 // where the bytes take 101 and the loads alone 111; 2.4 instructions a clock and SM, the ALU at half its rate, matrix instructions at a
-// quarter of theirs.  More warps an SM would fill the gaps, but 96 registers a thread spill (177 us with 16 compute warps), and V's loads
-// ahead of the weights spill as well (142 us).  Scales taken outside the matrix products, on weights and scores, cost as many instructions;
+// quarter of theirs.  More warps an SM would fill the gaps, but 96 registers a thread spill (166 us with 16 compute warps).  V's registers are
+// on their way while scores become weights, which needs the queries' fragments in shared memory: 16 of 192/128 74 -> 70 us (in registers
+// both spill: 142 us for the 128 requests).  Scales taken outside the matrix products, on weights and scores, cost as many instructions;
 // tcgen05 would read widened operands from shared memory, which takes longer than the whole kernel.
 #pragma once
 #include "decode.cuh"
@@ -236,7 +237,7 @@ struct Rows4 {
   static constexpr int kHeads = 8 * NS, kPiecesK = DQK / 32, kPieces = DV / 32;
   static constexpr uint32_t kQueryBytes = NS * kPiecesK * 512;  // B fragments in shared memory, a lane's of two steps of the contraction in 16 bytes
   // Runs of 16 keys whose scores are weighed together: both of a turn where registers hold them (128 requests 136 us, one by one 138; two
-  // sets of 64 channels 31.1 and 33.7; two sets of 128 would spill 144 bytes a thread: 51 instead of 45).
+  // sets of 64 channels 31.1 and 33.7; two sets of 128 would spill 144 bytes a thread: 51 us instead of 45).
   static constexpr int kTogether = NS == 1 || DV == 64 ? 2 : 1;
   static constexpr float kLift = 15.0f;             // weights in fp16 up to 2^15, so that light ones keep their bits
   static constexpr float kNoKey = 3.402823466e38f;  // ref before the first key: lifts every score above its negative over the limit
