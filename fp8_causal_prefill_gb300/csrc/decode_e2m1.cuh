@@ -465,7 +465,8 @@ struct Rows4 {
           const float by = !FULL ? 1.0f : e ? scale[c].y : scale[c].x;
           float top = m[c][e];
 #pragma unroll
-          for (int h = 0; h < H; ++h) top = fmaxf(top, by * (e ? fmaxf(x[h][c][0].y, x[h][c][1].y) : fmaxf(x[h][c][0].x, x[h][c][1].x)));
+          for (int h = 0; h < H; ++h)  // (of products, since a descale below 0 turns their order around)
+            top = fmaxf(top, e ? fmaxf(by * x[h][c][0].y, by * x[h][c][1].y) : fmaxf(by * x[h][c][0].x, by * x[h][c][1].x));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
