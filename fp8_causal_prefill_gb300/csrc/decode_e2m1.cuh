@@ -241,6 +241,9 @@ struct Rows4 {
   static constexpr int kTogether = NS == 1 || DV == 64 ? 2 : 1;
   static constexpr float kLift = 15.0f;             // weights in fp16 up to 2^15, so that light ones keep their bits
   static constexpr float kNoKey = 3.402823466e38f;  // ref before the first key: lifts every score above its negative over the limit
+  // From this magnitude of m on scores are rounded before m is subtracted.  Below, the product with `scale` and the sum with ref round as
+  // one, by less than 2^-13 of a weight's exponent; from 2^24 on by whole units, which took weights out of fp16.
+  static constexpr float kLoud = 1024.0f;
 
   uint32_t queries;
   float o[NS][kPieces][2][4], m[NS][2], l[NS][2];  // this lane's two heads of each set
@@ -445,7 +448,7 @@ struct Rows4 {
 #pragma unroll
     for (int c = 0; c < NS; ++c) {
       // log2 of the weights: scores in units of log2 over the reference m, which moves only when a key exceeds it: log2 of a weight is then
-      // above the lift.
+      // above the lift.  A loud m leaves ref at kNoKey, so that every run comes by here.
       F2 y[H][2];
       float over;
       auto log2_weights = [&]() {
@@ -460,20 +463,22 @@ struct Rows4 {
       };
       log2_weights();
       if (__any_sync(0xffffffffu, over > kLift)) {
+        // (rounded by itself; products, since a descale below 0 turns the order of sums around)
+        auto score = [&](int h, int j, int e) {
+          const float s = e ? x[h][c][j].y : x[h][c][j].x;
+          return FULL ? __fmul_rn(e ? scale[c].y : scale[c].x, s) : s;
+        };
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float by = !FULL ? 1.0f : e ? scale[c].y : scale[c].x;
           float top = m[c][e];
 #pragma unroll
-          for (int h = 0; h < H; ++h)  // (of products, since a descale below 0 turns their order around)
-            top = fmaxf(top, e ? fmaxf(by * x[h][c][0].y, by * x[h][c][1].y) : fmaxf(by * x[h][c][0].x, by * x[h][c][1].x));
+          for (int h = 0; h < H; ++h) top = fmaxf(top, fmaxf(score(h, 0, e), score(h, 1, e)));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const bool none = top == -INFINITY;
-          const float f = none ? 1.0f : exp2_approx(m[c][e] - top);
+          const float f = top == -INFINITY ? 1.0f : exp2_approx(m[c][e] - top);
           m[c][e] = top;
-          (e ? ref[c].y : ref[c].x) = none ? kNoKey : kLift - top;
+          (e ? ref[c].y : ref[c].x) = fabsf(top) < kLoud ? kLift - top : kNoKey;
           l[c][e] *= f;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i)
@@ -484,6 +489,13 @@ struct Rows4 {
             }
         }
         log2_weights();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (fabsf(m[c][e]) >= kLoud && m[c][e] != -INFINITY)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) (e ? y[h][j].y : y[h][j].x) = (score(h, j, e) - m[c][e]) + kLift;  // the greatest one's is the lift
       }
       // weights, transposed into the B operand (keys are now the contraction)
 #pragma unroll

@@ -1,4 +1,7 @@
-"""GPU tests of single-token attention where scores are turned around: descales below 0."""
+"""GPU tests of single-token attention where scores are turned around or far from 0: descales below 0, and a few equal keys beyond all
+others by more than fp32 resolves next to them."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -89,3 +92,67 @@ def test_descales_below_zero(kind, shape, H, H_kv, tile, page, per_head):
                 assert np.all(np.abs(out[b, h] - ref) <= tol + 2 * more * (w @ np.abs(v)) * abs(f)), (width, b, h)
                 assert abs(lse[b, h] - ref_lse) <= lse_tol + more + 2.0 ** -23 * abs(ref_lse), (width, b, h)
         assert np.isfinite(out).all() and np.isfinite(lse).all()
+
+
+# Levels of the loud channel, which e4m3 and bf16 hold; what e2m1 blocks hold of them is as far apart
+LEVELS = {"e2m1": np.array([1.0, 2.0, 3.0, 4.0, 6.0]) * 448.0, "fp8": np.array([64.0, 128.0, 192.0, 256.0, 448.0]),
+          "bf16": np.array([64.0, 128.0, 192.0, 256.0, 448.0])}
+
+
+@pytest.mark.parametrize("away", [1, -1])
+@pytest.mark.parametrize("exponent", [12, 20, 24, 25, 26, 27, 30, 40, 100])
+@pytest.mark.parametrize("page", [16, 7])
+@pytest.mark.parametrize("kind,kd", [("e2m1", 1.0), ("e2m1", -1.0), ("bf16", 1.0)])
+def test_scores_far_from_zero(kind, kd, page, exponent, away):
+    """The greatest scores lie at about `away` 2^exponent in units of log2 and the next ones a tenth of that and more away: all weight
+    is on those keys, equal ones share it, wherever they are among tiles, parts and the other heads of a warp.
+
+    Their weights and V are exact, so only a few sums and the quotient round (2^-24 each, 2^-22 in exp2) before out does to bf16 (2^-8).
+    A score is an fp32 sum of D products, rounded three times after.  Rows of queries of 0 weigh all keys alike.
+    """
+    rng = np.random.default_rng(exponent + page)
+    for i, (shape, H, H_kv, tile) in enumerate(FORMS):
+        d_qk, d_v = SHAPES[shape]
+        for lens, width, of in _ways(tile)[:2] if (i + exponent) % 3 else _ways(tile)[2:]:
+            c, B, levels, winners = _Cache(kind, shape, lens, H_kv, page, width, rng), len(of), LEVELS[kind], []
+            for b, n in enumerate(lens):
+                k = rng.standard_normal((n, H_kv, d_qk))
+                # three equal rows at the greatest level of channel 0, a few at each other one, most at the lowest
+                level = np.zeros(n, dtype=np.int64)
+                for j, t in enumerate(rng.permutation(n)[:12]):
+                    level[t] = j % 4
+                best = rng.permutation(n)[:3]
+                level[best] = 4
+                k[:, :, 0] = (levels[level] if away > 0 else -levels[4 - level])[:, None]
+                k[best] = k[best[0]]
+                c.put(0, b, k)
+                c.put(1, b, rng.standard_normal((n, H_kv, d_v)) * 64.0)
+                winners.append(best)
+            q64 = rng.standard_normal((B, H, d_qk)) / 8.0
+            q64[:, :, 0] = rng.integers(8, 16, (B, H)) * 8.0 * kd
+            quiet = rng.random((B, H)) < 0.2
+            q64[quiet] = 0.0
+            q = torch.from_numpy(q64).float().to(E4M3 if kind == "fp8" else torch.bfloat16).cuda()
+            q64 = f64(q)
+            scale = float(np.float32(2.0 ** exponent * math.log(2.0) / (96.0 * levels[4 if away > 0 else 0])))
+            out, lse = c.attend(q, of, scale, k_descale=None if kind == "bf16" else torch.tensor([kd], dtype=torch.float32, device="cuda"))
+            for b in range(0, B, 1 + B // 10):
+                for h in range(H):
+                    hk, best = h // (H // H_kv), winners[of[b]]
+                    k, v = c.rows[0][of[b]][:, hk], c.rows[1][of[b]][:, hk]
+                    n, where = len(k), (shape, H, width, b, h)
+                    if quiet[b, h]:
+                        ref, ref_lse = v.mean(0), math.log(n)
+                        tol = 2.0 ** -8 * np.abs(ref) * 1.01 + (n + 8) * 2.0 ** -23 * np.abs(v).mean(0)
+                        lse_tol = (n + 8) * 2.0 ** -23 + 2.0 ** -19
+                    else:
+                        x = k @ q64[b, h] * kd * scale
+                        rest = np.setdiff1d(np.arange(n), best)
+                        assert len(rest) == 0 or x[best].min() - x[rest].max() > 0.05 * 2.0 ** exponent, where  # e^-200: no weight
+                        ref, ref_lse = v[best].mean(0), x[best[0]] + math.log(len(best))
+                        tol = 2.0 ** -8 * np.abs(ref) * 1.01 + 2.0 ** -20 * np.abs(v[best]).mean(0)
+                        lse_tol = (d_qk + 8) * 2.0 ** -24 * (np.abs(k[best[0]]) @ np.abs(q64[b, h])) * scale + 2.0 ** -20
+                    err = np.abs(out[b, h] - ref)
+                    assert np.all(err <= tol), (where, out[b, h][:4], ref[:4])
+                    assert abs(lse[b, h] - ref_lse) <= lse_tol, (where, float(lse[b, h]), ref_lse)
+            assert np.isfinite(out).all() and np.isfinite(lse).all()
