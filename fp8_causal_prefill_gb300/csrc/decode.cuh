@@ -336,6 +336,9 @@ struct Rows {
   static constexpr int kScoreKind = FP8 ? kE4m3 : kBf16, kValueKind = FP8 ? kF16 : kBf16;
   static constexpr float kLift = FP8 ? 15.0f : 0.0f;  // e4m3: weights in fp16 up to 2^15, so that light ones keep their bits
   static constexpr float kNoKey = 3.402823466e38f;    // ref before the first key: lifts every score above its negative over the limit
+  // e4m3: from this magnitude of m (2^20) on kLift - m rounds by a sixteenth and more, from 2^24 on by so much that weights left fp16.
+  // Such a row subtracts m from its scores and then adds the lift.
+  static constexpr float kLoud = 1048576.0f;
 
   uint32_t qf[kKSteps][2];      // B fragments of the queries
   float o[kMTiles][4], m[2], l[2];  // this lane's two heads
@@ -392,7 +395,7 @@ struct Rows {
       clear();
     }
     // The reference m moves only when a key exceeds it: log2 of a weight is then above the lift.  (Before a part's first key
-    // with a score above -inf m is -inf, and the log2 weight of such a key huge.)
+    // with a score above -inf m is -inf, and the log2 weight of such a key huge; a loud m leaves ref there.)
     F2 y[KB][2];
     float over = -INFINITY;
     auto weigh = [&]() {
@@ -417,7 +420,7 @@ struct Rows {
         const bool none = t == -INFINITY;
         const float f = none ? 1.0f : exp2_approx(m[e] - t);
         m[e] = t;
-        (e ? ref.y : ref.x) = none ? kNoKey : kLift - t;
+        (e ? ref.y : ref.x) = none || (FP8 && fabsf(t) >= kLoud) ? kNoKey : kLift - t;
         l[e] *= f;
 #pragma unroll
         for (int i = 0; i < kMTiles; ++i) {
@@ -426,6 +429,15 @@ struct Rows {
         }
       }
       weigh();
+      if constexpr (FP8) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (fabsf(m[e]) >= kLoud && m[e] != -INFINITY)
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) (e ? y[kb][j].y : y[kb][j].x) = ((e ? x[kb][j].y : x[kb][j].x) - m[e]) + kLift;
+      }
     }
     // weights, transposed into the B operand (keys are now the contraction)
     uint32_t pf[KB][2], rest[KB][2];

@@ -102,7 +102,7 @@ LEVELS = {"e2m1": np.array([1.0, 2.0, 3.0, 4.0, 6.0]) * 448.0, "fp8": np.array([
 @pytest.mark.parametrize("away", [1, -1])
 @pytest.mark.parametrize("exponent", [12, 20, 24, 25, 26, 27, 30, 40, 100])
 @pytest.mark.parametrize("page", [16, 7])
-@pytest.mark.parametrize("kind,kd", [("e2m1", 1.0), ("e2m1", -1.0), ("bf16", 1.0)])
+@pytest.mark.parametrize("kind,kd", [("e2m1", 1.0), ("e2m1", -1.0), ("fp8", 1.0), ("fp8", -1.0), ("bf16", 1.0)])
 def test_scores_far_from_zero(kind, kd, page, exponent, away):
     """The greatest scores lie at about `away` 2^exponent in units of log2 and the next ones a tenth of that and more away: all weight
     is on those keys, equal ones share it, wherever they are among tiles, parts and the other heads of a warp.
