@@ -31,7 +31,7 @@ EXPORTED = ("zyfa_attn_fwd_causal", "zyfa_attn_fwd_causal_ex", "zyfa_attn_fwd_ca
             "zyfa_paged_plan", "zyfa_rope_paged_store", "zyfa_attn_decode_paged",
             "zyfa_attn_decode_paged_workspace_bytes", "zyfa_attn_decode_paged_launches",
             "zyfa_selftest_stalled_decode", "zyfa_rope_paged_store_e2m1", "zyfa_paged_read",
-            "zyfa_attn_decode_paged_e2m1", "zyfa_selftest_stalled_decode_e2m1")
+            "zyfa_attn_decode_paged_e2m1", "zyfa_attn_decode_paged_e2m1_launches", "zyfa_selftest_stalled_decode_e2m1")
 ZYFA_P_LEAN = 0
 ZYFA_P_EXACT = 1
 ZYFA_P_EXACT_NO_BLOCK_SCALE = 2
@@ -142,6 +142,8 @@ def load_library() -> ctypes.CDLL:
         lib.zyfa_attn_decode_paged_e2m1.argtypes = [vp, ll, cache, scales, vp, ll, ci, vp, vp, vp, ci, ci, cf, vp, vp, ci, vp,
                                                     sz, vp]
         lib.zyfa_attn_decode_paged_e2m1.restype = ci
+        lib.zyfa_attn_decode_paged_e2m1_launches.argtypes = [cache, scales, ci, ci, ci, ci, ctypes.POINTER(ci)]
+        lib.zyfa_attn_decode_paged_e2m1_launches.restype = ci
         lib.zyfa_selftest_stalled_decode_e2m1.argtypes = [vp, ll, cache, scales, vp, ll, ci, vp, vp, ci, ci, vp, sz, vp]
         lib.zyfa_selftest_stalled_decode_e2m1.restype = ci
         _lib = lib

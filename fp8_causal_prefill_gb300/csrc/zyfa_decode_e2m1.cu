@@ -24,9 +24,30 @@ zyfa_status_t attend(const void* q, long long q_batch_stride, const zyfa_paged_c
                               : launch4<192, 128>(a, nsm, dev, ws, stream);
 }
 
+template <int DQK, int DV>
+int launches4(Args& a, int sms) {
+  int smem;
+  if (!(a.group <= 8 ? plan4<DQK, DV, 1>(a, sms, &smem) : plan4<DQK, DV, 2>(a, sms, &smem))) return 0;
+  return a.whole ? 1 : 2;
+}
+
 }  // namespace
 
 extern "C" {
+
+int zyfa_attn_decode_paged_e2m1_launches(const zyfa_paged_cache_t* cache, const zyfa_paged_scales_t* scales, int max_pages, int B, int H,
+                                         int sms, int* boxes) {
+  Args a = {};
+  if (set_sizes(&a, cache, max_pages, B, H, zyfa::k4BitCaches) != ZYFA_OK || zyfa::check_scales(scales, &a.scales) != ZYFA_OK || B == 0 || sms < 0) return 0;
+  int dev = 0;
+  if (sms == 0 && (cudaGetDevice(&dev) != cudaSuccess || (sms = zyfa::device_sm_count(dev)) <= 0)) return 0;
+  sms = std::min(sms, kMaxSms);
+  const int n = cache->D_qk == 64    ? launches4<64, 64>(a, sms)
+                : cache->D_qk == 128 ? launches4<128, 128>(a, sms)
+                                     : launches4<192, 128>(a, sms);
+  if (n > 0 && boxes) *boxes = a.boxes;
+  return n;
+}
 
 zyfa_status_t zyfa_attn_decode_paged_e2m1(const void* q, long long q_batch_stride, const zyfa_paged_cache_t* cache, const zyfa_paged_scales_t* scales,
                                           const int* block_table, long long table_stride, int max_pages, const int* seq_lens, void* out,

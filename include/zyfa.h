@@ -445,6 +445,18 @@ size_t zyfa_attn_decode_paged_workspace_bytes(int B, int H, int H_kv, int D_v, l
  * what the call refuses.  Host arithmetic, for accounting in benchmarks. */
 int zyfa_attn_decode_paged_launches(const zyfa_paged_cache_t* cache, int max_pages, int B, int H, int sms);
 
+/* zyfa_attn_decode_paged_e2m1_launches - the same for zyfa_attn_decode_paged_e2m1.  `boxes` may be NULL; else, where the result is not 0,
+ * it receives 1 if the cache's tokens are loaded in boxes, many of a page at a time, and 0 if they are loaded piece by piece, which is
+ * two to four times as slow at length.  Boxes need pages of a multiple of 8 tokens, no stride of 0, and scales and their page strides at
+ * 16-byte boundaries.  Caches whose tokens follow one another within a head ([num_pages][H_kv][page_size][...]) then have them always.  In a
+ * dense [num_pages][page_size][H_kv][...] cache a block's scales have to be whole rows too:
+ *   - up to 16 query heads per KV head: 1 to 4 KV heads, and beyond multiples of 4, or of 2 with 128 channels;
+ *   - 17 to 32: 1 or 2 KV heads, or with 128 channels any even number;
+ *   - 33 and more: one KV head.
+ * (A cache whose tensor maps the driver refuses is loaded piece by piece all the same.) */
+int zyfa_attn_decode_paged_e2m1_launches(const zyfa_paged_cache_t* cache, const zyfa_paged_scales_t* scales, int max_pages, int B, int H,
+                                         int sms, int* boxes);
+
 /*
  * zyfa_check_errors - synchronise `stream`, then read and clear the current device's status word.
  * Returns ZYFA_ERR_TIMEOUT if any kernel of this library timed out since the last check, else
