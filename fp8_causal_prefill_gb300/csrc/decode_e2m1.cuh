@@ -1128,6 +1128,7 @@ template <int DQK, int DV, int NS>
 bool plan4(Args& a, int nsm, int* smem) {
   using T = Tile4<DQK, DV>;
   using Rows = Rows4<DQK, DV, NS>;
+  if (a.cache.num_pages == 1) a.cache.k_page = a.cache.v_page = a.scales.k_page = a.scales.v_page = 16;  // never taken; what maps can have
   a.chunks = (a.group + Rows::kHeads - 1) / Rows::kHeads;
   a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
   a.chunk_warps = piece(a.chunks, kWarps);

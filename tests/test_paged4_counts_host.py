@@ -70,6 +70,15 @@ def test_strides_that_boxes_cannot_have(lib):  # noqa: F811
     assert piece(scales=dict(k_token_stride=36)) and piece(scales=dict(v_page_stride=516)) and piece(scales=dict(k=FAR["ks"] + 8))
 
 
+@pytest.mark.parametrize("shape", ["64", "128", "mla"])
+def test_one_page_has_no_page_stride(lib, shape):  # noqa: F811
+    # (what a tensor of one page gives as the stride may be anything that the calls accept)
+    for H_kv in (1, 2, 4, 8):
+        for stride in (0, 4, 8, 12, 36):
+            caches = _dense(shape, H_kv, 4096, pages=1, cache=dict(k_page_stride=0, v_page_stride=32), scales=dict(k_page_stride=stride, v_page_stride=stride))
+            assert _count(lib, caches, 5, 4 * H_kv, 1) == (2, 1), (H_kv, stride)
+
+
 def test_counts_of_refused_calls(lib):  # noqa: F811
     c, s = _dense("128", 4, 16)
     assert _count(lib, (c, s), 5, 16, 64) == (2, 1)
