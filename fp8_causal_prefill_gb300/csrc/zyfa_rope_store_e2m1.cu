@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -25,7 +26,7 @@ namespace {
 
 using namespace zyfa::rope;
 
-// Blocks an SM holds of 256 (192 for 192 channels) threads of 64 registers, below which they spill
+// Blocks an SM is to hold of 256 (192 for 192 channels) threads where keys go the way of queries: 64 registers, below which they spill
 constexpr int kBlocks = 4, kBlocksOf192 = 5;
 
 struct Store4Args {
@@ -343,17 +344,38 @@ __global__ void __launch_bounds__(kThreads<DQK>, NEAT ? (DQK == 192 ? kBlocksOf1
   }
 }
 
-template <bool INTERLEAVED, bool NEAT>
-cudaError_t launch(const Store4Args& a, int D_qk, cudaStream_t stream) {
+// Tokens a block: so many that all blocks run at once, in as few such waves as 12 to 32 tokens of a few or more heads allow (8000 tokens of 8
+// heads of 192/128: 21.2 us in one wave, 26.1 where an eighth of the blocks waits).  An SM holds 4 blocks (5 of 192 channels) where keys
+// go the way of queries, 2 to 4 where a thread has a block of a key: 8000 tokens of 8 heads of 192/128 whose 48 channels from 136 on turn take
+// 32.8 us in waves of 3 blocks, 37.2 in waves of 5; 32768 of 32 and 8 heads of 128 with 48 148.0 (2) and 152.7 (4).
+template <bool INTERLEAVED, bool NEAT, int DQK, int DV>
+cudaError_t launch_of(Store4Args& a, int dev, cudaStream_t stream) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> held[kMaxDevices];
+  int blocks = dev < kMaxDevices ? held[dev].load(std::memory_order_relaxed) : 0;
+  if (blocks == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, store4_kernel<INTERLEAVED, NEAT, DQK, DV>, kThreads<DQK>, 0);
+    if (e != cudaSuccess) return e;
+    blocks = std::max(blocks, 1);
+    if (dev < kMaxDevices) held[dev].store(blocks, std::memory_order_relaxed);
+  }
+  const long long at_once = static_cast<long long>(blocks) * std::max(1, zyfa::device_sm_count(dev));
+  const long long most = std::min(kMaxTokens, std::max(12, 320 / (a.H + 2 * a.cache.H_kv))), waves = (a.N + most * at_once - 1) / (most * at_once);
+  a.tokens = static_cast<int>((a.N + at_once * waves - 1) / (at_once * waves));
   const dim3 grid(static_cast<unsigned>((a.N + a.tokens - 1) / a.tokens));
-  if (D_qk == 64) return zyfa::launch_dependent(store4_kernel<INTERLEAVED, NEAT, 64, 64>, grid, kThreads<64>, 0, stream, a);
-  if (D_qk == 128) return zyfa::launch_dependent(store4_kernel<INTERLEAVED, NEAT, 128, 128>, grid, kThreads<128>, 0, stream, a);
-  return zyfa::launch_dependent(store4_kernel<INTERLEAVED, NEAT, 192, 128>, grid, kThreads<192>, 0, stream, a);
+  return zyfa::launch_dependent(store4_kernel<INTERLEAVED, NEAT, DQK, DV>, grid, kThreads<DQK>, 0, stream, a);
+}
+
+template <bool INTERLEAVED, bool NEAT>
+cudaError_t launch(Store4Args& a, int D_qk, int dev, cudaStream_t stream) {
+  return D_qk == 64    ? launch_of<INTERLEAVED, NEAT, 64, 64>(a, dev, stream)
+         : D_qk == 128 ? launch_of<INTERLEAVED, NEAT, 128, 128>(a, dev, stream)
+                       : launch_of<INTERLEAVED, NEAT, 192, 128>(a, dev, stream);
 }
 
 template <bool INTERLEAVED>
-cudaError_t launch(const Store4Args& a, bool neat, int D_qk, cudaStream_t stream) {
-  return neat ? launch<INTERLEAVED, true>(a, D_qk, stream) : launch<INTERLEAVED, false>(a, D_qk, stream);
+cudaError_t launch(Store4Args& a, bool neat, int D_qk, int dev, cudaStream_t stream) {
+  return neat ? launch<INTERLEAVED, true>(a, D_qk, dev, stream) : launch<INTERLEAVED, false>(a, D_qk, dev, stream);
 }
 
 }  // namespace
@@ -430,13 +452,7 @@ extern "C" zyfa_status_t zyfa_rope_paged_store_e2m1(const void* q, const void* k
   a.desc_per_head = descale_per_kv_head;
   a.N = N;
   a.H = H;
-  // Tokens a block: so many that all blocks run at once, in as few such waves as 12 to 32 tokens of a few or more heads allow (8000 tokens of 8
-  // heads of 192/128: 21.2 us in one wave, 26.1 where an eighth of the blocks waits).
-  const long long slots_gpu = static_cast<long long>(D_qk == 192 ? kBlocksOf192 : kBlocks) * std::max(1, zyfa::device_sm_count(dev));
-  const long long most = std::min(kMaxTokens, std::max(12, 320 / (H + 2 * H_kv)));
-  const long long waves = (N + most * slots_gpu - 1) / (most * slots_gpu);
-  a.tokens = static_cast<int>((N + slots_gpu * waves - 1) / (slots_gpu * waves));
   const bool interleaved = rope && rope->interleaved, neat = a.offset % 16 == 0 && (interleaved || a.rot % 32 == 0);
-  const cudaError_t e = interleaved ? launch<true>(a, neat, D_qk, stream) : launch<false>(a, neat, D_qk, stream);
+  const cudaError_t e = interleaved ? launch<true>(a, neat, D_qk, dev, stream) : launch<false>(a, neat, D_qk, dev, stream);
   return e == cudaSuccess ? ZYFA_OK : ZYFA_ERR_CUDA;
 }

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_paged4_gpu as base
 from _paged4_util import fill4, make_cache4, random_codes, raw
 from _paged_util import SHAPES, bits, random_values
 from fp8_causal_prefill_gb300 import paged_decode_attn, paged_read, zyfa_check_errors
@@ -33,3 +34,12 @@ def test_a_cache_of_one_page(shape, H, H_kv, page, layout):
     for x, y in zip(*(paged_read(*c[:2], table[:1], cu, page, k_scales=c[2], v_scales=c[3]) for c in (one, two))):
         assert torch.equal(bits(x), bits(y))
     assert zyfa_check_errors() == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shape", ["64", "128", "mla"])
+def test_stores_of_any_number_of_waves(shape, interleaved):
+    """Rotations that split a block of 16 channels, whose kernels hold fewer blocks an SM, and one that does not."""
+    for N in (303, 305, 1217, 9729):
+        base._store_case(shape, N, 2, 1, interleaved=interleaved, rot=16, offset=8, seed=N)
+        base._store_case(shape, N, 1, 1, interleaved=interleaved, rot=32, offset=16, seed=N)
