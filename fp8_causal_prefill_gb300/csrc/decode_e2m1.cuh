@@ -53,7 +53,6 @@ struct Maps4 {
 template <int DQK, int DV>
 struct Tile4 {
   static constexpr int kRowK = DQK / 2, kRowV = DV / 2, kScaleK = DQK / 16, kScaleV = DV / 16;
-  static constexpr int kKeyBytes = kRowK + kRowV + kScaleK + kScaleV;
 };
 
 // Codes of a tile lie in shared memory box by box, a token's heads one after the other, in columns of 128 bytes [token][128] with

@@ -172,6 +172,15 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// Two products by one instruction.
+__device__ __forceinline__ float2 times(float a, float b, float f) {
+  float2 d;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a), "f"(b), "f"(f));
+  return d;
+}
+
 __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // A load that sees what had been written when it was issued (from L2, not from an earlier copy in this SM's L1).
 __device__ __forceinline__ int load_relaxed(const int* p) {

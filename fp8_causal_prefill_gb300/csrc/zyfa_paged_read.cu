@@ -40,7 +40,6 @@ struct ReadArgs {
   int step;  // from a sample of cu to the next
 };
 
-template <int DQK>
 constexpr int kReadThreads = 256;
 
 // What a thread reads of a head: 16 values of a cache type, and their scale.
@@ -111,14 +110,6 @@ __device__ __forceinline__ void put_words(uint8_t* to, const uint32_t (&w)[OUT_F
   }
 }
 
-// Two products by one instruction.
-__device__ __forceinline__ float2 times(float a, float b, float f) {
-  float2 d;
-  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a), "f"(b), "f"(f));
-  return d;
-}
 template <bool OUT_FP8>
 __device__ __forceinline__ void put(uint8_t* to, const float (&y)[16], float f, bool wide) {
   constexpr int kWords = OUT_FP8 ? 4 : 8;
@@ -126,13 +117,13 @@ __device__ __forceinline__ void put(uint8_t* to, const float (&y)[16], float f, 
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
     if constexpr (OUT_FP8) {
-      const float2 lo = times(y[4 * i], y[4 * i + 1], f), hi = times(y[4 * i + 2], y[4 * i + 3], f);
+      const float2 lo = zyfa::times(y[4 * i], y[4 * i + 1], f), hi = zyfa::times(y[4 * i + 2], y[4 * i + 3], f);
       asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
           "mov.b32 %0, {lo, hi};\n\t}"
           : "=r"(w[i])
           : "f"(lo.x), "f"(lo.y), "f"(hi.x), "f"(hi.y));
     } else {
-      const float2 x = times(y[2 * i], y[2 * i + 1], f);
+      const float2 x = zyfa::times(y[2 * i], y[2 * i + 1], f);
       asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x.y), "f"(x.x));
     }
   }
@@ -195,8 +186,8 @@ __device__ __forceinline__ void copy_rows(const ReadArgs& a, const Places& at, l
 }
 
 template <int KIND, bool OUT_FP8, int DQK, int DV>
-__global__ void __launch_bounds__(kReadThreads<DQK>) read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int kN = kReadThreads<DQK>;
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int kN = kReadThreads;
   __shared__ int s_cu[kN];
   __shared__ Places s_at;
   const int tid = threadIdx.x;
@@ -251,9 +242,9 @@ __global__ void __launch_bounds__(kReadThreads<DQK>) read_kernel(const __grid_co
 template <int KIND, bool OUT_FP8>
 cudaError_t launch(const ReadArgs& a, int D_qk, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.N + a.rows - 1) / a.rows));
-  if (D_qk == 64) return zyfa::launch_dependent(read_kernel<KIND, OUT_FP8, 64, 64>, grid, kReadThreads<64>, 0, stream, a);
-  if (D_qk == 128) return zyfa::launch_dependent(read_kernel<KIND, OUT_FP8, 128, 128>, grid, kReadThreads<128>, 0, stream, a);
-  return zyfa::launch_dependent(read_kernel<KIND, OUT_FP8, 192, 128>, grid, kReadThreads<192>, 0, stream, a);
+  if (D_qk == 64) return zyfa::launch_dependent(read_kernel<KIND, OUT_FP8, 64, 64>, grid, kReadThreads, 0, stream, a);
+  if (D_qk == 128) return zyfa::launch_dependent(read_kernel<KIND, OUT_FP8, 128, 128>, grid, kReadThreads, 0, stream, a);
+  return zyfa::launch_dependent(read_kernel<KIND, OUT_FP8, 192, 128>, grid, kReadThreads, 0, stream, a);
 }
 
 template <int KIND>
@@ -335,11 +326,10 @@ extern "C" zyfa_status_t zyfa_paged_read(const zyfa_paged_cache_t* cache, const 
   a.desc_request = descale_per_kv_head == 1 ? cache->H_kv : 0;
   a.out_per_head = out_descale_per_kv_head;
   zyfa::division_by(cache->page_size, 30, &a.page_magic, &a.page_shift);
-  const int threads = cache->D_qk == 192 ? kReadThreads<192> : kReadThreads<64>;
-  a.step = (B + threads - 1) / threads;
+  a.step = (B + kReadThreads - 1) / kReadThreads;
   // Rows of a block: whole passes of its threads, 64 KiB to write (96 in e4m3, where the start counts more), but blocks for every SM four
   // times over.  131072 tokens of 8 heads of 128 as bf16: 105.6 us, with 96 KiB 107.2; 32768 as e4m3 22.0 with 96 KiB, 24.2 with 64.
-  const long long bytes = heads * (cache->D_qk + cache->D_v) * es, pass = std::max(1ll, threads / std::max(1ll, heads * cache->D_qk / 16));
+  const long long bytes = heads * (cache->D_qk + cache->D_v) * es, pass = std::max(1ll, kReadThreads / std::max(1ll, heads * cache->D_qk / 16));
   const long long most = std::max(pass, (es == 2 ? 65536 : 98304) / bytes / pass * pass), wanted = (N + 4ll * nsm - 1) / (4ll * nsm);
   a.rows = static_cast<int>(std::min<long long>(kMaxRows, std::min(most, (wanted + pass - 1) / pass * pass)));
   cudaError_t e;

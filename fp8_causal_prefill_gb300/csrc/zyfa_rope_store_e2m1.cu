@@ -77,18 +77,10 @@ __device__ __forceinline__ uint8_t scale_of(uint32_t top, const float* reciproca
   *r = reciprocals[s8 & 0x7f];
   return static_cast<uint8_t>(s8);
 }
-// Two products by one instruction.
-__device__ __forceinline__ float2 times(float a, float b, float f) {
-  float2 d;
-  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a), "f"(b), "f"(f));
-  return d;
-}
 __device__ __forceinline__ void times8(float* z, float f) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    const float2 p = times(z[i], z[i + 1], f);
+    const float2 p = zyfa::times(z[i], z[i + 1], f);
     z[i] = p.x;
     z[i + 1] = p.y;
   }
@@ -96,7 +88,7 @@ __device__ __forceinline__ void times8(float* z, float f) {
 // Eight e2m1 codes, the first in the lowest bits.
 __device__ __forceinline__ uint32_t codes8(const float* z, float r) {
   uint32_t d;
-  const float2 x = times(z[0], z[1], r), y = times(z[2], z[3], r), u = times(z[4], z[5], r), v = times(z[6], z[7], r);
+  const float2 x = zyfa::times(z[0], z[1], r), y = zyfa::times(z[2], z[3], r), u = zyfa::times(z[4], z[5], r), v = zyfa::times(z[6], z[7], r);
   asm("{\n\t.reg .b8 a, b, c, e;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 e, %8, %7;\n\tmov.b32 %0, {a, b, c, e};\n\t}"
       : "=r"(d)
