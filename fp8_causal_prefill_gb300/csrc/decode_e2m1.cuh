@@ -14,7 +14,7 @@
 // * Codes are numbers whatever their bits, so what lies in shared memory behind a request's end only needs scales of 0.
 //
 // Bound: HBM, 9/16 byte a value, and next to it the SM's issue: 16 keys of a head of 128 channels are some 318 warp instructions for 2304
-// bytes, 64 of which convert, 64 multiply by scales and 16 are matrix products.  128 requests of up to 16384 tokens, 8 KV heads of 128: 135 us,
+// bytes, 64 of which convert, 64 multiply by scales and 16 are matrix products.  128 requests of up to 16384 tokens, 8 KV heads of 128: 134 us,
 // where the bytes take 101 and the loads alone 111; 2.4 instructions a clock and SM, the ALU at half its rate, matrix instructions at a
 // quarter of theirs.  More warps an SM would fill the gaps, but 96 registers a thread spill (166 us with 16 compute warps).  V's registers are
 // on their way while scores become weights, which needs the queries' fragments in shared memory: 16 of 192/128 74 -> 70 us (in registers
@@ -496,7 +496,8 @@ struct Rows4 {
 #pragma unroll
               for (int j = 0; j < 2; ++j) (e ? y[h][j].y : y[h][j].x) = (score(h, j, e) - m[c][e]) + kLift;  // the greatest one's is the lift
       }
-      // weights, transposed into the B operand (keys are now the contraction)
+      // Weights, transposed into the B operand (keys are now the contraction).  They round to the 11 bits of fp16, by an eighth
+      // of what out rounds by at most, beside a V that fp16 holds exactly; two terms would double the products.  Their sum takes them unrounded.
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -1094,7 +1095,8 @@ inline bool make_map4(CUtensorMap* m, const uint8_t* base, const Args& a, long l
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t*>(base), dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How a box's scales come, or -1.
+// How a box's scales come, or -1: copies of 16 bytes that a block's heads do not fill go piece by piece (dense caches [page][token][head] of 5
+// KV heads: 64 requests of 500 to 8000 tokens of 128 channels 127 us, of 6 heads by boxes 41).
 inline int scale_mode(const Args& a, const uint8_t* base, long long page, long long tok, long long head, int bytes) {
   const int H_kv = a.cache.H_kv, last = (H_kv - 1) % a.heads + 1;
   if (!aligned(base, 16) || page % 16 != 0 || page < 0 || tok <= 0) return -1;
@@ -1172,6 +1174,9 @@ bool plan4(Args& a, int nsm, int* smem) {
   if (a.stages < 2) return false;
   const long long most = std::max(1ll, (a.max_len + a.tile_tokens - 1ll) / a.tile_tokens), at_once = std::max(1ll, static_cast<long long>(nsm) * blocks / a.units);
   const long long turns_whole = (a.B + at_once - 1) / at_once * most, turns_split = (a.B * most + at_once - 1) / at_once;
+  // The wider caches' rule, whose both sides for this kernel are (2 heads of 64, 256 tokens each, in a graph): 4 requests 8.4 us whole and 8.5
+  // split, 16 8.4 and 8.4, 64 8.5 and 9.3, 256 9.7 and 13.4.  One alone takes 8.4 and 7.3, but called from a host that launches twice 8.4
+  // and 8.7.
   a.whole = most <= kLongest && turns_whole - turns_split <= kSerial;
   a.groups = static_cast<int>(a.whole ? a.B : std::min({at_once, a.B * most, parts_at_most(a.B, a.H, a.cache.H_kv, a.max_len)}));
   *smem = a.stages * stage + more;

@@ -3,9 +3,9 @@
 // Row n is token starts[b] + n - cu[b] of the request b whose run of rows n lies in.  A block takes some rows: it finds their requests
 // (the run starts, or samples of them, searched in shared memory), then their pages, then writes whole passes of its threads; a thread
 // keeps its 16 channels of a head (8 bytes of codes and a scale) while rows pass, so that where to read is an addition a row, has kBatch
-// loads on their way, and stores 32 bytes of bf16 at once, a line a quarter warp.  Bound by the memory: 131072 tokens of 8 heads of 128
-// channels from 4 bits to bf16 in 105.6 us, 96% of what their bytes take (150 us with places found a piece at a time and 16-byte stores).
-// Rows of e4m3 move half the bytes by as many loads and stores: 32768 tokens in 22 us, 70%.
+// loads on their way, and stores 32 bytes of bf16 at once, two lines a quarter warp.  Bound by the memory: 131072 tokens of 8 heads of 128
+// channels from 4 bits to bf16 in 105 to 106 us, 96% of what their bytes take (150 us with places found a piece at a time and 16-byte stores).
+// Rows of e4m3 move half the bytes by as many loads and stores: 32768 tokens in 21.3 us, 73%.
 //
 // A value is x * f rounded once, with x = code * scale (6 bits for 4-bit caches, exact in fp16) and f = descale * fl(1 / out descale).
 #include <cuda_bf16.h>
@@ -328,7 +328,8 @@ extern "C" zyfa_status_t zyfa_paged_read(const zyfa_paged_cache_t* cache, const 
   zyfa::division_by(cache->page_size, 30, &a.page_magic, &a.page_shift);
   a.step = (B + kReadThreads - 1) / kReadThreads;
   // Rows of a block: whole passes of its threads, 64 KiB to write (96 in e4m3, where the start counts more), but blocks for every SM four
-  // times over.  131072 tokens of 8 heads of 128 as bf16: 105.6 us, with 96 KiB 107.2; 32768 as e4m3 22.0 with 96 KiB, 24.2 with 64.
+  // times over.  131072 tokens of 8 heads of 128 as bf16: 105.9 us, with 96 KiB 107.5; 32768 as e4m3 from 4 bits 21.3 with 96 KiB,
+  // 23.4 with 64, from bf16 34.1 and 35.0, from e4m3 28.8 and 25.2.
   const long long bytes = heads * (cache->D_qk + cache->D_v) * es, pass = std::max(1ll, kReadThreads / std::max(1ll, heads * cache->D_qk / 16));
   const long long most = std::max(pass, (es == 2 ? 65536 : 98304) / bytes / pass * pass), wanted = (N + 4ll * nsm - 1) / (4ll * nsm);
   a.rows = static_cast<int>(std::min<long long>(kMaxRows, std::min(most, (wanted + pass - 1) / pass * pass)));

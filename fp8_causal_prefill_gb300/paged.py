@@ -5,7 +5,8 @@ A serving step runs ``paged_plan`` (pages, slots and positions of its tokens fro
 ``paged_decode_attn`` (one query token per request attends over its pages); prompts go through
 ``flash_attn_func`` on the dense copies that ``rope_paged_store`` can write in the same pass.
 
-``paged_read`` reads tokens back as dense rows, for a prompt whose beginning is cached.
+``paged_read`` reads tokens back as dense rows.  (``flash_attn_func`` takes as many queries as keys: for a prompt behind cached
+tokens it needs rows in the place of the cached tokens' queries, whose results the caller drops.)
 
 A paged cache is a pair of CUDA tensors [num_pages, page_size, H_kv, D]: ``torch.float8_e4m3fn`` (or
 ``torch.uint8`` holding e4m3 codes) or ``torch.bfloat16``.  Only D has to be contiguous, so permuted views
@@ -154,7 +155,7 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     ``seq_lens[b]`` tokens (int32 [B]) of the pages that ``block_table`` (int32 [B, max_pages]) names.
 
     Returns bfloat16 [B, H, D_v] (0 for a request without tokens), and with ``return_lse`` also the float32
-    log-sum-exp [B, H] (-inf without tokens).  e4m3 descales hold one value, H_kv values, as ``rope_paged_store`` takes
+    log-sum-exp [B, H] (-inf without tokens).  e4m3 and 4-bit descales, of either sign, hold one value, H_kv values, as ``rope_paged_store`` takes
     them, or B * H_kv values ([request][KV head]); for a bf16 cache they are not used.
     ``workspace`` (uint8 CUDA, ``paged_decode_workspace_bytes``) is allocated per call if not given; calls that
     may overlap on the GPU need one each.  A NaN among a row's scores makes the row NaN.

@@ -356,8 +356,8 @@ zyfa_status_t zyfa_rope_paged_store_e2m1(const void* q, const void* k, const voi
                                          cudaStream_t stream);
 
 /*
- * zyfa_paged_read - read tokens of a paged cache back as dense rows, as zyfa_attn_fwd_causal reads keys and values (a prompt
- * whose beginning is cached, a cache that moves).
+ * zyfa_paged_read - read tokens of a paged cache back as dense rows, laid out as zyfa_attn_fwd_causal reads keys and values (which takes as
+ * many queries as keys), for an attention of fewer queries than keys or a cache that moves.
  *
  * Row n holds token starts[b] + n - cu_tokens[b] of the request b with cu_tokens[b] <= n < cu_tokens[b + 1]:
  *
@@ -367,7 +367,8 @@ zyfa_status_t zyfa_rope_paged_store_e2m1(const void* q, const void* k, const voi
  *                       left as they were; tokens that N has no row for are not read.
  *   starts              [B] int32, or NULL: every run begins with token 0.
  *   k_out, v_out, N     dense [N][H_kv][D_qk] and [N][H_kv][D_v] of out_dtype, ZYFA_DTYPE_BF16 or ZYFA_DTYPE_E4M3, 16-byte
- *                       aligned; one of the two may be NULL.  They must not overlap one another, the inputs or the cache.
+ *                       aligned; one of the two may be NULL.  They must not overlap one another, the inputs or the cache (none of its
+ *                       bytes from the first row to the last one's end, also those between rows).
  *   k/v_descale         of the cache, not used if that is bf16: device pointers to one float, to [B][H_kv] floats with
  *                       descale_per_kv_head = 1, to [H_kv] floats with 3; NULL means 1.
  *   k/v_out_descale     of what is written, e4m3 only: one float, or [H_kv] floats with out_descale_per_kv_head = 1; NULL means 1.
@@ -397,7 +398,7 @@ zyfa_status_t zyfa_paged_read(const zyfa_paged_cache_t* cache, const zyfa_paged_
  *   lse               NULL, or [B][H] floats: ln sum_j exp(scale q.k) in real units, -inf without tokens.
  *   softmax_scale     0 selects 1/sqrt(D_qk); negative, NaN or infinite values are rejected.
  *   q/k/v_descale     e4m3 only: one float, or with descale_per_kv_head = 1 [B][H_kv] floats, with 3 [H_kv] floats that
- *                     all requests share, as zyfa_rope_paged_store takes them; NULL means 1.
+ *                     all requests share, as zyfa_rope_paged_store takes them; NULL means 1.  Of either sign.
  *                     out and lse must not overlap the inputs or the workspace.
  *   workspace         device scratch of zyfa_attn_decode_paged_workspace_bytes() bytes, 16-byte aligned; its
  *                     contents on entry do not matter.  Calls that may overlap on the GPU (other streams, two
