@@ -156,3 +156,39 @@ def test_scores_far_from_zero(kind, kd, page, exponent, away):
                     assert np.all(err <= tol), (where, out[b, h][:4], ref[:4])
                     assert abs(lse[b, h] - ref_lse) <= lse_tol, (where, float(lse[b, h]), ref_lse)
             assert np.isfinite(out).all() and np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("page", [16, 7])
+@pytest.mark.parametrize("shape,H,H_kv,tile", FORMS)
+@pytest.mark.parametrize("kind", ["e2m1", "fp8", "bf16"])
+def test_one_score_beyond_float32(kind, shape, H, H_kv, tile, page):
+    """One key's score overflows, anywhere among the tiles; all others are 0.  +inf makes the row NaN, -inf weighs nothing."""
+    rng = np.random.default_rng(page)
+    d_qk, d_v = SHAPES[shape]
+    for lens, width, of in _ways(tile):
+        c, B = _Cache(kind, shape, lens, H_kv, page, width, rng), len(of)
+        where = rng.integers(0, np.array(lens))
+        for b, n in enumerate(lens):
+            k = np.zeros((n, H_kv, d_qk))
+            k[where[b], :, 0] = 448.0
+            c.put(0, b, k)
+            c.put(1, b, rng.standard_normal((n, H_kv, d_v)) * 64.0)
+        sign = rng.choice([-1.0, 0.0, 1.0], (B, H))
+        q = torch.zeros((B, H, d_qk))
+        q[:, :, 0] = torch.from_numpy(sign * 448.0).float()
+        q[:, :, 1] = 0.5
+        out, lse = c.attend(q.to(E4M3 if kind == "fp8" else torch.bfloat16).cuda(), of, 1e37)
+        for b in range(0, B, 1 + B // 20):
+            for h in range(H):
+                v, at = c.rows[1][of[b]][:, h // (H // H_kv)], where[of[b]]
+                if sign[b, h] > 0:
+                    assert np.isnan(out[b, h]).all() and np.isnan(lse[b, h]), (width, b, h)
+                    continue
+                v = np.delete(v, at, axis=0) if sign[b, h] < 0 else v
+                if len(v) == 0:
+                    assert (out[b, h] == 0).all() and lse[b, h] == -math.inf, (width, b, h)
+                    continue
+                # equal weights are exact; n of them and of their products are summed in fp32, then out rounds to bf16
+                tol = 2.0 ** -8 * np.abs(v.mean(0)) * 1.01 + (len(v) + 8) * 2.0 ** -23 * np.abs(v).mean(0)
+                assert np.all(np.abs(out[b, h] - v.mean(0)) <= tol), (width, b, h)
+                assert abs(lse[b, h] - math.log(len(v))) <= (len(v) + 8) * 2.0 ** -23 + 2.0 ** -19, (width, b, h)
